@@ -7,8 +7,10 @@ fallback path).
 """
 from __future__ import annotations
 
+import collections
 import contextlib
 import ctypes
+import math
 import os
 
 import torch
@@ -48,6 +50,14 @@ EXPORTS = ("fp8_scaled_mm", "fp8_scaled_mm_with_config", "fp8_scaled_mm_with_pla
 (Q_OK, Q_ERR_NULL, Q_ERR_SHAPE, Q_ERR_ALIGN, Q_ERR_MODE, Q_ERR_DEVICE, Q_ERR_LAUNCH,
  Q_ERR_WORKSPACE) = range(8)
 _Q_ARG_ERRORS = {Q_ERR_NULL, Q_ERR_SHAPE, Q_ERR_ALIGN, Q_ERR_MODE, Q_ERR_WORKSPACE}
+
+# functions and status codes from include/fp8_layer_norm.h
+LAYER_NORM_EXPORTS = ("fp8_layer_norm", "fp8_layer_norm_backward",
+                      "fp8_layer_norm_backward_workspace_size", "fp8_layer_norm_status_string")
+(LN_OK, LN_ERR_NULL, LN_ERR_SHAPE, LN_ERR_ALIGN, LN_ERR_DTYPE, LN_ERR_DEVICE, LN_ERR_LAUNCH,
+ LN_ERR_WORKSPACE, LN_ERR_VALUE) = range(9)
+_LN_ARG_ERRORS = {LN_ERR_NULL, LN_ERR_SHAPE, LN_ERR_ALIGN, LN_ERR_DTYPE, LN_ERR_WORKSPACE,
+                  LN_ERR_VALUE}
 
 
 class Fp8MMError(RuntimeError):
@@ -109,6 +119,16 @@ def lib() -> ctypes.CDLL:
         L.fp8_quantize_set_wait_limit_us.restype = i64
         L.fp8_quantize_status_string.argtypes = [i32]
         L.fp8_quantize_status_string.restype = ctypes.c_char_p
+        f32 = ctypes.c_float
+        L.fp8_layer_norm.argtypes = [vp, i32, vp, vp, i32, f32, vp, vp, i32, vp, vp, vp, i64, i64, vp]
+        L.fp8_layer_norm.restype = i32
+        L.fp8_layer_norm_backward.argtypes = [vp, vp, i32, vp, vp, vp, i32, vp, vp, vp, vp, i64, i64,
+                                              vp, i64, vp]
+        L.fp8_layer_norm_backward.restype = i32
+        L.fp8_layer_norm_backward_workspace_size.argtypes = [i64, i64]
+        L.fp8_layer_norm_backward_workspace_size.restype = i64
+        L.fp8_layer_norm_status_string.argtypes = [i32]
+        L.fp8_layer_norm_status_string.restype = ctypes.c_char_p
         _lib = L
     return _lib
 
@@ -335,3 +355,166 @@ def fp8_quantize(x: torch.Tensor, mode="rowwise", q: torch.Tensor | None = None,
             raise ValueError(msg)
         raise RuntimeError(msg)
     return q, scale
+
+
+# element types of the layer norm (enum fp8ln_dtype)
+_LN_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+LayerNormResult = collections.namedtuple("LayerNormResult", "y q scale mean rstd")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _on_device(dev: int):
+    """The library launches on the current HIP device: a context that makes
+    `dev` current (nothing to do in the usual case)."""
+    return torch.cuda.device(dev) if torch.cuda.current_device() != dev else contextlib.nullcontext()
+
+
+def _ln_matrix(t, name: str, like: torch.Tensor | None = None) -> None:
+    if like is None:
+        if t.dtype not in _LN_DTYPES or t.dim() != 2 or not t.is_contiguous() or not t.is_cuda:
+            raise ValueError(f"{name} must be a contiguous 2-D bf16 or fp32 GPU tensor")
+    elif t.dtype != like.dtype or t.shape != like.shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {like.dtype} tensor of shape {tuple(like.shape)}")
+
+
+def _ln_params(cols: int, params) -> int:
+    """The common type of w and b (None skipped), as the library's code."""
+    code = None
+    for name, t in params:
+        if t is None:
+            continue
+        if t.dtype not in _LN_DTYPES or t.numel() != cols or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous fp32 or bf16 vector of {cols} elements")
+        if code is not None and code != _LN_DTYPES[t.dtype]:
+            raise ValueError("w and b must have one type")
+        code = _LN_DTYPES[t.dtype]
+    return 1 if code is None else code
+
+
+def _ln_vector(t, name: str, n: int) -> None:
+    if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of {n} elements")
+
+
+def _ln_check(fn: str, st: int) -> None:
+    if st == LN_OK:
+        return
+    msg = f"{fn}: {lib().fp8_layer_norm_status_string(st).decode()} (status {st})"
+    raise ValueError(msg) if st in _LN_ARG_ERRORS else RuntimeError(msg)
+
+
+def fp8_layer_norm(x: torch.Tensor, w: torch.Tensor | None = None, b: torch.Tensor | None = None,
+                   eps: float = 1e-5, *, y=True, fmt=None, stats: bool = False,
+                   q: torch.Tensor | None = None,
+                   scale: torch.Tensor | None = None) -> LayerNormResult:
+    """Layer norm over the last axis of a rows x cols bf16 or fp32 matrix, with
+    the row-wise float8 quantisation of its result:
+
+        y = (x - mean) * rstd * w + b,   rstd = 1 / sqrt(var + eps)
+        scale = max|y| / qmax for each row,   q = RNE(y / scale)
+
+    w and b (fp32 or bf16; None: ones, zeros) have cols elements.  `y` is True
+    (allocate), False (not wanted) or a tensor to write; fmt 'e4m3fn' or 'e5m2'
+    asks for the codes (uint8) and their scales, in `q` and `scale` if given
+    (then cols must be a multiple of 16); stats=True returns mean and rstd,
+    which fp8_layer_norm_backward takes.  The codes come from the fp32 y.  A row
+    that holds a NaN or an infinity gives NaN in all of its outputs."""
+    _ln_matrix(x, "x")
+    rows, cols = x.shape
+    if cols == 0:
+        raise ValueError("x needs at least one column")
+    if fmt is not None and fmt not in _FORMATS:
+        raise ValueError(f"fmt must be 'e4m3fn', 'e5m2' or None, got {fmt!r}")
+    if isinstance(y, torch.Tensor):
+        _ln_matrix(y, "y", x)
+    elif y not in (True, False):
+        raise ValueError("y must be True, False or a tensor to write")
+    if y is False and fmt is None:
+        raise ValueError("nothing to compute: y=False and fmt=None")
+    if fmt is None and (q is not None or scale is not None):
+        raise ValueError("q and scale need fmt")
+    if fmt is not None and cols % 16 != 0:
+        raise ValueError(f"codes need a number of columns that is a multiple of 16, got {cols}")
+    if not (math.isfinite(eps) and eps >= 0):
+        raise ValueError(f"eps must be finite and not negative, got {eps}")
+    pdt = _ln_params(cols, (("w", w), ("b", b)))
+    dev = x.get_device()
+    _check_devices(dev, (("w", w), ("b", b), ("q", q), ("scale", scale),
+                         ("y", y if isinstance(y, torch.Tensor) else None)))
+    device = x.device
+    out = y if isinstance(y, torch.Tensor) else torch.empty_like(x) if y else None
+    f = 0
+    if fmt is not None:
+        f = _FORMATS[fmt]
+        if q is None:
+            q = torch.empty((rows, cols), dtype=torch.uint8, device=device)
+        elif q.dtype not in (torch.uint8, torch.float8_e4m3fn if f == E4M3FN else torch.float8_e5m2) \
+                or tuple(q.shape) != (rows, cols) or not q.is_contiguous():
+            raise ValueError(f"q must be a contiguous uint8 (or float8_{fmt}) rows x cols tensor")
+        if scale is None:
+            scale = torch.empty(rows, dtype=torch.float32, device=device)
+        else:
+            _ln_vector(scale, "scale", rows)
+    mean = rstd = None
+    if stats:
+        mean = torch.empty(rows, dtype=torch.float32, device=device)
+        rstd = torch.empty(rows, dtype=torch.float32, device=device)
+    with _on_device(dev):
+        st = lib().fp8_layer_norm(x.data_ptr(), _LN_DTYPES[x.dtype], _ptr(w), _ptr(b), pdt, eps,
+                                  _ptr(out), _ptr(q), f, _ptr(scale), _ptr(mean), _ptr(rstd),
+                                  rows, cols, _stream_of(dev))
+    _ln_check("fp8_layer_norm", st)
+    return LayerNormResult(out, q, scale, mean, rstd)
+
+
+def fp8_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
+                            rstd: torch.Tensor, w: torch.Tensor | None = None, *,
+                            residual_grad: torch.Tensor | None = None,
+                            dx: torch.Tensor | None = None,
+                            workspace: torch.Tensor | None = None):
+    """(dx, dw, db) of the layer norm above, from the gradient dy of y, its
+    input x and the forward call's mean and rstd.  residual_grad is added to dx
+    (in fp32) where x also went along a residual path.  dx has x's type (`dx`
+    may be passed to reuse a buffer), dw and db are fp32.  The partial column
+    sums go to `workspace` (a GPU byte tensor) or to one that this module keeps
+    per stream.  The sums' order is fixed: equal calls give equal bits."""
+    _ln_matrix(x, "x")
+    _ln_matrix(dy, "dy", x)
+    rows, cols = x.shape
+    if cols == 0:
+        raise ValueError("x needs at least one column")
+    _ln_vector(mean, "mean", rows)
+    _ln_vector(rstd, "rstd", rows)
+    pdt = _ln_params(cols, (("w", w),))
+    for name, t in (("residual_grad", residual_grad), ("dx", dx)):
+        if t is not None:
+            _ln_matrix(t, name, x)
+    dev = x.get_device()
+    _check_devices(dev, (("dy", dy), ("mean", mean), ("rstd", rstd), ("w", w), ("dx", dx),
+                         ("residual_grad", residual_grad), ("workspace", workspace)))
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous GPU tensor")
+    if dx is None:
+        dx = torch.empty_like(x)
+    dw = torch.empty(cols, dtype=torch.float32, device=x.device)
+    db = torch.empty(cols, dtype=torch.float32, device=x.device)
+    L = lib()
+    stream = _stream_of(dev)
+    with _on_device(dev):
+        need = int(L.fp8_layer_norm_backward_workspace_size(rows, cols))
+        if workspace is not None:
+            ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        elif need > 0:
+            ws, ws_bytes = _workspace(x.device, stream, need, "layer_norm").data_ptr(), need
+        else:
+            ws, ws_bytes = None, 0
+        st = L.fp8_layer_norm_backward(dy.data_ptr(), x.data_ptr(), _LN_DTYPES[x.dtype],
+                                       mean.data_ptr(), rstd.data_ptr(), _ptr(w), pdt,
+                                       _ptr(residual_grad), dx.data_ptr(), dw.data_ptr(),
+                                       db.data_ptr(), rows, cols, ws, ws_bytes, stream)
+    _ln_check("fp8_layer_norm_backward", st)
+    return dx, dw, db

@@ -1,5 +1,5 @@
-"""Builds libfp8_scaled_mm.so (the HIP kernels -- scaled multiply and
-quantiser -- and their C ABI) for gfx950.
+"""Builds libfp8_scaled_mm.so (the HIP kernels -- scaled multiply,
+quantiser and layer norm -- and their C ABI) for gfx950.
 
 hipcc cross-compiles without a GPU.  The library is written next to this
 file so that it travels with the source tree.
@@ -15,10 +15,10 @@ import tempfile
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 # The host logic and C ABI, one translation unit per operand-format pair of
-# the multiply's kernels, and the quantiser.  They compile in parallel.
+# the multiply's kernels, the quantiser and the layer norm.  They compile in parallel.
 SRCS = [os.path.join(HERE, "csrc", f) for f in
-        ["fp8_scaled_mm.hip"] + [f"fp8_gemm_f{k}.hip" for k in range(4)] + ["fp8_quantize.hip"]]
-HEADERS = [os.path.join(HERE, "csrc", "fp8_gemm_kernels.h")]
+        ["fp8_scaled_mm.hip"] + [f"fp8_gemm_f{k}.hip" for k in range(4)] + ["fp8_quantize.hip", "fp8_layer_norm.hip"]]
+HEADERS = [os.path.join(HERE, "csrc", f) for f in ("fp8_gemm_kernels.h", "fp8_convert.h")]
 LIB = os.path.join(HERE, "libfp8_scaled_mm.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -46,7 +46,7 @@ def _run(cmd, verbose):
 SANITIZE_HOST = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
                  "-Xarch_host", "-fno-sanitize-recover=undefined",
                  "-Xarch_host", "-fno-omit-frame-pointer", "-Xarch_host", "-g"]
-HOST_LOGIC_SRCS = {"fp8_scaled_mm.hip", "fp8_quantize.hip"}
+HOST_LOGIC_SRCS = {"fp8_scaled_mm.hip", "fp8_quantize.hip", "fp8_layer_norm.hip"}
 
 
 def build(verbose: bool = False, sanitize: bool = False, out: str | None = None) -> str:

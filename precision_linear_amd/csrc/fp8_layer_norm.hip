@@ -1,0 +1,935 @@
+// Layer norm and its gradient for gfx950 (MI355X), with the float8
+// quantisation of the normalised rows (formulas: include/fp8_layer_norm.h).
+//
+// HBM-bound: every element is read once and written once.  A row stays in
+// registers between its statistics and its output.
+//
+// Layout: a row belongs to W waves (W = ceil(cols / 1024), at most 16); lane t
+// of them holds V = 2 vectors of 8 consecutive elements, vectors t and
+// t + 64 W, and where cols is no multiple of 8 the first cols % 8 lanes hold
+// one element more.  A thread's columns are the same for every row it meets, so
+// w and b (8 bytes of parameters to 2 bytes of bf16 x) and, in the gradient,
+// the sums of dw and db stay in registers over the workgroup's rows.  Rows of
+// more than 16384 + 7 elements take the *_long kernels, which sweep the row
+// (from L2) instead of holding it.
+//
+// Rows that do not start on a 16-byte boundary (cols % 8 != 0) are read and
+// written with the same 16-byte instructions: global memory takes any 2-byte
+// aligned address.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <cmath>
+
+#include "../../include/fp8_layer_norm.h"
+#include "fp8_convert.h"
+
+namespace {
+
+constexpr int kWaveSize = 64;
+constexpr int kVecs = 2;                     // vectors of 8 elements per lane
+constexpr int kMaxWaves = 16;                // waves per row (and per workgroup)
+constexpr int64_t kHeldCols = (int64_t)kMaxWaves * kWaveSize * kVecs * 8 + 7;
+constexpr int kLongThreads = 1024;
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
+
+typedef uint16_t bf16_t;
+
+// ------------------------------------------------------------ elements ---
+
+// 8 consecutive elements as they lie in memory.
+template <class T> struct Raw8;
+template <> struct Raw8<bf16_t> {
+    u32x4 v;
+    __device__ __forceinline__ void load(const bf16_t* p) { v = *reinterpret_cast<const u32x4_a2*>(p); }
+    __device__ __forceinline__ void zero() { v = u32x4{0u, 0u, 0u, 0u}; }
+    __device__ __forceinline__ float get(int i) const {
+        const uint32_t w = v[i / 2];
+        return i % 2 ? bf16_hi(w) : bf16_lo(w);
+    }
+};
+template <> struct Raw8<float> {
+    u32x4 v[2];
+    __device__ __forceinline__ void load(const float* p) {
+        v[0] = *reinterpret_cast<const u32x4_a4*>(p);
+        v[1] = *reinterpret_cast<const u32x4_a4*>(p + 4);
+    }
+    __device__ __forceinline__ void zero() { v[0] = v[1] = u32x4{0u, 0u, 0u, 0u}; }
+    __device__ __forceinline__ float get(int i) const { return __uint_as_float(v[i / 4][i % 4]); }
+};
+
+__device__ __forceinline__ float load1(const bf16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+
+// fp32 -> bf16, round to nearest even.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{lo, hi}, bf2));
+}
+
+__device__ __forceinline__ void store8(bf16_t* p, const float (&f)[8]) {
+    *reinterpret_cast<u32x4_a2*>(p) = u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
+                                            pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
+}
+__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<u32x4_a4*>(p + 4 * h) =
+            u32x4{__float_as_uint(f[4 * h]), __float_as_uint(f[4 * h + 1]), __float_as_uint(f[4 * h + 2]),
+                  __float_as_uint(f[4 * h + 3])};
+}
+__device__ __forceinline__ void store1(bf16_t* p, float f) { *p = (bf16_t)pack_bf16(f, f); }
+__device__ __forceinline__ void store1(float* p, float f) { *p = f; }
+
+// w or b at column c .. c + 7 (fp32 or bf16; null: `none`).
+__device__ __forceinline__ void load_param8(const void* p, int bf16, int64_t c, float none, float (&f)[8]) {
+    if (!p) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = none;
+    } else if (bf16) {
+        Raw8<bf16_t> r;
+        r.load(static_cast<const bf16_t*>(p) + c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = r.get(i);
+    } else {
+        Raw8<float> r;
+        r.load(static_cast<const float*>(p) + c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = r.get(i);
+    }
+}
+__device__ __forceinline__ float load_param1(const void* p, int bf16, int64_t c, float none) {
+    if (!p) return none;
+    return bf16 ? load1(static_cast<const bf16_t*>(p) + c) : load1(static_cast<const float*>(p) + c);
+}
+
+// ----------------------------------------------------------- reductions ---
+
+// Lane exchanges inside a row of 16 lanes (DPP: no LDS round trip).
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+constexpr int kSwap1 = 0xB1;         // quad_perm [1, 0, 3, 2]
+constexpr int kSwap2 = 0x4E;         // quad_perm [2, 3, 0, 1]
+constexpr int kHalfMirror = 0x141;   // lane i of 8 reads lane 7 - i
+constexpr int kMirror = 0x140;       // lane i of 16 reads lane 15 - i
+
+__device__ __forceinline__ float lane_value(float x, int lane) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
+}
+
+// Sum over each row of 16 lanes, in every lane of it.
+__device__ __forceinline__ float row16_sum(float x) {
+    x += dpp<kSwap1>(x);
+    x += dpp<kSwap2>(x);
+    x += dpp<kHalfMirror>(x);
+    return x + dpp<kMirror>(x);
+}
+__device__ __forceinline__ float row16_max(float x) {
+    x = fmaxf(x, dpp<kSwap1>(x));
+    x = fmaxf(x, dpp<kSwap2>(x));
+    x = fmaxf(x, dpp<kHalfMirror>(x));
+    return fmaxf(x, dpp<kMirror>(x));
+}
+// Over the wave; every lane active, every lane returns the same.
+__device__ __forceinline__ float wave_sum(float x) {
+    x = row16_sum(x);
+    return (lane_value(x, 0) + lane_value(x, 16)) + (lane_value(x, 32) + lane_value(x, 48));
+}
+__device__ __forceinline__ float wave_max(float x) {
+    x = row16_max(x);
+    return fmaxf(fmaxf(lane_value(x, 0), lane_value(x, 16)), fmaxf(lane_value(x, 32), lane_value(x, 48)));
+}
+
+// ------------------------------------------------------------- forward ---
+
+struct LnFwd {
+    const void* x;
+    const void* w;
+    const void* b;
+    int param_bf16;
+    float eps;
+    void* y;
+    uint8_t* q;
+    int q_format;
+    float* scale;
+    float* mean;
+    float* rstd;
+    int64_t rows;
+    int64_t cols;
+    int waves;   // W, waves per row
+};
+
+// 8 codes of y / scale.  `slow` covers scales outside the fast division's
+// range: 0 (every finite y is 0 or rounds to it), tiny, infinite and NaN ones.
+template <int FMT>
+__device__ __forceinline__ u32x2 codes8(const float (&y)[8], const Div& d) {
+    float t[8];
+    if (d.fast) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = div_fast(y[i], d);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = d.s == 0.f ? fabsf(y[i]) : quant1<FMT, false>(y[i], d);
+    }
+    u32x2 out;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        int pk = Fp8Fmt<FMT>::template cvt_pk<false>(t[4 * h], t[4 * h + 1], 0);
+        pk = Fp8Fmt<FMT>::template cvt_pk<true>(t[4 * h + 2], t[4 * h + 3], pk);
+        out[h] = (uint32_t)pk;
+    }
+    return out;
+}
+
+// The scale of a row from its largest |y| (NaN skipped): a row whose
+// statistics are NaN gets a NaN scale, not the 0 of an empty maximum.
+template <int FMT>
+__device__ __forceinline__ float row_scale(float amax, float rstd) {
+    return rstd != rstd ? rstd : amax / Fp8Fmt<FMT>::kMax;
+}
+
+// One row per W waves.  WIDE: the workgroup is the row's W > 1 waves, which
+// meet in LDS; otherwise each wave has a row of its own.
+//
+// Variance: each wave takes the mean of its own share and the squares around
+// that mean, and the shares are joined with
+//   M2 = sum_w( M2_w + n_w (mean_w - mean)^2 )
+// (T. Chan, G. Golub, R. LeVeque, 1979), which costs one meeting of the waves
+// and loses nothing to a mean far from 0.
+template <class T, bool WIDE>
+__global__ void __launch_bounds__(kMaxWaves* kWaveSize)
+ln_forward_kernel(LnFwd p) {
+    __shared__ float2 s_mom[2][kMaxWaves];
+    __shared__ float s_max[2][kMaxWaves];
+    const int lane = threadIdx.x % kWaveSize;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveSize);
+    const int W = WIDE ? p.waves : 1;
+    const int t = WIDE ? (int)threadIdx.x : lane;          // lane of the row
+    const int tw = W * kWaveSize;
+    const int cols = (int)p.cols;
+    const int nv = cols / 8;                               // whole vectors in a row
+    const bool has_tail = t < cols % 8;
+    const int ct = nv * 8 + t;                             // this lane's tail column
+    bool ok[kVecs];
+    float w[kVecs][8], b[kVecs][8], wt = 0.f, bt = 0.f;
+    int cnt = 0;
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+        ok[v] = t + v * tw < nv;
+        cnt += 8 * __popcll(__ballot(ok[v]));
+    }
+    cnt += __popcll(__ballot(has_tail));
+    const float n_w = (float)cnt;
+    const float inv_nw = cnt ? 1.f / n_w : 0.f;
+    const float inv_n = 1.f / (float)cols;
+
+    const T* x = static_cast<const T*>(p.x);
+    T* y = static_cast<T*>(p.y);
+    const int64_t first = WIDE ? blockIdx.x : (int64_t)blockIdx.x * (blockDim.x / kWaveSize) + wave;
+    const int64_t step = WIDE ? gridDim.x : (int64_t)gridDim.x * (blockDim.x / kWaveSize);
+
+    Raw8<T> next[kVecs];
+    float next_t = 0.f;
+    auto fetch = [&](int64_t r) {
+        const T* xr = x + r * p.cols;
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v)
+            if (ok[v]) next[v].load(xr + (t + v * tw) * 8);
+        if (has_tail) next_t = load1(xr + ct);
+    };
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) next[v].zero();
+    if (first < p.rows) fetch(first);
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+        if (ok[v]) {
+            load_param8(p.w, p.param_bf16, (t + v * tw) * 8, 1.f, w[v]);
+            load_param8(p.b, p.param_bf16, (t + v * tw) * 8, 0.f, b[v]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[v][i] = b[v][i] = 0.f;
+        }
+    }
+    if (has_tail) {
+        wt = load_param1(p.w, p.param_bf16, ct, 1.f);
+        bt = load_param1(p.b, p.param_bf16, ct, 0.f);
+    }
+
+    int parity = 0;
+    for (int64_t r = first; r < p.rows; r += step, parity ^= 1) {
+        float f[kVecs][8], ft = next_t;
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[v][i] = next[v].get(i);
+        if (r + step < p.rows) fetch(r + step);
+
+        float s = ft;   // lanes and vectors without elements hold zeros
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s += f[v][i];
+        s = wave_sum(s);
+        const float m_w = s * inv_nw;
+        float m2 = 0.f;
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v)
+            if (ok[v])
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float d = f[v][i] - m_w;
+                    m2 = fmaf(d, d, m2);
+                }
+        if (has_tail) m2 = fmaf(ft - m_w, ft - m_w, m2);
+        m2 = wave_sum(m2);
+        float mean = m_w;
+        if constexpr (WIDE) {
+            if (lane == 0) s_mom[parity][wave] = float2{s, m2};
+            __syncthreads();
+            // Lane l of each 16 takes wave l's share.
+            const int l = lane % 16;
+            const float2 mom = l < W ? s_mom[parity][l] : float2{0.f, 0.f};
+            mean = lane_value(row16_sum(mom.x), 0) * inv_n;
+            int c = 0;       // elements of wave l
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v)
+                c += 8 * min(kWaveSize, max(0, nv - v * tw - l * kWaveSize));
+            c += l == 0 ? cols % 8 : 0;
+            const float d = c ? mom.x / (float)c - mean : 0.f;
+            m2 = lane_value(row16_sum(l < W ? fmaf((float)c * d, d, mom.y) : 0.f), 0);
+        }
+        const float rstd = 1.f / sqrtf(m2 * inv_n + p.eps);
+
+        float amax = 0.f;
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                f[v][i] = fmaf((f[v][i] - mean) * rstd, w[v][i], b[v][i]);
+                if (ok[v]) amax = fmaxf(amax, fabsf(f[v][i]));
+            }
+        ft = fmaf((ft - mean) * rstd, wt, bt);
+        if (p.y) {
+            T* yr = y + r * p.cols;
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v)
+                if (ok[v]) store8(yr + (t + v * tw) * 8, f[v]);
+            if (has_tail) store1(yr + ct, ft);
+        }
+        if (p.q) {   // cols % 16 == 0: no tail
+            amax = wave_max(amax);
+            if constexpr (WIDE) {
+                if (lane == 0) s_max[parity][wave] = amax;
+                __syncthreads();
+                amax = lane_value(row16_max(lane % 16 < W ? s_max[parity][lane % 16] : 0.f), 0);
+            }
+            uint8_t* qr = p.q + r * p.cols;
+            auto write = [&](auto fmt) {
+                constexpr int FMT = decltype(fmt)::value;
+                const float sc = row_scale<FMT>(amax, rstd);
+                if (t == 0) p.scale[r] = sc;
+                const Div d = make_div(sc);
+#pragma unroll
+                for (int v = 0; v < kVecs; ++v)
+                    if (ok[v]) *reinterpret_cast<u32x2*>(qr + (t + v * tw) * 8) = codes8<FMT>(f[v], d);
+            };
+            if (p.q_format == FP8LN_E4M3FN) write(std::integral_constant<int, 0>{});
+            else write(std::integral_constant<int, 1>{});
+        }
+        if (p.mean && t == 0) {
+            p.mean[r] = mean;
+            p.rstd[r] = rstd;
+        }
+    }
+}
+
+// Sum and maximum over a workgroup of kLongThreads (every thread returns them).
+__device__ __forceinline__ float block_sum(float x, float* red) {
+    x = wave_sum(x);
+    __syncthreads();   // red may still be read by the last reduction
+    if (threadIdx.x % kWaveSize == 0) red[threadIdx.x / kWaveSize] = x;
+    __syncthreads();
+    return lane_value(row16_sum(red[threadIdx.x % 16]), 0);
+}
+__device__ __forceinline__ float block_maximum(float x, float* red) {
+    x = wave_max(x);
+    __syncthreads();
+    if (threadIdx.x % kWaveSize == 0) red[threadIdx.x / kWaveSize] = x;
+    __syncthreads();
+    return lane_value(row16_max(red[threadIdx.x % 16]), 0);
+}
+
+// Calls f(column, count) for this thread's vectors of 8 columns and, for the
+// last cols % 8 columns, single ones.
+template <class F8, class F1>
+__device__ __forceinline__ void for_columns(int64_t cols, F8 f8, F1 f1) {
+    const int64_t nv = cols / 8;
+    for (int64_t g = threadIdx.x; g < nv; g += kLongThreads) f8(g * 8);
+    if (threadIdx.x < cols % 8) f1(nv * 8 + threadIdx.x);
+}
+
+// Rows of any length, one workgroup each, swept once per step of the formula
+// (sum, squares, maximum where codes are made, output).
+template <class T>
+__global__ void __launch_bounds__(kLongThreads)
+ln_forward_long_kernel(LnFwd p) {
+    __shared__ float red[kMaxWaves];
+    for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
+        const T* xr = static_cast<const T*>(p.x) + r * p.cols;
+        float s = 0.f;
+        for_columns(p.cols,
+                    [&](int64_t c) {
+                        Raw8<T> v;
+                        v.load(xr + c);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) s += v.get(i);
+                    },
+                    [&](int64_t c) { s += load1(xr + c); });
+        const float mean = block_sum(s, red) / (float)p.cols;
+        float m2 = 0.f;
+        for_columns(p.cols,
+                    [&](int64_t c) {
+                        Raw8<T> v;
+                        v.load(xr + c);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) m2 = fmaf(v.get(i) - mean, v.get(i) - mean, m2);
+                    },
+                    [&](int64_t c) { m2 = fmaf(load1(xr + c) - mean, load1(xr + c) - mean, m2); });
+        const float rstd = 1.f / sqrtf(block_sum(m2, red) / (float)p.cols + p.eps);
+        auto y8 = [&](int64_t c, float (&f)[8]) {
+            Raw8<T> v;
+            float w[8], b[8];
+            v.load(xr + c);
+            load_param8(p.w, p.param_bf16, c, 1.f, w);
+            load_param8(p.b, p.param_bf16, c, 0.f, b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = fmaf((v.get(i) - mean) * rstd, w[i], b[i]);
+        };
+        if (p.y) {
+            T* yr = static_cast<T*>(p.y) + r * p.cols;
+            for_columns(p.cols,
+                        [&](int64_t c) {
+                            float f[8];
+                            y8(c, f);
+                            store8(yr + c, f);
+                        },
+                        [&](int64_t c) {
+                            store1(yr + c, fmaf((load1(xr + c) - mean) * rstd,
+                                                load_param1(p.w, p.param_bf16, c, 1.f),
+                                                load_param1(p.b, p.param_bf16, c, 0.f)));
+                        });
+        }
+        if (p.q) {
+            float amax = 0.f;
+            for_columns(p.cols,
+                        [&](int64_t c) {
+                            float f[8];
+                            y8(c, f);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
+                        },
+                        [&](int64_t) {});
+            amax = block_maximum(amax, red);
+            uint8_t* qr = p.q + r * p.cols;
+            auto write = [&](auto fmt) {
+                constexpr int FMT = decltype(fmt)::value;
+                const float sc = row_scale<FMT>(amax, rstd);
+                if (threadIdx.x == 0) p.scale[r] = sc;
+                const Div d = make_div(sc);
+                for_columns(p.cols,
+                            [&](int64_t c) {
+                                float f[8];
+                                y8(c, f);
+                                *reinterpret_cast<u32x2*>(qr + c) = codes8<FMT>(f, d);
+                            },
+                            [&](int64_t) {});
+            };
+            if (p.q_format == FP8LN_E4M3FN) write(std::integral_constant<int, 0>{});
+            else write(std::integral_constant<int, 1>{});
+        }
+        if (p.mean && threadIdx.x == 0) {
+            p.mean[r] = mean;
+            p.rstd[r] = rstd;
+        }
+    }
+}
+
+// ------------------------------------------------------------ backward ---
+
+struct LnBwd {
+    const void* dy;
+    const void* x;
+    const float* mean;
+    const float* rstd;
+    const void* w;
+    int param_bf16;
+    const void* res;   // residual gradient, may be null
+    void* dx;
+    float* partial;    // [2][parts][pitch]: sums of dy * xh, then of dy
+    int64_t rows;
+    int64_t cols;
+    int64_t pitch;
+    int waves;         // W
+    int subs;          // rows a workgroup works on at a time
+};
+
+// dx, and this workgroup's share of dw and db.  `subs` rows at a time, W waves
+// each; the sums over a workgroup's rows stay in registers and meet in LDS at
+// the end (a fixed tree over the subs), so a workgroup writes one partial row.
+template <class T>
+__global__ void __launch_bounds__(kMaxWaves* kWaveSize)
+ln_backward_kernel(LnBwd p) {
+    extern __shared__ float s_cols[];             // [subs / 2][2][pitch]
+    __shared__ float2 s_sum[2][kMaxWaves];
+    const int lane = threadIdx.x % kWaveSize;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveSize);
+    const int W = p.waves;
+    const int sub = wave / W;
+    const int wr = wave - sub * W;
+    const int t = wr * kWaveSize + lane;
+    const int tw = W * kWaveSize;
+    const int cols = (int)p.cols;
+    const int nv = cols / 8;
+    const bool has_tail = t < cols % 8;
+    const int ct = nv * 8 + t;
+    const float inv_n = 1.f / (float)cols;
+    bool ok[kVecs];
+    float w[kVecs][8], wt = 0.f;
+    float dw[kVecs][8], db[kVecs][8], dwt = 0.f, dbt = 0.f;
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+        ok[v] = t + v * tw < nv;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[v][i] = dw[v][i] = db[v][i] = 0.f;
+        if (ok[v]) load_param8(p.w, p.param_bf16, (t + v * tw) * 8, 1.f, w[v]);
+    }
+    if (has_tail) wt = load_param1(p.w, p.param_bf16, ct, 1.f);
+
+    const T* x = static_cast<const T*>(p.x);
+    const T* dy = static_cast<const T*>(p.dy);
+    const T* res = static_cast<const T*>(p.res);
+    T* dx = static_cast<T*>(p.dx);
+    const int64_t step = (int64_t)gridDim.x * p.subs;
+    // The residual is loaded with the row where registers allow (fp32 rows
+    // with it would spill).
+    constexpr bool kResEarly = sizeof(T) == 2;
+    int parity = 0;
+    // Every sub goes through the same number of steps (they share barriers);
+    // past the last row it works on zeros and stores nothing.
+    for (int64_t base = (int64_t)blockIdx.x * p.subs; base < p.rows; base += step, parity ^= 1) {
+        const int64_t r = base + sub;
+        const bool live = r < p.rows;
+        Raw8<T> rx[kVecs], rdy[kVecs], rr[kVecs];
+        float xt = 0.f, dyt = 0.f, rt = 0.f;
+        float mean = 0.f, rstd = 0.f;
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v) {
+            rx[v].zero();
+            rdy[v].zero();
+            rr[v].zero();
+        }
+        if (live) {
+            const int64_t off = r * p.cols;
+            mean = p.mean[r];
+            rstd = p.rstd[r];
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v)
+                if (ok[v]) {
+                    rx[v].load(x + off + (t + v * tw) * 8);
+                    rdy[v].load(dy + off + (t + v * tw) * 8);
+                    if (kResEarly && res) rr[v].load(res + off + (t + v * tw) * 8);
+                }
+            if (has_tail) {
+                xt = load1(x + off + ct);
+                dyt = load1(dy + off + ct);
+                if (res) rt = load1(res + off + ct);
+            }
+        }
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v)
+            if (ok[v])
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float d = rdy[v].get(i);
+                    const float xh = (rx[v].get(i) - mean) * rstd;
+                    const float g = d * w[v][i];
+                    s1 += g;
+                    s2 = fmaf(g, xh, s2);
+                    dw[v][i] = fmaf(d, xh, dw[v][i]);
+                    db[v][i] += d;
+                }
+        const float xht = (xt - mean) * rstd;
+        if (has_tail) {
+            const float g = dyt * wt;
+            s1 += g;
+            s2 = fmaf(g, xht, s2);
+            dwt = fmaf(dyt, xht, dwt);
+            dbt += dyt;
+        }
+        s1 = wave_sum(s1);
+        s2 = wave_sum(s2);
+        if (W > 1) {
+            if (lane == 0) s_sum[parity][wave] = float2{s1, s2};
+            __syncthreads();
+            const int l = lane % 16;
+            const float2 o = l < W ? s_sum[parity][sub * W + l] : float2{0.f, 0.f};
+            s1 = lane_value(row16_sum(o.x), 0);
+            s2 = lane_value(row16_sum(o.y), 0);
+        }
+        if (!live) continue;
+        const float c1 = s1 * inv_n, c2 = s2 * inv_n;
+        T* dxr = dx + r * p.cols;
+        if (!kResEarly && res)
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v)
+                if (ok[v]) rr[v].load(res + r * p.cols + (t + v * tw) * 8);
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v)
+            if (ok[v]) {
+                float f[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float xh = (rx[v].get(i) - mean) * rstd;
+                    const float g = rdy[v].get(i) * w[v][i];
+                    f[i] = fmaf(rstd, g - c1 - xh * c2, rr[v].get(i));
+                }
+                store8(dxr + (t + v * tw) * 8, f);
+            }
+        if (has_tail) store1(dxr + ct, fmaf(rstd, dyt * wt - c1 - xht * c2, rt));
+    }
+
+    // Join the subs: the upper half of them hands its sums to the lower half.
+    for (int n = p.subs; n > 1;) {
+        const int half = (n + 1) / 2;
+        float* slot = s_cols + (int64_t)(sub >= half ? sub - half : sub) * 2 * p.pitch;
+        __syncthreads();
+        if (sub >= half && sub < n) {
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v)
+                if (ok[v]) {
+                    store8(slot + (t + v * tw) * 8, dw[v]);
+                    store8(slot + p.pitch + (t + v * tw) * 8, db[v]);
+                }
+            if (has_tail) {
+                slot[ct] = dwt;
+                slot[p.pitch + ct] = dbt;
+            }
+        }
+        __syncthreads();
+        if (sub < n - half) {
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v)
+                if (ok[v])
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        dw[v][i] += slot[(t + v * tw) * 8 + i];
+                        db[v][i] += slot[p.pitch + (t + v * tw) * 8 + i];
+                    }
+            if (has_tail) {
+                dwt += slot[ct];
+                dbt += slot[p.pitch + ct];
+            }
+        }
+        n = half;
+    }
+    if (sub == 0) {
+        float* pw = p.partial + blockIdx.x * p.pitch;
+        float* pb = pw + gridDim.x * p.pitch;
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v)
+            if (ok[v]) {
+                store8(pw + (t + v * tw) * 8, dw[v]);
+                store8(pb + (t + v * tw) * 8, db[v]);
+            }
+        if (has_tail) {
+            pw[ct] = dwt;
+            pb[ct] = dbt;
+        }
+    }
+}
+
+// Long rows: dx, one workgroup per row.
+template <class T>
+__global__ void __launch_bounds__(kLongThreads)
+ln_backward_long_kernel(LnBwd p) {
+    __shared__ float red[kMaxWaves];
+    for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
+        const T* xr = static_cast<const T*>(p.x) + r * p.cols;
+        const T* dyr = static_cast<const T*>(p.dy) + r * p.cols;
+        const T* rr = p.res ? static_cast<const T*>(p.res) + r * p.cols : nullptr;
+        T* dxr = static_cast<T*>(p.dx) + r * p.cols;
+        const float mean = p.mean[r], rstd = p.rstd[r];
+        float s1 = 0.f, s2 = 0.f;
+        auto add = [&](float x, float d, float w) {
+            s1 = fmaf(d, w, s1);
+            s2 = fmaf(d * w, (x - mean) * rstd, s2);
+        };
+        for_columns(p.cols,
+                    [&](int64_t c) {
+                        Raw8<T> vx, vd;
+                        float w[8];
+                        vx.load(xr + c);
+                        vd.load(dyr + c);
+                        load_param8(p.w, p.param_bf16, c, 1.f, w);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) add(vx.get(i), vd.get(i), w[i]);
+                    },
+                    [&](int64_t c) {
+                        add(load1(xr + c), load1(dyr + c), load_param1(p.w, p.param_bf16, c, 1.f));
+                    });
+        const float c1 = block_sum(s1, red) / (float)p.cols;
+        const float c2 = block_sum(s2, red) / (float)p.cols;
+        auto out = [&](float x, float d, float w, float res) {
+            return fmaf(rstd, d * w - c1 - (x - mean) * rstd * c2, res);
+        };
+        for_columns(p.cols,
+                    [&](int64_t c) {
+                        Raw8<T> vx, vd, vr;
+                        float w[8], f[8];
+                        vx.load(xr + c);
+                        vd.load(dyr + c);
+                        if (rr) vr.load(rr + c); else vr.zero();
+                        load_param8(p.w, p.param_bf16, c, 1.f, w);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) f[i] = out(vx.get(i), vd.get(i), w[i], vr.get(i));
+                        store8(dxr + c, f);
+                    },
+                    [&](int64_t c) {
+                        store1(dxr + c, out(load1(xr + c), load1(dyr + c),
+                                            load_param1(p.w, p.param_bf16, c, 1.f), rr ? load1(rr + c) : 0.f));
+                    });
+    }
+}
+
+// Long rows: partial column sums.  Workgroup (part, column block): 256 columns,
+// one per thread, over the rows part, part + parts, ...
+constexpr int kColThreads = 256;
+
+template <class T>
+__global__ void __launch_bounds__(kColThreads)
+ln_column_sums_kernel(LnBwd p, int parts) {
+    const int64_t c = (int64_t)blockIdx.x * kColThreads + threadIdx.x;
+    const int part = blockIdx.y;
+    if (c >= p.cols) return;
+    const T* x = static_cast<const T*>(p.x);
+    const T* dy = static_cast<const T*>(p.dy);
+    float dw = 0.f, db = 0.f;
+    for (int64_t r = part; r < p.rows; r += parts) {
+        const float d = load1(dy + r * p.cols + c);
+        dw = fmaf(d, (load1(x + r * p.cols + c) - p.mean[r]) * p.rstd[r], dw);
+        db += d;
+    }
+    p.partial[part * p.pitch + c] = dw;
+    p.partial[(parts + part) * p.pitch + c] = db;
+}
+
+// dw and db from the partial rows (blockIdx.y 0: dw, 1: db).  A workgroup takes
+// 64 columns: 16 lanes of 4 columns each, 16 slices of the parts, joined in a
+// fixed order.  parts == 0 (no rows) gives zeros.
+__global__ void __launch_bounds__(256)
+ln_reduce_kernel(const float* partial, int parts, int64_t pitch, int64_t cols, float* dw, float* db) {
+    __shared__ float4 s[16][16];
+    const int cx = threadIdx.x % 16, slice = threadIdx.x / 16;
+    const int64_t c = (int64_t)blockIdx.x * 64 + cx * 4;
+    const float* src = partial + (int64_t)blockIdx.y * parts * pitch;
+    float4 a{0.f, 0.f, 0.f, 0.f};
+    for (int i = slice; i < parts; i += 16) {   // (the pitch covers whole 64-column blocks)
+        const float4 v = *reinterpret_cast<const float4*>(src + i * pitch + c);
+        a.x += v.x;
+        a.y += v.y;
+        a.z += v.z;
+        a.w += v.w;
+    }
+    s[slice][cx] = a;
+    __syncthreads();
+    if (threadIdx.x < 64) {
+        const int64_t col = (int64_t)blockIdx.x * 64 + threadIdx.x;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum += reinterpret_cast<const float*>(s[i])[threadIdx.x];
+        if (col < cols) (blockIdx.y ? db : dw)[col] = sum;
+    }
+}
+
+// ---------------------------------------------------------------- host ---
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
+int64_t max64(int64_t a, int64_t b) { return a > b ? a : b; }
+
+int device_cu_count() {
+    int dev = -1, cus = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return 0;
+    if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) return 0;
+    return cus;
+}
+
+bool aligned_to(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+int check_shape(int64_t rows, int64_t cols) {
+    if (rows < 0 || rows > INT32_MAX || cols < 1 || cols > (int64_t(1) << 24)) return FP8LN_ERR_SHAPE;
+    return FP8LN_OK;
+}
+
+int row_waves(int64_t cols) { return (int)max64(1, ceil_div(cols / 8, kWaveSize * kVecs)); }
+
+// How the gradient's rows are shared out.  It does not depend on the device:
+// the workspace size, and with it the sums' order, has to be known without one.
+constexpr int64_t kGradWorkgroups = 256;
+constexpr int64_t kLongParts = 64;
+struct GradPlan {
+    bool held;
+    int waves, subs;
+    int64_t parts, pitch;
+};
+
+GradPlan grad_plan(int64_t rows, int64_t cols) {
+    GradPlan g;
+    g.held = cols <= kHeldCols;
+    g.pitch = ceil_div(cols, 64) * 64;
+    if (!g.held) {
+        g.waves = g.subs = 0;
+        g.parts = min64(rows, kLongParts);
+        return g;
+    }
+    g.waves = row_waves(cols);
+    g.subs = (int)max64(1, min64(kMaxWaves / g.waves, ceil_div(rows, kGradWorkgroups)));
+    g.parts = min64(kGradWorkgroups, ceil_div(rows, g.subs));
+    return g;
+}
+
+int64_t grad_workspace(int64_t rows, int64_t cols) {
+    const GradPlan g = grad_plan(rows, cols);
+    return 2 * g.parts * g.pitch * (int64_t)sizeof(float);
+}
+
+}  // namespace
+
+extern "C" {
+
+int fp8_layer_norm(const void* x, int dtype, const void* w, const void* b, int param_dtype, float eps,
+                   void* y, void* q, int q_format, float* scale, float* mean, float* rstd,
+                   int64_t rows, int64_t cols, struct ihipStream_t* stream) {
+    if ((dtype != FP8LN_BF16 && dtype != FP8LN_FP32) || (param_dtype != FP8LN_BF16 && param_dtype != FP8LN_FP32))
+        return FP8LN_ERR_DTYPE;
+    if (q && q_format != FP8LN_E4M3FN && q_format != FP8LN_E5M2) return FP8LN_ERR_DTYPE;
+    const int st = check_shape(rows, cols);
+    if (st != FP8LN_OK) return st;
+    if (q && cols % 16 != 0) return FP8LN_ERR_SHAPE;
+    if (!(eps >= 0.f) || std::isinf(eps)) return FP8LN_ERR_VALUE;
+    if (rows == 0) return FP8LN_OK;
+    if (!x || (!y && !q) || !q != !scale || !mean != !rstd) return FP8LN_ERR_NULL;
+    const uintptr_t ea = dtype == FP8LN_BF16 ? 2 : 4, pa = param_dtype == FP8LN_BF16 ? 2 : 4;
+    if (!aligned_to(x, ea) || !aligned_to(y, ea) || !aligned_to(w, pa) || !aligned_to(b, pa) ||
+        !aligned_to(q, 16) || !aligned_to(scale, 4) || !aligned_to(mean, 4) || !aligned_to(rstd, 4))
+        return FP8LN_ERR_ALIGN;
+    const int cus = device_cu_count();
+    if (cus <= 0) return FP8LN_ERR_DEVICE;
+    const hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+    LnFwd p{x, w, b, param_dtype == FP8LN_BF16, eps, y, static_cast<uint8_t*>(q), q_format, scale, mean, rstd,
+            rows, cols, row_waves(cols)};
+    (void)hipGetLastError();
+    if (cols > kHeldCols) {
+        const dim3 grid((unsigned)min64(rows, (int64_t)cus * 8));
+        if (dtype == FP8LN_BF16)
+            hipLaunchKernelGGL(ln_forward_long_kernel<bf16_t>, grid, dim3(kLongThreads), 0, hs, p);
+        else
+            hipLaunchKernelGGL(ln_forward_long_kernel<float>, grid, dim3(kLongThreads), 0, hs, p);
+    } else if (p.waves == 1) {
+        constexpr int kRows = 4;   // waves, and so rows, per workgroup
+        const dim3 grid((unsigned)min64(ceil_div(rows, kRows), (int64_t)cus * 4));
+        if (dtype == FP8LN_BF16)
+            hipLaunchKernelGGL((ln_forward_kernel<bf16_t, false>), grid, dim3(kRows * kWaveSize), 0, hs, p);
+        else
+            hipLaunchKernelGGL((ln_forward_kernel<float, false>), grid, dim3(kRows * kWaveSize), 0, hs, p);
+    } else {
+        const dim3 grid((unsigned)min64(rows, (int64_t)cus * (kMaxWaves / p.waves)));
+        if (dtype == FP8LN_BF16)
+            hipLaunchKernelGGL((ln_forward_kernel<bf16_t, true>), grid, dim3(p.waves * kWaveSize), 0, hs, p);
+        else
+            hipLaunchKernelGGL((ln_forward_kernel<float, true>), grid, dim3(p.waves * kWaveSize), 0, hs, p);
+    }
+    if (hipGetLastError() != hipSuccess) return FP8LN_ERR_LAUNCH;
+    return FP8LN_OK;
+}
+
+int64_t fp8_layer_norm_backward_workspace_size(int64_t rows, int64_t cols) {
+    if (check_shape(rows, cols) != FP8LN_OK || rows == 0) return 0;
+    return grad_workspace(rows, cols);
+}
+
+int fp8_layer_norm_backward(const void* dy, const void* x, int dtype, const float* mean,
+                            const float* rstd, const void* w, int param_dtype,
+                            const void* residual_grad, void* dx, float* dw, float* db, int64_t rows,
+                            int64_t cols, void* workspace, int64_t workspace_bytes,
+                            struct ihipStream_t* stream) {
+    if ((dtype != FP8LN_BF16 && dtype != FP8LN_FP32) || (param_dtype != FP8LN_BF16 && param_dtype != FP8LN_FP32))
+        return FP8LN_ERR_DTYPE;
+    const int st = check_shape(rows, cols);
+    if (st != FP8LN_OK) return st;
+    if (!dw || !db || (rows > 0 && (!dy || !x || !mean || !rstd || !dx))) return FP8LN_ERR_NULL;
+    const uintptr_t ea = dtype == FP8LN_BF16 ? 2 : 4, pa = param_dtype == FP8LN_BF16 ? 2 : 4;
+    if (!aligned_to(dy, ea) || !aligned_to(x, ea) || !aligned_to(residual_grad, ea) || !aligned_to(dx, ea) ||
+        !aligned_to(w, pa) || !aligned_to(mean, 4) || !aligned_to(rstd, 4) || !aligned_to(dw, 4) ||
+        !aligned_to(db, 4))
+        return FP8LN_ERR_ALIGN;
+    if (rows > 0 && (!workspace || workspace_bytes < grad_workspace(rows, cols))) return FP8LN_ERR_WORKSPACE;
+    if (rows > 0 && !aligned_to(workspace, 256)) return FP8LN_ERR_ALIGN;
+    const int cus = device_cu_count();
+    if (cus <= 0) return FP8LN_ERR_DEVICE;
+    const hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+    const GradPlan g = grad_plan(rows, cols);
+    LnBwd p{dy, x, mean, rstd, w, param_dtype == FP8LN_BF16, residual_grad, dx, static_cast<float*>(workspace),
+            rows, cols, g.pitch, g.waves, g.subs};
+    (void)hipGetLastError();
+    if (rows > 0 && g.held) {
+        const dim3 grid((unsigned)g.parts), block(g.waves * g.subs * kWaveSize);
+        const unsigned lds = (unsigned)(g.subs / 2 * 2 * g.pitch * (int64_t)sizeof(float));
+        if (dtype == FP8LN_BF16)
+            hipLaunchKernelGGL(ln_backward_kernel<bf16_t>, grid, block, lds, hs, p);
+        else
+            hipLaunchKernelGGL(ln_backward_kernel<float>, grid, block, lds, hs, p);
+    } else if (rows > 0) {
+        const dim3 grid((unsigned)min64(rows, (int64_t)cus * 8));
+        const dim3 cgrid((unsigned)ceil_div(cols, kColThreads), (unsigned)g.parts);
+        if (dtype == FP8LN_BF16) {
+            hipLaunchKernelGGL(ln_column_sums_kernel<bf16_t>, cgrid, dim3(kColThreads), 0, hs, p, (int)g.parts);
+            hipLaunchKernelGGL(ln_backward_long_kernel<bf16_t>, grid, dim3(kLongThreads), 0, hs, p);
+        } else {
+            hipLaunchKernelGGL(ln_column_sums_kernel<float>, cgrid, dim3(kColThreads), 0, hs, p, (int)g.parts);
+            hipLaunchKernelGGL(ln_backward_long_kernel<float>, grid, dim3(kLongThreads), 0, hs, p);
+        }
+    }
+    hipLaunchKernelGGL(ln_reduce_kernel, dim3((unsigned)ceil_div(cols, 64), 2), dim3(256), 0, hs,
+                       static_cast<const float*>(workspace), (int)g.parts, g.pitch, cols, dw, db);
+    if (hipGetLastError() != hipSuccess) return FP8LN_ERR_LAUNCH;
+    return FP8LN_OK;
+}
+
+const char* fp8_layer_norm_status_string(int s) {
+    switch (s) {
+        case FP8LN_OK: return "ok";
+        case FP8LN_ERR_NULL: return "a required pointer is NULL (q comes with scale, mean with rstd)";
+        case FP8LN_ERR_SHAPE:
+            return "rows or cols out of range (need 0<=rows<2^31, 1<=cols<=2^24, cols%16==0 for codes)";
+        case FP8LN_ERR_ALIGN:
+            return "misaligned pointer (tensors: their element; q: 16 B; workspace: 256 B)";
+        case FP8LN_ERR_DTYPE: return "unknown element type or code format";
+        case FP8LN_ERR_DEVICE: return "no usable HIP device";
+        case FP8LN_ERR_LAUNCH: return "kernel launch failed";
+        case FP8LN_ERR_WORKSPACE:
+            return "workspace smaller than fp8_layer_norm_backward_workspace_size()";
+        case FP8LN_ERR_VALUE: return "eps must be finite and not negative";
+        default: return "unknown status";
+    }
+}
+
+}  // extern "C"
