@@ -85,7 +85,8 @@ enum fp8mm_status {
     FP8MM_ERR_CONFIG = 7,  /* unknown tile configuration id or split count */
     FP8MM_ERR_WORKSPACE = 8, /* caller workspace smaller than required */
     FP8MM_ERR_FORMAT = 9,    /* unknown operand format */
-    FP8MM_ERR_SCRATCH = 10   /* fp8_scaled_mm_noalloc: plan larger than its scratch */
+    FP8MM_ERR_SCRATCH = 10,  /* fp8_scaled_mm_noalloc: plan larger than its scratch */
+    FP8MM_ERR_ACTIVATION = 11 /* fp8_linear.h: unknown activation */
 };
 
 /* Operand formats (OCP 8-bit floating point).  The gist "matmul_fp8.py",

@@ -33,9 +33,9 @@ SPLITS_STREAM_K = -1
 
 # status codes from include/fp8_scaled_mm.h
 (OK, ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_MODE, ERR_DEVICE, ERR_LAUNCH, ERR_CONFIG, ERR_WORKSPACE,
- ERR_FORMAT, ERR_SCRATCH) = range(11)
+ ERR_FORMAT, ERR_SCRATCH, ERR_ACTIVATION) = range(12)
 _ARG_ERRORS = {ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_MODE, ERR_CONFIG, ERR_WORKSPACE, ERR_FORMAT,
-               ERR_SCRATCH}
+               ERR_SCRATCH, ERR_ACTIVATION}
 
 EXPORTS = ("fp8_scaled_mm", "fp8_scaled_mm_with_config", "fp8_scaled_mm_with_plan",
            "fp8_scaled_mm_typed", "fp8_scaled_mm_noalloc",
@@ -50,6 +50,11 @@ EXPORTS = ("fp8_scaled_mm", "fp8_scaled_mm_with_config", "fp8_scaled_mm_with_pla
 (Q_OK, Q_ERR_NULL, Q_ERR_SHAPE, Q_ERR_ALIGN, Q_ERR_MODE, Q_ERR_DEVICE, Q_ERR_LAUNCH,
  Q_ERR_WORKSPACE) = range(8)
 _Q_ARG_ERRORS = {Q_ERR_NULL, Q_ERR_SHAPE, Q_ERR_ALIGN, Q_ERR_MODE, Q_ERR_WORKSPACE}
+
+# functions from include/fp8_linear.h (status codes: those of fp8_scaled_mm.h)
+# and its activations (enum fp8mm_activation)
+LINEAR_EXPORTS = ("fp8_linear",)
+_ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 # functions and status codes from include/fp8_layer_norm.h
 LAYER_NORM_EXPORTS = ("fp8_layer_norm", "fp8_layer_norm_backward",
@@ -119,6 +124,9 @@ def lib() -> ctypes.CDLL:
         L.fp8_quantize_set_wait_limit_us.restype = i64
         L.fp8_quantize_status_string.argtypes = [i32]
         L.fp8_quantize_status_string.restype = ctypes.c_char_p
+        L.fp8_linear.argtypes = [vp, i32, vp, i32, vp, vp, vp, vp, i32, vp, vp, i64, i64, i64, i32, vp,
+                                 i32, i32, vp, i64]
+        L.fp8_linear.restype = i32
         f32 = ctypes.c_float
         L.fp8_layer_norm.argtypes = [vp, i32, vp, vp, i32, f32, vp, vp, i32, vp, vp, vp, i64, i64, vp]
         L.fp8_layer_norm.restype = i32
@@ -226,20 +234,10 @@ def _stream_of(dev: int) -> int:
 _ws_sizes: dict = {}
 
 
-def fp8_scaled_mm(a: torch.Tensor, b: torch.Tensor, scale_a: torch.Tensor, scale_b: torch.Tensor,
-                  bias: torch.Tensor | None = None, out: torch.Tensor | None = None,
-                  mode="per_tensor", config: int = -1, splits: int = 0,
-                  workspace: torch.Tensor | None = None, a_format=None,
-                  b_format=None) -> torch.Tensor:
-    """out = bf16(scale_a * scale_b * (a @ b^T) + bias) with a: M x K and b: N x K
-    (float8 codes, K contiguous).  b may also be given as a K x N column-major
-    view (stride (1, K)), which is the same memory.  Each operand is e4m3fn or
-    e5m2: taken from its torch dtype, or from a_format / b_format for uint8
-    codes (default e4m3fn).  `config` (-1: automatic) and `splits` (0:
-    automatic; SPLITS_STREAM_K: stream-K) select the plan.  When the plan
-    splits K, its workspace is
-    `workspace` (a GPU byte tensor, zero-filled before first use) or, if that
-    is None, one this module keeps per stream (allocated by torch)."""
+def _mm_args(a, b, scale_a, scale_b, bias, out, mode, workspace, a_format, b_format, extra=()):
+    """Checks the multiply's arguments (`extra`: more (name, tensor) pairs that
+    must be on the same GPU).  Returns (a, fa, b, fb, out, M, N, K, mode,
+    device index), with `out` allocated if it is None."""
     m = _MODES.get(mode) if isinstance(mode, (str, int)) else None
     if m is None:
         raise ValueError(f"mode must be 'per_tensor' or 'rowwise', got {mode!r}")
@@ -262,7 +260,7 @@ def fp8_scaled_mm(a: torch.Tensor, b: torch.Tensor, scale_a: torch.Tensor, scale
         raise ValueError("all tensors must be on the GPU")
     dev = a.get_device()
     _check_devices(dev, (("b", b), ("scale_a", scale_a), ("scale_b", scale_b), ("bias", bias),
-                         ("out", out), ("workspace", workspace)))
+                         ("out", out), ("workspace", workspace), *extra))
     for name, s in (("scale_a", scale_a), ("scale_b", scale_b)):
         if s.dtype != torch.float32 or not s.is_contiguous():
             raise ValueError(f"{name} must be contiguous float32")
@@ -277,38 +275,106 @@ def fp8_scaled_mm(a: torch.Tensor, b: torch.Tensor, scale_a: torch.Tensor, scale
         out = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
     elif out.dtype != torch.bfloat16 or out.shape != (M, N) or not out.is_contiguous():
         raise ValueError("out must be a contiguous bf16 M x N tensor")
+    return a, fa, b, fb, out, M, N, K, m, dev
+
+
+def _mm_workspace(L, device, dev, stream, M, N, K, m, has_bias, config, splits, workspace):
+    """(address, bytes) of the workspace of a call's plan: the caller's, or this
+    module's for the stream where the plan splits K."""
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous GPU tensor")
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if splits == 1:
+        return None, 0
+    key = (dev, M, N, K, m, has_bias, config, splits)
+    need = _ws_sizes.get(key)
+    if need is None:
+        need = int(L.fp8_scaled_mm_workspace_size(M, N, K, m, int(has_bias), int(config), int(splits)))
+        if len(_ws_sizes) >= 4096:      # many distinct shapes: start over
+            _ws_sizes.clear()
+        _ws_sizes[key] = need
+    if need <= 0:
+        return None, 0
+    ws = _workspace(device, stream, need)
+    return ws.data_ptr(), ws.numel()
+
+
+def fp8_scaled_mm(a: torch.Tensor, b: torch.Tensor, scale_a: torch.Tensor, scale_b: torch.Tensor,
+                  bias: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                  mode="per_tensor", config: int = -1, splits: int = 0,
+                  workspace: torch.Tensor | None = None, a_format=None,
+                  b_format=None) -> torch.Tensor:
+    """out = bf16(scale_a * scale_b * (a @ b^T) + bias) with a: M x K and b: N x K
+    (float8 codes, K contiguous).  b may also be given as a K x N column-major
+    view (stride (1, K)), which is the same memory.  Each operand is e4m3fn or
+    e5m2: taken from its torch dtype, or from a_format / b_format for uint8
+    codes (default e4m3fn).  `config` (-1: automatic) and `splits` (0:
+    automatic; SPLITS_STREAM_K: stream-K) select the plan.  When the plan
+    splits K, its workspace is
+    `workspace` (a GPU byte tensor, zero-filled before first use) or, if that
+    is None, one this module keeps per stream (allocated by torch)."""
+    a, fa, b, fb, out, M, N, K, m, dev = _mm_args(a, b, scale_a, scale_b, bias, out, mode, workspace,
+                                                  a_format, b_format)
     L = lib()
     stream = _stream_of(dev)
     # The library launches on the current HIP device: make it a's (calls
     # from that device, the usual case, skip the switch).
-    switch = torch.cuda.current_device() != dev
-    with torch.cuda.device(dev) if switch else contextlib.nullcontext():
-        ws_ptr, ws_bytes = None, 0
-        if workspace is not None:
-            if not workspace.is_contiguous():
-                raise ValueError("workspace must be a contiguous GPU tensor")
-            ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        elif splits != 1:
-            key = (dev, M, N, K, m, bias is not None, config, splits)
-            need = _ws_sizes.get(key)
-            if need is None:
-                need = int(L.fp8_scaled_mm_workspace_size(M, N, K, m, int(bias is not None),
-                                                          int(config), int(splits)))
-                if len(_ws_sizes) >= 4096:      # many distinct shapes: start over
-                    _ws_sizes.clear()
-                _ws_sizes[key] = need
-            if need > 0:
-                ws = _workspace(a.device, stream, need)
-                ws_ptr, ws_bytes = ws.data_ptr(), ws.numel()
+    with _on_device(dev):
+        ws_ptr, ws_bytes = _mm_workspace(L, a.device, dev, stream, M, N, K, m, bias is not None, config,
+                                         splits, workspace)
         st = L.fp8_scaled_mm_typed(
             a.data_ptr(), fa, b.data_ptr(), fb, scale_a.data_ptr(), scale_b.data_ptr(),
             bias.data_ptr() if bias is not None else None, out.data_ptr(),
             M, N, K, m, stream, int(config), int(splits), ws_ptr, ws_bytes)
-    if st != OK:
-        if st in _ARG_ERRORS:
-            raise ValueError(f"fp8_scaled_mm: {status_string(st)} (status {st})")
-        raise Fp8MMError(st)
+    _mm_check("fp8_scaled_mm", st)
     return out
+
+
+def fp8_linear(a: torch.Tensor, b: torch.Tensor, scale_a: torch.Tensor, scale_b: torch.Tensor,
+               bias: torch.Tensor | None = None, residual: torch.Tensor | None = None, *,
+               activation="none", preact: torch.Tensor | None = None,
+               out: torch.Tensor | None = None, mode="rowwise", config: int = -1, splits: int = 0,
+               workspace: torch.Tensor | None = None, a_format=None, b_format=None) -> torch.Tensor:
+    """out = bf16(act(z) + residual) with z = scale_a * scale_b * (a @ b^T) + bias:
+    fp8_scaled_mm with the rest of a linear layer in its epilogue, rounded once.
+
+    `activation` is 'none', 'relu', 'gelu' (z Phi(z)), 'gelu_tanh' or 'silu'.
+    `residual` (M x N bf16) may also be `out`.  `preact` (M x N bf16) receives
+    bf16(z), which fp8_linear_backward takes.  Operands, formats, plans and
+    workspaces are fp8_scaled_mm's (stream-K plans take no epilogue)."""
+    act = _activation(activation)
+    a, fa, b, fb, out, M, N, K, m, dev = _mm_args(a, b, scale_a, scale_b, bias, out, mode, workspace,
+                                                  a_format, b_format,
+                                                  (("residual", residual), ("preact", preact)))
+    for name, t in (("residual", residual), ("preact", preact)):
+        if t is not None and (t.dtype != torch.bfloat16 or t.shape != (M, N) or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous bf16 M x N tensor")
+    L = lib()
+    stream = _stream_of(dev)
+    with _on_device(dev):
+        ws_ptr, ws_bytes = _mm_workspace(L, a.device, dev, stream, M, N, K, m, bias is not None, config,
+                                         splits, workspace)
+        st = L.fp8_linear(a.data_ptr(), fa, b.data_ptr(), fb, scale_a.data_ptr(), scale_b.data_ptr(),
+                          _ptr(bias), _ptr(residual), act, _ptr(preact), out.data_ptr(), M, N, K, m,
+                          stream, int(config), int(splits), ws_ptr, ws_bytes)
+    _mm_check("fp8_linear", st)
+    return out
+
+
+def _activation(activation) -> int:
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of 'none', 'relu', 'gelu', 'gelu_tanh' and 'silu', "
+                         f"got {activation!r}")
+    return _ACTIVATIONS[activation]
+
+
+def _mm_check(fn: str, st: int) -> None:
+    if st == OK:
+        return
+    if st in _ARG_ERRORS:
+        raise ValueError(f"{fn}: {status_string(st)} (status {st})")
+    raise Fp8MMError(st)
 
 
 def fp8_quantize(x: torch.Tensor, mode="rowwise", q: torch.Tensor | None = None,

@@ -15,10 +15,10 @@ import tempfile
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 # The host logic and C ABI, one translation unit per operand-format pair of
-# the multiply's kernels, the quantiser and the layer norm.  They compile in parallel.
+# the multiply's kernels (and of those with the linear layer's epilogue), the quantiser and the layer norm.  They compile in parallel.
 SRCS = [os.path.join(HERE, "csrc", f) for f in
-        ["fp8_scaled_mm.hip"] + [f"fp8_gemm_f{k}.hip" for k in range(4)] + ["fp8_quantize.hip", "fp8_layer_norm.hip"]]
-HEADERS = [os.path.join(HERE, "csrc", f) for f in ("fp8_gemm_kernels.h", "fp8_convert.h")]
+        ["fp8_scaled_mm.hip"] + [f"fp8_{n}_f{k}.hip" for n in ("gemm", "linear") for k in range(4)] + ["fp8_quantize.hip", "fp8_layer_norm.hip"]]
+HEADERS = [os.path.join(HERE, "csrc", f) for f in ("fp8_gemm_kernels.h", "fp8_convert.h", "activation.h", "plan_cost_table.h")]
 LIB = os.path.join(HERE, "libfp8_scaled_mm.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -37,6 +37,10 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
+#include "activation.h"
+
 namespace fp8mm {
 
 struct Params {
@@ -66,6 +70,17 @@ struct Params {
     // counters as in split-K, `splits` then being the room per tile for
     // segments (an upper bound on their number).
 };
+
+// With the linear layer's epilogue (the EPI instantiations, which take this
+// in place of Params):
+//   z = s * sum + bias,  out = act(z) + residual,  preact = z
+// vec_store and vec16 then hold for residual and preact too.
+struct LinearParams : Params {
+    const uint16_t* residual;   // M x N bf16, may be null
+    uint16_t* preact;           // M x N bf16, may be null
+    int act;                    // enum Activation
+};
+template <bool EPI> using KernelParams = std::conditional_t<EPI, LinearParams, Params>;
 
 typedef void (*Launch)(const Params&, dim3, hipStream_t);
 struct LaunchPair {
@@ -117,6 +132,13 @@ extern LaunchPair kLaunchF0[kNumConfigs];
 extern LaunchPair kLaunchF1[kNumConfigs];
 extern LaunchPair kLaunchF2[kNumConfigs];
 extern LaunchPair kLaunchF3[kNumConfigs];
+
+// The same with the linear layer's epilogue, defined in fp8_linear_f<k>.hip (no
+// stream-K form).
+extern LaunchPair kLinearF0[kNumConfigs];
+extern LaunchPair kLinearF1[kNumConfigs];
+extern LaunchPair kLinearF2[kNumConfigs];
+extern LaunchPair kLinearF3[kNumConfigs];
 
 }  // namespace fp8mm
 
@@ -850,6 +872,156 @@ __device__ __forceinline__ void stage_and_store(
     }
 }
 
+// ------------------------------------------- the linear layer's epilogue ---
+//
+//   z = s * sum + bias,  out = bf16(act(z) + residual),  preact = bf16(z)
+//
+// z, the activation and the residual's addition are fp32; each output is
+// rounded once.  The tile's parameters are always in LDS (per-tensor scales as
+// s and 1, an absent bias as 0: the same values), so only the activation is a
+// compile-time choice, made by a wave-uniform branch at the tile's end.
+// The steps work on the accumulators in place, so that the activation is the
+// only code that there are five copies of.
+
+__device__ __forceinline__ float bf16_of_run(uint2 w, int c) {   // value c of 4 bf16
+    const uint32_t x = c < 2 ? w.x : w.y;
+    return __uint_as_float(c % 2 == 0 ? x << 16 : x & 0xffff0000u);
+}
+
+// Column, within the wave's block, of run g of block i for this lane.
+template <int MI>
+__device__ __forceinline__ int epi_col(int i, int g, int lane) {
+    return i * MI + (MI == 32 ? 8 * g + 4 * (lane / 32) : 4 * (lane / 16));
+}
+
+// acc = z
+template <int MI, int FN, int FM>
+__device__ __forceinline__ void epi_scale(typename Mfma<MI>::acc_t (&acc)[FN][FM], int mbase, int nbase,
+                                          const float* epi_sa, const float* epi_sb,
+                                          const uint16_t* epi_bias, int lane) {
+    float sa_r[FM];
+#pragma unroll
+    for (int j = 0; j < FM; ++j) sa_r[j] = epi_sa[mbase + j * MI + lane % MI];
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int g = 0; g < Mfma<MI>::NACC / 4; ++g) {
+            const int nl = nbase + epi_col<MI>(i, g, lane);
+            const v4f sb_r = *reinterpret_cast<const v4f*>(epi_sb + nl);
+            const uint2 b_r = *reinterpret_cast<const uint2*>(epi_bias + nl);
+#pragma unroll
+            for (int j = 0; j < FM; ++j)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    acc[i][j][4 * g + c] =
+                        __builtin_fmaf(acc[i][j][4 * g + c], sa_r[j] * sb_r[c], bf16_of_run(b_r, c));
+        }
+}
+
+// acc = act(acc)
+template <class A, int FN, int FM>
+__device__ __forceinline__ void epi_activate(A (&acc)[FN][FM], int act) {
+    with_activation(act, [&](auto a) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < FM; ++j)
+#pragma unroll
+                for (int e = 0; e < (int)(sizeof(A) / 4); ++e)
+                    acc[i][j][e] = activate<decltype(a)::value>(acc[i][j][e]);
+    });
+}
+
+// acc += residual, for the blocks whose first row and column are m0 and n0;
+// rows and columns outside the output are left alone.  Residuals are read in
+// the MFMA layout, 8 bytes per run of 4 columns where rows allow it: the reads
+// of a wave's blocks cover whole lines between them.
+template <int MI, int FN, int FM>
+__device__ __forceinline__ void epi_residual(typename Mfma<MI>::acc_t (&acc)[FN][FM],
+                                             const LinearParams& p, int m0, int n0, int lane) {
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+        const int m = m0 + j * MI + lane % MI;
+        if (m >= p.M) continue;
+        const uint16_t* row = p.residual + (size_t)m * p.N;
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int g = 0; g < Mfma<MI>::NACC / 4; ++g) {
+                const int n = n0 + epi_col<MI>(i, g, lane);
+                if (p.vec_store) {   // N % 4 == 0: a run is inside or outside
+                    if (n < p.N) {
+                        const uint2 r = *reinterpret_cast<const uint2*>(row + n);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) acc[i][j][4 * g + c] += bf16_of_run(r, c);
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (n + c < p.N) acc[i][j][4 * g + c] += __uint_as_float((uint32_t)row[n + c] << 16);
+                }
+            }
+    }
+}
+
+// 4 accumulators from 4 * g on, rounded to bf16.
+template <class A>
+__device__ __forceinline__ uint2 epi_pack(const A& a, int g) {
+    uint2 w;
+    w.x = pack_bf16x2(a[4 * g], a[4 * g + 1]);
+    w.y = pack_bf16x2(a[4 * g + 2], a[4 * g + 3]);
+    return w;
+}
+
+// Generic kernel: the wave's blocks, rounded, into the row-major copy of the
+// tile, laid out as in stage_tile_impl; then the copy to p.out.
+template <class C, bool PAD>
+__device__ __forceinline__ void epi_write(const typename Mfma<C::MI_>::acc_t (&acc)[C::FN][C::FM],
+                                          uint8_t* stg, const Params& p, int row0, int col0, int mbase,
+                                          int nbase, int lane, int tid) {
+    constexpr int MI = C::MI_;
+    constexpr int NCH = C::STG_CHUNKS;
+#pragma unroll
+    for (int i = 0; i < C::FN; ++i)
+#pragma unroll
+        for (int g = 0; g < Mfma<MI>::NACC / 4; ++g) {
+            const int byte = (nbase + epi_col<MI>(i, g, lane)) * 2;
+#pragma unroll
+            for (int j = 0; j < C::FM; ++j) {
+                const int ml = mbase + j * MI + lane % MI;
+                uint8_t* at = PAD ? stg + ml * ((NCH + 1) * 16) + byte
+                                  : stg + ml * (NCH * 16) + (((byte >> 4) + ml) % NCH) * 16 + (byte & 15);
+                *reinterpret_cast<uint2*>(at) = epi_pack(acc[i][j], g);
+            }
+        }
+    barrier_lds();
+    if constexpr (PAD) store_staged_unaligned<C>(stg, p, row0, col0, tid);
+    else store_staged<C>(stg, p, row0, col0, tid);
+}
+
+template <class C>
+__device__ __forceinline__ void epi_stage_and_store(
+    typename Mfma<C::MI_>::acc_t (&acc)[C::FN][C::FM], uint8_t* stg, const LinearParams& p,
+    int row0, int col0, int mbase, int nbase, const float* epi_sa, const float* epi_sb,
+    const uint16_t* epi_bias, int lane, int tid) {
+    asm volatile("" : "+v"(lane));
+    epi_scale<C::MI_, C::FN, C::FM>(acc, mbase, nbase, epi_sa, epi_sb, epi_bias, lane);
+    // preact first, then out, through the same code.
+    for (bool pre = p.preact != nullptr;; pre = false) {
+        Params to = p;
+        if (pre) {
+            to.out = p.preact;
+        } else {
+            epi_activate(acc, p.act);
+            if (p.residual) epi_residual<C::MI_, C::FN, C::FM>(acc, p, row0 + mbase, col0 + nbase, lane);
+        }
+        if (p.vec16) epi_write<C, false>(acc, stg, to, row0, col0, mbase, nbase, lane, tid);
+        else epi_write<C, true>(acc, stg, to, row0, col0, mbase, nbase, lane, tid);
+        if (!pre) break;
+        barrier_lds();   // the copy of preact has been read
+    }
+}
+
 // One K stage (BK bytes of K) of the software pipeline.  The fragments of
 // the stage's first K step are already in buffer CUR0.  Each step first
 // issues the LDS reads of the next step into the other buffer, then the MFMAs
@@ -929,10 +1101,10 @@ __device__ __forceinline__ void run_stage(typename Mfma<C::MI_>::acc_t (&acc)[C:
 }
 
 template <int BM, int BN, int BK, int WAVES_M, int WAVES_N, int STAGES, int MI, int GROUP_M,
-          bool NT_B, int FMT, bool SK = false>
+          bool NT_B, int FMT, bool SK = false, bool EPI = false>
 __global__ void __launch_bounds__(WAVES_M * WAVES_N * kWave,
                                   (Cfg<BM, BN, BK, WAVES_M, WAVES_N, STAGES, MI, GROUP_M>::OCCUPANCY))
-fp8_gemm_kernel(Params p) {
+fp8_gemm_kernel(KernelParams<EPI> p) {
     using C = Cfg<BM, BN, BK, WAVES_M, WAVES_N, STAGES, MI, GROUP_M, NT_B, FMT>;
     using F = Mfma<MI>;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS_BYTES];
@@ -995,13 +1167,13 @@ fp8_gemm_kernel(Params p) {
 #pragma unroll
         for (int i = 0; i < C::NSA; ++i) {
             const int r = tid + i * C::THREADS;
-            sa_v[i] = (p.rowwise && r < BM && row0 + r < p.M) ? p.scale_a[row0 + r] : 0.f;
+            sa_v[i] = (p.rowwise && r < BM && row0 + r < p.M) ? p.scale_a[row0 + r] : EPI ? s_pt : 0.f;
         }
 #pragma unroll
         for (int i = 0; i < C::NSB; ++i) {
             const int c = tid + i * C::THREADS;
             const bool ok = c < BN && col0 + c < p.N;
-            sb_v[i] = (p.rowwise && ok) ? p.scale_b[col0 + c] : 0.f;
+            sb_v[i] = (p.rowwise && ok) ? p.scale_b[col0 + c] : EPI && !p.rowwise ? 1.f : 0.f;
             bias_v[i] = (has_bias && ok) ? p.bias[col0 + c] : (uint16_t)0;
         }
 
@@ -1105,7 +1277,7 @@ fp8_gemm_kernel(Params p) {
         }
 
         // Epilogue parameters into LDS (beside the stage buffers).
-        if (p.rowwise || has_bias) {
+        if (EPI || p.rowwise || has_bias) {
 #pragma unroll
             for (int i = 0; i < C::NSA; ++i) {
                 const int r = tid + i * C::THREADS;
@@ -1125,8 +1297,12 @@ fp8_gemm_kernel(Params p) {
         // ones of slices past the end) must have landed.
         wait_vmcnt<0>();
         barrier_lds();
-        stage_and_store<C>(acc, smem, p, row0, col0, wm * C::WTM, wn * C::WTN, epi_sa, epi_sb,
-                           epi_bias, s_pt, has_bias, lane, tid);
+        if constexpr (EPI)
+            epi_stage_and_store<C>(acc, smem, p, row0, col0, wm * C::WTM, wn * C::WTN, epi_sa, epi_sb,
+                                   epi_bias, lane, tid);
+        else
+            stage_and_store<C>(acc, smem, p, row0, col0, wm * C::WTM, wn * C::WTN, epi_sa, epi_sb,
+                               epi_bias, s_pt, has_bias, lane, tid);
     };
 
     if constexpr (SK) {
@@ -1348,12 +1524,13 @@ struct PpParams {
     uint16_t bias;
 };
 
+template <bool EPI>
 __device__ __forceinline__ PpParams pp_params_load(const Params& p, const PpTile& T, int t,
-                                                   bool has_bias) {
+                                                   bool has_bias, float s_pt) {
     PpParams v;
     const bool row_ok = T.row0 + t < p.M, col_ok = T.col0 + t < p.N;
-    v.sa = (p.rowwise && row_ok) ? p.scale_a[T.row0 + t] : 0.f;
-    v.sb = (p.rowwise && col_ok) ? p.scale_b[T.col0 + t] : 0.f;
+    v.sa = (p.rowwise && row_ok) ? p.scale_a[T.row0 + t] : EPI ? s_pt : 0.f;
+    v.sb = (p.rowwise && col_ok) ? p.scale_b[T.col0 + t] : EPI && !p.rowwise ? 1.f : 0.f;
     v.bias = (has_bias && col_ok) ? p.bias[T.col0 + t] : (uint16_t)0;
     return v;
 }
@@ -1486,6 +1663,81 @@ __device__ __forceinline__ void pp_store(const pp::acc_t (&acc)[pp::FN][pp::FM],
     }
 }
 
+// The linear layer's epilogue of one wave (128 x 64 outputs), in bands of 32
+// rows (all 128 accumulators at once would spill): through the wave's staging
+// area as in pp_store_staged, or, where the block is not wholly inside the
+// output or 16-byte stores are not allowed, straight to memory, run by run.
+constexpr int kPpBandBlocks = 32 / pp::MI;   // MFMA row blocks per band
+
+__device__ __forceinline__ void pp_epi_write(const pp::acc_t (&z)[pp::FN][kPpBandBlocks], const Params& p,
+                                             uint16_t* out, int m0, int n0, bool full, int lane,
+                                             uint8_t* stg) {
+    constexpr int MI = pp::MI, FN = pp::FN;
+    static_assert(Mfma<MI>::NACC == 4, "one run of 4 columns per block and lane");
+    if (full) {
+#pragma unroll
+        for (int j = 0; j < kPpBandBlocks; ++j)
+#pragma unroll
+            for (int i = 0; i < FN; ++i) {
+                const int r = j * MI + lane % MI, cl = epi_col<MI>(i, 0, lane);
+                const int cpos = (cl / 8) ^ ((r >> 1) & 7);
+                *reinterpret_cast<uint2*>(stg + r * 128 + cpos * 16 + (cl % 8) * 2) = epi_pack(z[i][j], 0);
+            }
+#pragma unroll
+        for (int pass = 0; pass < 4; ++pass) {
+            const int rr = pass * 8 + lane / 8;
+            const int cc = lane % 8;
+            const v4i v = *reinterpret_cast<const v4i*>(stg + rr * 128 + ((cc ^ ((rr >> 1) & 7)) * 16));
+            *reinterpret_cast<v4i*>(out + (size_t)(m0 + rr) * p.N + n0 + cc * 8) = v;
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < kPpBandBlocks; ++j) {
+        const int m = m0 + j * MI + lane % MI;
+        if (m >= p.M) continue;
+#pragma unroll
+        for (int i = 0; i < FN; ++i) {
+            const int n = n0 + epi_col<MI>(i, 0, lane);
+            const uint2 w = epi_pack(z[i][j], 0);
+            uint16_t* dst = out + (size_t)m * p.N + n;
+            if (p.vec_store) {   // N % 4 == 0: a run is inside or outside
+                if (n < p.N) *reinterpret_cast<uint2*>(dst) = w;
+            } else {
+                const uint16_t h[4] = {(uint16_t)w.x, (uint16_t)(w.x >> 16), (uint16_t)w.y, (uint16_t)(w.y >> 16)};
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (n + c < p.N) dst[c] = h[c];
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void pp_epi_store(const pp::acc_t (&acc)[pp::FN][pp::FM], const LinearParams& p,
+                                             int row0, int col0, int mbase, int nbase,
+                                             const float* epi_sa, const float* epi_sb,
+                                             const uint16_t* epi_bias, uint8_t* stg) {
+    constexpr int MI = pp::MI, FN = pp::FN, JB = kPpBandBlocks;
+    const int n0 = col0 + nbase;
+    const bool full = p.vec16 && row0 + mbase + 128 <= p.M && n0 + 64 <= p.N;   // wave-uniform
+#pragma unroll
+    for (int band = 0; band < pp::FM / JB; ++band) {
+        const int mb = mbase + band * 32;
+        const int lane = pp_lane();
+        pp::acc_t z[FN][JB];
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < JB; ++j) z[i][j] = acc[i][band * JB + j];
+        epi_scale<MI, FN, JB>(z, mb, nbase, epi_sa, epi_sb, epi_bias, lane);
+        if (p.preact) pp_epi_write(z, p, p.preact, row0 + mb, n0, full, lane, stg);
+        epi_activate(z, p.act);
+        if (p.residual) epi_residual<MI, FN, JB>(z, p, row0 + mb, n0, lane);
+        pp_epi_write(z, p, p.out, row0 + mb, n0, full, lane, stg);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
 // Split-K for one wave of the ping-pong kernel.  The wave publishes its fp32
 // partial of unit u (each store is a 1 KiB run) and counts
 // its arrival on the counter of (tile, wave); the wave that arrives last sums
@@ -1519,8 +1771,8 @@ __device__ __forceinline__ bool pp_split_fixup(pp::acc_t (&acc)[pp::FN][pp::FM],
     return true;
 }
 
-template <int GROUP_M, int FMT>
-__global__ void __launch_bounds__(pp::THREADS) fp8_gemm_pp_kernel(Params p) {
+template <int GROUP_M, int FMT, bool EPI = false>
+__global__ void __launch_bounds__(pp::THREADS) fp8_gemm_pp_kernel(KernelParams<EPI> p) {
     using namespace pp;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[LDS_BYTES];
 
@@ -1551,7 +1803,7 @@ __global__ void __launch_bounds__(pp::THREADS) fp8_gemm_pp_kernel(Params p) {
 
     const float s_pt = p.rowwise ? 0.f : p.scale_a[0] * p.scale_b[0];
     const bool has_bias = p.bias != nullptr;
-    const bool need_epi = p.rowwise || has_bias;
+    const bool need_epi = EPI || p.rowwise || has_bias;
     auto epi_area = [&](int parity, float*& sa, float*& sb, uint16_t*& bias) {
         sa = reinterpret_cast<float*>(smem + MAIN_BYTES + parity * EPI_BYTES);
         sb = sa + BM;
@@ -1562,7 +1814,7 @@ __global__ void __launch_bounds__(pp::THREADS) fp8_gemm_pp_kernel(Params p) {
     PpTile T = pp_tile(p, wg, GROUP_M, xcd);
     if (grp == 0) {
         PpParams pv;
-        if (need_epi) pv = pp_params_load(p, T, tid, has_bias);
+        if (need_epi) pv = pp_params_load<EPI>(p, T, tid, has_bias, s_pt);
         pp_tile_start(smem, p, T, L, q);
         wait_vmcnt<0>();
         if (need_epi) {
@@ -1612,15 +1864,20 @@ __global__ void __launch_bounds__(pp::THREADS) fp8_gemm_pp_kernel(Params p) {
             // this group's wait, so the next unit's first reads, which take
             // rows all four waves of this group loaded, find them landed.
             const int un = u + G;
-            if (!split || pp_split_fixup(acc, p, u, T.t, wave, pp_lane()))
-                pp_store(acc, p, T.row0, T.col0, 0, q * 64, epi_sa, epi_sb, epi_bias, s_pt,
-                         has_bias, pp_lane(), smem + STG0 + q * STG_BYTES);
+            if (!split || pp_split_fixup(acc, p, u, T.t, wave, pp_lane())) {
+                if constexpr (EPI)
+                    pp_epi_store(acc, p, T.row0, T.col0, 0, q * 64, epi_sa, epi_sb, epi_bias,
+                                 smem + STG0 + q * STG_BYTES);
+                else
+                    pp_store(acc, p, T.row0, T.col0, 0, q * 64, epi_sa, epi_sb, epi_bias, s_pt,
+                             has_bias, pp_lane(), smem + STG0 + q * STG_BYTES);
+            }
             barrier_lds();   // pairs with group 1's last barrier of the tile
             __builtin_amdgcn_sched_barrier(0);
             if (un < num_units) {
                 T = pp_tile(p, un, GROUP_M, xcd);
                 PpParams pv;
-                if (need_epi) pv = pp_params_load(p, T, tid, has_bias);
+                if (need_epi) pv = pp_params_load<EPI>(p, T, tid, has_bias, s_pt);
                 pp_tile_start(smem, p, T, L, q);
                 wait_vmcnt<0>();
                 if (need_epi) {
@@ -1651,9 +1908,14 @@ __global__ void __launch_bounds__(pp::THREADS) fp8_gemm_pp_kernel(Params p) {
                 barrier_lds();
                 __builtin_amdgcn_sched_barrier(0);
             }
-            if (!split || pp_split_fixup(acc, p, u, T.t, wave, pp_lane()))
-                pp_store(acc, p, T.row0, T.col0, 128, q * 64, epi_sa, epi_sb, epi_bias, s_pt,
-                         has_bias, pp_lane(), smem + STG1 + q * STG_BYTES);
+            if (!split || pp_split_fixup(acc, p, u, T.t, wave, pp_lane())) {
+                if constexpr (EPI)
+                    pp_epi_store(acc, p, T.row0, T.col0, 128, q * 64, epi_sa, epi_sb, epi_bias,
+                                 smem + STG1 + q * STG_BYTES);
+                else
+                    pp_store(acc, p, T.row0, T.col0, 128, q * 64, epi_sa, epi_sb, epi_bias, s_pt,
+                             has_bias, pp_lane(), smem + STG1 + q * STG_BYTES);
+            }
             __builtin_amdgcn_s_barrier();   // group 0's first slices of the next unit have landed
             __builtin_amdgcn_sched_barrier(0);
             if (u + G < num_units) T = pp_tile(p, u + G, GROUP_M, xcd);
@@ -1661,17 +1923,19 @@ __global__ void __launch_bounds__(pp::THREADS) fp8_gemm_pp_kernel(Params p) {
     }
 }
 
-template <int GROUP_M, int FMT>
+template <int GROUP_M, int FMT, bool EPI = false>
 void launch_pp(const Params& p, dim3 grid, hipStream_t stream) {
-    hipLaunchKernelGGL((fp8_gemm_pp_kernel<GROUP_M, FMT>), grid, dim3(pp::THREADS), 0, stream, p);
+    hipLaunchKernelGGL((fp8_gemm_pp_kernel<GROUP_M, FMT, EPI>), grid, dim3(pp::THREADS), 0, stream,
+                       static_cast<const KernelParams<EPI>&>(p));
 }
 
 template <int BM, int BN, int BK, int WAVES_M, int WAVES_N, int STAGES, int MI, int GROUP_M,
-          bool NT_B, int FMT, bool SK = false>
+          bool NT_B, int FMT, bool SK = false, bool EPI = false>
 void launch_cfg(const Params& p, dim3 grid, hipStream_t stream) {
     using C = Cfg<BM, BN, BK, WAVES_M, WAVES_N, STAGES, MI, GROUP_M, NT_B, FMT>;
-    hipLaunchKernelGGL((fp8_gemm_kernel<BM, BN, BK, WAVES_M, WAVES_N, STAGES, MI, GROUP_M, NT_B, FMT, SK>),
-                       grid, dim3(C::THREADS), 0, stream, p);
+    hipLaunchKernelGGL((fp8_gemm_kernel<BM, BN, BK, WAVES_M, WAVES_N, STAGES, MI, GROUP_M, NT_B, FMT, SK, EPI>),
+                       grid, dim3(C::THREADS), 0, stream,
+                       static_cast<const KernelParams<EPI>&>(p));
 }
 
 // The stream-K launch of a configuration, or null where none is compiled.
@@ -1702,4 +1966,21 @@ constexpr Launch stream_k_launch() {
     LaunchPair NAME[kNumConfigs] = {                                              \
         FP8MM_GENERIC_CONFIGS(FP8MM_PAIR_F(FMT))                                  \
         LaunchPair{&launch_pp<8, FMT>, nullptr, nullptr}};                        \
+    }
+
+// The same for the linear layer's epilogue.
+#define FP8MM_LINEAR_PAIR(FMT, name, BM, BN, BK, WMW, WNW, ST, MI, GM)                        \
+    LaunchPair{&launch_cfg<BM, BN, BK, WMW, WNW, ST, MI, GM, false, FMT, false, true>,       \
+               &launch_cfg<BM, BN, BK, WMW, WNW, ST, MI, GM, true, FMT, false, true>, nullptr},
+#define FP8MM_LINEAR_F(FMT) FP8MM_LINEAR_F_##FMT
+#define FP8MM_LINEAR_F_0(...) FP8MM_LINEAR_PAIR(0, __VA_ARGS__)
+#define FP8MM_LINEAR_F_1(...) FP8MM_LINEAR_PAIR(1, __VA_ARGS__)
+#define FP8MM_LINEAR_F_2(...) FP8MM_LINEAR_PAIR(2, __VA_ARGS__)
+#define FP8MM_LINEAR_F_3(...) FP8MM_LINEAR_PAIR(3, __VA_ARGS__)
+
+#define FP8MM_DEFINE_LINEAR_TABLE(NAME, FMT)                                        \
+    namespace fp8mm {                                                             \
+    LaunchPair NAME[kNumConfigs] = {                                              \
+        FP8MM_GENERIC_CONFIGS(FP8MM_LINEAR_F(FMT))                                \
+        LaunchPair{&launch_pp<8, FMT, true>, nullptr, nullptr}};                  \
     }

@@ -27,7 +27,8 @@
 //     row alignment allows).
 //
 // The kernels and their launch wrappers are in fp8_gemm_kernels.h; each
-// operand format pair's instances come from fp8_gemm_f<k>.hip.
+// operand format pair's instances come from fp8_gemm_f<k>.hip, those with the
+// linear layer's epilogue (include/fp8_linear.h) from fp8_linear_f<k>.hip.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -35,6 +36,7 @@
 
 #include <mutex>
 
+#include "../../include/fp8_linear.h"
 #include "../../include/fp8_scaled_mm.h"
 #include "fp8_gemm_kernels.h"
 #include "plan_cost_table.h"
@@ -70,6 +72,11 @@ const ConfigInfo kConfigs[kNumConfigs] = {
 
 // Launch wrappers by operand formats, then configuration.
 LaunchPair* const kLaunch[kFormats] = {kLaunchF0, kLaunchF1, kLaunchF2, kLaunchF3};
+LaunchPair* const kLinear[kFormats] = {kLinearF0, kLinearF1, kLinearF2, kLinearF3};
+static_assert((int)kActNone == FP8MM_ACT_NONE && (int)kActRelu == FP8MM_ACT_RELU &&
+                  (int)kActGelu == FP8MM_ACT_GELU && (int)kActGeluTanh == FP8MM_ACT_GELU_TANH &&
+                  (int)kActSilu == FP8MM_ACT_SILU && kActCount == 5,
+              "the kernels' activations are the ABI's");
 constexpr int kNarrow16x32 = 0;       // "bm16_bn32_bk512_w1x2_s6_mfma16"
 constexpr int kSkinny16x64 = 1;       // "bm16_bn64_bk256_w1x4_s4_mfma16"
 constexpr int kSkinny16x112 = 2;      // "bm16_bn112_bk256_w1x7_s4_mfma16"
@@ -551,10 +558,17 @@ int run_stream_k(const void* A, int fmt, const void* B, const float* scale_a, co
     return FP8MM_OK;
 }
 
+// The linear layer's epilogue beyond scale and bias.
+struct Epilogue {
+    const void* residual;   // may be null
+    void* preact;           // may be null
+    int act;
+};
+
 int run_mm(const void* A, int a_format, const void* B, int b_format, const float* scale_a,
            const float* scale_b, const void* bias, void* out, int64_t M, int64_t N, int64_t K,
            int mode, struct ihipStream_t* stream, int config_id, int splits, void* workspace,
-           int64_t workspace_size, WsSource src) {
+           int64_t workspace_size, WsSource src, const Epilogue* epi = nullptr) {
     if ((a_format != FP8MM_E4M3FN && a_format != FP8MM_E5M2) ||
         (b_format != FP8MM_E4M3FN && b_format != FP8MM_E5M2))
         return FP8MM_ERR_FORMAT;
@@ -563,6 +577,7 @@ int run_mm(const void* A, int a_format, const void* B, int b_format, const float
     if (st != FP8MM_OK) return st;
     if (config_id >= kNumConfigs) return FP8MM_ERR_CONFIG;
     if (splits < FP8MM_SPLITS_STREAM_K || splits > 64) return FP8MM_ERR_CONFIG;
+    if (epi && splits == FP8MM_SPLITS_STREAM_K) return FP8MM_ERR_CONFIG;
     if (M == 0 || N == 0) return FP8MM_OK;
     if (splits == FP8MM_SPLITS_STREAM_K)
         return run_stream_k(A, fmt, B, scale_a, scale_b, bias, out, M, N, K, mode, stream, config_id,
@@ -608,16 +623,24 @@ int run_mm(const void* A, int a_format, const void* B, int b_format, const float
                            static_cast<unsigned*>(ws), n);
     }
 
-    Params p = base_params(A, B, scale_a, scale_b, bias, out, M, N, K, mode, c);
+    LinearParams p;
+    static_cast<Params&>(p) = base_params(A, B, scale_a, scale_b, bias, out, M, N, K, mode, c);
     p.splits = sp;
     p.k_chunk = (int)cdiv(k_iters, sp);
+    if (epi) {
+        p.residual = static_cast<const uint16_t*>(epi->residual);
+        p.preact = static_cast<uint16_t*>(epi->preact);
+        p.act = epi->act;
+        p.vec_store = p.vec_store && aligned(p.residual, 8) && aligned(p.preact, 8);
+        p.vec16 = p.vec16 && aligned(p.residual, 16) && aligned(p.preact, 16);
+    }
     if (sp > 1) {
         p.counters = static_cast<unsigned*>(ws);
         p.partials = reinterpret_cast<float*>(static_cast<char*>(ws) + kCounterBytes);
     }
 
     const dim3 grid((unsigned)grid_for(cfg, M, N, sp, cus));
-    const LaunchPair& l = kLaunch[fmt][cfg];
+    const LaunchPair& l = (epi ? kLinear : kLaunch)[fmt][cfg];
     if (p.tiles_m == 1 && l.stream) l.stream(p, grid, hs);
     else l.plain(p, grid, hs);
     if (hipGetLastError() != hipSuccess) return FP8MM_ERR_LAUNCH;
@@ -662,6 +685,7 @@ const char* fp8_scaled_mm_status_string(int s) {
         case FP8MM_ERR_SCRATCH:
             return "the requested split-K plan needs more than the 64 MiB device scratch of "
                    "fp8_scaled_mm_noalloc";
+        case FP8MM_ERR_ACTIVATION: return "unknown activation";
         default: return "unknown status";
     }
 }
@@ -675,6 +699,21 @@ int fp8_scaled_mm_typed(const void* A, int a_format, const void* B, int b_format
     return run_mm(A, a_format, B, b_format, scale_a, scale_b, bias, out, M, N, K, mode, stream,
                   config_id, splits, workspace, workspace_size,
                   workspace ? WsSource::kCaller : WsSource::kNone);
+}
+
+int fp8_linear(const void* A, int a_format, const void* B, int b_format, const float* scale_a,
+               const float* scale_b, const void* bias, const void* residual, int activation,
+               void* preact, void* out, int64_t M, int64_t N, int64_t K, int mode,
+               struct ihipStream_t* stream, int config_id, int splits, void* workspace,
+               int64_t workspace_size) {
+    if (activation < FP8MM_ACT_NONE || activation > FP8MM_ACT_SILU) return FP8MM_ERR_ACTIVATION;
+    if (!aligned(residual, 2) || !aligned(preact, 2)) return FP8MM_ERR_ALIGN;
+    // Scale and bias alone are fp8_scaled_mm_typed's epilogue.
+    const Epilogue e{residual, preact, activation};
+    const bool plain = !residual && !preact && activation == FP8MM_ACT_NONE;
+    return run_mm(A, a_format, B, b_format, scale_a, scale_b, bias, out, M, N, K, mode, stream,
+                  config_id, splits, workspace, workspace_size,
+                  workspace ? WsSource::kCaller : WsSource::kNone, plain ? nullptr : &e);
 }
 
 int fp8_scaled_mm_with_plan(const void* A, const void* B, const float* scale_a,
