@@ -47,6 +47,50 @@ int fp8_linear(const void* A, int a_format, const void* B, int b_format, const f
                int scaling_mode, struct ihipStream_t* stream, int config_id, int splits,
                void* workspace, int64_t workspace_bytes);
 
+/* The gradient of out = act(x W^T + bias) with float8 operands.  For dy, the
+ * gradient of act(z), and z = preact of the forward call:
+ *
+ *     dz    = dy * act'(z)                           (fp32)
+ *     dbias = sum over rows of dz                    (fp32)
+ *     dx    = bf16_rne( dz W ):    dz as e5m2 with one scale for each row
+ *     dw    = bf16_rne( dz^T x ):  dz as e5m2 with one scale for each column,
+ *                                  x as e4m3fn with one scale for each column
+ *
+ *   Scales are max / qmax (57344, 448) and codes RNE(value / scale), as in
+ *   fp8_quantize.h: for dz of none and relu and for x (values of few bits, whose
+ *   quotients meet ties) with the correctly rounded quotient, for the other
+ *   activations with the product by 1 / scale.  A row or column whose scale
+ *   would be below 2^-126 has scale 0 and codes 0.
+ *
+ *   dy, z  M x N bf16;  x  M x K bf16 (row-major).  z may be NULL for
+ *          FP8MM_ACT_NONE.  (dy also is the residual's gradient.)
+ *   wt     W transposed: K x N float8 codes of wt_format, row-major, with
+ *          wt_scale[k] for row k, laid out once for each update of the weights.
+ *   dx     M x K bf16, dw  N x K bf16, dbias  N fp32.  Each may be NULL: what
+ *          only it needs is then not computed (x, and wt with its scales, may
+ *          then be NULL too).  At least one of them is needed.
+ *
+ * A NaN in dz or x comes out in the outputs that it reaches, and so does an
+ * infinity (as a NaN).
+ * Preconditions: 0 <= M <= 2^31 - 1, 16 <= N, K <= 2^23, both multiples of 16;
+ * with dw also M <= 2^23.  wt 16-byte aligned, bf16 tensors 2-byte, fp32 ones
+ * 4-byte aligned.  Outputs must not overlap inputs or each other.  With M == 0, dw and dbias are zeros.
+ * `workspace` is 256-byte aligned, zero-filled before its first use, and at
+ * least fp8_linear_backward_workspace_size() bytes; its first 256 KiB are
+ * arrival counters, zero again after every call.  It may serve calls of any
+ * shape, one at a time.  Execution and status codes are those of
+ * fp8_scaled_mm.h; equal calls give equal bits. */
+int fp8_linear_backward(const void* dy, const void* x_or_null, const void* wt_or_null,
+                        int wt_format, const float* wt_scale_or_null, const void* z_or_null,
+                        int activation, void* dx_or_null, void* dw_or_null, float* dbias_or_null,
+                        int64_t M, int64_t N, int64_t K, struct ihipStream_t* stream,
+                        void* workspace, int64_t workspace_bytes);
+
+/* Bytes of workspace for the outputs asked for (host logic only; -1 for an
+ * invalid problem). */
+int64_t fp8_linear_backward_workspace_size(int64_t M, int64_t N, int64_t K, int want_dx,
+                                           int want_dw);
+
 #ifdef __cplusplus
 }
 #endif

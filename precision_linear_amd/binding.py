@@ -53,7 +53,7 @@ _Q_ARG_ERRORS = {Q_ERR_NULL, Q_ERR_SHAPE, Q_ERR_ALIGN, Q_ERR_MODE, Q_ERR_WORKSPA
 
 # functions from include/fp8_linear.h (status codes: those of fp8_scaled_mm.h)
 # and its activations (enum fp8mm_activation)
-LINEAR_EXPORTS = ("fp8_linear",)
+LINEAR_EXPORTS = ("fp8_linear", "fp8_linear_backward", "fp8_linear_backward_workspace_size")
 _ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 # functions and status codes from include/fp8_layer_norm.h
@@ -127,6 +127,11 @@ def lib() -> ctypes.CDLL:
         L.fp8_linear.argtypes = [vp, i32, vp, i32, vp, vp, vp, vp, i32, vp, vp, i64, i64, i64, i32, vp,
                                  i32, i32, vp, i64]
         L.fp8_linear.restype = i32
+        L.fp8_linear_backward.argtypes = [vp, vp, vp, i32, vp, vp, i32, vp, vp, vp, i64, i64, i64, vp, vp,
+                                          i64]
+        L.fp8_linear_backward.restype = i32
+        L.fp8_linear_backward_workspace_size.argtypes = [i64, i64, i64, i32, i32]
+        L.fp8_linear_backward_workspace_size.restype = i64
         f32 = ctypes.c_float
         L.fp8_layer_norm.argtypes = [vp, i32, vp, vp, i32, f32, vp, vp, i32, vp, vp, vp, i64, i64, vp]
         L.fp8_layer_norm.restype = i32
@@ -360,6 +365,99 @@ def fp8_linear(a: torch.Tensor, b: torch.Tensor, scale_a: torch.Tensor, scale_b:
                           stream, int(config), int(splits), ws_ptr, ws_bytes)
     _mm_check("fp8_linear", st)
     return out
+
+
+def fp8_linear_backward(dy: torch.Tensor, x: torch.Tensor | None, wt: torch.Tensor | None,
+                        wt_scale: torch.Tensor | None, z: torch.Tensor | None = None, *,
+                        activation="none", dx=True, dw=True, dbias: bool = True, wt_format=None,
+                        workspace: torch.Tensor | None = None):
+    """(dx, dw, dbias) of out = act(x W^T + bias) from dy, the gradient of act(z):
+
+        dz = dy act'(z),  dx = dz W,  dw = dz^T x,  dbias = sum of dz over the rows
+
+    with dz in e5m2 (a scale for each row in dx, for each column in dw), x in
+    e4m3fn (a scale for each column) and W as float8 codes.
+
+    dy and z (fp8_linear's preact; not needed for 'none') are M x N bf16, x is
+    M x K bf16, wt the K x N codes of W transposed with K scales wt_scale.  dx
+    (M x K) and dw (N x K) are bf16, dbias is fp32; True allocates one, False
+    leaves it (and what only it needs) out, and dx and dw may be buffers.  What is left out is None in
+    the result.  N and K are multiples of 16.  Codes, scales and partial sums
+    live in `workspace` (a GPU byte tensor, zero-filled before its first use) or
+    in one that this module keeps per stream."""
+    act = _activation(activation)
+
+    def matrix(name, t, rows, cols):
+        if t.dtype != torch.bfloat16 or t.dim() != 2 or not t.is_contiguous() or \
+                (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+            raise ValueError(f"{name} must be a contiguous bf16 {'M' if rows is None else rows} x "
+                             f"{'N' if cols is None else cols} tensor")
+
+    for name, want in (("dx", dx), ("dw", dw), ("dbias", dbias)):
+        if not isinstance(want, (bool, torch.Tensor)) or (name == "dbias" and not isinstance(want, bool)):
+            raise ValueError(f"{name} must be True, False" + ("" if name == "dbias" else " or a tensor to write"))
+    want_dx, want_dw = dx is not False, dw is not False
+    if not (want_dx or want_dw or dbias):
+        raise ValueError("nothing to compute: dx, dw and dbias are all False")
+    if not dy.is_cuda:
+        raise ValueError("all tensors must be on the GPU")
+    matrix("dy", dy, None, None)
+    M, N = dy.shape
+    if act != 0 and z is None:
+        raise ValueError(f"activation {activation!r} needs z")
+    if z is not None:
+        matrix("z", z, M, N)
+    K, fw = 16, E4M3FN      # (a problem without dx and dw has no K)
+    if want_dw:
+        if x is None:
+            raise ValueError("dw needs x")
+        matrix("x", x, M, None)
+        K = x.shape[1]
+    if want_dx:
+        if wt is None or wt_scale is None:
+            raise ValueError("dx needs wt and wt_scale")
+        wt, fw = _as_codes(wt, "wt", wt_format)
+        if wt.dim() != 2 or not wt.is_contiguous() or wt.shape[1] != N or (want_dw and wt.shape[0] != K):
+            raise ValueError(f"wt must be contiguous K x N codes with N = {N}" +
+                             (f" and K = {K}" if want_dw else "") + f", got {tuple(wt.shape)}")
+        K = wt.shape[0]
+        _ln_vector(wt_scale, "wt_scale", K)
+    if N < 16 or N % 16 != 0 or K < 16 or K % 16 != 0:
+        raise ValueError(f"N and K must be multiples of 16, got {N} and {K}")
+    dev = dy.get_device()
+    device = dy.device
+    used = [("z", z), ("workspace", workspace), ("dx", dx if want_dx and dx is not True else None),
+            ("dw", dw if want_dw and dw is not True else None)]
+    used += [("x", x)] if want_dw else []
+    used += [("wt", wt), ("wt_scale", wt_scale)] if want_dx else []
+    _check_devices(dev, used)
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous GPU tensor")
+    if dx is True:
+        dx = torch.empty((M, K), dtype=torch.bfloat16, device=device)
+    elif want_dx:
+        matrix("dx", dx, M, K)
+    if dw is True:
+        dw = torch.empty((N, K), dtype=torch.bfloat16, device=device)
+    elif want_dw:
+        matrix("dw", dw, N, K)
+    dx, dw = dx if want_dx else None, dw if want_dw else None
+    db = torch.empty(N, dtype=torch.float32, device=device) if dbias else None
+    L = lib()
+    stream = _stream_of(dev)
+    with _on_device(dev):
+        if workspace is not None:
+            ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        else:
+            need = int(L.fp8_linear_backward_workspace_size(M, N, K, want_dx, want_dw))
+            if need < 0:
+                raise ValueError(f"fp8_linear_backward: {status_string(ERR_SHAPE)}")
+            ws, ws_bytes = _workspace(device, stream, need, "linear_grad").data_ptr(), need
+        st = L.fp8_linear_backward(dy.data_ptr(), _ptr(x) if want_dw else None,
+                                   _ptr(wt) if want_dx else None, fw, _ptr(wt_scale) if want_dx else None,
+                                   _ptr(z), act, _ptr(dx), _ptr(dw), _ptr(db), M, N, K, stream, ws, ws_bytes)
+    _mm_check("fp8_linear_backward", st)
+    return dx, dw, db
 
 
 def _activation(activation) -> int:

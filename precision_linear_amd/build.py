@@ -1,5 +1,5 @@
 """Builds libfp8_scaled_mm.so (the HIP kernels -- scaled multiply,
-quantiser and layer norm -- and their C ABI) for gfx950.
+quantiser, layer norm and linear layer -- and their C ABI) for gfx950.
 
 hipcc cross-compiles without a GPU.  The library is written next to this
 file so that it travels with the source tree.
@@ -15,10 +15,13 @@ import tempfile
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 # The host logic and C ABI, one translation unit per operand-format pair of
-# the multiply's kernels (and of those with the linear layer's epilogue), the quantiser and the layer norm.  They compile in parallel.
+# the multiply's kernels (and of those with the linear layer's epilogue), the quantiser, the layer norm
+# and the linear layer's gradient.  They compile in parallel.
 SRCS = [os.path.join(HERE, "csrc", f) for f in
-        ["fp8_scaled_mm.hip"] + [f"fp8_{n}_f{k}.hip" for n in ("gemm", "linear") for k in range(4)] + ["fp8_quantize.hip", "fp8_layer_norm.hip"]]
-HEADERS = [os.path.join(HERE, "csrc", f) for f in ("fp8_gemm_kernels.h", "fp8_convert.h", "activation.h", "plan_cost_table.h")]
+        ["fp8_scaled_mm.hip"] + [f"fp8_{n}_f{k}.hip" for n in ("gemm", "linear") for k in range(4)] +
+        ["fp8_quantize.hip", "fp8_layer_norm.hip", "fp8_linear_grad.hip"]]
+HEADERS = [os.path.join(HERE, "csrc", f) for f in
+           ("fp8_gemm_kernels.h", "fp8_convert.h", "lane_ops.h", "activation.h", "plan_cost_table.h")]
 LIB = os.path.join(HERE, "libfp8_scaled_mm.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -46,7 +49,7 @@ def _run(cmd, verbose):
 SANITIZE_HOST = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
                  "-Xarch_host", "-fno-sanitize-recover=undefined",
                  "-Xarch_host", "-fno-omit-frame-pointer", "-Xarch_host", "-g"]
-HOST_LOGIC_SRCS = {"fp8_scaled_mm.hip", "fp8_quantize.hip", "fp8_layer_norm.hip"}
+HOST_LOGIC_SRCS = {"fp8_scaled_mm.hip", "fp8_quantize.hip", "fp8_layer_norm.hip", "fp8_linear_grad.hip"}
 
 
 def build(verbose: bool = False, sanitize: bool = False, out: str | None = None) -> str:

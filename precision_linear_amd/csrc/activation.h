@@ -11,9 +11,10 @@
 // polynomial P.  p and P's coefficients were fitted here (weighted least
 // squares, reweighted towards the least largest relative error, over 0 <= t <=
 // 14): degree 8 with p = 0.3, relative error at most 1.5e-7, so Phi keeps its
-// relative accuracy in the negative tail, where 1 + erf cancels.  The gradient
-// uses that one, as its sums are fp32 outputs.  The epilogue's results are
-// rounded to bf16 (half a step is 3.9e-3): degree 5 with p = 0.38, 3.6e-5.
+// relative accuracy in the negative tail, where 1 + erf cancels.  The slope
+// takes that one (FINE): it feeds fp32 sums, and has a root near z = -0.75,
+// where an error of Phi is large beside it.  The epilogue's results are rounded
+// to bf16 (half a step is 3.9e-3): degree 5 with p = 0.38, 3.6e-5.
 //
 // exp2 and the reciprocal are the hardware's (1 ulp).
 #pragma once

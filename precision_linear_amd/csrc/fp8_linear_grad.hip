@@ -1,0 +1,467 @@
+// The gradient of the FP8 linear layer for gfx950 (MI355X) (formulas:
+// include/fp8_linear.h).
+//
+// dz = dy act'(z) is needed in float8 twice, with one scale for each row (for
+// dx) and with one for each column, transposed (for dw, whose products run
+// over the rows).  Both scales need the maxima of whole rows and columns, so dz
+// is computed twice rather than written out in 32 bits:
+//   1. grad_stats_kernel: maxima of dz's rows and columns, sums of its columns
+//      (dbias), maxima of x's columns, as partial results;
+//   2. grad_scales_kernel: joins them into the scales and dbias;
+//   3. grad_quantize_kernel: the codes of dz (row-major, and transposed) and of
+//      x (transposed);
+//   4. the two products, on the scaled multiply's kernels.
+// Passes 1 and 3 are bound by memory (and, for the smooth activations, nearly
+// by the arithmetic of the slope): 2 x 4 bytes read and 2 bytes written for an
+// element of dz, against 4 K bytes' worth of matrix work.
+//
+// Nothing is summed in an order that depends on timing: sums go through
+// partial results joined in a fixed order.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/fp8_linear.h"
+#include "activation.h"
+#include "fp8_convert.h"
+#include "lane_ops.h"
+
+namespace {
+
+constexpr int kThreadsG = 256;
+constexpr int kTileCols = 128;                      // 16 lanes x 8 columns
+constexpr int kColLanes = kTileCols / 8;            // 16: a DPP row
+constexpr int kRowLanes = kThreadsG / kColLanes;    // 16
+constexpr int kTileRows = 128;                      // of the quantisation's tiles
+constexpr int kStatUnroll = 4;                      // rows in flight per thread
+
+struct Grad {
+    const bf16_t* dy;
+    const bf16_t* z;       // null for kActNone
+    const bf16_t* x;       // null without dw
+    int64_t M, N, K;
+    int64_t Mp;            // M rounded up to 16: row length of the transposed codes
+    int blocks_n, blocks_k;   // column blocks of dz and x (0 without dw)
+    int parts;             // row strips of pass 1
+    int64_t strip;         // rows of a strip
+    int want_rows, want_cols;   // dz codes by rows (dx), by columns (dw)
+    // Partial results: [blocks_n][M], [parts][N], [parts][N], [parts][K]
+    float* row_max;
+    float* col_max;
+    float* col_sum;
+    float* x_max;
+    // Scales, and their reciprocals right behind them: 2 M, 2 N, 2 K
+    float* row_scale;
+    float* col_scale;
+    float* x_scale;
+    float* dbias;          // may be null
+    uint8_t* q_rows;       // M x N
+    uint8_t* q_cols;       // N x Mp
+    uint8_t* q_x;          // K x Mp
+};
+
+// dz of 8 elements.
+template <int ACT>
+__device__ __forceinline__ void dz8(const Raw8<bf16_t>& dy, const Raw8<bf16_t>& z, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = dy.get(i) * slope<ACT>(z.get(i));
+}
+
+// Pass 1.  Workgroup: 128 columns of one strip of rows, of dz or (the last
+// blocks) of x.  16 lanes hold a row's 128 columns, 16 rows at a time.
+template <int ACT>
+__global__ void __launch_bounds__(kThreadsG)
+grad_stats_kernel(Grad p) {
+    __shared__ float s_max[kRowLanes][kTileCols], s_sum[kRowLanes][kTileCols];
+    const int cl = threadIdx.x % kColLanes, rl = threadIdx.x / kColLanes;
+    const int per_part = p.blocks_n + p.blocks_k;
+    const int part = blockIdx.x / per_part;
+    const int block = blockIdx.x - part * per_part;
+    const bool is_x = block >= p.blocks_n;
+    const int cb = is_x ? block - p.blocks_n : block;
+    const int64_t width = is_x ? p.K : p.N;
+    const int64_t col = (int64_t)cb * kTileCols + cl * 8;
+    const bool ok = col < width;                       // widths are multiples of 16
+    const int64_t r1 = min(p.M, (part + 1) * p.strip);
+    float cmax[8], csum[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) cmax[i] = csum[i] = 0.f;
+    for (int64_t r = part * p.strip + rl; r < r1; r += kRowLanes * kStatUnroll) {
+        Raw8<bf16_t> a[kStatUnroll], b[kStatUnroll];
+#pragma unroll
+        for (int u = 0; u < kStatUnroll; ++u) {
+            const int64_t row = r + u * kRowLanes;
+            a[u].zero();
+            b[u].zero();
+            if (ok && row < r1) {
+                a[u].load((is_x ? p.x : p.dy) + row * width + col);
+                if (ACT != kActNone && !is_x) b[u].load(p.z + row * width + col);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kStatUnroll; ++u) {
+            const int64_t row = r + u * kRowLanes;
+            float f[8];
+            if (is_x) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = a[u].get(i);
+            } else {
+                dz8<ACT>(a[u], b[u], f);
+            }
+            float rmax = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                cmax[i] = fmaxf(cmax[i], fabsf(f[i]));
+                rmax = fmaxf(rmax, fabsf(f[i]));
+                csum[i] += f[i];
+            }
+            if (!is_x && p.want_rows) {
+                rmax = row16_max(rmax);
+                if (cl == 0 && row < r1) p.row_max[cb * p.M + row] = rmax;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        s_max[rl][cl * 8 + i] = cmax[i];
+        s_sum[rl][cl * 8 + i] = csum[i];
+    }
+    __syncthreads();
+    const int t = threadIdx.x % kTileCols;
+    const int64_t c = (int64_t)cb * kTileCols + t;
+    if (c >= width) return;
+    if (threadIdx.x < kTileCols) {
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < kRowLanes; ++i) m = fmaxf(m, s_max[i][t]);
+        (is_x ? p.x_max : p.col_max)[part * width + c] = m;
+    } else if (!is_x) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kRowLanes; ++i) sum += s_sum[i][t];
+        p.col_sum[part * width + c] = sum;
+    }
+}
+
+// Pass 2.  Workgroup: 64 rows of dz, columns of dz or columns of x, 16 slices
+// of their partial results each.
+constexpr int kScaleThreads = 1024;
+
+__device__ __forceinline__ void put_scale(float amax, float qmax, float* scale, int64_t n, int64_t i) {
+    float s = amax / qmax;
+    if (s < 0x1p-126f) s = 0.f;       // (its reciprocal would leave fp32)
+    scale[i] = s;
+    scale[n + i] = s == 0.f ? 0.f : 1.f / s;
+}
+
+__global__ void __launch_bounds__(kScaleThreads)
+grad_scales_kernel(Grad p, int blocks_rows, int blocks_cols) {
+    __shared__ float s_max[16][64], s_sum[16][64];
+    const int lane = threadIdx.x % 64, slice = threadIdx.x / 64;
+    int b = blockIdx.x;
+    const float* part_max;
+    const float* part_sum = nullptr;
+    float* scale;
+    int64_t n;
+    int parts;
+    float qmax = Fp8Fmt<1>::kMax;
+    if (b < blocks_rows) {
+        part_max = p.row_max; n = p.M; parts = p.blocks_n; scale = p.row_scale;
+    } else if (b < blocks_rows + blocks_cols) {
+        b -= blocks_rows;
+        part_max = p.col_max; part_sum = p.dbias ? p.col_sum : nullptr; n = p.N; parts = p.parts;
+        scale = p.col_scale;
+    } else {
+        b -= blocks_rows + blocks_cols;
+        part_max = p.x_max; n = p.K; parts = p.parts; scale = p.x_scale; qmax = Fp8Fmt<0>::kMax;
+    }
+    const int64_t i = (int64_t)b * 64 + lane;
+    float m = 0.f, sum = 0.f;
+    if (i < n)
+        for (int q = slice; q < parts; q += 16) {
+            m = fmaxf(m, part_max[q * n + i]);
+            if (part_sum) sum += part_sum[q * n + i];
+        }
+    s_max[slice][lane] = m;
+    s_sum[slice][lane] = sum;
+    __syncthreads();
+    if (slice != 0 || i >= n) return;
+#pragma unroll
+    for (int q = 1; q < 16; ++q) {
+        m = fmaxf(m, s_max[q][lane]);
+        sum += s_sum[q][lane];
+    }
+    put_scale(m, qmax, scale, n, i);
+    if (part_sum) p.dbias[i] = sum;
+}
+
+// value / s: EXACT correctly rounded, else the product by r = 1 / s.  With s =
+// r = 0 every finite value gives 0, with s infinite (r = 0) an infinity gives
+// NaN; NaN stays NaN.
+template <bool EXACT>
+__device__ __forceinline__ float over_scale(float v, float s, float r) {
+    if constexpr (EXACT) return div_fast(v, Div{s, r, true});
+    else return v * r;
+}
+
+// Pass 3.  Workgroup: a tile of 128 rows x 128 columns of dz or (the last
+// blocks) of x.  A thread takes 4 consecutive rows of 8 columns at a time, so
+// that 4 codes of a column make one word of the transposed tile in LDS: 128
+// rows of 8 16-byte chunks, chunk c of column n at c ^ ((n >> 3) & 7), which
+// spreads the 16 column lanes over the banks.
+template <int ACT>
+__global__ void __launch_bounds__(kThreadsG)
+grad_quantize_kernel(Grad p) {
+    __shared__ __attribute__((aligned(16))) uint32_t s_t[kTileCols][kTileRows / 4];
+    constexpr bool kExactDz = ACT == kActNone || ACT == kActRelu;
+    const int cl = threadIdx.x % kColLanes, rl = threadIdx.x / kColLanes;
+    const int per_strip = p.blocks_n + p.blocks_k;
+    const int64_t strip = blockIdx.x / per_strip;
+    const int block = (int)(blockIdx.x - strip * per_strip);
+    const bool is_x = block >= p.blocks_n;
+    const int cb = is_x ? block - p.blocks_n : block;
+    const int64_t width = is_x ? p.K : p.N;
+    const int64_t col = (int64_t)cb * kTileCols + cl * 8;
+    const int64_t row0 = strip * kTileRows;
+    const bool ok = col < width;
+    const bool transposed = is_x || p.want_cols;
+    float cs[8], cr[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) cs[i] = cr[i] = 0.f;
+    if (ok && transposed) {
+        const float* s = (is_x ? p.x_scale : p.col_scale) + col;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            cs[i] = s[i];
+            cr[i] = s[width + i];
+        }
+    }
+#pragma unroll
+    for (int it = 0; it < kTileRows / (4 * kRowLanes); ++it) {
+        const int mg = it * kRowLanes + rl;            // group of 4 rows in the tile
+        const int64_t r = row0 + mg * 4;
+        Raw8<bf16_t> a[4], b[4];
+        float rs[4], rr[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            a[k].zero();
+            b[k].zero();
+            rs[k] = rr[k] = 0.f;
+            if (ok && r + k < p.M) {
+                a[k].load((is_x ? p.x : p.dy) + (r + k) * width + col);
+                if (ACT != kActNone && !is_x) b[k].load(p.z + (r + k) * width + col);
+                if (!is_x && p.want_rows) {
+                    rs[k] = p.row_scale[r + k];
+                    rr[k] = p.row_scale[p.M + r + k];
+                }
+            }
+        }
+        float f[4][8];
+        uint32_t words[8];
+        if (is_x) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[k][i] = over_scale<true>(a[k].get(i), cs[i], cr[i]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                int w = Fp8Fmt<0>::cvt_pk<false>(f[0][i], f[1][i], 0);
+                words[i] = (uint32_t)Fp8Fmt<0>::cvt_pk<true>(f[2][i], f[3][i], w);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) dz8<ACT>(a[k], b[k], f[k]);
+            if (p.want_rows) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float t[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) t[i] = over_scale<kExactDz>(f[k][i], rs[k], rr[k]);
+                    u32x2 codes;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        int w = Fp8Fmt<1>::cvt_pk<false>(t[4 * h], t[4 * h + 1], 0);
+                        codes[h] = (uint32_t)Fp8Fmt<1>::cvt_pk<true>(t[4 * h + 2], t[4 * h + 3], w);
+                    }
+                    if (ok && r + k < p.M)
+                        *reinterpret_cast<u32x2*>(p.q_rows + (r + k) * p.N + col) = codes;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                int w = Fp8Fmt<1>::cvt_pk<false>(over_scale<kExactDz>(f[0][i], cs[i], cr[i]),
+                                                 over_scale<kExactDz>(f[1][i], cs[i], cr[i]), 0);
+                words[i] = (uint32_t)Fp8Fmt<1>::cvt_pk<true>(over_scale<kExactDz>(f[2][i], cs[i], cr[i]),
+                                                             over_scale<kExactDz>(f[3][i], cs[i], cr[i]), w);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            s_t[cl * 8 + i][(((mg >> 2) ^ (cl & 7)) << 2) | (mg & 3)] = words[i];
+    }
+    if (!transposed) return;
+    __syncthreads();
+    uint8_t* out = is_x ? p.q_x : p.q_cols;
+#pragma unroll
+    for (int it = 0; it < kTileCols * (kTileRows / 16) / kThreadsG; ++it) {
+        const int q = it * kThreadsG + threadIdx.x;
+        const int n = q / (kTileRows / 16), c = q % (kTileRows / 16);
+        const int64_t row = (int64_t)cb * kTileCols + n, m = row0 + c * 16;
+        if (row < width && m < p.Mp)
+            *reinterpret_cast<u32x4*>(out + row * p.Mp + m) =
+                *reinterpret_cast<const u32x4*>(&s_t[n][(c ^ ((n >> 3) & 7)) << 2]);
+    }
+}
+
+// n values of 0 (the gradients of a batch without rows).
+__global__ void __launch_bounds__(kThreadsG) zero_fill_kernel(uint16_t* p, int64_t n) {
+    for (int64_t i = blockIdx.x * (int64_t)kThreadsG + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreadsG)
+        p[i] = 0;
+}
+
+// ---------------------------------------------------------------- host ---
+
+int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t align256(int64_t n) { return up(n, 256) * 256; }
+bool at(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+constexpr int64_t kMaxDim = int64_t(1) << 23;
+constexpr int64_t kCounterArea = int64_t(256) << 10;   // the multiply's arrival counters
+
+int grad_shape(int64_t M, int64_t N, int64_t K, bool want_dw) {
+    if (M < 0 || M > (want_dw ? kMaxDim : INT32_MAX) || N < 16 || N > kMaxDim || N % 16 != 0 || K < 16 ||
+        K > kMaxDim || K % 16 != 0)
+        return FP8MM_ERR_SHAPE;
+    // One-dimensional grids of 128 x 128 tiles.
+    if (up(M, kTileRows) * (up(N, kTileCols) + up(K, kTileCols)) > INT32_MAX) return FP8MM_ERR_SHAPE;
+    return FP8MM_OK;
+}
+
+// Rows of a strip of pass 1: 64 (one round of loads per thread), more where
+// there are strips enough without that, up to 256.
+int64_t strip_rows(int64_t M, int64_t blocks) {
+    int64_t s = kRowLanes * kStatUnroll;
+    while (s < 256 && up(M, 2 * s) * blocks >= 2048) s *= 2;
+    return s;
+}
+
+struct GradSpace {
+    int64_t mm, q_rows, q_cols, q_x, scales, partials, total;   // byte offsets
+    Grad p;
+};
+
+// Everything about a call but its pointers.
+GradSpace grad_space(int64_t M, int64_t N, int64_t K, bool want_dx, bool want_dw) {
+    GradSpace g;
+    Grad& p = g.p;
+    p.M = M; p.N = N; p.K = K;
+    p.Mp = up(M, 16) * 16;
+    p.want_rows = want_dx;
+    p.want_cols = want_dw;
+    p.blocks_n = (int)up(N, kTileCols);
+    p.blocks_k = want_dw ? (int)up(K, kTileCols) : 0;
+    p.strip = strip_rows(M, p.blocks_n + p.blocks_k);
+    p.parts = (int)up(M, p.strip);
+    int64_t mm = kCounterArea;
+    if (want_dx && M > 0) {
+        const int64_t n = fp8_scaled_mm_workspace_size(M, K, N, FP8MM_ROWWISE, 0, -1, 0);
+        mm = n > mm ? n : mm;
+    }
+    if (want_dw && M > 0) {
+        const int64_t n = fp8_scaled_mm_workspace_size(N, K, p.Mp, FP8MM_ROWWISE, 0, -1, 0);
+        mm = n > mm ? n : mm;
+    }
+    g.mm = align256(mm);
+    g.q_rows = g.mm;
+    g.q_cols = g.q_rows + (want_dx ? align256(M * N) : 0);
+    g.q_x = g.q_cols + (want_dw ? align256(N * p.Mp) : 0);
+    g.scales = g.q_x + (want_dw ? align256(K * p.Mp) : 0);
+    g.partials = g.scales + align256(8 * (M + N + K));
+    g.total = g.partials + align256(4 * ((want_dx ? p.blocks_n * M : 0) + 2 * p.parts * N + p.parts * K));
+    return g;
+}
+
+template <int ACT>
+void launch_passes(const Grad& p, hipStream_t hs) {
+    const int per = p.blocks_n + p.blocks_k;
+    hipLaunchKernelGGL(grad_stats_kernel<ACT>, dim3((unsigned)(p.parts * per)), dim3(kThreadsG), 0, hs, p);
+    const int rows = p.want_rows ? (int)up(p.M, 64) : 0, cols = (int)up(p.N, 64);
+    const int xs = p.blocks_k ? (int)up(p.K, 64) : 0;
+    hipLaunchKernelGGL(grad_scales_kernel, dim3((unsigned)(rows + cols + xs)), dim3(kScaleThreads), 0, hs, p, rows,
+                       cols);
+    if (p.want_rows || p.want_cols)
+        hipLaunchKernelGGL(grad_quantize_kernel<ACT>, dim3((unsigned)(up(p.M, kTileRows) * per)), dim3(kThreadsG),
+                           0, hs, p);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t fp8_linear_backward_workspace_size(int64_t M, int64_t N, int64_t K, int want_dx, int want_dw) {
+    if (grad_shape(M, N, K, want_dw != 0) != FP8MM_OK) return -1;
+    return grad_space(M, N, K, want_dx != 0, want_dw != 0).total;
+}
+
+int fp8_linear_backward(const void* dy, const void* x, const void* wt, int wt_format, const float* wt_scale,
+                        const void* z, int activation, void* dx, void* dw, float* dbias, int64_t M, int64_t N,
+                        int64_t K, struct ihipStream_t* stream, void* workspace, int64_t workspace_bytes) {
+    if (activation < FP8MM_ACT_NONE || activation > FP8MM_ACT_SILU) return FP8MM_ERR_ACTIVATION;
+    if (dx && wt_format != FP8MM_E4M3FN && wt_format != FP8MM_E5M2) return FP8MM_ERR_FORMAT;
+    int st = grad_shape(M, N, K, dw != nullptr);
+    if (st != FP8MM_OK) return st;
+    if (!dx && !dw && !dbias && M > 0) return FP8MM_ERR_NULL;
+    if (M > 0 && (!dy || (activation != FP8MM_ACT_NONE && !z) || (dx && (!wt || !wt_scale)) || (dw && !x)))
+        return FP8MM_ERR_NULL;
+    if (!at(dy, 2) || !at(z, 2) || !at(x, 2) || !at(dx, 2) || !at(dw, 2) || !at(dbias, 4) || !at(wt, 16) ||
+        !at(wt_scale, 4) || !at(workspace, 256))
+        return FP8MM_ERR_ALIGN;
+    GradSpace g = grad_space(M, N, K, dx != nullptr, dw != nullptr);
+    if (M > 0 && (!workspace || workspace_bytes < g.total)) return FP8MM_ERR_WORKSPACE;
+    int dev = -1;
+    if (hipGetDevice(&dev) != hipSuccess) return FP8MM_ERR_DEVICE;
+    const hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+    (void)hipGetLastError();
+    if (M == 0) {
+        if (dw)
+            hipLaunchKernelGGL(zero_fill_kernel, dim3(2048), dim3(kThreadsG), 0, hs, static_cast<uint16_t*>(dw), N * K);
+        if (dbias)
+            hipLaunchKernelGGL(zero_fill_kernel, dim3(64), dim3(kThreadsG), 0, hs, reinterpret_cast<uint16_t*>(dbias),
+                               2 * N);
+        return hipGetLastError() == hipSuccess ? FP8MM_OK : FP8MM_ERR_LAUNCH;
+    }
+    char* ws = static_cast<char*>(workspace);
+    Grad& p = g.p;
+    p.dy = static_cast<const bf16_t*>(dy);
+    p.z = static_cast<const bf16_t*>(z);
+    p.x = static_cast<const bf16_t*>(x);
+    p.q_rows = reinterpret_cast<uint8_t*>(ws + g.q_rows);
+    p.q_cols = reinterpret_cast<uint8_t*>(ws + g.q_cols);
+    p.q_x = reinterpret_cast<uint8_t*>(ws + g.q_x);
+    p.row_scale = reinterpret_cast<float*>(ws + g.scales);
+    p.col_scale = p.row_scale + 2 * M;
+    p.x_scale = p.col_scale + 2 * N;
+    p.col_max = reinterpret_cast<float*>(ws + g.partials);
+    p.col_sum = p.col_max + p.parts * N;
+    p.x_max = p.col_sum + p.parts * N;
+    p.row_max = p.x_max + p.parts * K;
+    p.dbias = dbias;
+    switch (activation) {
+        case kActRelu: launch_passes<kActRelu>(p, hs); break;
+        case kActGelu: launch_passes<kActGelu>(p, hs); break;
+        case kActGeluTanh: launch_passes<kActGeluTanh>(p, hs); break;
+        case kActSilu: launch_passes<kActSilu>(p, hs); break;
+        default: launch_passes<kActNone>(p, hs); break;
+    }
+    if (hipGetLastError() != hipSuccess) return FP8MM_ERR_LAUNCH;
+    if (dx) {
+        st = fp8_scaled_mm_typed(p.q_rows, FP8MM_E5M2, wt, wt_format, p.row_scale, wt_scale, nullptr, dx, M, K, N,
+                                 FP8MM_ROWWISE, stream, -1, 0, ws, g.mm);
+        if (st != FP8MM_OK) return st;
+    }
+    if (dw)
+        st = fp8_scaled_mm_typed(p.q_cols, FP8MM_E5M2, p.q_x, FP8MM_E4M3FN, p.col_scale, p.x_scale, nullptr, dw, N,
+                                 K, p.Mp, FP8MM_ROWWISE, stream, -1, 0, ws, g.mm);
+    return st;
+}
+
+}  // extern "C"

@@ -71,3 +71,58 @@ def test_binding_refuses_before_the_library():
     for kw in (dict(), dict(activation="tanh"), dict(mode="columnwise")):
         with pytest.raises(ValueError):
             binding.fp8_linear(a, a, s, s, **kw)
+
+
+BIG = 1 << 45
+
+
+def bwd(L, dy=P, x=P, wt=P, fw=0, sw=P, z=P, act=2, dx=P, dw=P, db=P, M=64, N=64, K=64, ws=P, nbytes=BIG):
+    return L.fp8_linear_backward(dy, x, wt, fw, sw, z, act, dx, dw, db, M, N, K, None, ws, nbytes)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(act=-1), binding.ERR_ACTIVATION), (dict(act=5), binding.ERR_ACTIVATION),
+    (dict(fw=2), binding.ERR_FORMAT), (dict(dy=None), binding.ERR_NULL), (dict(z=None), binding.ERR_NULL),
+    (dict(x=None), binding.ERR_NULL), (dict(wt=None), binding.ERR_NULL), (dict(sw=None), binding.ERR_NULL),
+    (dict(dx=None, dw=None, db=None), binding.ERR_NULL),
+    (dict(M=-1), binding.ERR_SHAPE), (dict(M=2 ** 23 + 1), binding.ERR_SHAPE),
+    (dict(N=0), binding.ERR_SHAPE), (dict(N=24), binding.ERR_SHAPE), (dict(K=8), binding.ERR_SHAPE),
+    (dict(K=2 ** 23 + 16), binding.ERR_SHAPE), (dict(M=2 ** 23, N=2 ** 23), binding.ERR_SHAPE),
+    (dict(dy=P + 1), binding.ERR_ALIGN), (dict(z=P + 1), binding.ERR_ALIGN), (dict(x=P + 1), binding.ERR_ALIGN),
+    (dict(wt=P + 8), binding.ERR_ALIGN), (dict(sw=P + 2), binding.ERR_ALIGN), (dict(dx=P + 1), binding.ERR_ALIGN),
+    (dict(dw=P + 1), binding.ERR_ALIGN), (dict(db=P + 2), binding.ERR_ALIGN), (dict(ws=P + 64), binding.ERR_ALIGN),
+    (dict(ws=None), binding.ERR_WORKSPACE), (dict(nbytes=1 << 18), binding.ERR_WORKSPACE),
+])
+def test_backward_refusals(L, kw, code):
+    assert bwd(L, **kw) == code
+
+
+def test_backward_needs_only_what_its_outputs_need(L):
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present: these cases would launch on fake pointers")
+    # what passes the checks gets as far as the missing device
+    for kw in (dict(act=0, z=None), dict(dx=None, wt=None, sw=None), dict(dw=None, x=None),
+               dict(dx=None, dw=None, wt=None, sw=None, x=None), dict(db=None), dict(M=0, dy=None, x=None, ws=None)):
+        assert bwd(L, **kw) == binding.ERR_DEVICE, kw
+
+
+def test_backward_workspace_sizes(L):
+    size = L.fp8_linear_backward_workspace_size
+    assert size(-1, 64, 64, 1, 1) == -1 and size(64, 24, 64, 1, 1) == -1 and size(64, 64, 0, 1, 1) == -1
+    for M, N, K in ((0, 16, 16), (1, 16, 16), (500, 2048, 2048), (8191, 1008, 4160), (4096, 28672, 8192)):
+        both, dx, dw, none = (size(M, N, K, a, b) for a, b in ((1, 1), (1, 0), (0, 1), (0, 0)))
+        mp = (M + 15) // 16 * 16
+        assert both >= (256 << 10) + M * N + N * mp + K * mp     # counters, then the codes
+        assert none <= dx <= both and none <= dw <= both
+        for kw, n in ((dict(), both), (dict(dw=None), dx), (dict(dx=None), dw), (dict(dx=None, dw=None), none)):
+            if M:
+                assert bwd(L, M=M, N=N, K=K, nbytes=n - 1, **kw) == binding.ERR_WORKSPACE
+
+
+def test_backward_binding_refuses_before_the_library():
+    dy = torch.zeros(4, 32, dtype=torch.bfloat16)
+    w = torch.zeros(16, 32, dtype=torch.uint8)
+    s = torch.ones(16)
+    for kw in (dict(), dict(activation="tanh"), dict(dx=False, dw=False, dbias=False), dict(dx=3), dict(dbias=s)):
+        with pytest.raises(ValueError):
+            binding.fp8_linear_backward(dy, dy, w, s, **kw)
