@@ -234,9 +234,28 @@ def _stream_of(dev: int) -> int:
     return torch.cuda.current_stream(dev).cuda_stream
 
 
+# The current HIP device's index (torch's direct accessor where it has one).
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _call(dev: int, fn, *args) -> int:
+    """fn(*args) with `dev` as the current HIP device (the library launches on
+    the current one): calls from that device, the usual case, skip the switch."""
+    if _current_device() == dev:
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
 # Workspace bytes of automatic plans, per (device, M, N, K, mode, bias, config,
 # splits): the plan depends on nothing else, so the size is asked once.
 _ws_sizes: dict = {}
+
+
+def _keep_size(key, need: int) -> None:
+    if len(_ws_sizes) >= 4096:      # many distinct shapes: start over
+        _ws_sizes.clear()
+    _ws_sizes[key] = need
 
 
 def _mm_args(a, b, scale_a, scale_b, bias, out, mode, workspace, a_format, b_format, extra=()):
@@ -296,9 +315,7 @@ def _mm_workspace(L, device, dev, stream, M, N, K, m, has_bias, config, splits, 
     need = _ws_sizes.get(key)
     if need is None:
         need = int(L.fp8_scaled_mm_workspace_size(M, N, K, m, int(has_bias), int(config), int(splits)))
-        if len(_ws_sizes) >= 4096:      # many distinct shapes: start over
-            _ws_sizes.clear()
-        _ws_sizes[key] = need
+        _keep_size(key, need)
     if need <= 0:
         return None, 0
     ws = _workspace(device, stream, need)
@@ -323,16 +340,13 @@ def fp8_scaled_mm(a: torch.Tensor, b: torch.Tensor, scale_a: torch.Tensor, scale
                                                   a_format, b_format)
     L = lib()
     stream = _stream_of(dev)
-    # The library launches on the current HIP device: make it a's (calls
-    # from that device, the usual case, skip the switch).
-    with _on_device(dev):
-        ws_ptr, ws_bytes = _mm_workspace(L, a.device, dev, stream, M, N, K, m, bias is not None, config,
-                                         splits, workspace)
-        st = L.fp8_scaled_mm_typed(
-            a.data_ptr(), fa, b.data_ptr(), fb, scale_a.data_ptr(), scale_b.data_ptr(),
-            bias.data_ptr() if bias is not None else None, out.data_ptr(),
-            M, N, K, m, stream, int(config), int(splits), ws_ptr, ws_bytes)
-    _mm_check("fp8_scaled_mm", st)
+    ws_ptr, ws_bytes = _mm_workspace(L, a.device, dev, stream, M, N, K, m, bias is not None, config,
+                                     splits, workspace)
+    st = _call(dev, L.fp8_scaled_mm_typed, a.data_ptr(), fa, b.data_ptr(), fb, scale_a.data_ptr(),
+               scale_b.data_ptr(), bias.data_ptr() if bias is not None else None, out.data_ptr(),
+               M, N, K, m, stream, int(config), int(splits), ws_ptr, ws_bytes)
+    if st != OK:
+        _mm_error("fp8_scaled_mm", st)
     return out
 
 
@@ -357,13 +371,13 @@ def fp8_linear(a: torch.Tensor, b: torch.Tensor, scale_a: torch.Tensor, scale_b:
             raise ValueError(f"{name} must be a contiguous bf16 M x N tensor")
     L = lib()
     stream = _stream_of(dev)
-    with _on_device(dev):
-        ws_ptr, ws_bytes = _mm_workspace(L, a.device, dev, stream, M, N, K, m, bias is not None, config,
-                                         splits, workspace)
-        st = L.fp8_linear(a.data_ptr(), fa, b.data_ptr(), fb, scale_a.data_ptr(), scale_b.data_ptr(),
-                          _ptr(bias), _ptr(residual), act, _ptr(preact), out.data_ptr(), M, N, K, m,
-                          stream, int(config), int(splits), ws_ptr, ws_bytes)
-    _mm_check("fp8_linear", st)
+    ws_ptr, ws_bytes = _mm_workspace(L, a.device, dev, stream, M, N, K, m, bias is not None, config,
+                                     splits, workspace)
+    st = _call(dev, L.fp8_linear, a.data_ptr(), fa, b.data_ptr(), fb, scale_a.data_ptr(),
+               scale_b.data_ptr(), _ptr(bias), _ptr(residual), act, _ptr(preact), out.data_ptr(), M, N,
+               K, m, stream, int(config), int(splits), ws_ptr, ws_bytes)
+    if st != OK:
+        _mm_error("fp8_linear", st)
     return out
 
 
@@ -445,18 +459,22 @@ def fp8_linear_backward(dy: torch.Tensor, x: torch.Tensor | None, wt: torch.Tens
     db = torch.empty(N, dtype=torch.float32, device=device) if dbias else None
     L = lib()
     stream = _stream_of(dev)
-    with _on_device(dev):
-        if workspace is not None:
-            ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        else:
+    if workspace is not None:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    else:
+        key = ("linear_grad", M, N, K, want_dx, want_dw)
+        need = _ws_sizes.get(key)
+        if need is None:
             need = int(L.fp8_linear_backward_workspace_size(M, N, K, want_dx, want_dw))
             if need < 0:
                 raise ValueError(f"fp8_linear_backward: {status_string(ERR_SHAPE)}")
-            ws, ws_bytes = _workspace(device, stream, need, "linear_grad").data_ptr(), need
-        st = L.fp8_linear_backward(dy.data_ptr(), _ptr(x) if want_dw else None,
-                                   _ptr(wt) if want_dx else None, fw, _ptr(wt_scale) if want_dx else None,
-                                   _ptr(z), act, _ptr(dx), _ptr(dw), _ptr(db), M, N, K, stream, ws, ws_bytes)
-    _mm_check("fp8_linear_backward", st)
+            _keep_size(key, need)
+        ws, ws_bytes = _workspace(device, stream, need, "linear_grad").data_ptr(), need
+    st = _call(dev, L.fp8_linear_backward, dy.data_ptr(), _ptr(x) if want_dw else None,
+               _ptr(wt) if want_dx else None, fw, _ptr(wt_scale) if want_dx else None, _ptr(z), act,
+               _ptr(dx), _ptr(dw), _ptr(db), M, N, K, stream, ws, ws_bytes)
+    if st != OK:
+        _mm_error("fp8_linear_backward", st)
     return dx, dw, db
 
 
@@ -467,9 +485,7 @@ def _activation(activation) -> int:
     return _ACTIVATIONS[activation]
 
 
-def _mm_check(fn: str, st: int) -> None:
-    if st == OK:
-        return
+def _mm_error(fn: str, st: int) -> None:
     if st in _ARG_ERRORS:
         raise ValueError(f"{fn}: {status_string(st)} (status {st})")
     raise Fp8MMError(st)
@@ -531,12 +547,6 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _on_device(dev: int):
-    """The library launches on the current HIP device: a context that makes
-    `dev` current (nothing to do in the usual case)."""
-    return torch.cuda.device(dev) if torch.cuda.current_device() != dev else contextlib.nullcontext()
-
-
 def _ln_matrix(t, name: str, like: torch.Tensor | None = None) -> None:
     if like is None:
         if t.dtype not in _LN_DTYPES or t.dim() != 2 or not t.is_contiguous() or not t.is_cuda:
@@ -545,18 +555,16 @@ def _ln_matrix(t, name: str, like: torch.Tensor | None = None) -> None:
         raise ValueError(f"{name} must be a contiguous {like.dtype} tensor of shape {tuple(like.shape)}")
 
 
-def _ln_params(cols: int, params) -> int:
-    """The common type of w and b (None skipped), as the library's code."""
-    code = None
-    for name, t in params:
-        if t is None:
-            continue
-        if t.dtype not in _LN_DTYPES or t.numel() != cols or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous fp32 or bf16 vector of {cols} elements")
-        if code is not None and code != _LN_DTYPES[t.dtype]:
-            raise ValueError("w and b must have one type")
-        code = _LN_DTYPES[t.dtype]
-    return 1 if code is None else code
+def _ln_param(t, name: str, cols: int, dev: int) -> int:
+    """The library's code for the type of w or b (None: -1)."""
+    if t is None:
+        return -1
+    code = _LN_DTYPES.get(t.dtype)
+    if code is None or t.numel() != cols or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous fp32 or bf16 vector of {cols} elements")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    return code
 
 
 def _ln_vector(t, name: str, n: int) -> None:
@@ -564,9 +572,7 @@ def _ln_vector(t, name: str, n: int) -> None:
         raise ValueError(f"{name} must be a contiguous float32 tensor of {n} elements")
 
 
-def _ln_check(fn: str, st: int) -> None:
-    if st == LN_OK:
-        return
+def _ln_error(fn: str, st: int) -> None:
     msg = f"{fn}: {lib().fp8_layer_norm_status_string(st).decode()} (status {st})"
     raise ValueError(msg) if st in _LN_ARG_ERRORS else RuntimeError(msg)
 
@@ -605,10 +611,12 @@ def fp8_layer_norm(x: torch.Tensor, w: torch.Tensor | None = None, b: torch.Tens
         raise ValueError(f"codes need a number of columns that is a multiple of 16, got {cols}")
     if not (math.isfinite(eps) and eps >= 0):
         raise ValueError(f"eps must be finite and not negative, got {eps}")
-    pdt = _ln_params(cols, (("w", w), ("b", b)))
     dev = x.get_device()
-    _check_devices(dev, (("w", w), ("b", b), ("q", q), ("scale", scale),
-                         ("y", y if isinstance(y, torch.Tensor) else None)))
+    pw, pb = _ln_param(w, "w", cols, dev), _ln_param(b, "b", cols, dev)
+    if pw >= 0 and pb >= 0 and pw != pb:
+        raise ValueError("w and b must have one type")
+    pdt = pw if pw >= 0 else pb if pb >= 0 else 1
+    _check_devices(dev, (("q", q), ("scale", scale), ("y", y if isinstance(y, torch.Tensor) else None)))
     device = x.device
     out = y if isinstance(y, torch.Tensor) else torch.empty_like(x) if y else None
     f = 0
@@ -627,11 +635,10 @@ def fp8_layer_norm(x: torch.Tensor, w: torch.Tensor | None = None, b: torch.Tens
     if stats:
         mean = torch.empty(rows, dtype=torch.float32, device=device)
         rstd = torch.empty(rows, dtype=torch.float32, device=device)
-    with _on_device(dev):
-        st = lib().fp8_layer_norm(x.data_ptr(), _LN_DTYPES[x.dtype], _ptr(w), _ptr(b), pdt, eps,
-                                  _ptr(out), _ptr(q), f, _ptr(scale), _ptr(mean), _ptr(rstd),
-                                  rows, cols, _stream_of(dev))
-    _ln_check("fp8_layer_norm", st)
+    st = _call(dev, lib().fp8_layer_norm, x.data_ptr(), _LN_DTYPES[x.dtype], _ptr(w), _ptr(b), pdt, eps,
+               _ptr(out), _ptr(q), f, _ptr(scale), _ptr(mean), _ptr(rstd), rows, cols, _stream_of(dev))
+    if st != LN_OK:
+        _ln_error("fp8_layer_norm", st)
     return LayerNormResult(out, q, scale, mean, rstd)
 
 
@@ -653,12 +660,14 @@ def fp8_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tenso
         raise ValueError("x needs at least one column")
     _ln_vector(mean, "mean", rows)
     _ln_vector(rstd, "rstd", rows)
-    pdt = _ln_params(cols, (("w", w),))
+    dev = x.get_device()
+    pdt = _ln_param(w, "w", cols, dev)
+    if pdt < 0:
+        pdt = 1
     for name, t in (("residual_grad", residual_grad), ("dx", dx)):
         if t is not None:
             _ln_matrix(t, name, x)
-    dev = x.get_device()
-    _check_devices(dev, (("dy", dy), ("mean", mean), ("rstd", rstd), ("w", w), ("dx", dx),
+    _check_devices(dev, (("dy", dy), ("mean", mean), ("rstd", rstd), ("dx", dx),
                          ("residual_grad", residual_grad), ("workspace", workspace)))
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous GPU tensor")
@@ -668,17 +677,20 @@ def fp8_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tenso
     db = torch.empty(cols, dtype=torch.float32, device=x.device)
     L = lib()
     stream = _stream_of(dev)
-    with _on_device(dev):
-        need = int(L.fp8_layer_norm_backward_workspace_size(rows, cols))
-        if workspace is not None:
-            ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        elif need > 0:
+    if workspace is not None:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    else:
+        key = ("layer_norm", rows, cols)
+        need = _ws_sizes.get(key)
+        if need is None:
+            need = int(L.fp8_layer_norm_backward_workspace_size(rows, cols))
+            _keep_size(key, need)
+        ws, ws_bytes = None, 0
+        if need > 0:
             ws, ws_bytes = _workspace(x.device, stream, need, "layer_norm").data_ptr(), need
-        else:
-            ws, ws_bytes = None, 0
-        st = L.fp8_layer_norm_backward(dy.data_ptr(), x.data_ptr(), _LN_DTYPES[x.dtype],
-                                       mean.data_ptr(), rstd.data_ptr(), _ptr(w), pdt,
-                                       _ptr(residual_grad), dx.data_ptr(), dw.data_ptr(),
-                                       db.data_ptr(), rows, cols, ws, ws_bytes, stream)
-    _ln_check("fp8_layer_norm_backward", st)
+    st = _call(dev, L.fp8_layer_norm_backward, dy.data_ptr(), x.data_ptr(), _LN_DTYPES[x.dtype],
+               mean.data_ptr(), rstd.data_ptr(), _ptr(w), pdt, _ptr(residual_grad), dx.data_ptr(),
+               dw.data_ptr(), db.data_ptr(), rows, cols, ws, ws_bytes, stream)
+    if st != LN_OK:
+        _ln_error("fp8_layer_norm_backward", st)
     return dx, dw, db

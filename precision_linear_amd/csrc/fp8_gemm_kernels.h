@@ -294,6 +294,9 @@ struct Cfg {
     // instantiation of the kernel; the others would double the library for a
     // plan that measured slower on every workload here).
     static constexpr bool STREAM_K_OK = SPLIT_OK && BM == 128 && BN == 128;
+    // The linear layer's residual is loaded ahead of the K loop (a lane's share
+    // takes PER_LANE_ACC / 2 registers).
+    static constexpr bool EARLY_RESIDUAL = PER_LANE_ACC <= 32;
     // Spread a stage's loads between MFMAs only where a K step has enough
     // MFMAs to hide them (the big, MFMA-bound tiles).
     static constexpr bool INTERLEAVE = MI == 32 && FM * FN >= 8;
@@ -918,51 +921,90 @@ __device__ __forceinline__ void epi_scale(typename Mfma<MI>::acc_t (&acc)[FN][FM
         }
 }
 
-// acc = act(acc)
+// acc = act(acc), a block column at a time (all at once, the scheduler would
+// take a register for every intermediate value)
 template <class A, int FN, int FM>
 __device__ __forceinline__ void epi_activate(A (&acc)[FN][FM], int act) {
     with_activation(act, [&](auto a) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < FN; ++i)
+        for (int i = 0; i < FN; ++i) {
 #pragma unroll
             for (int j = 0; j < FM; ++j)
 #pragma unroll
                 for (int e = 0; e < (int)(sizeof(A) / 4); ++e)
                     acc[i][j][e] = activate<decltype(a)::value>(acc[i][j][e]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
     });
 }
 
-// acc += residual, for the blocks whose first row and column are m0 and n0;
-// rows and columns outside the output are left alone.  Residuals are read in
-// the MFMA layout, 8 bytes per run of 4 columns where rows allow it: the reads
-// of a wave's blocks cover whole lines between them.
+// Residual values in the MFMA layout: 4 bf16 for each run of 4 accumulators.
+// The reads are 8 bytes a lane (the reads of a wave's blocks cover whole lines
+// between them) and go out together, ahead of their use.
 template <int MI, int FN, int FM>
-__device__ __forceinline__ void epi_residual(typename Mfma<MI>::acc_t (&acc)[FN][FM],
-                                             const LinearParams& p, int m0, int n0, int lane) {
+struct EpiResidual {
+    static constexpr int G = Mfma<MI>::NACC / 4;
+    uint2 v[FM][FN][G];
+
+    // The blocks whose first row and column are m0 and n0; zeros outside the
+    // output.
+    __device__ __forceinline__ void load(const LinearParams& p, int m0, int n0, int lane) {
 #pragma unroll
-    for (int j = 0; j < FM; ++j) {
-        const int m = m0 + j * MI + lane % MI;
-        if (m >= p.M) continue;
-        const uint16_t* row = p.residual + (size_t)m * p.N;
+        for (int j = 0; j < FM; ++j) {
+            const int m = m0 + j * MI + lane % MI;
+            const uint16_t* row = p.residual + (size_t)m * p.N;
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const int n = n0 + epi_col<MI>(i, g, lane);
+                    uint2 r{0u, 0u};
+                    if (m < p.M) {
+                        if (p.vec_store) {   // N % 4 == 0: a run is inside or outside
+                            if (n < p.N) r = *reinterpret_cast<const uint2*>(row + n);
+                        } else {
+                            uint16_t h[4];
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) h[c] = n + c < p.N ? row[n + c] : (uint16_t)0;
+                            r = uint2{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
+                        }
+                    }
+                    v[j][i][g] = r;
+                }
+        }
+    }
+
+    // The same where the blocks lie inside the output, 8-byte reads are allowed
+    // and FM * MI rows are under 2^31 bytes: through a buffer, whose one
+    // 32-bit offset a lane leaves the registers to the values.
+    __device__ __forceinline__ void load_inside(const LinearParams& p, int m0, int n0, int lane) {
+        const __amdgpu_buffer_rsrc_t r =
+            make_rsrc(p.residual + (size_t)m0 * p.N + n0, (uint32_t)(FM * MI) * (uint32_t)p.N * 2u);
+        const int off = (lane % MI) * p.N * 2 + epi_col<MI>(0, 0, lane) * 2;
+#pragma unroll
+        for (int j = 0; j < FM; ++j)
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+                    v[j][i][g] = __builtin_bit_cast(
+                        uint2, __builtin_amdgcn_raw_buffer_load_b64(r, off + epi_col<MI>(i, g, 0) * 2,
+                                                                    j * MI * p.N * 2, 0));
+    }
+
+    // acc += rows j0 .. j0 + JN - 1 of the residual's blocks.
+    template <int JN>
+    __device__ __forceinline__ void add(typename Mfma<MI>::acc_t (&acc)[FN][JN], int j0) const {
 #pragma unroll
         for (int i = 0; i < FN; ++i)
 #pragma unroll
-            for (int g = 0; g < Mfma<MI>::NACC / 4; ++g) {
-                const int n = n0 + epi_col<MI>(i, g, lane);
-                if (p.vec_store) {   // N % 4 == 0: a run is inside or outside
-                    if (n < p.N) {
-                        const uint2 r = *reinterpret_cast<const uint2*>(row + n);
+            for (int j = 0; j < JN; ++j)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) acc[i][j][4 * g + c] += bf16_of_run(r, c);
-                    }
-                } else {
+                for (int g = 0; g < G; ++g)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if (n + c < p.N) acc[i][j][4 * g + c] += __uint_as_float((uint32_t)row[n + c] << 16);
-                }
-            }
+                    for (int c = 0; c < 4; ++c) acc[i][j][4 * g + c] += bf16_of_run(v[j0 + j][i][g], c);
     }
-}
+};
 
 // 4 accumulators from 4 * g on, rounded to bf16.
 template <class A>
@@ -1003,7 +1045,7 @@ template <class C>
 __device__ __forceinline__ void epi_stage_and_store(
     typename Mfma<C::MI_>::acc_t (&acc)[C::FN][C::FM], uint8_t* stg, const LinearParams& p,
     int row0, int col0, int mbase, int nbase, const float* epi_sa, const float* epi_sb,
-    const uint16_t* epi_bias, int lane, int tid) {
+    const uint16_t* epi_bias, const EpiResidual<C::MI_, C::FN, C::FM>& res, int lane, int tid) {
     asm volatile("" : "+v"(lane));
     epi_scale<C::MI_, C::FN, C::FM>(acc, mbase, nbase, epi_sa, epi_sb, epi_bias, lane);
     // preact first, then out, through the same code.
@@ -1013,7 +1055,7 @@ __device__ __forceinline__ void epi_stage_and_store(
             to.out = p.preact;
         } else {
             epi_activate(acc, p.act);
-            if (p.residual) epi_residual<C::MI_, C::FN, C::FM>(acc, p, row0 + mbase, col0 + nbase, lane);
+            if (p.residual) res.template add<C::FM>(acc, 0);
         }
         if (p.vec16) epi_write<C, false>(acc, stg, to, row0, col0, mbase, nbase, lane, tid);
         else epi_write<C, true>(acc, stg, to, row0, col0, mbase, nbase, lane, tid);
@@ -1177,6 +1219,18 @@ fp8_gemm_kernel(KernelParams<EPI> p) {
             bias_v[i] = (has_bias && ok) ? p.bias[col0 + c] : (uint16_t)0;
         }
 
+        // So is the residual, where a lane's share of it is small enough to be
+        // held through the loop and this unit will need it for certain.
+        EpiResidual<MI, EPI ? C::FN : 1, EPI ? C::FM : 1> res;
+        bool res_late = false;
+        if constexpr (EPI) {
+            res_late = p.residual != nullptr;
+            if (C::EARLY_RESIDUAL && res_late && nparts == 1) {
+                res.load(p, row0 + wm * C::WTM, col0 + wn * C::WTN, lane);
+                res_late = false;
+            }
+        }
+
         typename F::acc_t acc[C::FN][C::FM];
 #pragma unroll
         for (int i = 0; i < C::FN; ++i)
@@ -1276,6 +1330,9 @@ fp8_gemm_kernel(KernelParams<EPI> p) {
             }
         }
 
+        if constexpr (EPI)
+            if (res_late) res.load(p, row0 + wm * C::WTM, col0 + wn * C::WTN, lane);
+
         // Epilogue parameters into LDS (beside the stage buffers).
         if (EPI || p.rowwise || has_bias) {
 #pragma unroll
@@ -1299,7 +1356,7 @@ fp8_gemm_kernel(KernelParams<EPI> p) {
         barrier_lds();
         if constexpr (EPI)
             epi_stage_and_store<C>(acc, smem, p, row0, col0, wm * C::WTM, wn * C::WTN, epi_sa, epi_sb,
-                                   epi_bias, lane, tid);
+                                   epi_bias, res, lane, tid);
         else
             stage_and_store<C>(acc, smem, p, row0, col0, wm * C::WTM, wn * C::WTN, epi_sa, epi_sb,
                                epi_bias, s_pt, has_bias, lane, tid);
@@ -1481,6 +1538,17 @@ __device__ __forceinline__ int pp_lane() {
     int l;
     asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
     return l;
+}
+
+// The offsets of PpLoads, made anew after the linear layer's epilogue so that
+// they take no registers from it.
+__device__ __forceinline__ PpLoads pp_loads(int K, int q, int lane) {
+    PpLoads L;
+    L.cbyte = (uint32_t)(((lane % 8) ^ chunk_swizzle<pp::CPR>((q & 1) * 8 + lane / 8)) * 16);
+#pragma unroll
+    for (int i = 0; i < pp::NOFF; ++i) L.off[i] = (uint32_t)((8 * (q + 4 * i) + lane / 8) * K) + L.cbyte;
+    L.bot = 128u * (uint32_t)K;
+    return L;
 }
 
 struct PpTile {
@@ -1665,7 +1733,7 @@ __device__ __forceinline__ void pp_store(const pp::acc_t (&acc)[pp::FN][pp::FM],
 
 // The linear layer's epilogue of one wave (128 x 64 outputs), in bands of 32
 // rows (all 128 accumulators at once would spill): through the wave's staging
-// area as in pp_store_staged, or, where the block is not wholly inside the
+// area as in pp_store_staged, then out through a buffer (32-bit offsets), or, where the block is not wholly inside the
 // output or 16-byte stores are not allowed, straight to memory, run by run.
 constexpr int kPpBandBlocks = 32 / pp::MI;   // MFMA row blocks per band
 
@@ -1683,12 +1751,16 @@ __device__ __forceinline__ void pp_epi_write(const pp::acc_t (&z)[pp::FN][kPpBan
                 const int cpos = (cl / 8) ^ ((r >> 1) & 7);
                 *reinterpret_cast<uint2*>(stg + r * 128 + cpos * 16 + (cl % 8) * 2) = epi_pack(z[i][j], 0);
             }
+        const __amdgpu_buffer_rsrc_t r = make_rsrc(out + (size_t)m0 * p.N + n0, 32u * (uint32_t)p.N * 2u);
+        const int off = (lane / 8) * p.N * 2 + (lane % 8) * 16;
 #pragma unroll
         for (int pass = 0; pass < 4; ++pass) {
             const int rr = pass * 8 + lane / 8;
-            const int cc = lane % 8;
-            const v4i v = *reinterpret_cast<const v4i*>(stg + rr * 128 + ((cc ^ ((rr >> 1) & 7)) * 16));
-            *reinterpret_cast<v4i*>(out + (size_t)(m0 + rr) * p.N + n0 + cc * 8) = v;
+            const v4u v = *reinterpret_cast<const v4u*>(stg + rr * 128 + (((lane % 8) ^ ((rr >> 1) & 7)) * 16));
+            // No scalar offset: with one, the compiler leaves out the wait that a
+            // store of more than 8 bytes needs before a VALU instruction may write
+            // its first data register, and wrong values were stored.
+            __builtin_amdgcn_raw_buffer_store_b128(v, r, off + pass * 8 * p.N * 2, 0, 0);
         }
         return;
     }
@@ -1713,29 +1785,57 @@ __device__ __forceinline__ void pp_epi_write(const pp::acc_t (&z)[pp::FN][kPpBan
     }
 }
 
-__device__ __forceinline__ void pp_epi_store(const pp::acc_t (&acc)[pp::FN][pp::FM], const LinearParams& p,
+template <bool FULL, bool RES>
+__device__ __forceinline__ void pp_epi_bands(const pp::acc_t (&acc)[pp::FN][pp::FM], const LinearParams& p,
                                              int row0, int col0, int mbase, int nbase,
                                              const float* epi_sa, const float* epi_sb,
                                              const uint16_t* epi_bias, uint8_t* stg) {
     constexpr int MI = pp::MI, FN = pp::FN, JB = kPpBandBlocks;
     const int n0 = col0 + nbase;
-    const bool full = p.vec16 && row0 + mbase + 128 <= p.M && n0 + 64 <= p.N;   // wave-uniform
+    // Inside the output, the residual is loaded kAhead bands ahead (two bands
+    // ahead, or the whole block's at once, spills).
+    constexpr int kBands = pp::FM / JB, kAhead = 1;
+    EpiResidual<MI, FN, JB> res[kBands];
+    if constexpr (FULL && RES)
 #pragma unroll
-    for (int band = 0; band < pp::FM / JB; ++band) {
+        for (int b = 0; b < kAhead; ++b) res[b].load_inside(p, row0 + mbase + b * 32, n0, pp_lane());
+#pragma unroll
+    for (int band = 0; band < kBands; ++band) {
         const int mb = mbase + band * 32;
         const int lane = pp_lane();
+        if constexpr (RES) {
+            if constexpr (!FULL) res[band].load(p, row0 + mb, n0, lane);
+            else if (band + kAhead < kBands) res[band + kAhead].load_inside(p, row0 + mb + kAhead * 32, n0, lane);
+            __builtin_amdgcn_sched_barrier(0);
+        }
         pp::acc_t z[FN][JB];
 #pragma unroll
         for (int i = 0; i < FN; ++i)
 #pragma unroll
             for (int j = 0; j < JB; ++j) z[i][j] = acc[i][band * JB + j];
         epi_scale<MI, FN, JB>(z, mb, nbase, epi_sa, epi_sb, epi_bias, lane);
-        if (p.preact) pp_epi_write(z, p, p.preact, row0 + mb, n0, full, lane, stg);
+        if (p.preact) pp_epi_write(z, p, p.preact, row0 + mb, n0, FULL, lane, stg);
         epi_activate(z, p.act);
-        if (p.residual) epi_residual<MI, FN, JB>(z, p, row0 + mb, n0, lane);
-        pp_epi_write(z, p, p.out, row0 + mb, n0, full, lane, stg);
+        if constexpr (RES) res[band].template add<JB>(z, 0);
+        pp_epi_write(z, p, p.out, row0 + mb, n0, FULL, lane, stg);
         __builtin_amdgcn_sched_barrier(0);
     }
+}
+
+__device__ __forceinline__ void pp_epi_store(const pp::acc_t (&acc)[pp::FN][pp::FM], const LinearParams& p,
+                                             int row0, int col0, int mbase, int nbase,
+                                             const float* epi_sa, const float* epi_sb,
+                                             const uint16_t* epi_bias, uint8_t* stg) {
+    const bool full = p.vec16 && p.N <= (1 << 22) && row0 + mbase + 128 <= p.M &&
+                      col0 + nbase + 64 <= p.N;   // wave-uniform
+#define FP8MM_BANDS(FULL, RES) \
+    pp_epi_bands<FULL, RES>(acc, p, row0, col0, mbase, nbase, epi_sa, epi_sb, epi_bias, stg)
+    if (full) {
+        if (p.residual) FP8MM_BANDS(true, true); else FP8MM_BANDS(true, false);
+    } else {
+        if (p.residual) FP8MM_BANDS(false, true); else FP8MM_BANDS(false, false);
+    }
+#undef FP8MM_BANDS
 }
 
 // Split-K for one wave of the ping-pong kernel.  The wave publishes its fp32
@@ -1872,8 +1972,15 @@ __global__ void __launch_bounds__(pp::THREADS) fp8_gemm_pp_kernel(KernelParams<E
                     pp_store(acc, p, T.row0, T.col0, 0, q * 64, epi_sa, epi_sb, epi_bias, s_pt,
                              has_bias, pp_lane(), smem + STG0 + q * STG_BYTES);
             }
-            barrier_lds();   // pairs with group 1's last barrier of the tile
+            // With the linear layer's epilogue, which has more arithmetic and
+            // waits, the groups do not meet here: group 1 starts its own as soon
+            // as its last compute phase ends, so that one group's works in the
+            // other's waits (4096 x 28672 x 8192 on one MI355X, gelu 720 -> 700 us,
+            // gelu and residual 740 -> 722 us).  Nothing else hangs on that barrier:
+            // group 1's last reads of the stage buffers ended before the one above.
+            if constexpr (!EPI) barrier_lds();   // pairs with group 1's last barrier of the tile
             __builtin_amdgcn_sched_barrier(0);
+            if constexpr (EPI) L = pp_loads(p.K, q, pp_lane());
             if (un < num_units) {
                 T = pp_tile(p, un, GROUP_M, xcd);
                 PpParams pv;
@@ -1905,7 +2012,7 @@ __global__ void __launch_bounds__(pp::THREADS) fp8_gemm_pp_kernel(KernelParams<E
                 pp_compute<FMT>(acc, fa, fb);
                 __builtin_amdgcn_sched_barrier(0);
                 wait_vmcnt<0>();
-                barrier_lds();
+                if (!EPI || s + 1 < T.n) barrier_lds();
                 __builtin_amdgcn_sched_barrier(0);
             }
             if (!split || pp_split_fixup(acc, p, u, T.t, wave, pp_lane())) {
@@ -1918,6 +2025,7 @@ __global__ void __launch_bounds__(pp::THREADS) fp8_gemm_pp_kernel(KernelParams<E
             }
             __builtin_amdgcn_s_barrier();   // group 0's first slices of the next unit have landed
             __builtin_amdgcn_sched_barrier(0);
+            if constexpr (EPI) L = pp_loads(p.K, q, pp_lane());
             if (u + G < num_units) T = pp_tile(p, u + G, GROUP_M, xcd);
         }
     }
