@@ -387,82 +387,83 @@ struct LnBwd {
     int subs;          // rows a workgroup works on at a time
 };
 
-// dx, and this workgroup's share of dw and db.  `subs` rows at a time, W waves
-// each; the sums over a workgroup's rows stay in registers and meet in LDS at
-// the end (a fixed tree over the subs), so a workgroup writes one partial row.
-template <class T>
-__global__ void __launch_bounds__(kMaxWaves* kWaveSize)
-ln_backward_kernel(LnBwd p) {
-    extern __shared__ float s_cols[];             // [subs / 2][2][pitch]
+// A lane's share of the columns: V vectors of 8 and at most one tail column.
+template <int V>
+struct Share {
+    int t, tw;          // lane of the row, lanes of a row
+    bool ok[V];
+    bool has_tail;
+    int tail;           // column
+    __device__ __forceinline__ Share(int lane_of_row, int lanes, int cols)
+        : t(lane_of_row), tw(lanes), has_tail(lane_of_row < cols % 8), tail(cols / 8 * 8 + lane_of_row) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) ok[v] = t + v * tw < cols / 8;
+    }
+    __device__ __forceinline__ int col(int v) const { return (t + v * tw) * 8; }
+};
+
+// The rows blk * subs, + blocks * subs, ... of dx, `subs` rows at a time, W waves
+// each.  SUMS: dw and db over these rows are added to the sums given.
+template <class T, int V, bool SUMS>
+__device__ __forceinline__ void backward_rows(const LnBwd& p, const Share<V>& c, int blk, int blocks,
+                                              float (&dw)[V][8], float (&db)[V][8], float& dwt, float& dbt) {
     __shared__ float2 s_sum[2][kMaxWaves];
     const int lane = threadIdx.x % kWaveSize;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveSize);
     const int W = p.waves;
     const int sub = wave / W;
-    const int wr = wave - sub * W;
-    const int t = wr * kWaveSize + lane;
-    const int tw = W * kWaveSize;
-    const int cols = (int)p.cols;
-    const int nv = cols / 8;
-    const bool has_tail = t < cols % 8;
-    const int ct = nv * 8 + t;
-    const float inv_n = 1.f / (float)cols;
-    bool ok[kVecs];
-    float w[kVecs][8], wt = 0.f;
-    float dw[kVecs][8], db[kVecs][8], dwt = 0.f, dbt = 0.f;
+    const float inv_n = 1.f / (float)(int)p.cols;
+    float w[V][8], wt = 0.f;
 #pragma unroll
-    for (int v = 0; v < kVecs; ++v) {
-        ok[v] = t + v * tw < nv;
+    for (int v = 0; v < V; ++v) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[v][i] = dw[v][i] = db[v][i] = 0.f;
-        if (ok[v]) load_param8(p.w, p.param_bf16, (t + v * tw) * 8, 1.f, w[v]);
+        for (int i = 0; i < 8; ++i) w[v][i] = 0.f;
+        if (c.ok[v]) load_param8(p.w, p.param_bf16, c.col(v), 1.f, w[v]);
     }
-    if (has_tail) wt = load_param1(p.w, p.param_bf16, ct, 1.f);
-
+    if (c.has_tail) wt = load_param1(p.w, p.param_bf16, c.tail, 1.f);
     const T* x = static_cast<const T*>(p.x);
     const T* dy = static_cast<const T*>(p.dy);
     const T* res = static_cast<const T*>(p.res);
     T* dx = static_cast<T*>(p.dx);
-    const int64_t step = (int64_t)gridDim.x * p.subs;
-    // The residual is loaded with the row where registers allow (fp32 rows
-    // with it would spill).
-    constexpr bool kResEarly = sizeof(T) == 2;
+    const int64_t step = (int64_t)blocks * p.subs;
+    // The residual is loaded with the row where registers allow.
+    constexpr bool kResEarly = V * sizeof(T) <= 4;
     int parity = 0;
     // Every sub goes through the same number of steps (they share barriers);
     // past the last row it works on zeros and stores nothing.
-    for (int64_t base = (int64_t)blockIdx.x * p.subs; base < p.rows; base += step, parity ^= 1) {
+    for (int64_t base = (int64_t)blk * p.subs; base < p.rows; base += step, parity ^= 1) {
         const int64_t r = base + sub;
         const bool live = r < p.rows;
-        Raw8<T> rx[kVecs], rdy[kVecs], rr[kVecs];
+        Raw8<T> rx[V], rdy[V], rr[V];
         float xt = 0.f, dyt = 0.f, rt = 0.f;
         float mean = 0.f, rstd = 0.f;
 #pragma unroll
-        for (int v = 0; v < kVecs; ++v) {
+        for (int v = 0; v < V; ++v) {
             rx[v].zero();
             rdy[v].zero();
             rr[v].zero();
         }
+        const int64_t off = r * p.cols;
         if (live) {
-            const int64_t off = r * p.cols;
             mean = p.mean[r];
             rstd = p.rstd[r];
 #pragma unroll
-            for (int v = 0; v < kVecs; ++v)
-                if (ok[v]) {
-                    rx[v].load(x + off + (t + v * tw) * 8);
-                    rdy[v].load(dy + off + (t + v * tw) * 8);
-                    if (kResEarly && res) rr[v].load(res + off + (t + v * tw) * 8);
+            for (int v = 0; v < V; ++v)
+                if (c.ok[v]) {
+                    rx[v].load(x + off + c.col(v));
+                    rdy[v].load(dy + off + c.col(v));
+                    if (kResEarly && res) rr[v].load(res + off + c.col(v));
                 }
-            if (has_tail) {
-                xt = load1(x + off + ct);
-                dyt = load1(dy + off + ct);
-                if (res) rt = load1(res + off + ct);
+            if (c.has_tail) {
+                xt = load1(x + off + c.tail);
+                dyt = load1(dy + off + c.tail);
+                if (res) rt = load1(res + off + c.tail);
             }
         }
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
-        for (int v = 0; v < kVecs; ++v)
-            if (ok[v])
+        for (int v = 0; v < V; ++v)
+            if (c.ok[v])
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float d = rdy[v].get(i);
@@ -470,16 +471,20 @@ ln_backward_kernel(LnBwd p) {
                     const float g = d * w[v][i];
                     s1 += g;
                     s2 = fmaf(g, xh, s2);
-                    dw[v][i] = fmaf(d, xh, dw[v][i]);
-                    db[v][i] += d;
+                    if constexpr (SUMS) {
+                        dw[v][i] = fmaf(d, xh, dw[v][i]);
+                        db[v][i] += d;
+                    }
                 }
         const float xht = (xt - mean) * rstd;
-        if (has_tail) {
+        if (c.has_tail) {
             const float g = dyt * wt;
             s1 += g;
             s2 = fmaf(g, xht, s2);
-            dwt = fmaf(dyt, xht, dwt);
-            dbt += dyt;
+            if constexpr (SUMS) {
+                dwt = fmaf(dyt, xht, dwt);
+                dbt += dyt;
+            }
         }
         s1 = wave_sum(s1);
         s2 = wave_sum(s2);
@@ -493,14 +498,13 @@ ln_backward_kernel(LnBwd p) {
         }
         if (!live) continue;
         const float c1 = s1 * inv_n, c2 = s2 * inv_n;
-        T* dxr = dx + r * p.cols;
         if (!kResEarly && res)
 #pragma unroll
-            for (int v = 0; v < kVecs; ++v)
-                if (ok[v]) rr[v].load(res + r * p.cols + (t + v * tw) * 8);
+            for (int v = 0; v < V; ++v)
+                if (c.ok[v]) rr[v].load(res + off + c.col(v));
 #pragma unroll
-        for (int v = 0; v < kVecs; ++v)
-            if (ok[v]) {
+        for (int v = 0; v < V; ++v)
+            if (c.ok[v]) {
                 float f[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -508,41 +512,72 @@ ln_backward_kernel(LnBwd p) {
                     const float g = rdy[v].get(i) * w[v][i];
                     f[i] = fmaf(rstd, g - c1 - xh * c2, rr[v].get(i));
                 }
-                store8(dxr + (t + v * tw) * 8, f);
+                store8(dx + off + c.col(v), f);
             }
-        if (has_tail) store1(dxr + ct, fmaf(rstd, dyt * wt - c1 - xht * c2, rt));
+        if (c.has_tail) store1(dx + off + c.tail, fmaf(rstd, dyt * wt - c1 - xht * c2, rt));
     }
+}
+
+// dx, and this workgroup's share of dw and db: the sums over a workgroup's rows
+// stay in registers and meet in LDS at the end (a fixed tree over the subs), so
+// a workgroup writes one partial row.
+template <class T, int V>
+__global__ void __launch_bounds__(kMaxWaves* kWaveSize)
+ln_backward_kernel(LnBwd p) {
+    extern __shared__ float4 s_cols[];            // [subs / 2][dw, db][V][2][lanes of a row]
+    __shared__ float s_tail[kMaxWaves / 2][2][8];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveSize);
+    const int sub = wave / p.waves;
+    const int tw = p.waves * kWaveSize;
+    const Share<V> c((int)threadIdx.x - sub * tw, tw, (int)p.cols);
+    float dw[V][8], db[V][8], dwt = 0.f, dbt = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dw[v][i] = db[v][i] = 0.f;
+    backward_rows<T, V, true>(p, c, blockIdx.x, gridDim.x, dw, db, dwt, dbt);
 
     // Join the subs: the upper half of them hands its sums to the lower half.
+    // Lane t's four values of a vector's half h lie at [v][h][t]: no two lanes
+    // meet in a bank.
     for (int n = p.subs; n > 1;) {
         const int half = (n + 1) / 2;
-        float* slot = s_cols + (int64_t)(sub >= half ? sub - half : sub) * 2 * p.pitch;
+        const int slot = sub >= half ? sub - half : sub;
+        float4* at = s_cols + (int64_t)slot * 4 * V * tw + c.t;
         __syncthreads();
         if (sub >= half && sub < n) {
 #pragma unroll
-            for (int v = 0; v < kVecs; ++v)
-                if (ok[v]) {
-                    store8(slot + (t + v * tw) * 8, dw[v]);
-                    store8(slot + p.pitch + (t + v * tw) * 8, db[v]);
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    at[(v * 2 + h) * tw] = float4{dw[v][4 * h], dw[v][4 * h + 1], dw[v][4 * h + 2], dw[v][4 * h + 3]};
+                    at[((V + v) * 2 + h) * tw] =
+                        float4{db[v][4 * h], db[v][4 * h + 1], db[v][4 * h + 2], db[v][4 * h + 3]};
                 }
-            if (has_tail) {
-                slot[ct] = dwt;
-                slot[p.pitch + ct] = dbt;
+            if (c.has_tail) {
+                s_tail[slot][0][c.t] = dwt;
+                s_tail[slot][1][c.t] = dbt;
             }
         }
         __syncthreads();
         if (sub < n - half) {
 #pragma unroll
-            for (int v = 0; v < kVecs; ++v)
-                if (ok[v])
+            for (int v = 0; v < V; ++v)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        dw[v][i] += slot[(t + v * tw) * 8 + i];
-                        db[v][i] += slot[p.pitch + (t + v * tw) * 8 + i];
-                    }
-            if (has_tail) {
-                dwt += slot[ct];
-                dbt += slot[p.pitch + ct];
+                for (int h = 0; h < 2; ++h) {
+                    const float4 a = at[(v * 2 + h) * tw], b = at[((V + v) * 2 + h) * tw];
+                    dw[v][4 * h] += a.x;
+                    dw[v][4 * h + 1] += a.y;
+                    dw[v][4 * h + 2] += a.z;
+                    dw[v][4 * h + 3] += a.w;
+                    db[v][4 * h] += b.x;
+                    db[v][4 * h + 1] += b.y;
+                    db[v][4 * h + 2] += b.z;
+                    db[v][4 * h + 3] += b.w;
+                }
+            if (c.has_tail) {
+                dwt += s_tail[slot][0][c.t];
+                dbt += s_tail[slot][1][c.t];
             }
         }
         n = half;
@@ -551,16 +586,82 @@ ln_backward_kernel(LnBwd p) {
         float* pw = p.partial + blockIdx.x * p.pitch;
         float* pb = pw + gridDim.x * p.pitch;
 #pragma unroll
-        for (int v = 0; v < kVecs; ++v)
-            if (ok[v]) {
-                store8(pw + (t + v * tw) * 8, dw[v]);
-                store8(pb + (t + v * tw) * 8, db[v]);
+        for (int v = 0; v < V; ++v)
+            if (c.ok[v]) {
+                store8(pw + c.col(v), dw[v]);
+                store8(pb + c.col(v), db[v]);
             }
-        if (has_tail) {
-            pw[ct] = dwt;
-            pb[ct] = dbt;
+        if (c.has_tail) {
+            pw[c.tail] = dwt;
+            pb[c.tail] = dbt;
         }
     }
+}
+
+// Few rows: one launch, no partial results.  The first row_blocks workgroups
+// write dx; the others take 64 columns each and sum dw and db over all the
+// rows, reading dy and x again (from L2, where the first have just brought
+// them): 16 lanes of 4 columns, blockDim / 16 slices of the rows, joined in a
+// fixed order.
+template <class T>
+__device__ __forceinline__ void load4(const T* row, int64_t c, int64_t cols, float (&f)[4]) {
+    if (c + 3 < cols) {
+        if constexpr (sizeof(T) == 2) {
+            typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+            const u32x2 v = *reinterpret_cast<const u32x2_a2*>(row + c);
+            f[0] = bf16_lo(v[0]);
+            f[1] = bf16_hi(v[0]);
+            f[2] = bf16_lo(v[1]);
+            f[3] = bf16_hi(v[1]);
+        } else {
+            const u32x4 v = *reinterpret_cast<const u32x4_a4*>(row + c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(v[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = c + i < cols ? load1(row + c + i) : 0.f;
+    }
+}
+
+template <class T, int V>
+__global__ void __launch_bounds__(kMaxWaves* kWaveSize)
+ln_backward_few_kernel(LnBwd p, int row_blocks, float* dw_out, float* db_out) {
+    __shared__ float4 s_dw[kMaxWaves * 4][16], s_db[kMaxWaves * 4][16];
+    if ((int)blockIdx.x < row_blocks) {
+        const int tw = p.waves * kWaveSize;
+        const Share<V> c((int)threadIdx.x % tw, tw, (int)p.cols);
+        float dw[V][8], db[V][8], dwt, dbt;   // (not touched)
+        backward_rows<T, V, false>(p, c, blockIdx.x, row_blocks, dw, db, dwt, dbt);
+        return;
+    }
+    const int cx = threadIdx.x % 16, slice = threadIdx.x / 16, slices = blockDim.x / 16;
+    const int64_t c0 = (int64_t)((int)blockIdx.x - row_blocks) * 64;
+    const int64_t c = c0 + cx * 4;
+    const T* x = static_cast<const T*>(p.x);
+    const T* dy = static_cast<const T*>(p.dy);
+    float dw[4] = {0.f, 0.f, 0.f, 0.f}, db[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int r = slice; r < (int)p.rows; r += slices) {
+        float fx[4], fd[4];
+        load4(x + r * p.cols, c, p.cols, fx);
+        load4(dy + r * p.cols, c, p.cols, fd);
+        const float mean = p.mean[r], rstd = p.rstd[r];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            dw[i] = fmaf(fd[i], (fx[i] - mean) * rstd, dw[i]);
+            db[i] += fd[i];
+        }
+    }
+    s_dw[slice][cx] = float4{dw[0], dw[1], dw[2], dw[3]};
+    s_db[slice][cx] = float4{db[0], db[1], db[2], db[3]};
+    __syncthreads();
+    const int col = threadIdx.x % 64;
+    if (threadIdx.x >= 128 || c0 + col >= p.cols) return;
+    const float* src = reinterpret_cast<const float*>(threadIdx.x < 64 ? s_dw[0] : s_db[0]) + col;
+    float sum = 0.f;
+    for (int i = 0; i < slices; ++i) sum += src[i * 64];
+    (threadIdx.x < 64 ? dw_out : db_out)[c0 + col] = sum;
 }
 
 // Long rows: dx, one workgroup per row.
@@ -639,21 +740,32 @@ ln_column_sums_kernel(LnBwd p, int parts) {
 }
 
 // dw and db from the partial rows (blockIdx.y 0: dw, 1: db).  A workgroup takes
-// 64 columns: 16 lanes of 4 columns each, 16 slices of the parts, joined in a
-// fixed order.  parts == 0 (no rows) gives zeros.
-__global__ void __launch_bounds__(256)
+// 64 columns: 16 lanes of 4 columns each, 32 slices of the parts (8 of 256 parts,
+// all loaded before the first is added), joined in a fixed order.  parts == 0
+// (no rows) gives zeros.
+constexpr int kReduceSlices = 32;
+
+__global__ void __launch_bounds__(kReduceSlices * 16)
 ln_reduce_kernel(const float* partial, int parts, int64_t pitch, int64_t cols, float* dw, float* db) {
-    __shared__ float4 s[16][16];
+    __shared__ float4 s[kReduceSlices][16];
     const int cx = threadIdx.x % 16, slice = threadIdx.x / 16;
     const int64_t c = (int64_t)blockIdx.x * 64 + cx * 4;
     const float* src = partial + (int64_t)blockIdx.y * parts * pitch;
     float4 a{0.f, 0.f, 0.f, 0.f};
-    for (int i = slice; i < parts; i += 16) {   // (the pitch covers whole 64-column blocks)
-        const float4 v = *reinterpret_cast<const float4*>(src + i * pitch + c);
-        a.x += v.x;
-        a.y += v.y;
-        a.z += v.z;
-        a.w += v.w;
+    for (int i0 = slice; i0 < parts; i0 += 8 * kReduceSlices) {   // (the pitch covers whole 64-column blocks)
+        float4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = i0 + k * kReduceSlices;
+            v[k] = i < parts ? *reinterpret_cast<const float4*>(src + i * pitch + c) : float4{0.f, 0.f, 0.f, 0.f};
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            a.x += v[k].x;
+            a.y += v[k].y;
+            a.z += v[k].z;
+            a.w += v[k].w;
+        }
     }
     s[slice][cx] = a;
     __syncthreads();
@@ -661,7 +773,7 @@ ln_reduce_kernel(const float* partial, int parts, int64_t pitch, int64_t cols, f
         const int64_t col = (int64_t)blockIdx.x * 64 + threadIdx.x;
         float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sum += reinterpret_cast<const float*>(s[i])[threadIdx.x];
+        for (int i = 0; i < kReduceSlices; ++i) sum += reinterpret_cast<const float*>(s[i])[threadIdx.x];
         if (col < cols) (blockIdx.y ? db : dw)[col] = sum;
     }
 }
@@ -686,36 +798,67 @@ int check_shape(int64_t rows, int64_t cols) {
     return FP8LN_OK;
 }
 
-int row_waves(int64_t cols) { return (int)max64(1, ceil_div(cols / 8, kWaveSize * kVecs)); }
+int row_waves(int64_t cols, int vecs) { return (int)max64(1, ceil_div(cols / 8, kWaveSize * vecs)); }
 
 // How the gradient's rows are shared out.  It does not depend on the device:
-// the workspace size, and with it the sums' order, has to be known without one.
+// the sums' order has to be the same on every one.
 constexpr int64_t kGradWorkgroups = 256;
 constexpr int64_t kLongParts = 64;
 struct GradPlan {
-    bool held;
-    int waves, subs;
+    bool held, few;
+    int vecs, waves, subs;
     int64_t parts, pitch;
 };
 
-GradPlan grad_plan(int64_t rows, int64_t cols) {
+// Few rows: one launch that reads dy and x twice beats partial sums (MI355X,
+// bf16 / fp32 with a residual, one launch against two: 64 x 8192 3.9 / 5.2 us
+// against 8.6 / 9.1, 128 x 1000 5.0 / 5.2 against 5.9 / 5.7, 512 x 4096 7.6 / 10.7
+// against 12.2 / 13.7) until each workgroup's columns are too long a walk
+// (512 x 1000 7.3 / 7.5 against 7.2 / 7.1, 1024 x 8192 21.7 / 26.1 against 19.9 / 22.8).
+bool few_rows(int64_t rows, int64_t cols) { return rows <= min64(768, 256 + cols / 8); }
+
+GradPlan grad_plan(int64_t rows, int64_t cols, int dtype) {
     GradPlan g;
     g.held = cols <= kHeldCols;
+    g.few = g.held && few_rows(rows, cols);
     g.pitch = ceil_div(cols, 64) * 64;
+    g.vecs = kVecs;
     if (!g.held) {
         g.waves = g.subs = 0;
         g.parts = min64(rows, kLongParts);
         return g;
     }
-    g.waves = row_waves(cols);
+    // fp32 rows take one vector a lane where 16 waves reach (two would spill).
+    if (dtype == FP8LN_FP32 && cols / 8 <= kMaxWaves * kWaveSize) g.vecs = 1;
+    g.waves = row_waves(cols, g.vecs);
+    if (g.few) {
+        // A column workgroup has 4 slices of rows for each wave: about 4 rows each.
+        g.subs = (int)max64(1, min64(kMaxWaves, max64(4, rows / 16)) / g.waves);
+        g.parts = 0;
+        return g;
+    }
     g.subs = (int)max64(1, min64(kMaxWaves / g.waves, ceil_div(rows, kGradWorkgroups)));
     g.parts = min64(kGradWorkgroups, ceil_div(rows, g.subs));
     return g;
 }
 
+// Partial results: the most that either element type takes.
 int64_t grad_workspace(int64_t rows, int64_t cols) {
-    const GradPlan g = grad_plan(rows, cols);
-    return 2 * g.parts * g.pitch * (int64_t)sizeof(float);
+    const int64_t pitch = ceil_div(cols, 64) * 64;
+    return 2 * min64(rows, cols <= kHeldCols ? kGradWorkgroups : kLongParts) * pitch * (int64_t)sizeof(float);
+}
+
+template <class T, int V>
+void launch_backward(const LnBwd& p, const GradPlan& g, float* dw, float* db, hipStream_t hs) {
+    const dim3 block(g.waves * g.subs * kWaveSize);
+    if (g.few) {
+        const int row_blocks = (int)ceil_div(p.rows, g.subs);
+        hipLaunchKernelGGL((ln_backward_few_kernel<T, V>), dim3((unsigned)(row_blocks + ceil_div(p.cols, 64))), block,
+                           0, hs, p, row_blocks, dw, db);
+        return;
+    }
+    const unsigned lds = (unsigned)(g.subs / 2 * 4 * V * g.waves * kWaveSize * sizeof(float4));
+    hipLaunchKernelGGL((ln_backward_kernel<T, V>), dim3((unsigned)g.parts), block, lds, hs, p);
 }
 
 }  // namespace
@@ -742,7 +885,7 @@ int fp8_layer_norm(const void* x, int dtype, const void* w, const void* b, int p
     if (cus <= 0) return FP8LN_ERR_DEVICE;
     const hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
     LnFwd p{x, w, b, param_dtype == FP8LN_BF16, eps, y, static_cast<uint8_t*>(q), q_format, scale, mean, rstd,
-            rows, cols, row_waves(cols)};
+            rows, cols, row_waves(cols, kVecs)};
     (void)hipGetLastError();
     if (cols > kHeldCols) {
         const dim3 grid((unsigned)min64(rows, (int64_t)cus * 8));
@@ -793,17 +936,14 @@ int fp8_layer_norm_backward(const void* dy, const void* x, int dtype, const floa
     const int cus = device_cu_count();
     if (cus <= 0) return FP8LN_ERR_DEVICE;
     const hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
-    const GradPlan g = grad_plan(rows, cols);
+    const GradPlan g = grad_plan(rows, cols, dtype);
     LnBwd p{dy, x, mean, rstd, w, param_dtype == FP8LN_BF16, residual_grad, dx, static_cast<float*>(workspace),
             rows, cols, g.pitch, g.waves, g.subs};
     (void)hipGetLastError();
     if (rows > 0 && g.held) {
-        const dim3 grid((unsigned)g.parts), block(g.waves * g.subs * kWaveSize);
-        const unsigned lds = (unsigned)(g.subs / 2 * 2 * g.pitch * (int64_t)sizeof(float));
-        if (dtype == FP8LN_BF16)
-            hipLaunchKernelGGL(ln_backward_kernel<bf16_t>, grid, block, lds, hs, p);
-        else
-            hipLaunchKernelGGL(ln_backward_kernel<float>, grid, block, lds, hs, p);
+        if (dtype == FP8LN_BF16) launch_backward<bf16_t, 2>(p, g, dw, db, hs);
+        else if (g.vecs == 1) launch_backward<float, 1>(p, g, dw, db, hs);
+        else launch_backward<float, 2>(p, g, dw, db, hs);
     } else if (rows > 0) {
         const dim3 grid((unsigned)min64(rows, (int64_t)cus * 8));
         const dim3 cgrid((unsigned)ceil_div(cols, kColThreads), (unsigned)g.parts);
@@ -815,8 +955,9 @@ int fp8_layer_norm_backward(const void* dy, const void* x, int dtype, const floa
             hipLaunchKernelGGL(ln_backward_long_kernel<float>, grid, dim3(kLongThreads), 0, hs, p);
         }
     }
-    hipLaunchKernelGGL(ln_reduce_kernel, dim3((unsigned)ceil_div(cols, 64), 2), dim3(256), 0, hs,
-                       static_cast<const float*>(workspace), (int)g.parts, g.pitch, cols, dw, db);
+    if (rows == 0 || !g.few)
+        hipLaunchKernelGGL(ln_reduce_kernel, dim3((unsigned)ceil_div(cols, 64), 2), dim3(kReduceSlices * 16), 0, hs,
+                           static_cast<const float*>(workspace), (int)g.parts, g.pitch, cols, dw, db);
     if (hipGetLastError() != hipSuccess) return FP8LN_ERR_LAUNCH;
     return FP8LN_OK;
 }

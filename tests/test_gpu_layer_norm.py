@@ -369,3 +369,11 @@ def test_refusals_with_gpu_tensors():
                  lambda: g(x, x, s, s, dx=x.float()), lambda: g(x, x, s.cpu(), s)):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("cols", [8, 72, 1000, 4104, 8208])
+@pytest.mark.parametrize("rows", [63, 65, 97, 255, 260, 300, 769])
+def test_backward_on_both_sides_of_the_row_counts_where_its_launches_change(rows, cols, dtype):
+    x, w, _ = make(rows, cols, dtype, rows + cols)
+    check_backward(x, w, 6, residual=True)
