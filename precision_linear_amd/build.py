@@ -19,9 +19,10 @@ ROOT = os.path.dirname(HERE)
 # and the linear layer's gradient.  They compile in parallel.
 SRCS = [os.path.join(HERE, "csrc", f) for f in
         ["fp8_scaled_mm.hip"] + [f"fp8_{n}_f{k}.hip" for n in ("gemm", "linear") for k in range(4)] +
-        ["fp8_quantize.hip", "fp8_layer_norm.hip", "fp8_linear_grad.hip"]]
+        ["fp8_linear_pair.hip", "fp8_quantize.hip", "fp8_layer_norm.hip", "fp8_linear_grad.hip"]]
 HEADERS = [os.path.join(HERE, "csrc", f) for f in
-           ("fp8_gemm_kernels.h", "fp8_convert.h", "lane_ops.h", "activation.h", "plan_cost_table.h")]
+           ("fp8_gemm_kernels.h", "fp8_convert.h", "lane_ops.h", "activation.h", "fp8_pair.h",
+            "plan_cost_table.h")]
 LIB = os.path.join(HERE, "libfp8_scaled_mm.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

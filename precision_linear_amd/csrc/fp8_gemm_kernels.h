@@ -82,6 +82,14 @@ struct LinearParams : Params {
 };
 template <bool EPI> using KernelParams = std::conditional_t<EPI, LinearParams, Params>;
 
+// Two independent products in one launch (the PAIR instantiations; row-wise
+// scales, no bias): the grid's workgroups walk the units of p[0], then those of
+// p[1].
+struct PairParams {
+    Params p[2];
+};
+typedef void (*PairLaunch)(const PairParams&, dim3, hipStream_t);
+
 typedef void (*Launch)(const Params&, dim3, hipStream_t);
 struct LaunchPair {
     Launch plain;
@@ -139,6 +147,10 @@ extern LaunchPair kLinearF0[kNumConfigs];
 extern LaunchPair kLinearF1[kNumConfigs];
 extern LaunchPair kLinearF2[kNumConfigs];
 extern LaunchPair kLinearF3[kNumConfigs];
+
+// The generic configurations' pair launches for A in e5m2 and B in e4m3fn (the
+// linear layer's gradient), defined in fp8_linear_pair.hip.
+extern PairLaunch kPairF1[kNumGenericConfigs];
 
 }  // namespace fp8mm
 
@@ -1142,11 +1154,17 @@ __device__ __forceinline__ void run_stage(typename Mfma<C::MI_>::acc_t (&acc)[C:
     }
 }
 
+__device__ __forceinline__ const Params& first_product(const Params& p) { return p; }
+__device__ __forceinline__ const LinearParams& first_product(const LinearParams& p) { return p; }
+__device__ __forceinline__ const Params& first_product(const PairParams& p) { return p.p[0]; }
+
 template <int BM, int BN, int BK, int WAVES_M, int WAVES_N, int STAGES, int MI, int GROUP_M,
-          bool NT_B, int FMT, bool SK = false, bool EPI = false>
+          bool NT_B, int FMT, bool SK = false, bool EPI = false, bool PAIR = false>
 __global__ void __launch_bounds__(WAVES_M * WAVES_N * kWave,
                                   (Cfg<BM, BN, BK, WAVES_M, WAVES_N, STAGES, MI, GROUP_M>::OCCUPANCY))
-fp8_gemm_kernel(KernelParams<EPI> p) {
+fp8_gemm_kernel(std::conditional_t<PAIR, PairParams, KernelParams<EPI>> args) {
+    // A pair kernel works on a copy that it changes from one product to the next.
+    std::conditional_t<PAIR, Params, const KernelParams<EPI>&> p = first_product(args);
     using C = Cfg<BM, BN, BK, WAVES_M, WAVES_N, STAGES, MI, GROUP_M, NT_B, FMT>;
     using F = Mfma<MI>;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[C::LDS_BYTES];
@@ -1162,11 +1180,11 @@ fp8_gemm_kernel(KernelParams<EPI> p) {
     int wg = blockIdx.x;
     if (G % kXcds == 0) wg = (blockIdx.x % kXcds) * (G / kXcds) + blockIdx.x / kXcds;
 
-    const float s_pt = p.rowwise ? 0.f : p.scale_a[0] * p.scale_b[0];
+    const float s_pt = PAIR || p.rowwise ? 0.f : p.scale_a[0] * p.scale_b[0];
     float* epi_sa = reinterpret_cast<float*>(smem + C::MAIN_BYTES);
     float* epi_sb = epi_sa + BM;
     uint16_t* epi_bias = reinterpret_cast<uint16_t*>(epi_sb + BN);
-    const bool has_bias = p.bias != nullptr;
+    const bool has_bias = !PAIR && p.bias != nullptr;
 
     __shared__ unsigned arrival;
     // One work unit: K slices [kb, kb + k_iters) of tile t, part `part` of the
@@ -1382,6 +1400,22 @@ fp8_gemm_kernel(KernelParams<EPI> p) {
             const int64_t last = wg_of((int64_t)(t + 1) * p.k_iters - 1);
             unit(t, kb, kn, (int)(wg - first), (int)(last - first + 1));
             it += kn;
+        }
+    } else if constexpr (PAIR) {
+        int first = wg;   // this workgroup's first unit of the product
+#pragma unroll 1
+        for (int which = 0;; ++which) {
+            const int num_units = p.num_tiles * p.splits;
+            int u = first;
+            for (; u < num_units; u += G) {
+                const int t = u / p.splits;
+                const int split = u - t * p.splits;
+                const int kb = split * p.k_chunk;
+                unit(t, kb, max(0, min(p.k_chunk, p.k_iters - kb)), split, p.splits);
+            }
+            if (which == 1) break;
+            first = u - num_units;
+            p = args.p[1];
         }
     } else {
         const int num_units = p.num_tiles * p.splits;
@@ -2044,6 +2078,14 @@ void launch_cfg(const Params& p, dim3 grid, hipStream_t stream) {
     hipLaunchKernelGGL((fp8_gemm_kernel<BM, BN, BK, WAVES_M, WAVES_N, STAGES, MI, GROUP_M, NT_B, FMT, SK, EPI>),
                        grid, dim3(C::THREADS), 0, stream,
                        static_cast<const KernelParams<EPI>&>(p));
+}
+
+template <int BM, int BN, int BK, int WAVES_M, int WAVES_N, int STAGES, int MI, int GROUP_M, int FMT>
+void launch_pair(const PairParams& p, dim3 grid, hipStream_t stream) {
+    using C = Cfg<BM, BN, BK, WAVES_M, WAVES_N, STAGES, MI, GROUP_M>;
+    hipLaunchKernelGGL((fp8_gemm_kernel<BM, BN, BK, WAVES_M, WAVES_N, STAGES, MI, GROUP_M, false, FMT, false,
+                                        false, true>),
+                       grid, dim3(C::THREADS), 0, stream, p);
 }
 
 // The stream-K launch of a configuration, or null where none is compiled.

@@ -7,10 +7,12 @@
 // is computed twice rather than written out in 32 bits:
 //   1. grad_stats_kernel: maxima of dz's rows and columns, sums of its columns
 //      (dbias), maxima of x's columns, as partial results;
-//   2. grad_scales_kernel: joins them into the scales and dbias;
+//   2. grad_scales_kernel: joins them into the scales and dbias; with few
+//      partial results the third pass does that itself;
 //   3. grad_quantize_kernel: the codes of dz (row-major, and transposed) and of
 //      x (transposed);
-//   4. the two products, on the scaled multiply's kernels.
+//   4. the two products, on the scaled multiply's kernels: in one launch where
+//      they fill the GPU better together (small ones), else in two.
 // Passes 1 and 3 are bound by memory (and, for the smooth activations, nearly
 // by the arithmetic of the slope): 2 x 4 bytes read and 2 bytes written for an
 // element of dz, against 4 K bytes' worth of matrix work.
@@ -23,6 +25,7 @@
 #include "../../include/fp8_linear.h"
 #include "activation.h"
 #include "fp8_convert.h"
+#include "fp8_pair.h"
 #include "lane_ops.h"
 
 namespace {
@@ -31,7 +34,7 @@ constexpr int kThreadsG = 256;
 constexpr int kTileCols = 128;                      // 16 lanes x 8 columns
 constexpr int kColLanes = kTileCols / 8;            // 16: a DPP row
 constexpr int kRowLanes = kThreadsG / kColLanes;    // 16
-constexpr int kTileRows = 128;                      // of the quantisation's tiles
+constexpr int kTileRows = 128;                      // of the quantisation's tiles (64 in small grids)
 constexpr int kStatUnroll = 4;                      // rows in flight per thread
 
 struct Grad {
@@ -99,7 +102,6 @@ grad_stats_kernel(Grad p) {
         }
 #pragma unroll
         for (int u = 0; u < kStatUnroll; ++u) {
-            const int64_t row = r + u * kRowLanes;
             float f[8];
             if (is_x) {
 #pragma unroll
@@ -115,6 +117,7 @@ grad_stats_kernel(Grad p) {
                 csum[i] += f[i];
             }
             if (!is_x && p.want_rows) {
+                const int64_t row = r + u * kRowLanes;
                 rmax = row16_max(rmax);
                 if (cl == 0 && row < r1) p.row_max[cb * p.M + row] = rmax;
             }
@@ -146,11 +149,11 @@ grad_stats_kernel(Grad p) {
 // of their partial results each.
 constexpr int kScaleThreads = 1024;
 
-__device__ __forceinline__ void put_scale(float amax, float qmax, float* scale, int64_t n, int64_t i) {
+// (scale, its reciprocal)
+__device__ __forceinline__ float2 scale_of(float amax, float qmax) {
     float s = amax / qmax;
     if (s < 0x1p-126f) s = 0.f;       // (its reciprocal would leave fp32)
-    scale[i] = s;
-    scale[n + i] = s == 0.f ? 0.f : 1.f / s;
+    return float2{s, s == 0.f ? 0.f : 1.f / s};
 }
 
 __global__ void __launch_bounds__(kScaleThreads)
@@ -177,9 +180,19 @@ grad_scales_kernel(Grad p, int blocks_rows, int blocks_cols) {
     const int64_t i = (int64_t)b * 64 + lane;
     float m = 0.f, sum = 0.f;
     if (i < n)
-        for (int q = slice; q < parts; q += 16) {
-            m = fmaxf(m, part_max[q * n + i]);
-            if (part_sum) sum += part_sum[q * n + i];
+        for (int q0 = slice; q0 < parts; q0 += 16 * 8) {
+            float v[8], w[8];   // loaded together: the pass is one memory latency or two long
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int q = q0 + 16 * k;
+                v[k] = q < parts ? part_max[q * n + i] : 0.f;
+                w[k] = part_sum && q < parts ? part_sum[q * n + i] : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                m = fmaxf(m, v[k]);
+                sum += w[k];
+            }
         }
     s_max[slice][lane] = m;
     s_sum[slice][lane] = sum;
@@ -190,7 +203,9 @@ grad_scales_kernel(Grad p, int blocks_rows, int blocks_cols) {
         m = fmaxf(m, s_max[q][lane]);
         sum += s_sum[q][lane];
     }
-    put_scale(m, qmax, scale, n, i);
+    const float2 sr = scale_of(m, qmax);
+    scale[i] = sr.x;
+    scale[n + i] = sr.y;
     if (part_sum) p.dbias[i] = sum;
 }
 
@@ -203,57 +218,120 @@ __device__ __forceinline__ float over_scale(float v, float s, float r) {
     else return v * r;
 }
 
-// Pass 3.  Workgroup: a tile of 128 rows x 128 columns of dz or (the last
+// Pass 3.  Workgroup: a tile of ROWS rows x 128 columns of dz or (the last
 // blocks) of x.  A thread takes 4 consecutive rows of 8 columns at a time, so
 // that 4 codes of a column make one word of the transposed tile in LDS: 128
-// rows of 8 16-byte chunks, chunk c of column n at c ^ ((n >> 3) & 7), which
-// spreads the 16 column lanes over the banks.
-template <int ACT>
+// rows of ROWS / 16 chunks of 16 bytes, chunk c of column n at
+// c ^ ((n >> 3) % (ROWS / 16)), which spreads the 16 column lanes over the banks.
+//
+// JOIN: the workgroup joins the partial maxima of its columns and rows itself
+// (at most kJoinParts of each), in place of pass 2; those of the first strip
+// write the columns' scales and dbias, those of the first column block the
+// rows' scales.
+constexpr int kJoinParts = 32;
+
+// ROWS: 128, or 64 (half the work a workgroup) where the grid is small.
+template <int ACT, bool JOIN, int ROWS>
 __global__ void __launch_bounds__(kThreadsG)
 grad_quantize_kernel(Grad p) {
-    __shared__ __attribute__((aligned(16))) uint32_t s_t[kTileCols][kTileRows / 4];
+    constexpr int kChunks = ROWS / 16;           // of a transposed row
+    __shared__ __attribute__((aligned(16))) uint32_t s_t[kTileCols][ROWS / 4];
+    __shared__ __attribute__((aligned(16))) float s_col[2][kTileCols];   // scales, reciprocals
+    __shared__ float s_row[2][ROWS];
     constexpr bool kExactDz = ACT == kActNone || ACT == kActRelu;
     const int cl = threadIdx.x % kColLanes, rl = threadIdx.x / kColLanes;
     const int per_strip = p.blocks_n + p.blocks_k;
-    const int64_t strip = blockIdx.x / per_strip;
-    const int block = (int)(blockIdx.x - strip * per_strip);
+    // Last strips first: they were pass 1's last, and what the caches still hold
+    // of dy, z and x is theirs.
+    const int64_t turn = blockIdx.x / per_strip;
+    const int block = (int)(blockIdx.x - turn * per_strip);
+    const int64_t strip = gridDim.x / per_strip - 1 - turn;
     const bool is_x = block >= p.blocks_n;
     const int cb = is_x ? block - p.blocks_n : block;
     const int64_t width = is_x ? p.K : p.N;
     const int64_t col = (int64_t)cb * kTileCols + cl * 8;
-    const int64_t row0 = strip * kTileRows;
+    const int64_t row0 = strip * ROWS;
     const bool ok = col < width;
     const bool transposed = is_x || p.want_cols;
+    constexpr int kSteps = ROWS / (4 * kRowLanes);
+    Raw8<bf16_t> a[kSteps][4], b[kSteps][4];
+    auto fetch = [&](int it) __attribute__((always_inline)) {
+        const int64_t r = row0 + (it * kRowLanes + rl) * 4;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            a[it][k].zero();
+            b[it][k].zero();
+            if (ok && r + k < p.M) {
+                a[it][k].load((is_x ? p.x : p.dy) + (r + k) * width + col);
+                if (ACT != kActNone && !is_x) b[it][k].load(p.z + (r + k) * width + col);
+            }
+        }
+    };
+    fetch(0);   // under way while the scales are found
+    {   // scales: the first 128 threads the columns', the others the rows'
+        static_assert(kThreadsG >= kTileCols + ROWS, "one thread for each row and column");
+        const int t = threadIdx.x % kTileCols;
+        if (threadIdx.x < kTileCols) {
+            const int64_t c = (int64_t)cb * kTileCols + t;
+            float* scale = is_x ? p.x_scale : p.col_scale;
+            float2 sr{0.f, 0.f};
+            if (c < width) {
+                if constexpr (JOIN) {
+                    const float* part = is_x ? p.x_max : p.col_max;
+                    float m = 0.f;
+#pragma unroll 8
+                    for (int q = 0; q < p.parts; ++q) m = fmaxf(m, part[q * width + c]);
+                    sr = scale_of(m, is_x ? Fp8Fmt<0>::kMax : Fp8Fmt<1>::kMax);
+                    if (strip == 0) {
+                        scale[c] = sr.x;
+                        if (!is_x && p.dbias) {
+                            float sum = 0.f;
+#pragma unroll 8
+                            for (int q = 0; q < p.parts; ++q) sum += p.col_sum[q * width + c];
+                            p.dbias[c] = sum;
+                        }
+                    }
+                } else {
+                    sr = float2{scale[c], scale[width + c]};
+                }
+            }
+            s_col[0][t] = sr.x;
+            s_col[1][t] = sr.y;
+        } else if (t < ROWS) {
+            const int64_t r = row0 + t;
+            float2 sr{0.f, 0.f};
+            if (!is_x && p.want_rows && r < p.M) {
+                if constexpr (JOIN) {
+                    float m = 0.f;
+#pragma unroll 8
+                    for (int q = 0; q < p.blocks_n; ++q) m = fmaxf(m, p.row_max[q * p.M + r]);
+                    sr = scale_of(m, Fp8Fmt<1>::kMax);
+                    if (block == 0) p.row_scale[r] = sr.x;
+                } else {
+                    sr = float2{p.row_scale[r], p.row_scale[p.M + r]};
+                }
+            }
+            s_row[0][t] = sr.x;
+            s_row[1][t] = sr.y;
+        }
+        __syncthreads();
+    }
     float cs[8], cr[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) cs[i] = cr[i] = 0.f;
-    if (ok && transposed) {
-        const float* s = (is_x ? p.x_scale : p.col_scale) + col;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            cs[i] = s[i];
-            cr[i] = s[width + i];
-        }
+    for (int i = 0; i < 8; ++i) {
+        cs[i] = s_col[0][cl * 8 + i];
+        cr[i] = s_col[1][cl * 8 + i];
     }
 #pragma unroll
-    for (int it = 0; it < kTileRows / (4 * kRowLanes); ++it) {
+    for (int it = 0; it < kSteps; ++it) {
         const int mg = it * kRowLanes + rl;            // group of 4 rows in the tile
         const int64_t r = row0 + mg * 4;
-        Raw8<bf16_t> a[4], b[4];
+        if (it > 0) fetch(it);   // (a step ahead, the registers would cost a wave of four)
         float rs[4], rr[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            a[k].zero();
-            b[k].zero();
-            rs[k] = rr[k] = 0.f;
-            if (ok && r + k < p.M) {
-                a[k].load((is_x ? p.x : p.dy) + (r + k) * width + col);
-                if (ACT != kActNone && !is_x) b[k].load(p.z + (r + k) * width + col);
-                if (!is_x && p.want_rows) {
-                    rs[k] = p.row_scale[r + k];
-                    rr[k] = p.row_scale[p.M + r + k];
-                }
-            }
+            rs[k] = s_row[0][mg * 4 + k];
+            rr[k] = s_row[1][mg * 4 + k];
         }
         float f[4][8];
         uint32_t words[8];
@@ -261,7 +339,7 @@ grad_quantize_kernel(Grad p) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) f[k][i] = over_scale<true>(a[k].get(i), cs[i], cr[i]);
+                for (int i = 0; i < 8; ++i) f[k][i] = over_scale<true>(a[it][k].get(i), cs[i], cr[i]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 int w = Fp8Fmt<0>::cvt_pk<false>(f[0][i], f[1][i], 0);
@@ -269,7 +347,7 @@ grad_quantize_kernel(Grad p) {
             }
         } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) dz8<ACT>(a[k], b[k], f[k]);
+            for (int k = 0; k < 4; ++k) dz8<ACT>(a[it][k], b[it][k], f[k]);
             if (p.want_rows) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -296,19 +374,19 @@ grad_quantize_kernel(Grad p) {
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            s_t[cl * 8 + i][(((mg >> 2) ^ (cl & 7)) << 2) | (mg & 3)] = words[i];
+            s_t[cl * 8 + i][(((mg >> 2) ^ (cl % kChunks)) << 2) | (mg & 3)] = words[i];
     }
     if (!transposed) return;
     __syncthreads();
     uint8_t* out = is_x ? p.q_x : p.q_cols;
 #pragma unroll
-    for (int it = 0; it < kTileCols * (kTileRows / 16) / kThreadsG; ++it) {
+    for (int it = 0; it < kTileCols * kChunks / kThreadsG; ++it) {
         const int q = it * kThreadsG + threadIdx.x;
-        const int n = q / (kTileRows / 16), c = q % (kTileRows / 16);
+        const int n = q / kChunks, c = q % kChunks;
         const int64_t row = (int64_t)cb * kTileCols + n, m = row0 + c * 16;
         if (row < width && m < p.Mp)
             *reinterpret_cast<u32x4*>(out + row * p.Mp + m) =
-                *reinterpret_cast<const u32x4*>(&s_t[n][(c ^ ((n >> 3) & 7)) << 2]);
+                *reinterpret_cast<const u32x4*>(&s_t[n][(c ^ ((n >> 3) % kChunks)) << 2]);
     }
 }
 
@@ -336,12 +414,25 @@ int grad_shape(int64_t M, int64_t N, int64_t K, bool want_dw) {
     return FP8MM_OK;
 }
 
+// Pass 3 joins the partial results itself where there are at most kJoinParts
+// for a row (column blocks) and for a column (strips).
+bool joins(const Grad& p) { return p.blocks_n <= kJoinParts && p.parts <= kJoinParts; }
+
 // Rows of a strip of pass 1: 64 (one round of loads per thread), more where
-// there are strips enough without that, up to 256.
-int64_t strip_rows(int64_t M, int64_t blocks) {
-    int64_t s = kRowLanes * kStatUnroll;
+// there are strips enough without that, up to 256, or where that leaves few
+// enough strips for pass 3 to join.
+int64_t strip_rows(int64_t M, int64_t blocks_n, int64_t blocks) {
+    const int64_t round = kRowLanes * kStatUnroll;
+    int64_t s = round;
     while (s < 256 && up(M, 2 * s) * blocks >= 2048) s *= 2;
+    if (blocks_n <= kJoinParts && up(M, s) > kJoinParts) s = up(up(M, kJoinParts), round) * round;
     return s;
+}
+
+// The two products of a call (sizes only).
+void products(int64_t M, int64_t N, int64_t K, int64_t Mp, fp8mm::Product (&q)[2]) {
+    q[0] = fp8mm::Product{nullptr, nullptr, nullptr, nullptr, nullptr, M, K, N};
+    q[1] = fp8mm::Product{nullptr, nullptr, nullptr, nullptr, nullptr, N, K, Mp};
 }
 
 struct GradSpace {
@@ -359,7 +450,7 @@ GradSpace grad_space(int64_t M, int64_t N, int64_t K, bool want_dx, bool want_dw
     p.want_cols = want_dw;
     p.blocks_n = (int)up(N, kTileCols);
     p.blocks_k = want_dw ? (int)up(K, kTileCols) : 0;
-    p.strip = strip_rows(M, p.blocks_n + p.blocks_k);
+    p.strip = strip_rows(M, p.blocks_n, p.blocks_n + p.blocks_k);
     p.parts = (int)up(M, p.strip);
     int64_t mm = kCounterArea;
     if (want_dx && M > 0) {
@@ -368,6 +459,13 @@ GradSpace grad_space(int64_t M, int64_t N, int64_t K, bool want_dx, bool want_dw
     }
     if (want_dw && M > 0) {
         const int64_t n = fp8_scaled_mm_workspace_size(N, K, p.Mp, FP8MM_ROWWISE, 0, -1, 0);
+        mm = n > mm ? n : mm;
+    }
+    if (want_dx && want_dw && M > 0) {
+        fp8mm::Product q[2];
+        products(M, N, K, p.Mp, q);
+        const fp8mm::PairPlan plan = fp8mm::plan_pair(q);
+        const int64_t n = plan.cfg >= 0 ? fp8mm::pair_workspace(q, plan) : 0;
         mm = n > mm ? n : mm;
     }
     g.mm = align256(mm);
@@ -380,17 +478,29 @@ GradSpace grad_space(int64_t M, int64_t N, int64_t K, bool want_dx, bool want_dw
     return g;
 }
 
+// Tiles of 128 rows below which 64 rows a workgroup are faster.
+constexpr int64_t kSmallGrid = 512;
+
 template <int ACT>
 void launch_passes(const Grad& p, hipStream_t hs) {
     const int per = p.blocks_n + p.blocks_k;
     hipLaunchKernelGGL(grad_stats_kernel<ACT>, dim3((unsigned)(p.parts * per)), dim3(kThreadsG), 0, hs, p);
-    const int rows = p.want_rows ? (int)up(p.M, 64) : 0, cols = (int)up(p.N, 64);
-    const int xs = p.blocks_k ? (int)up(p.K, 64) : 0;
-    hipLaunchKernelGGL(grad_scales_kernel, dim3((unsigned)(rows + cols + xs)), dim3(kScaleThreads), 0, hs, p, rows,
-                       cols);
-    if (p.want_rows || p.want_cols)
-        hipLaunchKernelGGL(grad_quantize_kernel<ACT>, dim3((unsigned)(up(p.M, kTileRows) * per)), dim3(kThreadsG),
-                           0, hs, p);
+    const bool join = joins(p);
+    if (!join || !(p.want_rows || p.want_cols)) {
+        const int rows = p.want_rows ? (int)up(p.M, 64) : 0, cols = (int)up(p.N, 64);
+        const int xs = p.blocks_k ? (int)up(p.K, 64) : 0;
+        hipLaunchKernelGGL(grad_scales_kernel, dim3((unsigned)(rows + cols + xs)), dim3(kScaleThreads), 0, hs, p,
+                           rows, cols);
+    }
+    if (!(p.want_rows || p.want_cols)) return;
+    const int64_t tiles = up(p.M, kTileRows) * per;
+    const dim3 block(kThreadsG);
+    if (!join)
+        hipLaunchKernelGGL((grad_quantize_kernel<ACT, false, kTileRows>), dim3((unsigned)tiles), block, 0, hs, p);
+    else if (tiles >= kSmallGrid)
+        hipLaunchKernelGGL((grad_quantize_kernel<ACT, true, kTileRows>), dim3((unsigned)tiles), block, 0, hs, p);
+    else
+        hipLaunchKernelGGL((grad_quantize_kernel<ACT, true, 64>), dim3((unsigned)(up(p.M, 64) * per)), block, 0, hs, p);
 }
 
 }  // namespace
@@ -453,6 +563,16 @@ int fp8_linear_backward(const void* dy, const void* x, const void* wt, int wt_fo
         default: launch_passes<kActNone>(p, hs); break;
     }
     if (hipGetLastError() != hipSuccess) return FP8MM_ERR_LAUNCH;
+    if (dx && dw && wt_format == FP8MM_E4M3FN) {
+        fp8mm::Product q[2];
+        products(M, N, K, p.Mp, q);
+        const fp8mm::PairPlan plan = fp8mm::plan_pair(q);
+        if (plan.cfg >= 0) {
+            q[0] = fp8mm::Product{p.q_rows, wt, p.row_scale, wt_scale, dx, M, K, N};
+            q[1] = fp8mm::Product{p.q_cols, p.q_x, p.col_scale, p.x_scale, dw, N, K, p.Mp};
+            return fp8mm::run_pair(q, plan, hs, ws);
+        }
+    }
     if (dx) {
         st = fp8_scaled_mm_typed(p.q_rows, FP8MM_E5M2, wt, wt_format, p.row_scale, wt_scale, nullptr, dx, M, K, N,
                                  FP8MM_ROWWISE, stream, -1, 0, ws, g.mm);
