@@ -197,8 +197,8 @@ _TORCH_FORMATS = {torch.float8_e4m3fn: E4M3FN, torch.float8_e5m2: E5M2}
 
 
 def _as_codes(t: torch.Tensor, name: str, fmt) -> tuple:
-    """(uint8 view, format id).  A float8 tensor carries its format; uint8
-    codes take `fmt` (default e4m3fn)."""
+    """(tensor, format id).  A float8 tensor carries its format; uint8 codes
+    take `fmt` (default e4m3fn)."""
     dt = t.dtype
     if fmt is None and dt == torch.uint8:
         return t, E4M3FN
@@ -208,7 +208,7 @@ def _as_codes(t: torch.Tensor, name: str, fmt) -> tuple:
         f = _TORCH_FORMATS[dt]
         if fmt is not None and _FORMATS[fmt] != f:
             raise ValueError(f"{name} is {dt} but {name}_format={fmt!r}")
-        return t.view(torch.uint8), f
+        return t, f
     if dt == torch.uint8:
         return t, _FORMATS[fmt]
     raise ValueError(f"{name} must be float8_e4m3fn, float8_e5m2 or uint8 codes, got {dt}")
@@ -395,38 +395,36 @@ def fp8_linear_backward(dy: torch.Tensor, x: torch.Tensor | None, wt: torch.Tens
     dy and z (fp8_linear's preact; not needed for 'none') are M x N bf16, x is
     M x K bf16, wt the K x N codes of W transposed with K scales wt_scale.  dx
     (M x K) and dw (N x K) are bf16, dbias is fp32; True allocates one, False
-    leaves it (and what only it needs) out, and dx and dw may be buffers.  What is left out is None in
-    the result.  N and K are multiples of 16.  Codes, scales and partial sums
+    leaves it (and what only it needs) out, and dx and dw may be buffers.  What is
+    left out is None in the result.  N and K are multiples of 16.  Codes, scales and partial sums
     live in `workspace` (a GPU byte tensor, zero-filled before its first use) or
     in one that this module keeps per stream."""
     act = _activation(activation)
-
-    def matrix(name, t, rows, cols):
-        if t.dtype != torch.bfloat16 or t.dim() != 2 or not t.is_contiguous() or \
-                (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
-            raise ValueError(f"{name} must be a contiguous bf16 {'M' if rows is None else rows} x "
-                             f"{'N' if cols is None else cols} tensor")
-
-    for name, want in (("dx", dx), ("dw", dw), ("dbias", dbias)):
-        if not isinstance(want, (bool, torch.Tensor)) or (name == "dbias" and not isinstance(want, bool)):
-            raise ValueError(f"{name} must be True, False" + ("" if name == "dbias" else " or a tensor to write"))
     want_dx, want_dw = dx is not False, dw is not False
+    out_dx, out_dw = want_dx and dx is not True, want_dw and dw is not True      # buffers given
+    if (out_dx and not isinstance(dx, torch.Tensor)) or (out_dw and not isinstance(dw, torch.Tensor)):
+        raise ValueError("dx and dw must be True, False or a tensor to write")
+    if dbias is not True and dbias is not False:
+        raise ValueError("dbias must be True or False")
     if not (want_dx or want_dw or dbias):
         raise ValueError("nothing to compute: dx, dw and dbias are all False")
     if not dy.is_cuda:
         raise ValueError("all tensors must be on the GPU")
-    matrix("dy", dy, None, None)
+    if dy.dtype != torch.bfloat16 or dy.dim() != 2 or not dy.is_contiguous():
+        raise ValueError("dy must be a contiguous bf16 M x N tensor")
     M, N = dy.shape
-    if act != 0 and z is None:
-        raise ValueError(f"activation {activation!r} needs z")
     if z is not None:
-        matrix("z", z, M, N)
+        _bf16_matrix("z", z, (M, N))
+    elif act != 0:
+        raise ValueError(f"activation {activation!r} needs z")
     K, fw = 16, E4M3FN      # (a problem without dx and dw has no K)
     if want_dw:
         if x is None:
             raise ValueError("dw needs x")
-        matrix("x", x, M, None)
+        if x.dim() != 2:
+            raise ValueError("x must be a contiguous bf16 M x K tensor")
         K = x.shape[1]
+        _bf16_matrix("x", x, (M, K))
     if want_dx:
         if wt is None or wt_scale is None:
             raise ValueError("dx needs wt and wt_scale")
@@ -438,24 +436,22 @@ def fp8_linear_backward(dy: torch.Tensor, x: torch.Tensor | None, wt: torch.Tens
         _ln_vector(wt_scale, "wt_scale", K)
     if N < 16 or N % 16 != 0 or K < 16 or K % 16 != 0:
         raise ValueError(f"N and K must be multiples of 16, got {N} and {K}")
+    if out_dx:
+        _bf16_matrix("dx", dx, (M, K))
+    if out_dw:
+        _bf16_matrix("dw", dw, (N, K))
     dev = dy.get_device()
     device = dy.device
-    used = [("z", z), ("workspace", workspace), ("dx", dx if want_dx and dx is not True else None),
-            ("dw", dw if want_dw and dw is not True else None)]
-    used += [("x", x)] if want_dw else []
-    used += [("wt", wt), ("wt_scale", wt_scale)] if want_dx else []
-    _check_devices(dev, used)
+    x = x if want_dw else None
+    wt, wt_scale = (wt, wt_scale) if want_dx else (None, None)
+    _check_devices(dev, (("z", z), ("x", x), ("wt", wt), ("wt_scale", wt_scale), ("workspace", workspace),
+                         ("dx", dx if out_dx else None), ("dw", dw if out_dw else None)))
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous GPU tensor")
-    if dx is True:
-        dx = torch.empty((M, K), dtype=torch.bfloat16, device=device)
-    elif want_dx:
-        matrix("dx", dx, M, K)
-    if dw is True:
-        dw = torch.empty((N, K), dtype=torch.bfloat16, device=device)
-    elif want_dw:
-        matrix("dw", dw, N, K)
-    dx, dw = dx if want_dx else None, dw if want_dw else None
+    if not out_dx:
+        dx = torch.empty((M, K), dtype=torch.bfloat16, device=device) if want_dx else None
+    if not out_dw:
+        dw = torch.empty((N, K), dtype=torch.bfloat16, device=device) if want_dw else None
     db = torch.empty(N, dtype=torch.float32, device=device) if dbias else None
     L = lib()
     stream = _stream_of(dev)
@@ -470,12 +466,16 @@ def fp8_linear_backward(dy: torch.Tensor, x: torch.Tensor | None, wt: torch.Tens
                 raise ValueError(f"fp8_linear_backward: {status_string(ERR_SHAPE)}")
             _keep_size(key, need)
         ws, ws_bytes = _workspace(device, stream, need, "linear_grad").data_ptr(), need
-    st = _call(dev, L.fp8_linear_backward, dy.data_ptr(), _ptr(x) if want_dw else None,
-               _ptr(wt) if want_dx else None, fw, _ptr(wt_scale) if want_dx else None, _ptr(z), act,
+    st = _call(dev, L.fp8_linear_backward, dy.data_ptr(), _ptr(x), _ptr(wt), fw, _ptr(wt_scale), _ptr(z), act,
                _ptr(dx), _ptr(dw), _ptr(db), M, N, K, stream, ws, ws_bytes)
     if st != OK:
         _mm_error("fp8_linear_backward", st)
     return dx, dw, db
+
+
+def _bf16_matrix(name: str, t: torch.Tensor, shape: tuple) -> None:
+    if t.dtype != torch.bfloat16 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous bf16 {shape[0]} x {shape[1]} tensor")
 
 
 def _activation(activation) -> int:
@@ -595,30 +595,33 @@ def fp8_layer_norm(x: torch.Tensor, w: torch.Tensor | None = None, b: torch.Tens
     that holds a NaN or an infinity gives NaN in all of its outputs."""
     _ln_matrix(x, "x")
     rows, cols = x.shape
+    given = isinstance(y, torch.Tensor)
     if cols == 0:
         raise ValueError("x needs at least one column")
-    if fmt is not None and fmt not in _FORMATS:
+    if fmt is None:
+        if q is not None or scale is not None:
+            raise ValueError("q and scale need fmt")
+        if y is False:
+            raise ValueError("nothing to compute: y=False and fmt=None")
+    elif fmt not in _FORMATS:
         raise ValueError(f"fmt must be 'e4m3fn', 'e5m2' or None, got {fmt!r}")
-    if isinstance(y, torch.Tensor):
-        _ln_matrix(y, "y", x)
-    elif y not in (True, False):
-        raise ValueError("y must be True, False or a tensor to write")
-    if y is False and fmt is None:
-        raise ValueError("nothing to compute: y=False and fmt=None")
-    if fmt is None and (q is not None or scale is not None):
-        raise ValueError("q and scale need fmt")
-    if fmt is not None and cols % 16 != 0:
+    elif cols % 16 != 0:
         raise ValueError(f"codes need a number of columns that is a multiple of 16, got {cols}")
-    if not (math.isfinite(eps) and eps >= 0):
+    if not 0 <= eps < math.inf:
         raise ValueError(f"eps must be finite and not negative, got {eps}")
     dev = x.get_device()
     pw, pb = _ln_param(w, "w", cols, dev), _ln_param(b, "b", cols, dev)
-    if pw >= 0 and pb >= 0 and pw != pb:
+    if pw != pb and pw >= 0 and pb >= 0:
         raise ValueError("w and b must have one type")
     pdt = pw if pw >= 0 else pb if pb >= 0 else 1
-    _check_devices(dev, (("q", q), ("scale", scale), ("y", y if isinstance(y, torch.Tensor) else None)))
+    if given:
+        _ln_matrix(y, "y", x)
+    elif y is not True and y is not False:
+        raise ValueError("y must be True, False or a tensor to write")
+    if given or q is not None or scale is not None:
+        _check_devices(dev, (("q", q), ("scale", scale), ("y", y if given else None)))
     device = x.device
-    out = y if isinstance(y, torch.Tensor) else torch.empty_like(x) if y else None
+    out = y if given else torch.empty_like(x) if y else None
     f = 0
     if fmt is not None:
         f = _FORMATS[fmt]

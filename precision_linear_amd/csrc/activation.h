@@ -84,8 +84,9 @@ __device__ __forceinline__ float activate(float z) {
     }
 }
 
-// Beyond |z| = 16 the smooth slopes are 0 or 1 in fp32; their terms with a
-// factor z are left out there, so that they cannot turn into inf * 0.
+// Beyond |z| = 16 the gelus' slopes are 0 or 1 in fp32, beyond 88 silu's; their
+// terms with a factor z are bounded or left out there, so that they cannot turn
+// into inf * 0.
 template <int ACT>
 __device__ __forceinline__ float slope(float z) {
     if constexpr (ACT == kActRelu) {
@@ -93,8 +94,8 @@ __device__ __forceinline__ float slope(float z) {
     } else if constexpr (ACT == kActGelu) {
         const float e = bell(z);
         const float q = normal_tail<true>(fabsf(z)) * e;
-        const float phi = z > 0.f ? 1.f - q : z <= 0.f ? q : z;
-        return fabsf(z) < 16.f ? fmaf(z * kInvSqrt2Pi, e, phi) : phi;
+        const float phi = z > 0.f ? 1.f - q : q;                      // (NaN for a NaN)
+        return fmaf(fminf(fmaxf(z, -16.f), 16.f) * kInvSqrt2Pi, e, phi);   // e is 0 from |z| = 16 on
     } else if constexpr (ACT == kActGeluTanh) {
         const float z2 = z * z;
         const float p = logistic(z * fmaf(kTanhA2 * kTanhB * kLog2E, z2, kTanhA2 * kLog2E));
