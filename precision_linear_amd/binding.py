@@ -3,7 +3,8 @@
 Every step of the multiply runs in the HIP library; this module turns torch
 tensors into device pointers, sizes and the current stream, and turns
 status codes into exceptions.  A missing library is an error (there is no
-fallback path).
+fallback path).  The ordinary calls of the layer norm and the linear layer go
+through _calls (csrc/torch_calls.cpp), which does the same with less host time.
 """
 from __future__ import annotations
 
@@ -14,6 +15,11 @@ import math
 import os
 
 import torch
+
+try:
+    from . import _calls
+except ImportError as e:      # (lib() raises it)
+    _calls, _calls_error = None, e
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(HERE, "libfp8_scaled_mm.so")
@@ -65,6 +71,12 @@ _LN_ARG_ERRORS = {LN_ERR_NULL, LN_ERR_SHAPE, LN_ERR_ALIGN, LN_ERR_DTYPE, LN_ERR_
                   LN_ERR_VALUE}
 
 
+# The entry points that _calls uses, in its order.
+_CALLS_ENTRIES = ("fp8_layer_norm", "fp8_layer_norm_backward", "fp8_layer_norm_backward_workspace_size",
+                  "fp8_linear", "fp8_scaled_mm_workspace_size", "fp8_linear_backward",
+                  "fp8_linear_backward_workspace_size")
+
+
 class Fp8MMError(RuntimeError):
     def __init__(self, status: int):
         self.status = status
@@ -81,6 +93,9 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(
                 f"{library_path} is missing: build it with "
                 "`python -m precision_linear_amd.build` (there is no non-HIP fallback)")
+        if _calls is None:
+            raise RuntimeError("the extension _calls does not load: build it with "
+                               "`python -m precision_linear_amd.build`") from _calls_error
         L = ctypes.CDLL(library_path)
         vp, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
         L.fp8_scaled_mm.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, vp]
@@ -142,6 +157,8 @@ def lib() -> ctypes.CDLL:
         L.fp8_layer_norm_backward_workspace_size.restype = i64
         L.fp8_layer_norm_status_string.argtypes = [i32]
         L.fp8_layer_norm_status_string.restype = ctypes.c_char_p
+        _calls.use_library(tuple(ctypes.cast(getattr(L, name), ctypes.c_void_p).value
+                                 for name in _CALLS_ENTRIES), _workspace)
         _lib = L
     return _lib
 
@@ -363,6 +380,13 @@ def fp8_linear(a: torch.Tensor, b: torch.Tensor, scale_a: torch.Tensor, scale_b:
     bf16(z), which fp8_linear_backward takes.  Operands, formats, plans and
     workspaces are fp8_scaled_mm's (stream-K plans take no epilogue)."""
     act = _activation(activation)
+    if (_calls is not None and out is None and config == -1 and splits == 0 and workspace is None
+            and a_format is None and b_format is None and isinstance(mode, (str, int))):
+        got = _calls.linear(a, b, scale_a, scale_b, bias, residual, act, preact, _MODES.get(mode, -1))
+        if got.__class__ is tuple:
+            return got[0]
+        if got is not None:
+            _mm_error("fp8_linear", got)
     a, fa, b, fb, out, M, N, K, m, dev = _mm_args(a, b, scale_a, scale_b, bias, out, mode, workspace,
                                                   a_format, b_format,
                                                   (("residual", residual), ("preact", preact)))
@@ -400,6 +424,12 @@ def fp8_linear_backward(dy: torch.Tensor, x: torch.Tensor | None, wt: torch.Tens
     live in `workspace` (a GPU byte tensor, zero-filled before its first use) or
     in one that this module keeps per stream."""
     act = _activation(activation)
+    if _calls is not None and dx is dw is dbias is True and workspace is None and wt_format is None:
+        got = _calls.linear_backward(dy, x, wt, wt_scale, z, act)
+        if got.__class__ is tuple:
+            return got
+        if got is not None:
+            _mm_error("fp8_linear_backward", got)
     want_dx, want_dw = dx is not False, dw is not False
     out_dx, out_dw = want_dx and dx is not True, want_dw and dw is not True      # buffers given
     if (out_dx and not isinstance(dx, torch.Tensor)) or (out_dw and not isinstance(dw, torch.Tensor)):
@@ -541,6 +571,7 @@ def fp8_quantize(x: torch.Tensor, mode="rowwise", q: torch.Tensor | None = None,
 _LN_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 
 LayerNormResult = collections.namedtuple("LayerNormResult", "y q scale mean rstd")
+_result = tuple.__new__
 
 
 def _ptr(t):
@@ -593,6 +624,12 @@ def fp8_layer_norm(x: torch.Tensor, w: torch.Tensor | None = None, b: torch.Tens
     (then cols must be a multiple of 16); stats=True returns mean and rstd,
     which fp8_layer_norm_backward takes.  The codes come from the fp32 y.  A row
     that holds a NaN or an infinity gives NaN in all of its outputs."""
+    if _calls is not None and q is None and scale is None:
+        got = _calls.layer_norm(x, w, b, eps, y, -1 if fmt is None else _FORMATS.get(fmt, -2), stats)
+        if got.__class__ is tuple:
+            return _result(LayerNormResult, got)
+        if got is not None:
+            _ln_error("fp8_layer_norm", got)
     _ln_matrix(x, "x")
     rows, cols = x.shape
     given = isinstance(y, torch.Tensor)
@@ -656,6 +693,12 @@ def fp8_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tenso
     may be passed to reuse a buffer), dw and db are fp32.  The partial column
     sums go to `workspace` (a GPU byte tensor) or to one that this module keeps
     per stream.  The sums' order is fixed: equal calls give equal bits."""
+    if _calls is not None and dx is None and workspace is None:
+        got = _calls.layer_norm_backward(dy, x, mean, rstd, w, residual_grad)
+        if got.__class__ is tuple:
+            return got
+        if got is not None:
+            _ln_error("fp8_layer_norm_backward", got)
     _ln_matrix(x, "x")
     _ln_matrix(dy, "dy", x)
     rows, cols = x.shape

@@ -1,5 +1,6 @@
 """Builds libfp8_scaled_mm.so (the HIP kernels -- scaled multiply,
-quantiser, layer norm and linear layer -- and their C ABI) for gfx950.
+quantiser, layer norm and linear layer -- and their C ABI) for gfx950, and
+_calls.so (the binding's short calls into it, host code).
 
 hipcc cross-compiles without a GPU.  The library is written next to this
 file so that it travels with the source tree.
@@ -24,6 +25,9 @@ HEADERS = [os.path.join(HERE, "csrc", f) for f in
            ("fp8_gemm_kernels.h", "fp8_convert.h", "lane_ops.h", "activation.h", "fp8_pair.h",
             "plan_cost_table.h")]
 LIB = os.path.join(HERE, "libfp8_scaled_mm.so")
+# The binding's short calls from torch tensors to the C ABI (host code only).
+CALLS_SRC = os.path.join(HERE, "csrc", "torch_calls.cpp")
+CALLS = os.path.join(HERE, "_calls.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
@@ -53,6 +57,20 @@ SANITIZE_HOST = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize
 HOST_LOGIC_SRCS = {"fp8_scaled_mm.hip", "fp8_quantize.hip", "fp8_layer_norm.hip", "fp8_linear_grad.hip"}
 
 
+def _calls_command(out):
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return [HIPCC, "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-isystem", os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(HIPCC))), "include"),
+            *(f"-I{p}" for p in include_paths()), f"-I{sysconfig.get_paths()['include']}", CALLS_SRC,
+            f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip", "-ltorch_hip",
+            "-o", out]
+
+
 def build(verbose: bool = False, sanitize: bool = False, out: str | None = None) -> str:
     """Compile every source to an object (in parallel), then link the
     shared library; always rebuilds.  sanitize=True builds the host logic
@@ -67,12 +85,17 @@ def build(verbose: bool = False, sanitize: bool = False, out: str | None = None)
         for src, obj in zip(SRCS, objs):
             extra = SANITIZE_HOST if sanitize and os.path.basename(src) in HOST_LOGIC_SRCS else []
             jobs.append([HIPCC, *FLAGS, *extra, "-c", src, "-o", obj])
+        calls = os.path.join(objdir, "_calls.so")
+        if out is None:
+            jobs.insert(0, _calls_command(calls))
         workers = max(1, min(len(jobs), os.cpu_count() or 1))
         with ThreadPoolExecutor(max_workers=workers) as ex:
             list(ex.map(lambda c: _run(c, verbose), jobs))
         tmp = target + ".tmp"
         _run([HIPCC, "--offload-arch=gfx950", "-shared", *objs, "-o", tmp], verbose)
         shutil.move(tmp, target)
+        if out is None:
+            shutil.move(calls, CALLS)
     finally:
         shutil.rmtree(objdir, ignore_errors=True)
     return target
