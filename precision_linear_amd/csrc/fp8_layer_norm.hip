@@ -16,10 +16,22 @@
 // Rows that do not start on a 16-byte boundary (cols % 8 != 0) are read and
 // written with the same 16-byte instructions: global memory takes any 2-byte
 // aligned address.
+//
+// Non-temporal hints: bf16 calls that move more than the memory-side cache holds
+// take them on the loads, on the codes and, in long rows, on dx; each load and
+// store was measured on its own.  us on one MI355X, without and with: forward
+// with y and codes 16384 x 8192 134 and 126, 32768 x 4096 142 and 112, 65536 x
+// 1024 64 and 59; y alone 16384 x 8192 97 and 83; gradient with a residual 16384
+// x 8192 201 and 183, 65536 x 1024 108 and 93.  With the hint on y as well the
+// forward's gain is lost (32768 x 4096 137, y alone 89).  Smaller calls find
+// their inputs in the cache and lose with it (4095 x 4097 14.5 and 20.0).  fp32
+// loses too (gradient 8192 x 8192 198 and 212): a lane's two 16-byte halves lie
+// in lines that it shares with its neighbours.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/fp8_layer_norm.h"
 #include "fp8_convert.h"
@@ -110,7 +122,7 @@ __device__ __forceinline__ float row_scale(float amax, float rstd) {
 //   M2 = sum_w( M2_w + n_w (mean_w - mean)^2 )
 // (T. Chan, G. Golub, R. LeVeque, 1979), which costs one meeting of the waves
 // and loses nothing to a mean far from 0.
-template <class T, bool WIDE>
+template <class T, bool WIDE, bool NT>
 __global__ void __launch_bounds__(kMaxWaves* kWaveSize)
 ln_forward_kernel(LnFwd p) {
     __shared__ float2 s_mom[2][kMaxWaves];
@@ -148,7 +160,7 @@ ln_forward_kernel(LnFwd p) {
         const T* xr = x + r * p.cols;
 #pragma unroll
         for (int v = 0; v < kVecs; ++v)
-            if (ok[v]) next[v].load(xr + (t + v * tw) * 8);
+            if (ok[v]) next[v].template load<NT>(xr + (t + v * tw) * 8);
         if (has_tail) next_t = load1(xr + ct);
     };
 #pragma unroll
@@ -245,7 +257,8 @@ ln_forward_kernel(LnFwd p) {
                 const Div d = make_div(sc);
 #pragma unroll
                 for (int v = 0; v < kVecs; ++v)
-                    if (ok[v]) *reinterpret_cast<u32x2*>(qr + (t + v * tw) * 8) = codes8<FMT>(f[v], d);
+                    if (ok[v])
+                        store_hinted<NT>(reinterpret_cast<u32x2*>(qr + (t + v * tw) * 8), codes8<FMT>(f[v], d));
             };
             if (p.q_format == FP8LN_E4M3FN) write(std::integral_constant<int, 0>{});
             else write(std::integral_constant<int, 1>{});
@@ -402,9 +415,12 @@ struct Share {
     __device__ __forceinline__ int col(int v) const { return (t + v * tw) * 8; }
 };
 
+// Which of a gradient's accesses take the non-temporal hint.
+enum Stream { kStreamNone = 0, kStreamLoads = 1, kStreamAll = 2 };
+
 // The rows blk * subs, + blocks * subs, ... of dx, `subs` rows at a time, W waves
 // each.  SUMS: dw and db over these rows are added to the sums given.
-template <class T, int V, bool SUMS>
+template <class T, int V, bool SUMS, int NT>
 __device__ __forceinline__ void backward_rows(const LnBwd& p, const Share<V>& c, int blk, int blocks,
                                               float (&dw)[V][8], float (&db)[V][8], float& dwt, float& dbt) {
     __shared__ float2 s_sum[2][kMaxWaves];
@@ -450,9 +466,9 @@ __device__ __forceinline__ void backward_rows(const LnBwd& p, const Share<V>& c,
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 if (c.ok[v]) {
-                    rx[v].load(x + off + c.col(v));
-                    rdy[v].load(dy + off + c.col(v));
-                    if (kResEarly && res) rr[v].load(res + off + c.col(v));
+                    rx[v].template load<NT != kStreamNone>(x + off + c.col(v));
+                    rdy[v].template load<NT != kStreamNone>(dy + off + c.col(v));
+                    if (kResEarly && res) rr[v].template load<NT != kStreamNone>(res + off + c.col(v));
                 }
             if (c.has_tail) {
                 xt = load1(x + off + c.tail);
@@ -501,7 +517,7 @@ __device__ __forceinline__ void backward_rows(const LnBwd& p, const Share<V>& c,
         if (!kResEarly && res)
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                if (c.ok[v]) rr[v].load(res + off + c.col(v));
+                if (c.ok[v]) rr[v].template load<NT != kStreamNone>(res + off + c.col(v));
 #pragma unroll
         for (int v = 0; v < V; ++v)
             if (c.ok[v]) {
@@ -512,7 +528,7 @@ __device__ __forceinline__ void backward_rows(const LnBwd& p, const Share<V>& c,
                     const float g = rdy[v].get(i) * w[v][i];
                     f[i] = fmaf(rstd, g - c1 - xh * c2, rr[v].get(i));
                 }
-                store8(dx + off + c.col(v), f);
+                store8<NT == kStreamAll>(dx + off + c.col(v), f);
             }
         if (c.has_tail) store1(dx + off + c.tail, fmaf(rstd, dyt * wt - c1 - xht * c2, rt));
     }
@@ -521,7 +537,7 @@ __device__ __forceinline__ void backward_rows(const LnBwd& p, const Share<V>& c,
 // dx, and this workgroup's share of dw and db: the sums over a workgroup's rows
 // stay in registers and meet in LDS at the end (a fixed tree over the subs), so
 // a workgroup writes one partial row.
-template <class T, int V>
+template <class T, int V, int NT>
 __global__ void __launch_bounds__(kMaxWaves* kWaveSize)
 ln_backward_kernel(LnBwd p) {
     extern __shared__ float4 s_cols[];            // [subs / 2][dw, db][V][2][lanes of a row]
@@ -535,7 +551,7 @@ ln_backward_kernel(LnBwd p) {
     for (int v = 0; v < V; ++v)
 #pragma unroll
         for (int i = 0; i < 8; ++i) dw[v][i] = db[v][i] = 0.f;
-    backward_rows<T, V, true>(p, c, blockIdx.x, gridDim.x, dw, db, dwt, dbt);
+    backward_rows<T, V, true, NT>(p, c, blockIdx.x, gridDim.x, dw, db, dwt, dbt);
 
     // Join the subs: the upper half of them hands its sums to the lower half.
     // Lane t's four values of a vector's half h lie at [v][h][t]: no two lanes
@@ -632,7 +648,7 @@ ln_backward_few_kernel(LnBwd p, int row_blocks, float* dw_out, float* db_out) {
         const int tw = p.waves * kWaveSize;
         const Share<V> c((int)threadIdx.x % tw, tw, (int)p.cols);
         float dw[V][8], db[V][8], dwt, dbt;   // (not touched)
-        backward_rows<T, V, false>(p, c, blockIdx.x, row_blocks, dw, db, dwt, dbt);
+        backward_rows<T, V, false, kStreamNone>(p, c, blockIdx.x, row_blocks, dw, db, dwt, dbt);
         return;
     }
     const int cx = threadIdx.x % 16, slice = threadIdx.x / 16, slices = blockDim.x / 16;
@@ -848,6 +864,14 @@ int64_t grad_workspace(int64_t rows, int64_t cols) {
     return 2 * min64(rows, cols <= kHeldCols ? kGradWorkgroups : kLongParts) * pitch * (int64_t)sizeof(float);
 }
 
+template <bool WIDE>
+void launch_forward(const LnFwd& p, int dtype, dim3 grid, dim3 block, hipStream_t hs) {
+    const int64_t bytes = p.rows * p.cols * (2 + (p.y ? 2 : 0) + (p.q ? 1 : 0));   // (bf16)
+    if (dtype == FP8LN_FP32) hipLaunchKernelGGL((ln_forward_kernel<float, WIDE, false>), grid, block, 0, hs, p);
+    else if (bytes > kCachedBytes) hipLaunchKernelGGL((ln_forward_kernel<bf16_t, WIDE, true>), grid, block, 0, hs, p);
+    else hipLaunchKernelGGL((ln_forward_kernel<bf16_t, WIDE, false>), grid, block, 0, hs, p);
+}
+
 template <class T, int V>
 void launch_backward(const LnBwd& p, const GradPlan& g, float* dw, float* db, hipStream_t hs) {
     const dim3 block(g.waves * g.subs * kWaveSize);
@@ -858,7 +882,14 @@ void launch_backward(const LnBwd& p, const GradPlan& g, float* dw, float* db, hi
         return;
     }
     const unsigned lds = (unsigned)(g.subs / 2 * 4 * V * g.waves * kWaveSize * sizeof(float4));
-    hipLaunchKernelGGL((ln_backward_kernel<T, V>), dim3((unsigned)g.parts), block, lds, hs, p);
+    const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3((unsigned)g.parts), block, lds, hs, p); };
+    if constexpr (std::is_same_v<T, bf16_t>) {
+        // dx too where a row is long (16384 x 8192 183 us against 198 with the
+        // hint on the loads alone, 32768 x 2048 77 against 74).
+        if (p.rows * p.cols * (p.res ? 4 : 3) * (int64_t)sizeof(T) > kCachedBytes)
+            return p.cols >= 4096 ? go(ln_backward_kernel<T, V, kStreamAll>) : go(ln_backward_kernel<T, V, kStreamLoads>);
+    }
+    go(ln_backward_kernel<T, V, kStreamNone>);
 }
 
 }  // namespace
@@ -896,16 +927,10 @@ int fp8_layer_norm(const void* x, int dtype, const void* w, const void* b, int p
     } else if (p.waves == 1) {
         constexpr int kRows = 4;   // waves, and so rows, per workgroup
         const dim3 grid((unsigned)min64(ceil_div(rows, kRows), (int64_t)cus * 4));
-        if (dtype == FP8LN_BF16)
-            hipLaunchKernelGGL((ln_forward_kernel<bf16_t, false>), grid, dim3(kRows * kWaveSize), 0, hs, p);
-        else
-            hipLaunchKernelGGL((ln_forward_kernel<float, false>), grid, dim3(kRows * kWaveSize), 0, hs, p);
+        launch_forward<false>(p, dtype, grid, dim3(kRows * kWaveSize), hs);
     } else {
         const dim3 grid((unsigned)min64(rows, (int64_t)cus * (kMaxWaves / p.waves)));
-        if (dtype == FP8LN_BF16)
-            hipLaunchKernelGGL((ln_forward_kernel<bf16_t, true>), grid, dim3(p.waves * kWaveSize), 0, hs, p);
-        else
-            hipLaunchKernelGGL((ln_forward_kernel<float, true>), grid, dim3(p.waves * kWaveSize), 0, hs, p);
+        launch_forward<true>(p, dtype, grid, dim3(p.waves * kWaveSize), hs);
     }
     if (hipGetLastError() != hipSuccess) return FP8LN_ERR_LAUNCH;
     return FP8LN_OK;

@@ -72,7 +72,7 @@ __device__ __forceinline__ void dz8(const Raw8<bf16_t>& dy, const Raw8<bf16_t>& 
 
 // Pass 1.  Workgroup: 128 columns of one strip of rows, of dz or (the last
 // blocks) of x.  16 lanes hold a row's 128 columns, 16 rows at a time.
-template <int ACT>
+template <int ACT, bool NT>
 __global__ void __launch_bounds__(kThreadsG)
 grad_stats_kernel(Grad p) {
     __shared__ float s_max[kRowLanes][kTileCols], s_sum[kRowLanes][kTileCols];
@@ -97,8 +97,8 @@ grad_stats_kernel(Grad p) {
             a[u].zero();
             b[u].zero();
             if (ok && row < r1) {
-                a[u].load((is_x ? p.x : p.dy) + row * width + col);
-                if (ACT != kActNone && !is_x) b[u].load(p.z + row * width + col);
+                a[u].template load<NT>((is_x ? p.x : p.dy) + row * width + col);
+                if (ACT != kActNone && !is_x) b[u].template load<NT>(p.z + row * width + col);
             }
         }
 #pragma unroll
@@ -249,7 +249,7 @@ __device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); 
 __device__ __forceinline__ float added(float a, float b) { return a + b; }
 
 // ROWS: 128, or 64 (half the work a workgroup) where the grid is small.
-template <int ACT, bool JOIN, int ROWS>
+template <int ACT, bool JOIN, int ROWS, bool NT>
 __global__ void __launch_bounds__(kThreadsG)
 grad_quantize_kernel(Grad p) {
     constexpr int kChunks = ROWS / 16;           // of a transposed row
@@ -280,8 +280,8 @@ grad_quantize_kernel(Grad p) {
             a[it][k].zero();
             b[it][k].zero();
             if (ok && r + k < p.M) {
-                a[it][k].load((is_x ? p.x : p.dy) + (r + k) * width + col);
-                if (ACT != kActNone && !is_x) b[it][k].load(p.z + (r + k) * width + col);
+                a[it][k].template load<NT>((is_x ? p.x : p.dy) + (r + k) * width + col);
+                if (ACT != kActNone && !is_x) b[it][k].template load<NT>(p.z + (r + k) * width + col);
             }
         }
     };
@@ -368,7 +368,7 @@ grad_quantize_kernel(Grad p) {
                         codes[h] = (uint32_t)Fp8Fmt<1>::cvt_pk<true>(t[4 * h + 2], t[4 * h + 3], w);
                     }
                     if (ok && r + k < p.M)
-                        *reinterpret_cast<u32x2*>(p.q_rows + (r + k) * p.N + col) = codes;
+                        store_hinted<NT>(reinterpret_cast<u32x2*>(p.q_rows + (r + k) * p.N + col), codes);
                 }
             }
 #pragma unroll
@@ -488,10 +488,14 @@ GradSpace grad_space(int64_t M, int64_t N, int64_t K, bool want_dx, bool want_dw
 // Tiles of 128 rows below which 64 rows a workgroup are faster.
 constexpr int64_t kSmallGrid = 512;
 
-template <int ACT>
+// NT: for inputs beyond the memory-side cache, which pass 3 would not find there
+// (the whole gradient of 4096 x 28672 x 8192 on one MI355X, us without and with:
+// gelu 1631 and 1612, relu 1572 and 1545; where they fit, 1000 x 4000 x 2000,
+// 50.0 and 51.5).
+template <int ACT, bool NT>
 void launch_passes(const Grad& p, hipStream_t hs) {
     const int per = p.blocks_n + p.blocks_k;
-    hipLaunchKernelGGL(grad_stats_kernel<ACT>, dim3((unsigned)(p.parts * per)), dim3(kThreadsG), 0, hs, p);
+    hipLaunchKernelGGL((grad_stats_kernel<ACT, NT>), dim3((unsigned)(p.parts * per)), dim3(kThreadsG), 0, hs, p);
     const bool join = joins(p);
     if (!join || !(p.want_rows || p.want_cols)) {
         const int rows = p.want_rows ? (int)up(p.M, 64) : 0, cols = (int)up(p.N, 64);
@@ -503,11 +507,18 @@ void launch_passes(const Grad& p, hipStream_t hs) {
     const int64_t tiles = up(p.M, kTileRows) * per;
     const dim3 block(kThreadsG);
     if (!join)
-        hipLaunchKernelGGL((grad_quantize_kernel<ACT, false, kTileRows>), dim3((unsigned)tiles), block, 0, hs, p);
+        hipLaunchKernelGGL((grad_quantize_kernel<ACT, false, kTileRows, NT>), dim3((unsigned)tiles), block, 0, hs, p);
     else if (tiles >= kSmallGrid)
-        hipLaunchKernelGGL((grad_quantize_kernel<ACT, true, kTileRows>), dim3((unsigned)tiles), block, 0, hs, p);
+        hipLaunchKernelGGL((grad_quantize_kernel<ACT, true, kTileRows, NT>), dim3((unsigned)tiles), block, 0, hs, p);
     else
-        hipLaunchKernelGGL((grad_quantize_kernel<ACT, true, 64>), dim3((unsigned)(up(p.M, 64) * per)), block, 0, hs, p);
+        hipLaunchKernelGGL((grad_quantize_kernel<ACT, true, 64, false>), dim3((unsigned)(up(p.M, 64) * per)), block, 0, hs, p);
+}
+
+template <int ACT>
+void launch_passes(const Grad& p, hipStream_t hs) {
+    const int64_t bytes = 2 * p.M * ((ACT == kActNone ? 1 : 2) * p.N + (p.blocks_k ? p.K : 0));
+    if (bytes > kCachedBytes) launch_passes<ACT, true>(p, hs);
+    else launch_passes<ACT, false>(p, hs);
 }
 
 }  // namespace

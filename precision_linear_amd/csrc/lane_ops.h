@@ -19,11 +19,29 @@ typedef uint16_t bf16_t;
 
 // ------------------------------------------------------------ elements ---
 
+// Memory that a launch reads or writes once, more of it than the 256 MB of the
+// memory-side cache: with the non-temporal hint (NT) it does not push out of the
+// L2 what the launch still needs, or what it has yet to write back whole.
+constexpr int64_t kCachedBytes = int64_t(256) << 20;
+template <bool NT, class V, class P>
+__device__ __forceinline__ V load_hinted(const P* p) {
+    if constexpr (NT) return __builtin_nontemporal_load(p);
+    else return *p;
+}
+template <bool NT, class V, class P>
+__device__ __forceinline__ void store_hinted(P* p, V v) {
+    if constexpr (NT) __builtin_nontemporal_store(v, p);
+    else *p = v;
+}
+
 // 8 consecutive elements as they lie in memory.
 template <class T> struct Raw8;
 template <> struct Raw8<bf16_t> {
     u32x4 v;
-    __device__ __forceinline__ void load(const bf16_t* p) { v = *reinterpret_cast<const u32x4_a2*>(p); }
+    template <bool NT = false>
+    __device__ __forceinline__ void load(const bf16_t* p) {
+        v = load_hinted<NT, u32x4>(reinterpret_cast<const u32x4_a2*>(p));
+    }
     __device__ __forceinline__ void zero() { v = u32x4{0u, 0u, 0u, 0u}; }
     __device__ __forceinline__ float get(int i) const {
         const uint32_t w = v[i / 2];
@@ -32,7 +50,9 @@ template <> struct Raw8<bf16_t> {
 };
 template <> struct Raw8<float> {
     u32x4 v[2];
+    template <bool NT = false>
     __device__ __forceinline__ void load(const float* p) {
+        static_assert(!NT, "a lane's two halves share lines with its neighbours': the hint would drop them half used");
         v[0] = *reinterpret_cast<const u32x4_a4*>(p);
         v[1] = *reinterpret_cast<const u32x4_a4*>(p + 4);
     }
@@ -50,11 +70,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{lo, hi}, bf2));
 }
 
+template <bool NT = false>
 __device__ __forceinline__ void store8(bf16_t* p, const float (&f)[8]) {
-    *reinterpret_cast<u32x4_a2*>(p) = u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
-                                            pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])};
+    store_hinted<NT>(reinterpret_cast<u32x4_a2*>(p), u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
+                                                           pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])});
 }
+template <bool NT = false>
 __device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
+    static_assert(!NT, "as for the loads");
 #pragma unroll
     for (int h = 0; h < 2; ++h)
         *reinterpret_cast<u32x4_a4*>(p + 4 * h) =
