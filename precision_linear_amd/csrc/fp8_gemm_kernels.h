@@ -1794,7 +1794,13 @@ __device__ __forceinline__ void pp_epi_write(const pp::acc_t (&z)[pp::FN][kPpBan
             // No scalar offset: with one, the compiler leaves out the wait that a
             // store of more than 8 bytes needs before a VALU instruction may write
             // its first data register, and wrong values were stored.
-            __builtin_amdgcn_raw_buffer_store_b128(v, r, off + pass * 8 * p.N * 2, 0, 0);
+            // Non-temporal: the two outputs' bytes do not push A and B out of the L2
+            // (us on one MI355X without and with: 4096 x 28672 x 8192, gelu_tanh and
+            // pre-activation, 731 and 703; 8192 x 16384 x 4096 with both and the
+            // residual 548 and 516; 4096 x 4096 x 4096 62 and 61; a quantisation
+            // that reads the outputs next is as fast after either).
+            constexpr int kNonTemporal = 2;
+            __builtin_amdgcn_raw_buffer_store_b128(v, r, off + pass * 8 * p.N * 2, 0, kNonTemporal);
         }
         return;
     }
