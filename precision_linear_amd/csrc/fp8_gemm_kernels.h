@@ -55,6 +55,7 @@ struct Params {
     int rowwise;
     int vec_store;         // N % 4 == 0 and out 8-byte aligned
     int vec16;             // N % 8 == 0 and out 16-byte aligned
+    int stream_out;        // A, B and out are more than the memory-side cache holds, N <= kStreamCols
     // Split-K: each output tile is computed by `splits` work units, unit s
     // covering K slices [s*k_chunk, (s+1)*k_chunk).  With splits > 1 the fp32
     // partial tiles go to `partials` and the unit that arrives last at the
@@ -1655,6 +1656,27 @@ __device__ __forceinline__ void pp_tile_start(uint8_t* smem, const Params& p, co
     if (T.n > 1) pp_load_a_half<false>(smem, 1, q, pp_slice(T, 1), T.ra, L, p.K);
 }
 
+// The 32 x 64 outputs staged in `stg` (pp_store_staged's layout), whose first is
+// out[m0][n0], stored with the non-temporal hint.  Through a buffer: 32-bit
+// offsets (N <= kStreamCols), and the hint is the instruction's own (on a plain
+// store, the compiler drops it where it merges two branches' stores).
+constexpr int kStreamCols = 1 << 22;
+__device__ __forceinline__ void pp_stream_band(uint16_t* out, const Params& p, int m0, int n0, int lane,
+                                               const uint8_t* stg) {
+    const __amdgpu_buffer_rsrc_t r = make_rsrc(out + (size_t)m0 * p.N + n0, 32u * (uint32_t)p.N * 2u);
+    const int off = (lane / 8) * p.N * 2 + (lane % 8) * 16;
+#pragma unroll
+    for (int pass = 0; pass < 4; ++pass) {
+        const int rr = pass * 8 + lane / 8;
+        const v4u v = *reinterpret_cast<const v4u*>(stg + rr * 128 + (((lane % 8) ^ ((rr >> 1) & 7)) * 16));
+        // No scalar offset: with one, the compiler leaves out the wait that a
+        // store of more than 8 bytes needs before a VALU instruction may write
+        // its first data register, and wrong values were stored.
+        constexpr int kNonTemporal = 2;
+        __builtin_amdgcn_raw_buffer_store_b128(v, r, off + pass * 8 * p.N * 2, 0, kNonTemporal);
+    }
+}
+
 // Epilogue of wave (g, q) of the ping-pong kernel through a private 4 KiB LDS
 // area: each band of 32 x 64 outputs is written to LDS in the MFMA layout (a
 // lane holds runs of 4 consecutive columns of one row) and read back as 8 rows
@@ -1662,7 +1684,12 @@ __device__ __forceinline__ void pp_tile_start(uint8_t* smem, const Params& p, co
 // lines (instead of 32 pieces of 16 bytes).  LDS operations of one wave
 // complete in order, so no barrier is needed.  In the LDS area, 16-byte chunk c
 // of row r sits at c ^ ((r >> 1) & 7) (at most 2-way bank conflicts on the
-// writes).  Falls back to store_tile where the block is not wholly inside the
+// writes).  Large problems' outputs take non-temporal stores, which leave the L2
+// to A and B (us on one MI355X without and with: 4096 x 28672 x 8192 651 and 599,
+// 28672 x 8192 x 4096 655 and 637, 8192 x 28672 x 1024 223 and 213, 4096 x 8192 x
+// 28672 and 16384 x 16384 x 8192 the same within 0.4%; problems that the
+// memory-side cache holds lose 1 to 2%: 8192 x 8192 x 8192 334 and 337, 8192 x 8192
+// x 2048 101 and 103).  Falls back to store_tile where the block is not wholly inside the
 // output or 16-byte stores are not allowed.
 template <bool RW, bool BIAS>
 __device__ __forceinline__ void pp_store_staged(const pp::acc_t (&acc)[pp::FN][pp::FM],
@@ -1722,6 +1749,10 @@ __device__ __forceinline__ void pp_store_staged(const pp::acc_t (&acc)[pp::FN][p
                     *reinterpret_cast<uint2*>(stg + r * 128 + cpos * 16 + (cl % 8) * 2) = w;
                 }
         }
+        if (p.stream_out) {
+            pp_stream_band(p.out, p, row0 + mbase + band * 32, col0 + nbase, lane, stg);
+            continue;
+        }
 #pragma unroll
         for (int pass = 0; pass < 4; ++pass) {
             const int rr = pass * 8 + lane / 8;
@@ -1767,8 +1798,9 @@ __device__ __forceinline__ void pp_store(const pp::acc_t (&acc)[pp::FN][pp::FM],
 
 // The linear layer's epilogue of one wave (128 x 64 outputs), in bands of 32
 // rows (all 128 accumulators at once would spill): through the wave's staging
-// area as in pp_store_staged, then out through a buffer (32-bit offsets), or, where the block is not wholly inside the
-// output or 16-byte stores are not allowed, straight to memory, run by run.
+// area as in pp_store_staged, then out through a buffer, or, where the block is
+// not wholly inside the output or 16-byte stores are not allowed, straight to
+// memory, run by run.
 constexpr int kPpBandBlocks = 32 / pp::MI;   // MFMA row blocks per band
 
 __device__ __forceinline__ void pp_epi_write(const pp::acc_t (&z)[pp::FN][kPpBandBlocks], const Params& p,
@@ -1785,23 +1817,12 @@ __device__ __forceinline__ void pp_epi_write(const pp::acc_t (&z)[pp::FN][kPpBan
                 const int cpos = (cl / 8) ^ ((r >> 1) & 7);
                 *reinterpret_cast<uint2*>(stg + r * 128 + cpos * 16 + (cl % 8) * 2) = epi_pack(z[i][j], 0);
             }
-        const __amdgpu_buffer_rsrc_t r = make_rsrc(out + (size_t)m0 * p.N + n0, 32u * (uint32_t)p.N * 2u);
-        const int off = (lane / 8) * p.N * 2 + (lane % 8) * 16;
-#pragma unroll
-        for (int pass = 0; pass < 4; ++pass) {
-            const int rr = pass * 8 + lane / 8;
-            const v4u v = *reinterpret_cast<const v4u*>(stg + rr * 128 + (((lane % 8) ^ ((rr >> 1) & 7)) * 16));
-            // No scalar offset: with one, the compiler leaves out the wait that a
-            // store of more than 8 bytes needs before a VALU instruction may write
-            // its first data register, and wrong values were stored.
-            // Non-temporal: the two outputs' bytes do not push A and B out of the L2
-            // (us on one MI355X without and with: 4096 x 28672 x 8192, gelu_tanh and
-            // pre-activation, 731 and 703; 8192 x 16384 x 4096 with both and the
-            // residual 548 and 516; 4096 x 4096 x 4096 62 and 61; a quantisation
-            // that reads the outputs next is as fast after either).
-            constexpr int kNonTemporal = 2;
-            __builtin_amdgcn_raw_buffer_store_b128(v, r, off + pass * 8 * p.N * 2, 0, kNonTemporal);
-        }
+        // Non-temporal: the two outputs' bytes do not push A and B out of the L2
+        // (us on one MI355X without and with: 4096 x 28672 x 8192, gelu_tanh and
+        // pre-activation, 731 and 703; 8192 x 16384 x 4096 with both and the
+        // residual 548 and 516; 4096 x 4096 x 4096 62 and 61; a quantisation
+        // that reads the outputs next is as fast after either).
+        pp_stream_band(out, p, m0, n0, lane, stg);
         return;
     }
 #pragma unroll
@@ -1866,7 +1887,7 @@ __device__ __forceinline__ void pp_epi_store(const pp::acc_t (&acc)[pp::FN][pp::
                                              int row0, int col0, int mbase, int nbase,
                                              const float* epi_sa, const float* epi_sb,
                                              const uint16_t* epi_bias, uint8_t* stg) {
-    const bool full = p.vec16 && p.N <= (1 << 22) && row0 + mbase + 128 <= p.M &&
+    const bool full = p.vec16 && p.N <= kStreamCols && row0 + mbase + 128 <= p.M &&
                       col0 + nbase + 64 <= p.N;   // wave-uniform
 #define FP8MM_BANDS(FULL, RES) \
     pp_epi_bands<FULL, RES>(acc, p, row0, col0, mbase, nbase, epi_sa, epi_sb, epi_bias, stg)

@@ -499,6 +499,7 @@ Params base_params(const void* A, const void* B, const float* scale_a, const flo
     p.rowwise = mode == FP8MM_ROWWISE;
     p.vec_store = (N % 4 == 0) && aligned(out, 8);
     p.vec16 = (N % 8 == 0) && aligned(out, 16);
+    p.stream_out = N <= kStreamCols && M * K + N * K + 2 * M * N > (int64_t(256) << 20);
     p.splits = 1;
     p.k_chunk = p.k_iters;
     p.counters = nullptr;
