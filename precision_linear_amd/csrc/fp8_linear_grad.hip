@@ -71,15 +71,60 @@ __device__ __forceinline__ void dz8(const Raw8<bf16_t>& dy, const Raw8<bf16_t>& 
     for (int i = 0; i < 8; ++i) f[i] = dy.get(i) * slope<ACT>(z.get(i));
 }
 
+// The gelus' slopes from a table in LDS.  z has 16 bits, and the slope of -z is 1
+// less that of z, so the 1664 values of slope(t) - 1/2 for 2^-9 <= t < 16 are all
+// there is: below, it is sqrt(2 / pi) t (within 5e-9), above, 1/2 (in fp32).  Off by
+// two roundings more than slope() itself.  About 12 instructions for some 30, which
+// the passes are bound by where the caches feed them (the whole gradient on one
+// MI355X, gelu, us without and with: 4069 x 12720 x 176 176 and 169, 8192 x 4096 x
+// 1024 170 and 162, 4096 x 28672 x 8192 1583 and 1547; under 512 tiles of dz the
+// table's filling costs as much, 1024 x 2048 x 8192 64 and 65).
+template <int ACT> constexpr bool kHasTable = ACT == kActGelu || ACT == kActGeluTanh;
+constexpr uint32_t kTableFirst = 0x3b00, kTableEnd = 0x4180;   // bf16 2^-9 and 16
+constexpr int kTableSize = (int)(kTableEnd - kTableFirst);
+
+template <int ACT>
+__device__ __forceinline__ void fill_table(float* table) {
+    for (int i = threadIdx.x; i < kTableSize; i += kThreadsG)
+        table[i] = slope<ACT>(__uint_as_float((kTableFirst + (uint32_t)i) << 16)) - 0.5f;
+}
+
+__device__ __forceinline__ void dz8_table(const Raw8<bf16_t>& dy, const Raw8<bf16_t>& z, const float* table,
+                                          float (&f)[8]) {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 most{0, 0};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const u16x2 t = __builtin_bit_cast(u16x2, z.v[w] & 0x7fff7fffu);
+        most = __builtin_elementwise_max(most, t);
+        u16x2 at = __builtin_elementwise_sub_sat(t, u16x2{kTableFirst, kTableFirst});
+        at = __builtin_elementwise_min(at, u16x2{kTableSize - 1, kTableSize - 1});
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float v = z.get(2 * w + k);
+            const float h = fabsf(v) < 0x1p-9f ? fabsf(v) * (0.5f * kTanhA2) : table[at[k]];
+            f[2 * w + k] = dy.get(2 * w + k) * (0.5f + copysignf(h, v));
+        }
+    }
+    if (most[0] > 0x7f80 || most[1] > 0x7f80) {   // a NaN stays one
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float v = z.get(i);
+            f[i] = v != v ? v : f[i];
+        }
+    }
+}
+
 // Pass 1.  Workgroup: 128 columns of one strip of rows, of dz or (the last
 // blocks) of x.  16 lanes hold a row's 128 columns, 16 rows at a time.  4096 x
 // 28672 with 8192 columns of x: 126 us with gelu (4.3 TB/s; slope's arithmetic
 // and memory about even), 500 x 2048 with 2048 4.9 us.  512 columns a row
 // (whole waves, so that a row's maximum takes more lane exchanges) and strips of
 // 64 to 1024 rows measured no faster.
-template <int ACT, bool NT>
+template <int ACT, bool TABLE, bool NT>
 __global__ void __launch_bounds__(kThreadsG)
 grad_stats_kernel(Grad p) {
+    __shared__ float s_table[TABLE ? kTableSize : 1];
     __shared__ float s_max[kRowLanes][kTileCols], s_sum[kRowLanes][kTileCols];
     const int cl = threadIdx.x % kColLanes, rl = threadIdx.x / kColLanes;
     const int per_part = p.blocks_n + p.blocks_k;
@@ -91,6 +136,10 @@ grad_stats_kernel(Grad p) {
     const int64_t col = (int64_t)cb * kTileCols + cl * 8;
     const bool ok = col < width;                       // widths are multiples of 16
     const int64_t r1 = min(p.M, (part + 1) * p.strip);
+    if (TABLE && !is_x) {
+        fill_table<ACT>(s_table);
+        __syncthreads();
+    }
     float cmax[8], csum[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) cmax[i] = csum[i] = 0.f;
@@ -112,6 +161,8 @@ grad_stats_kernel(Grad p) {
             if (is_x) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) f[i] = a[u].get(i);
+            } else if constexpr (TABLE) {
+                dz8_table(a[u], b[u], s_table, f);
             } else {
                 dz8<ACT>(a[u], b[u], f);
             }
@@ -257,13 +308,14 @@ __device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); 
 __device__ __forceinline__ float added(float a, float b) { return a + b; }
 
 // ROWS: 128, or 64 (half the work a workgroup) where the grid is small.
-template <int ACT, bool JOIN, int ROWS, bool NT>
+template <int ACT, bool TABLE, bool JOIN, int ROWS, bool NT>
 __global__ void __launch_bounds__(kThreadsG)
 grad_quantize_kernel(Grad p) {
     constexpr int kChunks = ROWS / 16;           // of a transposed row
     __shared__ __attribute__((aligned(16))) uint32_t s_t[kTileCols][ROWS / 4];
     __shared__ __attribute__((aligned(16))) float s_col[2][kTileCols];   // scales, reciprocals
     __shared__ float s_row[2][ROWS];
+    __shared__ float s_table[TABLE ? kTableSize : 1];
     constexpr bool kExactDz = ACT == kActNone || ACT == kActRelu;
     const int cl = threadIdx.x % kColLanes, rl = threadIdx.x / kColLanes;
     const int per_strip = p.blocks_n + p.blocks_k;
@@ -294,6 +346,7 @@ grad_quantize_kernel(Grad p) {
         }
     };
     fetch(0);   // under way while the scales are found
+    if (TABLE && !is_x) fill_table<ACT>(s_table);
     {   // scales: the first 128 threads the columns', the others the rows'
         static_assert(kThreadsG >= kTileCols + ROWS, "one thread for each row and column");
         const int t = threadIdx.x % kTileCols;
@@ -362,7 +415,10 @@ grad_quantize_kernel(Grad p) {
             }
         } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) dz8<ACT>(a[it][k], b[it][k], f[k]);
+            for (int k = 0; k < 4; ++k) {
+                if constexpr (TABLE) dz8_table(a[it][k], b[it][k], s_table, f[k]);
+                else dz8<ACT>(a[it][k], b[it][k], f[k]);
+            }
             if (p.want_rows) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -500,10 +556,12 @@ constexpr int64_t kSmallGrid = 512;
 // (the whole gradient of 4096 x 28672 x 8192 on one MI355X, us without and with:
 // gelu 1631 and 1612, relu 1572 and 1545; where they fit, 1000 x 4000 x 2000,
 // 50.0 and 51.5).
-template <int ACT, bool NT>
+template <int ACT, bool TABLE, bool NT>
 void launch_passes(const Grad& p, hipStream_t hs) {
     const int per = p.blocks_n + p.blocks_k;
-    hipLaunchKernelGGL((grad_stats_kernel<ACT, NT>), dim3((unsigned)(p.parts * per)), dim3(kThreadsG), 0, hs, p);
+    const int64_t tiles = up(p.M, kTileRows) * per;
+    const dim3 block(kThreadsG);
+    hipLaunchKernelGGL((grad_stats_kernel<ACT, TABLE, NT>), dim3((unsigned)(p.parts * per)), block, 0, hs, p);
     const bool join = joins(p);
     if (!join || !(p.want_rows || p.want_cols)) {
         const int rows = p.want_rows ? (int)up(p.M, 64) : 0, cols = (int)up(p.N, 64);
@@ -512,21 +570,25 @@ void launch_passes(const Grad& p, hipStream_t hs) {
                            rows, cols);
     }
     if (!(p.want_rows || p.want_cols)) return;
-    const int64_t tiles = up(p.M, kTileRows) * per;
-    const dim3 block(kThreadsG);
     if (!join)
-        hipLaunchKernelGGL((grad_quantize_kernel<ACT, false, kTileRows, NT>), dim3((unsigned)tiles), block, 0, hs, p);
+        hipLaunchKernelGGL((grad_quantize_kernel<ACT, TABLE, false, kTileRows, NT>), dim3((unsigned)tiles), block, 0, hs, p);
     else if (tiles >= kSmallGrid)
-        hipLaunchKernelGGL((grad_quantize_kernel<ACT, true, kTileRows, NT>), dim3((unsigned)tiles), block, 0, hs, p);
+        hipLaunchKernelGGL((grad_quantize_kernel<ACT, TABLE, true, kTileRows, NT>), dim3((unsigned)tiles), block, 0, hs, p);
     else
-        hipLaunchKernelGGL((grad_quantize_kernel<ACT, true, 64, false>), dim3((unsigned)(up(p.M, 64) * per)), block, 0, hs, p);
+        hipLaunchKernelGGL((grad_quantize_kernel<ACT, false, true, 64, false>), dim3((unsigned)(up(p.M, 64) * per)), block, 0, hs, p);
 }
 
 template <int ACT>
 void launch_passes(const Grad& p, hipStream_t hs) {
     const int64_t bytes = 2 * p.M * ((ACT == kActNone ? 1 : 2) * p.N + (p.blocks_k ? p.K : 0));
-    if (bytes > kCachedBytes) launch_passes<ACT, true>(p, hs);
-    else launch_passes<ACT, false>(p, hs);
+    const bool stream = bytes > kCachedBytes;
+    if constexpr (kHasTable<ACT>) {
+        // (dz has tiles enough to be bound by its arithmetic.)
+        if (up(p.M, kTileRows) * p.blocks_n >= kSmallGrid)
+            return stream ? launch_passes<ACT, true, true>(p, hs) : launch_passes<ACT, true, false>(p, hs);
+    }
+    if (stream) launch_passes<ACT, false, true>(p, hs);
+    else launch_passes<ACT, false, false>(p, hs);
 }
 
 }  // namespace
