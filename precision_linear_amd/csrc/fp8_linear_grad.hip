@@ -13,10 +13,10 @@
 //      x (transposed);
 //   4. the two products, on the scaled multiply's kernels: in one launch where
 //      they fill the GPU better together (small ones), else in two.
-// Passes 1 and 3 are bound by memory (pass 1, for the smooth activations, as much
-// by the arithmetic of the slope): 2 x 4 bytes read and 2 bytes written for an
-// element of dz, against 4 K operations of the products.  4096 x 28672 x 8192 with
-// gelu: 126 + 6 + 157 us of 1550; the products run at 2.9 to 3.1 PFLOP/s.
+// Passes 1 and 3 are bound by memory (where the caches feed them, by arithmetic):
+// 2 x 4 bytes read and 2 bytes written for an element of dz, against 4 K operations
+// of the products.  4096 x 28672 x 8192 with gelu: 95 + 5 + 140 us of 1545; the
+// products run at 2.9 to 3.1 PFLOP/s.
 //
 // Nothing is summed in an order that depends on timing: sums go through
 // partial results joined in a fixed order.
@@ -117,8 +117,8 @@ __device__ __forceinline__ void dz8_table(const Raw8<bf16_t>& dy, const Raw8<bf1
 
 // Pass 1.  Workgroup: 128 columns of one strip of rows, of dz or (the last
 // blocks) of x.  16 lanes hold a row's 128 columns, 16 rows at a time.  4096 x
-// 28672 with 8192 columns of x: 126 us with gelu (4.3 TB/s; slope's arithmetic
-// and memory about even), 500 x 2048 with 2048 4.9 us.  512 columns a row
+// 28672 with 8192 columns of x: 95 us with gelu (5.6 TB/s), 500 x 2048 with 2048
+// 4.3 us.  512 columns a row
 // (whole waves, so that a row's maximum takes more lane exchanges) and strips of
 // 64 to 1024 rows measured no faster.
 template <int ACT, bool TABLE, bool NT>
@@ -282,7 +282,7 @@ __device__ __forceinline__ float over_scale(float v, float s, float r) {
 // c ^ ((n >> 3) % (ROWS / 16)), which spreads the 16 column lanes over the banks.
 //
 // Bound by memory at training sizes (4096 x 28672 with 8192 columns of x, gelu:
-// 157 us, 5.1 TB/s), by latency at small ones (500 x 2048 with 2048: 6.8 us).
+// 140 us, 5.8 TB/s), by latency at small ones (500 x 2048 with 2048: 7 us).
 //
 // JOIN: the workgroup joins the partial maxima of its columns and rows itself
 // (at most kJoinParts of each), in place of pass 2; those of the first strip
