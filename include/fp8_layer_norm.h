@@ -85,7 +85,8 @@ int fp8_layer_norm(const void* x, int dtype, const void* w, const void* b, int p
  * dx is rounded.  `workspace` holds the workgroups' partial column sums: at
  * least fp8_layer_norm_backward_workspace_size(rows, cols) bytes, 256-byte
  * aligned, with any contents; it must not be used by two calls that can run at
- * the same time. */
+ * the same time.  Calls on one stream may share it, from any host threads (the
+ * launches of a call are enqueued without another's between them). */
 int fp8_layer_norm_backward(const void* dy, const void* x, int dtype, const float* mean,
                             const float* rstd, const void* w, int param_dtype,
                             const void* residual_grad, void* dx, float* dw, float* db,

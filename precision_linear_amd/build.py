@@ -23,7 +23,7 @@ SRCS = [os.path.join(HERE, "csrc", f) for f in
         ["fp8_linear_pair.hip", "fp8_quantize.hip", "fp8_layer_norm.hip", "fp8_linear_grad.hip"]]
 HEADERS = [os.path.join(HERE, "csrc", f) for f in
            ("fp8_gemm_kernels.h", "fp8_convert.h", "lane_ops.h", "activation.h", "fp8_pair.h",
-            "plan_cost_table.h")]
+            "enqueue_lock.h", "plan_cost_table.h")]
 LIB = os.path.join(HERE, "libfp8_scaled_mm.so")
 # The binding's short calls from torch tensors to the C ABI (host code only).
 CALLS_SRC = os.path.join(HERE, "csrc", "torch_calls.cpp")

@@ -34,6 +34,7 @@
 #include <type_traits>
 
 #include "../../include/fp8_layer_norm.h"
+#include "enqueue_lock.h"
 #include "fp8_convert.h"
 #include "lane_ops.h"
 
@@ -969,6 +970,7 @@ int fp8_layer_norm_backward(const void* dy, const void* x, int dtype, const floa
     const GradPlan g = grad_plan(rows, cols, dtype);
     LnBwd p{dy, x, mean, rstd, w, param_dtype == FP8LN_BF16, residual_grad, dx, static_cast<float*>(workspace),
             rows, cols, g.pitch, g.waves, g.subs};
+    std::lock_guard<std::mutex> together(fp8mm::enqueue_lock(workspace));
     (void)hipGetLastError();
     if (rows > 0 && g.held) {
         if (dtype == FP8LN_BF16) launch_backward<bf16_t, 2>(p, g, dw, db, hs);

@@ -25,6 +25,7 @@
 
 #include "../../include/fp8_linear.h"
 #include "activation.h"
+#include "enqueue_lock.h"
 #include "fp8_convert.h"
 #include "fp8_pair.h"
 #include "lane_ops.h"
@@ -627,6 +628,7 @@ int fp8_linear_backward(const void* dy, const void* x, const void* wt, int wt_fo
                                2 * N);
         return hipGetLastError() == hipSuccess ? FP8MM_OK : FP8MM_ERR_LAUNCH;
     }
+    std::lock_guard<std::mutex> together(fp8mm::enqueue_lock(workspace));
     char* ws = static_cast<char*>(workspace);
     Grad& p = g.p;
     p.dy = static_cast<const bf16_t*>(dy);
