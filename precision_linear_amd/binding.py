@@ -190,24 +190,50 @@ def workspace_size(M, N, K, mode, has_bias=False, config=-1, splits=0) -> int:
                                                   int(config), int(splits)))
 
 
-# Split-K workspaces handed to the library, per (device, stream): zero-filled
+# Workspaces handed to the library, per (device, stream, kind): zero-filled
 # torch allocations (the library allocates nothing itself).  Calls on one
 # stream are ordered, so they can share one; a larger one replaces it for
-# later calls, but none is ever freed, because a captured HIP graph may still
-# hold its address.
+# later calls, but none is freed, because another thread may be enqueuing a
+# call with it.
 _workspaces: dict = {}
+# While a graph is captured, the calls on a stream share one of the capture's
+# own, (capture, workspace): its fill is recorded, to run with each replay, so no
+# other call may count on it, and the graph may be replayed beside any other work.
+_captured: dict = {}
 
 
 def _workspace(device: torch.device, stream: int, nbytes: int, kind: str = "mm") -> torch.Tensor:
     key = (device.index, stream, kind)
+    capture = _capture_id(device, stream)
+    if capture is not None:
+        have = _captured.get(key)
+        if have is None or have[0] != capture or have[1].numel() < nbytes:
+            # (What is replaced goes back to its graph's memory, as any temporary
+            # tensor of a capture does.)
+            have = _captured[key] = (capture, _new_workspace(device, nbytes))
+        return have[1]
     have = _workspaces.get(key)
     if have and have[-1].numel() >= nbytes:
         return have[-1]
-    size = max(nbytes, 2 * have[-1].numel() if have else 0)
-    size = (size + (1 << 20) - 1) >> 20 << 20
-    ws = torch.zeros(size, dtype=torch.uint8, device=device)   # a fill kernel on this stream
+    ws = _new_workspace(device, max(nbytes, 2 * have[-1].numel() if have else 0))
     _workspaces.setdefault(key, []).append(ws)
     return ws
+
+
+def _new_workspace(device: torch.device, nbytes: int) -> torch.Tensor:
+    size = (nbytes + (1 << 20) - 1) >> 20 << 20
+    return torch.zeros(size, dtype=torch.uint8, device=device)   # a fill kernel on the current stream
+
+
+def _capture_id(device: torch.device, stream: int):
+    """Which graph capture `stream`, the device's current one, is part of (None: no capture)."""
+    if not _call(device.index, torch.cuda.is_current_stream_capturing):
+        return None
+    status, ident = ctypes.c_int(), ctypes.c_ulonglong()
+    err = lib().hipStreamGetCaptureInfo(ctypes.c_void_p(stream), ctypes.byref(status), ctypes.byref(ident))
+    if err != 0:
+        raise RuntimeError(f"hipStreamGetCaptureInfo failed: {err}")
+    return ident.value
 
 
 _TORCH_FORMATS = {torch.float8_e4m3fn: E4M3FN, torch.float8_e5m2: E5M2}

@@ -113,6 +113,7 @@ PyObject* tuple_of(const at::Tensor (&t)[N]) {
 
 // Workspaces that binding.py has handed out, by GPU, stream and kind.  They are
 // its own (it never frees one); the reference here only keeps the address valid.
+// While a graph is captured, binding.py is asked each time: a capture has its own.
 enum Kind { kMm, kNorm, kLinearGrad };
 const char* const kKindNames[] = {"mm", "layer_norm", "linear_grad"};
 struct Workspace {
@@ -125,8 +126,10 @@ struct Workspace {
 // False: a Python error is set.
 bool workspace(int dev, hipStream_t stream, Kind kind, int64_t bytes, const at::Tensor& like, void** out) {
     static std::vector<Workspace>* held = new std::vector<Workspace>;   // (not destroyed after the interpreter)
+    hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
+    const bool eager = hipStreamIsCapturing(stream, &capture) != hipSuccess || capture == hipStreamCaptureStatusNone;
     for (Workspace& w : *held)
-        if (w.dev == dev && w.stream == stream && w.kind == kind) {
+        if (eager && w.dev == dev && w.stream == stream && w.kind == kind) {
             if (w.t.numel() >= bytes) {
                 *out = w.t.data_ptr();
                 return true;
@@ -140,9 +143,9 @@ bool workspace(int dev, hipStream_t stream, Kind kind, int64_t bytes, const at::
     PyObject* r = PyObject_CallFunction(g_workspace, "NKLs", device, (unsigned long long)(uintptr_t)stream,
                                         (long long)bytes, kKindNames[kind]);
     if (!r) return false;
-    held->push_back(Workspace{dev, stream, kind, THPVariable_Unpack(r)});
+    *out = THPVariable_Unpack(r).data_ptr();
+    if (eager) held->push_back(Workspace{dev, stream, kind, THPVariable_Unpack(r)});
     Py_DECREF(r);
-    *out = held->back().t.data_ptr();
     return true;
 }
 
