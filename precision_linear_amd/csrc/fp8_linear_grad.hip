@@ -72,13 +72,14 @@ __device__ __forceinline__ void dz8(const Raw8<bf16_t>& dy, const Raw8<bf16_t>& 
     for (int i = 0; i < 8; ++i) f[i] = dy.get(i) * slope<ACT>(z.get(i));
 }
 
-// The gelus' slopes from a table in LDS.  z has 16 bits, and the slope of -z is 1
-// less that of z, so the 1664 values of slope(t) - 1/2 for 2^-9 <= t < 16 are all
-// there is: below, it is sqrt(2 / pi) t (within 5e-9), above, 1/2 (in fp32).  Off by
-// two roundings more than slope() itself.  About 12 instructions for some 30, which
-// the passes are bound by where the caches feed them (the whole gradient on one
-// MI355X, gelu, us without and with: 4069 x 12720 x 176 176 and 169, 8192 x 4096 x
-// 1024 170 and 162, 4096 x 28672 x 8192 1583 and 1547; under 512 tiles of dz the
+// The gelus' slopes from a table in LDS.  z has 16 bits, and the slope of z is 1
+// less that of -z, so the 1664 values of slope(-t) for 2^-9 <= t < 16 are all there
+// is: below, it is 1/2 - sqrt(2 / pi) t (within 5e-9), above, 0 (in fp32).  The
+// small side is the one that is kept: far below 0 the slope has slope()'s own
+// relative accuracy, above 0 one rounding more.  About 13 instructions for some 30,
+// which the passes are bound by where the caches feed them (the whole gradient on
+// one MI355X, gelu, us without and with: 4069 x 12720 x 176 176 and 169, 8192 x 4096
+// x 1024 170 and 162, 4096 x 28672 x 8192 1583 and 1547; under 512 tiles of dz the
 // table's filling costs as much, 1024 x 2048 x 8192 64 and 65).
 template <int ACT> constexpr bool kHasTable = ACT == kActGelu || ACT == kActGeluTanh;
 constexpr uint32_t kTableFirst = 0x3b00, kTableEnd = 0x4180;   // bf16 2^-9 and 16
@@ -87,7 +88,7 @@ constexpr int kTableSize = (int)(kTableEnd - kTableFirst);
 template <int ACT>
 __device__ __forceinline__ void fill_table(float* table) {
     for (int i = threadIdx.x; i < kTableSize; i += kThreadsG)
-        table[i] = slope<ACT>(__uint_as_float((kTableFirst + (uint32_t)i) << 16)) - 0.5f;
+        table[i] = slope<ACT>(-__uint_as_float((kTableFirst + (uint32_t)i) << 16));
 }
 
 __device__ __forceinline__ void dz8_table(const Raw8<bf16_t>& dy, const Raw8<bf16_t>& z, const float* table,
@@ -103,8 +104,8 @@ __device__ __forceinline__ void dz8_table(const Raw8<bf16_t>& dy, const Raw8<bf1
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const float v = z.get(2 * w + k);
-            const float h = fabsf(v) < 0x1p-9f ? fabsf(v) * (0.5f * kTanhA2) : table[at[k]];
-            f[2 * w + k] = dy.get(2 * w + k) * (0.5f + copysignf(h, v));
+            const float h = fabsf(v) < 0x1p-9f ? fmaf(fabsf(v), -0.5f * kTanhA2, 0.5f) : table[at[k]];   // slope(-|z|)
+            f[2 * w + k] = dy.get(2 * w + k) * (v < 0.f ? h : 1.f - h);
         }
     }
     if (most[0] > 0x7f80 || most[1] > 0x7f80) {   // a NaN stays one
