@@ -11,10 +11,9 @@
 // polynomial P.  p and P's coefficients were fitted here (weighted least
 // squares, reweighted towards the least largest relative error, over 0 <= t <=
 // 14): degree 8 with p = 0.3, relative error at most 1.5e-7, so Phi keeps its
-// relative accuracy in the negative tail, where 1 + erf cancels.  The slope
-// takes that one (FINE): it feeds fp32 sums, and has a root near z = -0.75,
-// where an error of Phi is large beside it.  The epilogue's results are rounded
-// to bf16 (half a step is 3.9e-3): degree 5 with p = 0.38, 3.6e-5.
+// relative accuracy in the negative tail, where 1 + erf cancels.  (A shorter fit
+// would do where the rounding to bf16 follows at once, but a residual that cancels
+// the activation leaves its last fp32 bits.)
 //
 // exp2 and the reciprocal are the hardware's (1 ulp).
 #pragma once
@@ -33,28 +32,17 @@ constexpr float kTanhB = 0.044715f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 
 // Q(t) exp(t^2 / 2) for t >= 0.
-template <bool FINE>
 __device__ __forceinline__ float normal_tail(float t) {
-    if constexpr (FINE) {
-        const float s = __builtin_amdgcn_rcpf(fmaf(0.3f, t, 1.f));
-        float q = 0.03567469557679612f;
-        q = fmaf(q, s, -0.15720273304111515f);
-        q = fmaf(q, s, 0.20635286920959425f);
-        q = fmaf(q, s, -0.053683029549290925f);
-        q = fmaf(q, s, 0.12856128835779043f);
-        q = fmaf(q, s, 0.09991359800531395f);
-        q = fmaf(q, s, 0.12075393860757816f);
-        q = fmaf(q, s, 0.11962929999040094f);
-        return q * s;
-    } else {
-        const float s = __builtin_amdgcn_rcpf(fmaf(0.38f, t, 1.f));
-        float q = -0.08992725504450005f;
-        q = fmaf(q, s, 0.1888740920206601f);
-        q = fmaf(q, s, 0.09198153833219586f);
-        q = fmaf(q, s, 0.15782892080127015f);
-        q = fmaf(q, s, 0.15122519455980082f);
-        return q * s;
-    }
+    const float s = __builtin_amdgcn_rcpf(fmaf(0.3f, t, 1.f));
+    float q = 0.03567469557679612f;
+    q = fmaf(q, s, -0.15720273304111515f);
+    q = fmaf(q, s, 0.20635286920959425f);
+    q = fmaf(q, s, -0.053683029549290925f);
+    q = fmaf(q, s, 0.12856128835779043f);
+    q = fmaf(q, s, 0.09991359800531395f);
+    q = fmaf(q, s, 0.12075393860757816f);
+    q = fmaf(q, s, 0.11962929999040094f);
+    return q * s;
 }
 
 // exp(-z^2 / 2)
@@ -72,7 +60,7 @@ __device__ __forceinline__ float activate(float z) {
     if constexpr (ACT == kActRelu) {
         return z < 0.f ? 0.f : z;   // (NaN stays NaN)
     } else if constexpr (ACT == kActGelu) {
-        const float q = normal_tail<false>(fabsf(z)) * bell(z);
+        const float q = normal_tail(fabsf(z)) * bell(z);
         return z * (z > 0.f ? 1.f - q : q);
     } else if constexpr (ACT == kActGeluTanh) {
         const float z2 = z * z;
@@ -93,7 +81,7 @@ __device__ __forceinline__ float slope(float z) {
         return z > 0.f ? 1.f : z <= 0.f ? 0.f : z;
     } else if constexpr (ACT == kActGelu) {
         const float e = bell(z);
-        const float q = normal_tail<true>(fabsf(z)) * e;
+        const float q = normal_tail(fabsf(z)) * e;
         const float phi = z > 0.f ? 1.f - q : q;                      // (NaN for a NaN)
         return fmaf(fminf(fmaxf(z, -16.f), 16.f) * kInvSqrt2Pi, e, phi);   // e is 0 from |z| = 16 on
     } else if constexpr (ACT == kActGeluTanh) {
