@@ -27,9 +27,10 @@
  * Everything between the loads and the final rounding of an output is fp32.
  * Two calls with the same inputs give the same bits (no atomics in any sum).
  *
- * Rows that hold a NaN or an infinity: every y of the row is NaN, its scale is
- * NaN and its codes are NaN codes, so a product made from them shows it.  (So is
- * an fp32 row whose sum leaves the fp32 range.)
+ * Rows that hold a NaN or an infinity: every y of the row is NaN, and so are rstd
+ * and its scale, and its codes are NaN codes, so that a product made from them
+ * shows it.  The same holds for rows of finite values whose sum, or whose sum of
+ * (x - mean)^2, leaves the fp32 range (|x - mean| of about 1.8e19 / sqrt(n)).
  *
  * Pointers are DEVICE pointers on the current HIP device; the caller owns them
  * and the library keeps none after the call.  No entry point allocates,

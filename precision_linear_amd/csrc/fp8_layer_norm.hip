@@ -108,6 +108,12 @@ __device__ __forceinline__ u32x2 codes8(const float (&y)[8], const Div& d) {
     return out;
 }
 
+// 1 / sqrt(variance + eps).  Squares beyond the fp32 range give NaN, not the 0 that
+// would make every y of the row b.
+__device__ __forceinline__ float inverse_spread(float variance, float eps) {
+    return variance < __builtin_inff() ? 1.f / sqrtf(variance + eps) : __builtin_nanf("");
+}
+
 // The scale of a row from its largest |y| (NaN skipped): a row whose
 // statistics are NaN gets a NaN scale, not the 0 of an empty maximum.
 template <int FMT>
@@ -229,7 +235,7 @@ ln_forward_kernel(LnFwd p) {
             const float d = c ? mom.x / (float)c - mean : 0.f;
             m2 = lane_value(row16_sum(l < W ? fmaf((float)c * d, d, mom.y) : 0.f), 0);
         }
-        const float rstd = 1.f / sqrtf(m2 * inv_n + p.eps);
+        const float rstd = inverse_spread(m2 * inv_n, p.eps);
 
         float amax = 0.f;
 #pragma unroll
@@ -329,7 +335,7 @@ ln_forward_long_kernel(LnFwd p) {
                         for (int i = 0; i < 8; ++i) m2 = fmaf(v.get(i) - mean, v.get(i) - mean, m2);
                     },
                     [&](int64_t c) { m2 = fmaf(load1(xr + c) - mean, load1(xr + c) - mean, m2); });
-        const float rstd = 1.f / sqrtf(block_sum(m2, red) / (float)p.cols + p.eps);
+        const float rstd = inverse_spread(block_sum(m2, red) / (float)p.cols, p.eps);
         auto y8 = [&](int64_t c, float (&f)[8]) {
             Raw8<T> v;
             float w[8], b[8];
