@@ -268,9 +268,19 @@ grad_scales_kernel(Grad p, int blocks_rows, int blocks_cols) {
     if (part_sum) p.dbias[i] = sum;
 }
 
-// value / s: EXACT correctly rounded, else the product by r = 1 / s.  With s =
-// r = 0 every finite value gives 0, with s infinite (r = 0) an infinity gives
-// NaN; NaN stays NaN.
+// A scale and its reciprocal (0 and 0 included) as the exact division takes them.
+// It is proved for scales from 2^-60 on: a smaller one is lifted by 2^66, and so are
+// the values that it divides (all of it exact: the quotients stay the same).
+// Returns the values' factor.
+__device__ __forceinline__ float lift(float2& sr) {
+    if (!(sr.x > 0.f && sr.x < 0x1p-60f)) return 1.f;
+    sr = float2{sr.x * 0x1p66f, sr.y * 0x1p-66f};
+    return 0x1p66f;
+}
+
+// value / s: EXACT correctly rounded (s lifted, or from 2^-60 on), else the product
+// by r = 1 / s.  With s = r = 0 every finite value gives 0, with s infinite (r = 0)
+// an infinity gives NaN; NaN stays NaN.
 template <bool EXACT>
 __device__ __forceinline__ float over_scale(float v, float s, float r) {
     if constexpr (EXACT) return div_fast(v, Div{s, r, true});
@@ -315,8 +325,9 @@ __global__ void __launch_bounds__(kThreadsG)
 grad_quantize_kernel(Grad p) {
     constexpr int kChunks = ROWS / 16;           // of a transposed row
     __shared__ __attribute__((aligned(16))) uint32_t s_t[kTileCols][ROWS / 4];
-    __shared__ __attribute__((aligned(16))) float s_col[2][kTileCols];   // scales, reciprocals
-    __shared__ float s_row[2][ROWS];
+    __shared__ __attribute__((aligned(16))) float s_col[3][kTileCols];   // scales, reciprocals, factors (lift())
+    __shared__ float s_row[3][ROWS];
+    __shared__ int s_lifted[kThreadsG / kWaveSize];
     __shared__ float s_table[TABLE ? kTableSize : 1];
     constexpr bool kExactDz = ACT == kActNone || ACT == kActRelu;
     const int cl = threadIdx.x % kColLanes, rl = threadIdx.x / kColLanes;
@@ -349,6 +360,8 @@ grad_quantize_kernel(Grad p) {
     };
     fetch(0);   // under way while the scales are found
     if (TABLE && !is_x) fill_table<ACT>(s_table);
+    // Whether the exact division of this workgroup's values meets a lifted scale.
+    int lifted = 0;
     {   // scales: the first 128 threads the columns', the others the rows'
         static_assert(kThreadsG >= kTileCols + ROWS, "one thread for each row and column");
         const int t = threadIdx.x % kTileCols;
@@ -368,8 +381,11 @@ grad_quantize_kernel(Grad p) {
                     sr = float2{scale[c], scale[width + c]};
                 }
             }
+            const float up = kExactDz || is_x ? lift(sr) : 1.f;
+            lifted = up != 1.f;
             s_col[0][t] = sr.x;
             s_col[1][t] = sr.y;
+            s_col[2][t] = up;
         } else if (t < ROWS) {
             const int64_t r = row0 + t;
             float2 sr{0.f, 0.f};
@@ -381,10 +397,17 @@ grad_quantize_kernel(Grad p) {
                     sr = float2{p.row_scale[r], p.row_scale[p.M + r]};
                 }
             }
+            const float up = kExactDz ? lift(sr) : 1.f;
+            lifted = up != 1.f;
             s_row[0][t] = sr.x;
             s_row[1][t] = sr.y;
+            s_row[2][t] = up;
         }
+        const bool any = __ballot(lifted) != 0;
+        if (threadIdx.x % kWaveSize == 0) s_lifted[threadIdx.x / kWaveSize] = any;
         __syncthreads();
+        static_assert(kThreadsG / kWaveSize == 4, "four waves' flags");
+        lifted = __builtin_amdgcn_readfirstlane(s_lifted[0] | s_lifted[1] | s_lifted[2] | s_lifted[3]);
     }
     float cs[8], cr[8];
 #pragma unroll
@@ -405,11 +428,22 @@ grad_quantize_kernel(Grad p) {
         }
         float f[4][8];
         uint32_t words[8];
+        const auto lift_columns = [&]() __attribute__((always_inline)) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[k][i] *= s_col[2][cl * 8 + i];
+        };
         if (is_x) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) f[k][i] = over_scale<true>(a[it][k].get(i), cs[i], cr[i]);
+                for (int i = 0; i < 8; ++i) f[k][i] = a[it][k].get(i);
+            if (lifted) lift_columns();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[k][i] = over_scale<true>(f[k][i], cs[i], cr[i]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 int w = Fp8Fmt<0>::cvt_pk<false>(f[0][i], f[1][i], 0);
@@ -426,7 +460,13 @@ grad_quantize_kernel(Grad p) {
                 for (int k = 0; k < 4; ++k) {
                     float t[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) t[i] = over_scale<kExactDz>(f[k][i], rs[k], rr[k]);
+                    for (int i = 0; i < 8; ++i) t[i] = f[k][i];
+                    if constexpr (kExactDz)
+                        if (lifted)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) t[i] *= s_row[2][mg * 4 + k];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) t[i] = over_scale<kExactDz>(t[i], rs[k], rr[k]);
                     u32x2 codes;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -437,6 +477,8 @@ grad_quantize_kernel(Grad p) {
                         store_hinted<NT>(reinterpret_cast<u32x2*>(p.q_rows + (r + k) * p.N + col), codes);
                 }
             }
+            if constexpr (kExactDz)
+                if (lifted) lift_columns();
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 int w = Fp8Fmt<1>::cvt_pk<false>(over_scale<kExactDz>(f[0][i], cs[i], cr[i]),
