@@ -4,7 +4,8 @@ Every step of the multiply runs in the HIP library; this module turns torch
 tensors into device pointers, sizes and the current stream, and turns
 status codes into exceptions.  A missing library is an error (there is no
 fallback path).  The ordinary calls of the layer norm and the linear layer go
-through _calls (csrc/torch_calls.cpp), which does the same with less host time.
+through _calls (csrc/torch_calls.cpp), which does the same with less host time;
+without it they take the same path as the others.
 """
 from __future__ import annotations
 
@@ -13,15 +14,19 @@ import contextlib
 import ctypes
 import math
 import os
+import warnings
 
 import torch
 
+HERE = os.path.dirname(os.path.abspath(__file__))
 try:
     from . import _calls
-except ImportError as e:      # (lib() raises it)
-    _calls, _calls_error = None, e
+except ImportError as e:
+    _calls = None
+    if os.path.exists(os.path.join(HERE, "_calls.so")):
+        warnings.warn(f"the extension _calls does not load ({e}): short calls take some microseconds more; build it "
+                      "again with `python -m precision_linear_amd.build`")
 
-HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(HERE, "libfp8_scaled_mm.so")
 
 PER_TENSOR = 0
@@ -93,9 +98,6 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(
                 f"{library_path} is missing: build it with "
                 "`python -m precision_linear_amd.build` (there is no non-HIP fallback)")
-        if _calls is None:
-            raise RuntimeError("the extension _calls does not load: build it with "
-                               "`python -m precision_linear_amd.build`") from _calls_error
         L = ctypes.CDLL(library_path)
         vp, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
         L.fp8_scaled_mm.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, vp]
@@ -157,8 +159,9 @@ def lib() -> ctypes.CDLL:
         L.fp8_layer_norm_backward_workspace_size.restype = i64
         L.fp8_layer_norm_status_string.argtypes = [i32]
         L.fp8_layer_norm_status_string.restype = ctypes.c_char_p
-        _calls.use_library(tuple(ctypes.cast(getattr(L, name), ctypes.c_void_p).value
-                                 for name in _CALLS_ENTRIES), _workspace)
+        if _calls is not None:
+            _calls.use_library(tuple(ctypes.cast(getattr(L, name), ctypes.c_void_p).value
+                                     for name in _CALLS_ENTRIES), _workspace)
         _lib = L
     return _lib
 

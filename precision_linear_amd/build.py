@@ -1,6 +1,6 @@
 """Builds libfp8_scaled_mm.so (the HIP kernels -- scaled multiply,
-quantiser, layer norm and linear layer -- and their C ABI) for gfx950, and
-_calls.so (the binding's short calls into it, host code).
+quantiser, layer norm and linear layer -- and their C ABI) for gfx950, and,
+where it compiles, _calls.so (the binding's short calls into it, host code).
 
 hipcc cross-compiles without a GPU.  The library is written next to this
 file so that it travels with the source tree.
@@ -71,6 +71,20 @@ def _calls_command(out):
             "-o", out]
 
 
+def _build_calls(out: str, verbose: bool) -> None:
+    """Compile _calls to `out` and put it in place.  It only saves host time, so
+    where it does not compile (no headers of torch or Python, say) the library is
+    built without it, and none of an earlier build stays behind."""
+    try:
+        _run(_calls_command(out), verbose)
+    except (ImportError, OSError, RuntimeError) as e:
+        sys.stderr.write(f"_calls is not built, short calls take some microseconds more: {e}\n")
+        if os.path.exists(CALLS):
+            os.remove(CALLS)
+        return
+    shutil.move(out, CALLS)
+
+
 def build(verbose: bool = False, sanitize: bool = False, out: str | None = None) -> str:
     """Compile every source to an object (in parallel), then link the
     shared library; always rebuilds.  sanitize=True builds the host logic
@@ -85,17 +99,15 @@ def build(verbose: bool = False, sanitize: bool = False, out: str | None = None)
         for src, obj in zip(SRCS, objs):
             extra = SANITIZE_HOST if sanitize and os.path.basename(src) in HOST_LOGIC_SRCS else []
             jobs.append([HIPCC, *FLAGS, *extra, "-c", src, "-o", obj])
-        calls = os.path.join(objdir, "_calls.so")
-        if out is None:
-            jobs.insert(0, _calls_command(calls))
         workers = max(1, min(len(jobs), os.cpu_count() or 1))
         with ThreadPoolExecutor(max_workers=workers) as ex:
+            calls = ex.submit(_build_calls, os.path.join(objdir, "_calls.so"), verbose) if out is None else None
             list(ex.map(lambda c: _run(c, verbose), jobs))
+            if calls is not None:
+                calls.result()
         tmp = target + ".tmp"
         _run([HIPCC, "--offload-arch=gfx950", "-shared", *objs, "-o", tmp], verbose)
         shutil.move(tmp, target)
-        if out is None:
-            shutil.move(calls, CALLS)
     finally:
         shutil.rmtree(objdir, ignore_errors=True)
     return target
