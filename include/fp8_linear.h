@@ -75,11 +75,11 @@ int fp8_linear(const void* A, int a_format, const void* B, int b_format, const f
  * Preconditions: 0 <= M <= 2^31 - 1, 16 <= N, K <= 2^23, both multiples of 16;
  * with dw also M <= 2^23.  wt 16-byte aligned, bf16 tensors 2-byte, fp32 ones
  * 4-byte aligned.  Outputs must not overlap inputs or each other.  With M == 0, dw and dbias are zeros.
- * `workspace` is 256-byte aligned, zero-filled before its first use, and at
- * least fp8_linear_backward_workspace_size() bytes; its first 256 KiB are
- * arrival counters, zero again after every call.  It may serve calls of any
- * shape, one at a time: those of one stream, from any host threads (the launches
- * of a call are enqueued without another's between them).  Execution and status codes are those of
+ * `workspace` is 256-byte aligned, of any contents, and at least
+ * fp8_linear_backward_workspace_size() bytes (the first 256 KiB of it are arrival
+ * counters, which the call clears).  It may serve calls of any shape, one at a
+ * time: those of one stream, from any host threads (the launches of a call are
+ * enqueued without another's between them).  Execution and status codes are those of
  * fp8_scaled_mm.h; equal calls give equal bits. */
 int fp8_linear_backward(const void* dy, const void* x_or_null, const void* wt_or_null,
                         int wt_format, const float* wt_scale_or_null, const void* z_or_null,

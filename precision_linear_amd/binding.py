@@ -193,10 +193,10 @@ def workspace_size(M, N, K, mode, has_bias=False, config=-1, splits=0) -> int:
                                                   int(config), int(splits)))
 
 
-# Workspaces handed to the library, per (device, stream, kind): zero-filled
-# torch allocations (the library allocates nothing itself).  Calls on one
-# stream are ordered, so they can share one; a larger one replaces it for
-# later calls, but none is freed, because another thread may be enqueuing a
+# Workspaces handed to the library, per (device, stream, kind): torch allocations
+# (the library allocates nothing itself), zeros where the kind counts on them.
+# Calls on one stream are ordered, so they can share one; a larger one replaces it
+# for later calls, but none is freed, because another thread may be enqueuing a
 # call with it.
 _workspaces: dict = {}
 # While a graph is captured, the calls on a stream share one of the capture's
@@ -213,19 +213,26 @@ def _workspace(device: torch.device, stream: int, nbytes: int, kind: str = "mm")
         if have is None or have[0] != capture or have[1].numel() < nbytes:
             # (What is replaced goes back to its graph's memory, as any temporary
             # tensor of a capture does.)
-            have = _captured[key] = (capture, _new_workspace(device, nbytes))
+            have = _captured[key] = (capture, _new_workspace(device, nbytes, kind))
         return have[1]
     have = _workspaces.get(key)
     if have and have[-1].numel() >= nbytes:
         return have[-1]
-    ws = _new_workspace(device, max(nbytes, 2 * have[-1].numel() if have else 0))
+    ws = _new_workspace(device, max(nbytes, 2 * have[-1].numel() if have else 0), kind)
     _workspaces.setdefault(key, []).append(ws)
     return ws
 
 
-def _new_workspace(device: torch.device, nbytes: int) -> torch.Tensor:
-    size = (nbytes + (1 << 20) - 1) >> 20 << 20
-    return torch.zeros(size, dtype=torch.uint8, device=device)   # a fill kernel on the current stream
+# Bytes at a workspace's start that have to be zero before its first use: the
+# arrival counters of a split K, all of the per-tensor quantisation's.
+_ZEROED = {"mm": 256 << 10, "quantize": 1 << 20, "layer_norm": 0}
+
+
+def _new_workspace(device: torch.device, nbytes: int, kind: str) -> torch.Tensor:
+    ws = torch.empty((nbytes + (1 << 20) - 1) >> 20 << 20, dtype=torch.uint8, device=device)
+    if _ZEROED[kind]:
+        ws[:_ZEROED[kind]].zero_()      # a fill kernel on the current stream
+    return ws
 
 
 def _capture_id(device: torch.device, stream: int):
@@ -450,8 +457,8 @@ def fp8_linear_backward(dy: torch.Tensor, x: torch.Tensor | None, wt: torch.Tens
     (M x K) and dw (N x K) are bf16, dbias is fp32; True allocates one, False
     leaves it (and what only it needs) out, and dx and dw may be buffers.  What is
     left out is None in the result.  N and K are multiples of 16.  Codes, scales and partial sums
-    live in `workspace` (a GPU byte tensor, zero-filled before its first use) or
-    in one that this module keeps per stream."""
+    live in `workspace` (a GPU byte tensor with any contents) or in memory that torch
+    has back after the call."""
     act = _activation(activation)
     if _calls is not None and dx is dw is dbias is True and workspace is None and wt_format is None:
         got = _calls.linear_backward(dy, x, wt, wt_scale, z, act)
@@ -515,7 +522,7 @@ def fp8_linear_backward(dy: torch.Tensor, x: torch.Tensor | None, wt: torch.Tens
     L = lib()
     stream = _stream_of(dev)
     if workspace is not None:
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        ws, ws_bytes = workspace, workspace.numel() * workspace.element_size()
     else:
         key = ("linear_grad", M, N, K, want_dx, want_dw)
         need = _ws_sizes.get(key)
@@ -524,9 +531,9 @@ def fp8_linear_backward(dy: torch.Tensor, x: torch.Tensor | None, wt: torch.Tens
             if need < 0:
                 raise ValueError(f"fp8_linear_backward: {status_string(ERR_SHAPE)}")
             _keep_size(key, need)
-        ws, ws_bytes = _workspace(device, stream, need, "linear_grad").data_ptr(), need
+        ws, ws_bytes = torch.empty(need, dtype=torch.uint8, device=device), need
     st = _call(dev, L.fp8_linear_backward, dy.data_ptr(), _ptr(x), _ptr(wt), fw, _ptr(wt_scale), _ptr(z), act,
-               _ptr(dx), _ptr(dw), _ptr(db), M, N, K, stream, ws, ws_bytes)
+               _ptr(dx), _ptr(dw), _ptr(db), M, N, K, stream, ws.data_ptr(), ws_bytes)
     if st != OK:
         _mm_error("fp8_linear_backward", st)
     return dx, dw, db

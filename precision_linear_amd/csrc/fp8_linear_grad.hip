@@ -6,7 +6,8 @@
 // over the rows).  Both scales need the maxima of whole rows and columns, so dz
 // is computed twice rather than written out in 32 bits:
 //   1. grad_stats_kernel: maxima of dz's rows and columns, sums of its columns
-//      (dbias), maxima of x's columns, as partial results;
+//      (dbias), maxima of x's columns, as partial results; it also clears the
+//      products' arrival counters, so that the workspace may hold anything;
 //   2. grad_scales_kernel: joins them into the scales and dbias; with few
 //      partial results the third pass does that itself;
 //   3. grad_quantize_kernel: the codes of dz (row-major, and transposed) and of
@@ -63,6 +64,8 @@ struct Grad {
     uint8_t* q_rows;       // M x N
     uint8_t* q_cols;       // N x Mp
     uint8_t* q_x;          // K x Mp
+    uint32_t* counters;    // of the products
+    int num_counters;
 };
 
 // dz of 8 elements.
@@ -138,6 +141,9 @@ grad_stats_kernel(Grad p) {
     const int64_t col = (int64_t)cb * kTileCols + cl * 8;
     const bool ok = col < width;                       // widths are multiples of 16
     const int64_t r1 = min(p.M, (part + 1) * p.strip);
+    for (int64_t i = (int64_t)blockIdx.x * kThreadsG + threadIdx.x; i < p.num_counters;
+         i += (int64_t)gridDim.x * kThreadsG)
+        p.counters[i] = 0u;
     if (TABLE && !is_x) {
         fill_table<ACT>(s_table);
         __syncthreads();
@@ -688,6 +694,17 @@ int fp8_linear_backward(const void* dy, const void* x, const void* wt, int wt_fo
     p.x_max = p.col_sum + p.parts * N;
     p.row_max = p.x_max + p.parts * K;
     p.dbias = dbias;
+    fp8mm::Product q[2];
+    products(M, N, K, p.Mp, q);
+    fp8mm::PairPlan pair{-1, {1, 1}};
+    if (dx && dw && wt_format == FP8MM_E4M3FN) pair = fp8mm::plan_pair(q);
+    p.counters = reinterpret_cast<uint32_t*>(ws);
+    if (pair.cfg >= 0) {
+        p.num_counters = fp8mm::pair_counters(q, pair);
+    } else {
+        const int of_dx = dx ? fp8mm::product_counters(q[0]) : 0, of_dw = dw ? fp8mm::product_counters(q[1]) : 0;
+        p.num_counters = of_dx > of_dw ? of_dx : of_dw;   // (a product leaves its counters at zero)
+    }
     switch (activation) {
         case kActRelu: launch_passes<kActRelu>(p, hs); break;
         case kActGelu: launch_passes<kActGelu>(p, hs); break;
@@ -696,15 +713,10 @@ int fp8_linear_backward(const void* dy, const void* x, const void* wt, int wt_fo
         default: launch_passes<kActNone>(p, hs); break;
     }
     if (hipGetLastError() != hipSuccess) return FP8MM_ERR_LAUNCH;
-    if (dx && dw && wt_format == FP8MM_E4M3FN) {
-        fp8mm::Product q[2];
-        products(M, N, K, p.Mp, q);
-        const fp8mm::PairPlan plan = fp8mm::plan_pair(q);
-        if (plan.cfg >= 0) {
-            q[0] = fp8mm::Product{p.q_rows, wt, p.row_scale, wt_scale, dx, M, K, N};
-            q[1] = fp8mm::Product{p.q_cols, p.q_x, p.col_scale, p.x_scale, dw, N, K, p.Mp};
-            return fp8mm::run_pair(q, plan, hs, ws);
-        }
+    if (pair.cfg >= 0) {
+        q[0] = fp8mm::Product{p.q_rows, wt, p.row_scale, wt_scale, dx, M, K, N};
+        q[1] = fp8mm::Product{p.q_cols, p.q_x, p.col_scale, p.x_scale, dw, N, K, p.Mp};
+        return fp8mm::run_pair(q, pair, hs, ws);
     }
     if (dx) {
         st = fp8_scaled_mm_typed(p.q_rows, FP8MM_E5M2, wt, wt_format, p.row_scale, wt_scale, nullptr, dx, M, K, N,

@@ -1,5 +1,6 @@
-// Two independent products in one launch, for the linear layer's gradient
-// (defined in fp8_scaled_mm.hip; host code).
+// What the linear layer's gradient needs of the multiply: two independent products in
+// one launch, and the arrival counters that products use (defined in
+// fp8_scaled_mm.hip; host code).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -27,6 +28,11 @@ PairPlan plan_pair(const Product (&p)[2]);
 
 // Bytes of workspace of a plan with cfg >= 0.
 int64_t pair_workspace(const Product (&p)[2], const PairPlan& plan);
+
+// Arrival counters (32 bits each, from the workspace's start on) that have to be
+// zero before a product of its own under the automatic plan, or before a pair.
+int product_counters(const Product& p);
+int pair_counters(const Product (&p)[2], const PairPlan& plan);
 
 // An FP8MM_* status.  The pointers have been checked; `workspace` is as for
 // fp8_scaled_mm_typed.

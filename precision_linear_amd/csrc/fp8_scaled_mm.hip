@@ -732,6 +732,21 @@ int64_t pair_workspace(const Product (&p)[2], const PairPlan& plan) {
     return bytes;
 }
 
+int product_counters(const Product& p) {
+    const int cfg = choose_config(p.M, p.N, p.K, FP8MM_ROWWISE, false, true);
+    if (plan_splits(cfg, p.M, p.N, p.K, 0) <= 1) return 0;
+    const ConfigInfo& c = kConfigs[cfg];
+    return (int)(cdiv(p.M, c.bm) * cdiv(p.N, c.bn) * counters_per_tile(cfg));
+}
+
+int pair_counters(const Product (&p)[2], const PairPlan& plan) {
+    if (plan.splits[0] <= 1 && plan.splits[1] <= 1) return 0;
+    const ConfigInfo& c = kConfigs[plan.cfg];
+    int64_t tiles = 0;
+    for (int i = 0; i < 2; ++i) tiles += cdiv(p[i].M, c.bm) * cdiv(p[i].N, c.bn);
+    return (int)tiles;
+}
+
 int run_pair(const Product (&q)[2], const PairPlan& plan, hipStream_t stream, void* workspace) {
     int dev = -1;
     if (hipGetDevice(&dev) != hipSuccess) return FP8MM_ERR_DEVICE;

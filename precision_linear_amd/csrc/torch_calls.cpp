@@ -114,8 +114,8 @@ PyObject* tuple_of(const at::Tensor (&t)[N]) {
 // Workspaces that binding.py has handed out, by GPU, stream and kind.  They are
 // its own (it never frees one); the reference here only keeps the address valid.
 // While a graph is captured, binding.py is asked each time: a capture has its own.
-enum Kind { kMm, kNorm, kLinearGrad };
-const char* const kKindNames[] = {"mm", "layer_norm", "linear_grad"};
+enum Kind { kMm, kNorm };
+const char* const kKindNames[] = {"mm", "layer_norm"};
 struct Workspace {
     int dev;
     hipStream_t stream;
@@ -304,8 +304,7 @@ PyObject* linear_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t need = g_lib.linear_backward_workspace(M, N, K, 1, 1);
     if (need < 0) Py_RETURN_NONE;
     const hipStream_t stream = c10::hip::getCurrentHIPStream(dev).stream();
-    void* ws = nullptr;
-    if (!workspace(dev, stream, kLinearGrad, need, *dy.t, &ws)) return nullptr;
+    const at::Tensor ws = allocate(*dy.t, {need}, at::kByte);
     at::Tensor out[3];
     out[0] = allocate(*dy.t, {M, K}, at::kBFloat16);
     out[1] = allocate(*dy.t, {N, K}, at::kBFloat16);
@@ -315,7 +314,7 @@ PyObject* linear_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         pybind11::gil_scoped_release free_interpreter;
         st = g_lib.linear_backward(dy.ptr(), x.ptr(), wt.ptr(), fw, static_cast<const float*>(swt.ptr()), z.ptr(),
                                    act, out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr<float>(), M, N, K,
-                                   reinterpret_cast<ihipStream_t*>(stream), ws, need);
+                                   reinterpret_cast<ihipStream_t*>(stream), ws.data_ptr(), need);
     }
     if (st != FP8MM_OK) return PyLong_FromLong(st);
     return tuple_of(out);
