@@ -31,6 +31,7 @@
  * and its scale, and its codes are NaN codes, so that a product made from them
  * shows it.  The same holds for rows of finite values whose sum, or whose sum of
  * (x - mean)^2, leaves the fp32 range (|x - mean| of about 1.8e19 / sqrt(n)).
+ * With eps == 0 a row without variance has an infinite rstd and is NaN likewise.
  *
  * Pointers are DEVICE pointers on the current HIP device; the caller owns them
  * and the library keeps none after the call.  No entry point allocates,

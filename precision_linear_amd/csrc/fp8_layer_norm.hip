@@ -114,11 +114,12 @@ __device__ __forceinline__ float inverse_spread(float variance, float eps) {
     return variance < __builtin_inff() ? 1.f / sqrtf(variance + eps) : __builtin_nanf("");
 }
 
-// The scale of a row from its largest |y| (NaN skipped): a row whose
-// statistics are NaN gets a NaN scale, not the 0 of an empty maximum.
+// The scale of a row from its largest |y| (NaN skipped): a row whose statistics
+// are NaN, or whose rstd is infinite (no variance, no eps: every y is 0 times
+// that), gets a NaN scale, not the 0 of an empty maximum.
 template <int FMT>
 __device__ __forceinline__ float row_scale(float amax, float rstd) {
-    return rstd != rstd ? rstd : amax / Fp8Fmt<FMT>::kMax;
+    return rstd < __builtin_inff() ? amax / Fp8Fmt<FMT>::kMax : __builtin_nanf("");
 }
 
 // One row per W waves.  WIDE: the workgroup is the row's W > 1 waves, which
