@@ -235,9 +235,13 @@ def _new_workspace(device: torch.device, nbytes: int, kind: str) -> torch.Tensor
     return ws
 
 
+# Whether the current stream is captured (torch's direct accessor where it has one).
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or torch.cuda.is_current_stream_capturing
+
+
 def _capture_id(device: torch.device, stream: int):
     """Which graph capture `stream`, the device's current one, is part of (None: no capture)."""
-    if not _call(device.index, torch.cuda.is_current_stream_capturing):
+    if not (_capturing() if _current_device() == device.index else _call(device.index, _capturing)):
         return None
     status, ident = ctypes.c_int(), ctypes.c_ulonglong()
     err = lib().hipStreamGetCaptureInfo(ctypes.c_void_p(stream), ctypes.byref(status), ctypes.byref(ident))
