@@ -80,7 +80,8 @@ int fp8_linear(const void* A, int a_format, const void* B, int b_format, const f
  * counters, which the call clears).  It may serve calls of any shape, one at a
  * time: those of one stream, from any host threads (the launches of a call are
  * enqueued without another's between them).  Execution and status codes are those of
- * fp8_scaled_mm.h; equal calls give equal bits. */
+ * fp8_scaled_mm.h; equal calls give equal bits (what else a call asks for may
+ * change the plan, and with it the order of an output's fp32 sums). */
 int fp8_linear_backward(const void* dy, const void* x_or_null, const void* wt_or_null,
                         int wt_format, const float* wt_scale_or_null, const void* z_or_null,
                         int activation, void* dx_or_null, void* dw_or_null, float* dbias_or_null,

@@ -2036,8 +2036,8 @@ __global__ void __launch_bounds__(pp::THREADS) fp8_gemm_pp_kernel(KernelParams<E
             // With the linear layer's epilogue, which has more arithmetic and
             // waits, the groups do not meet here: group 1 starts its own as soon
             // as its last compute phase ends, so that one group's works in the
-            // other's waits (4096 x 28672 x 8192 on one MI355X, gelu 720 -> 700 us,
-            // gelu and residual 740 -> 722 us).  Nothing else hangs on that barrier:
+            // other's waits (4096 x 28672 x 8192 on one MI355X, gelu 678 -> 643 us,
+            // gelu and residual 739 -> 716 us).  Nothing else hangs on that barrier:
             // group 1's last reads of the stage buffers ended before the one above.
             if constexpr (!EPI) barrier_lds();   // pairs with group 1's last barrier of the tile
             __builtin_amdgcn_sched_barrier(0);

@@ -310,7 +310,8 @@ __device__ __forceinline__ void for_columns(int64_t cols, F8 f8, F1 f1) {
 // Rows of any length, one workgroup each, swept once per step of the formula
 // (sum, squares, y with its maximum, codes).  Bound by the L2: each sweep over y
 // reads the parameters, four bytes for one of x (4096 x 32768 bf16, y and codes,
-// 282 us; 321 with y and its maximum in sweeps of their own).
+// 250 to 282 us by the card; on the latter 321 with y and its maximum in sweeps of
+// their own).
 template <class T>
 __global__ void __launch_bounds__(kLongThreads)
 ln_forward_long_kernel(LnFwd p) {

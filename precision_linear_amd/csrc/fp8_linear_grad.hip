@@ -16,7 +16,7 @@
 //      they fill the GPU better together (small ones), else in two.
 // Passes 1 and 3 are bound by memory (where the caches feed them, by arithmetic):
 // 2 x 4 bytes read and 2 bytes written for an element of dz, against 4 K operations
-// of the products.  4096 x 28672 x 8192 with gelu: 95 + 5 + 140 us of 1545; the
+// of the products.  4096 x 28672 x 8192 with gelu: 98 + 5 + 142 us of 1542; the
 // products run at 2.9 to 3.1 PFLOP/s.
 //
 // Nothing is summed in an order that depends on timing: sums go through
@@ -81,9 +81,9 @@ __device__ __forceinline__ void dz8(const Raw8<bf16_t>& dy, const Raw8<bf16_t>& 
 // small side is the one that is kept: far below 0 the slope has slope()'s own
 // relative accuracy, above 0 one rounding more.  About 13 instructions for some 30,
 // which the passes are bound by where the caches feed them (the whole gradient on
-// one MI355X, gelu, us without and with: 4069 x 12720 x 176 176 and 169, 8192 x 4096
-// x 1024 170 and 162, 4096 x 28672 x 8192 1583 and 1547; under 512 tiles of dz the
-// table's filling costs as much, 1024 x 2048 x 8192 64 and 65).
+// one MI355X, gelu, us without and with: 4069 x 12720 x 176 174 and 167, 8192 x 4096
+// x 1024 155 and 148, 4096 x 28672 x 8192 1538 and 1513; under 512 tiles of dz the
+// table's filling costs more, 1024 x 2048 x 8192 62 and 64).
 template <int ACT> constexpr bool kHasTable = ACT == kActGelu || ACT == kActGeluTanh;
 constexpr uint32_t kTableFirst = 0x3b00, kTableEnd = 0x4180;   // bf16 2^-9 and 16
 constexpr int kTableSize = (int)(kTableEnd - kTableFirst);
@@ -122,8 +122,8 @@ __device__ __forceinline__ void dz8_table(const Raw8<bf16_t>& dy, const Raw8<bf1
 
 // Pass 1.  Workgroup: 128 columns of one strip of rows, of dz or (the last
 // blocks) of x.  16 lanes hold a row's 128 columns, 16 rows at a time.  4096 x
-// 28672 with 8192 columns of x: 95 us with gelu (5.6 TB/s), 500 x 2048 with 2048
-// 4.3 us.  512 columns a row
+// 28672 with 8192 columns of x: 98 us with gelu (5.4 TB/s), 500 x 2048 with 2048
+// 4.7 us.  512 columns a row
 // (whole waves, so that a row's maximum takes more lane exchanges) and strips of
 // 64 to 1024 rows measured no faster.
 template <int ACT, bool TABLE, bool NT>
@@ -300,7 +300,7 @@ __device__ __forceinline__ float over_scale(float v, float s, float r) {
 // c ^ ((n >> 3) % (ROWS / 16)), which spreads the 16 column lanes over the banks.
 //
 // Bound by memory at training sizes (4096 x 28672 with 8192 columns of x, gelu:
-// 140 us, 5.8 TB/s), by latency at small ones (500 x 2048 with 2048: 7 us).
+// 142 us, 5.7 TB/s), by latency at small ones (500 x 2048 with 2048: 8 us).
 //
 // JOIN: the workgroup joins the partial maxima of its columns and rows itself
 // (at most kJoinParts of each), in place of pass 2; those of the first strip

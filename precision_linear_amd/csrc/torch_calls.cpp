@@ -1,13 +1,12 @@
 // The binding's short calls: a Python extension that takes the ordinary call of
-// an operator (outputs allocated here, automatic plan, the module's own
-// workspace) from torch tensors to the C ABI in one step.
+// an operator (outputs allocated here, automatic plan, no workspace given) from torch tensors to the C ABI in one step.
 //
 // A small call's time is the host's, and what binding.py does for it, attribute
-// by attribute, costs 6 to 9 us beside the 4 us of a launch.  Host time of a
-// call, there and here (MI355X's host, one row of 64 columns): linear 9.8 and
-// 5.0 us, layer norm 10.5 and 6.7 (with codes 12.9 and 7.8), its gradient 12.1
-// and 6.7, linear's gradient (three launches) 19.1 and 13.2.  What is left beside
-// the launches is the outputs' tensors, 0.8 us each.
+// by attribute, costs 5 to 7 us beside the 4 us of a launch.  Host time of a
+// call, there and here (MI355X's host, one row of 64 columns): linear 9.2 and
+// 4.3 us, layer norm with its statistics 10.0 and 5.2, its gradient 11.6 and 5.4,
+// linear's gradient (three launches) 20.1 and 13.0.  What is left beside the
+// launches is the tensors of outputs and scratch memory, some 0.5 us each.
 //
 // Each function returns the outputs as a tuple, the library's status where it
 // refuses the call, or None where an argument is not the ordinary one: wrong
