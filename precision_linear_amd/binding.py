@@ -202,6 +202,7 @@ _workspaces: dict = {}
 # While a graph is captured, the calls on a stream share one of the capture's
 # own, (capture, workspace): its fill is recorded, to run with each replay, so no
 # other call may count on it, and the graph may be replayed beside any other work.
+# (torch.cuda.graph keeps the memory of a capture to its graph.)
 _captured: dict = {}
 
 
@@ -462,7 +463,8 @@ def fp8_linear_backward(dy: torch.Tensor, x: torch.Tensor | None, wt: torch.Tens
     leaves it (and what only it needs) out, and dx and dw may be buffers.  What is
     left out is None in the result.  N and K are multiples of 16.  Codes, scales and partial sums
     live in `workspace` (a GPU byte tensor with any contents) or in memory that torch
-    has back after the call."""
+    has back after the call (a graph captured without torch.cuda.graph needs one
+    that stays)."""
     act = _activation(activation)
     if _calls is not None and dx is dw is dbias is True and workspace is None and wt_format is None:
         got = _calls.linear_backward(dy, x, wt, wt_scale, z, act)
