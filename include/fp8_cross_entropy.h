@@ -1,0 +1,90 @@
+/*
+ * fp8_cross_entropy.h -- C ABI of the MI355X (gfx950) softmax cross entropy of an
+ * FP8 linear layer over a large vocabulary, and its gradient.  The logits are made
+ * tile by tile in the multiply and are never written.
+ *
+ * Forward (A: M x K, one row for each position; B: V x K, one row for each entry of
+ * the vocabulary; s and the operand formats as in fp8_scaled_mm.h):
+ *
+ *     z[m][j] = s[m][j] * sum_{k<K} A[m][k] * B[j][k]                   (fp32)
+ *     lse[m]  = log sum_{j<V} exp(z[m][j])
+ *     loss[m] = lse[m] - z[m][target[m]],  0 where target[m] == ignore_index
+ *
+ *   Sums, maxima and both outputs are fp32.  A target outside 0 .. V - 1 that is not
+ *   ignore_index gives a NaN, and so does a row with a NaN or infinite logit (lse of
+ *   ignored rows included).
+ */
+#ifndef FP8_CROSS_ENTROPY_H
+#define FP8_CROSS_ENTROPY_H
+
+#include <stdint.h>
+
+#include "fp8_scaled_mm.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Operands, scaling modes, execution and status codes are fp8_scaled_mm_typed's
+ * (plans are automatic).  target is M int64, 8-byte aligned; loss and lse are M fp32
+ * each, 4-byte aligned, and overlap nothing else.
+ * Preconditions: 0 <= M <= 2^23, 1 <= V <= 2^23, 16 <= K <= 2^23, K % 16 == 0.
+ * `workspace` is 256-byte aligned, of any contents, and at least
+ * fp8_linear_cross_entropy_workspace_size() bytes; it may serve calls of any shape,
+ * one at a time (those of one stream, from any host threads). */
+int fp8_linear_cross_entropy(const void* A, int a_format, const void* B, int b_format, const float* scale_a,
+                             const float* scale_b, const int64_t* target, int64_t ignore_index, float* loss,
+                             float* lse, int64_t M, int64_t V, int64_t K, int scaling_mode,
+                             struct ihipStream_t* stream, void* workspace, int64_t workspace_bytes);
+
+/* Bytes of workspace (host logic only; -1 for an invalid problem). */
+int64_t fp8_linear_cross_entropy_workspace_size(int64_t M, int64_t V, int64_t K);
+
+/* The gradient, for dloss, the gradient of loss, and the forward call's loss and lse.
+ * With p = exp(z - lse), h[m] = 1 - p[m][target[m]] = -expm1(-loss[m]) (0 in ignored
+ * rows and where loss <= 0) and r = dloss h:
+ *
+ *     dz = dloss (p - onehot(target)) = r / 57344 * q,
+ *     q  = e5m2_RNE(min(57344 p / h, 57344)),  -57344 at the target
+ *     dx = bf16_rne( r / 57344 * sum_j q[m][j] W[j][k] )
+ *     dw = bf16_rne( 1 / 57344 * sum_m q[m][j] xr[m][k] ),
+ *     xr = r[m] x[m][k] as e4m3fn with one scale for each column, as in fp8_quantize.h
+ *
+ *   No element of a row's gradient is larger than the target's, which is why the
+ *   row's scale is known before its logits.  The vocabulary is taken in pieces, each
+ *   with its logits made anew, its codes in the workspace, its rows of dw and its
+ *   share of dx, whose sums stay in fp32 from piece to piece.
+ *
+ *   dloss  M fp32, dloss_stride 1, or one value for all rows, dloss_stride 0.
+ *   x      M x K bf16: what A holds the codes of.
+ *   wt     W transposed: K x Vp float8 codes of wt_format, row-major, Vp = V rounded
+ *          up to 16, zeros past V, with wt_scale[k] for row k.
+ *   dx     M x K bf16, dw V x K bf16.  Each may be NULL: what only it needs is then
+ *          not computed (wt with its scales, or x, may then be NULL too).  At least
+ *          one of them is needed.
+ *
+ * Ignored rows and rows with dloss 0 take no part, whatever they hold.  A NaN in
+ * dloss, loss or lse, an infinite lse, and a target outside the vocabulary that is
+ * not ignore_index, come out as NaN in their row of dx and in dw.
+ * Preconditions: as for the forward call; fp32 tensors are 4-byte aligned, bf16 ones
+ * 2-byte, wt 16-byte.  Outputs must not overlap inputs or each other.  With M == 0,
+ * dw is zeros.  The workspace is as for the forward call, of its own size.  Equal
+ * calls give equal bits. */
+int fp8_linear_cross_entropy_backward(const float* dloss, int64_t dloss_stride, const void* A, int a_format,
+                                      const void* B, int b_format, const float* scale_a, const float* scale_b,
+                                      const int64_t* target, int64_t ignore_index, const float* loss,
+                                      const float* lse, const void* x_or_null, const void* wt_or_null,
+                                      int wt_format, const float* wt_scale_or_null, void* dx_or_null,
+                                      void* dw_or_null, int64_t M, int64_t V, int64_t K, int scaling_mode,
+                                      struct ihipStream_t* stream, void* workspace, int64_t workspace_bytes);
+
+/* Bytes of workspace for the outputs asked for (host logic only; -1 for an invalid
+ * problem). */
+int64_t fp8_linear_cross_entropy_backward_workspace_size(int64_t M, int64_t V, int64_t K, int want_dx,
+                                                         int want_dw);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* FP8_CROSS_ENTROPY_H */

@@ -67,6 +67,11 @@ _Q_ARG_ERRORS = {Q_ERR_NULL, Q_ERR_SHAPE, Q_ERR_ALIGN, Q_ERR_MODE, Q_ERR_WORKSPA
 LINEAR_EXPORTS = ("fp8_linear", "fp8_linear_backward", "fp8_linear_backward_workspace_size")
 _ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
+# functions from include/fp8_cross_entropy.h (status codes: those of fp8_scaled_mm.h)
+CROSS_ENTROPY_EXPORTS = ("fp8_linear_cross_entropy", "fp8_linear_cross_entropy_workspace_size",
+                         "fp8_linear_cross_entropy_backward",
+                         "fp8_linear_cross_entropy_backward_workspace_size")
+
 # functions and status codes from include/fp8_layer_norm.h
 LAYER_NORM_EXPORTS = ("fp8_layer_norm", "fp8_layer_norm_backward",
                       "fp8_layer_norm_backward_workspace_size", "fp8_layer_norm_status_string")
@@ -149,6 +154,16 @@ def lib() -> ctypes.CDLL:
         L.fp8_linear_backward.restype = i32
         L.fp8_linear_backward_workspace_size.argtypes = [i64, i64, i64, i32, i32]
         L.fp8_linear_backward_workspace_size.restype = i64
+        L.fp8_linear_cross_entropy.argtypes = [vp, i32, vp, i32, vp, vp, vp, i64, vp, vp, i64, i64, i64, i32,
+                                               vp, vp, i64]
+        L.fp8_linear_cross_entropy.restype = i32
+        L.fp8_linear_cross_entropy_workspace_size.argtypes = [i64, i64, i64]
+        L.fp8_linear_cross_entropy_workspace_size.restype = i64
+        L.fp8_linear_cross_entropy_backward.argtypes = [vp, i64, vp, i32, vp, i32, vp, vp, vp, i64, vp, vp, vp,
+                                                        vp, i32, vp, vp, vp, i64, i64, i64, i32, vp, vp, i64]
+        L.fp8_linear_cross_entropy_backward.restype = i32
+        L.fp8_linear_cross_entropy_backward_workspace_size.argtypes = [i64, i64, i64, i32, i32]
+        L.fp8_linear_cross_entropy_backward_workspace_size.restype = i64
         f32 = ctypes.c_float
         L.fp8_layer_norm.argtypes = [vp, i32, vp, vp, i32, f32, vp, vp, i32, vp, vp, vp, i64, i64, vp]
         L.fp8_layer_norm.restype = i32
@@ -543,6 +558,165 @@ def fp8_linear_backward(dy: torch.Tensor, x: torch.Tensor | None, wt: torch.Tens
     if st != OK:
         _mm_error("fp8_linear_backward", st)
     return dx, dw, db
+
+
+# The largest size of the cross entropy's rows, vocabulary and features.
+_LOSS_MAX = 1 << 23
+
+
+def _loss_args(a, b, scale_a, scale_b, target, ignore_index, mode, a_format, b_format, extra):
+    """Checks what the cross entropy and its gradient share (`extra`: more (name,
+    tensor) pairs that must be on the same GPU).  Returns (a, fa, b, fb, M, V, K,
+    mode, device index)."""
+    m = _MODES.get(mode) if isinstance(mode, (str, int)) else None
+    if m is None:
+        raise ValueError(f"mode must be 'per_tensor' or 'rowwise', got {mode!r}")
+    a, fa = _as_codes(a, "a", a_format)
+    b, fb = _as_codes(b, "b", b_format)
+    if a.dim() != 2 or b.dim() != 2 or not a.is_contiguous() or not b.is_contiguous() or a.shape[1] != b.shape[1]:
+        raise ValueError(f"a and b must be contiguous M x K and V x K codes, got {tuple(a.shape)} and {tuple(b.shape)}")
+    M, K = a.shape
+    V = b.shape[0]
+    if K < 16 or K % 16 != 0:
+        raise ValueError(f"K must be a multiple of 16, got {K}")
+    if V < 1 or max(M, V, K) > _LOSS_MAX:
+        raise ValueError(f"M, V and K must be at most {_LOSS_MAX} and V at least 1, got {M}, {V} and {K}")
+    if not a.is_cuda:
+        raise ValueError("all tensors must be on the GPU")
+    dev = a.get_device()
+    _check_devices(dev, (("b", b), ("scale_a", scale_a), ("scale_b", scale_b), ("target", target), *extra))
+    for name, s, n in (("scale_a", scale_a, M), ("scale_b", scale_b, V)):
+        _ln_vector(s, name, 1 if m == PER_TENSOR else n)
+    if target.dtype != torch.int64 or target.shape != (M,) or not target.is_contiguous():
+        raise ValueError(f"target must be a contiguous int64 vector of {M} elements")
+    if not isinstance(ignore_index, int) or not -(1 << 63) <= ignore_index < 1 << 63:
+        raise ValueError(f"ignore_index must be an int of 64 bits, got {ignore_index!r}")
+    return a, fa, b, fb, M, V, K, m, dev
+
+
+def _scratch(device, workspace, key, size, fn):
+    """A call's own workspace: the caller's, or memory that torch has back after the call."""
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous GPU tensor")
+        return workspace, workspace.numel() * workspace.element_size()
+    need = _ws_sizes.get(key)
+    if need is None:
+        need = int(size())
+        if need < 0:
+            raise ValueError(f"{fn}: {status_string(ERR_SHAPE)}")
+        _keep_size(key, need)
+    return torch.empty(need, dtype=torch.uint8, device=device), need
+
+
+def fp8_linear_cross_entropy(a: torch.Tensor, b: torch.Tensor, scale_a: torch.Tensor, scale_b: torch.Tensor,
+                             target: torch.Tensor, *, ignore_index: int = -100, mode="rowwise", a_format=None,
+                             b_format=None, workspace: torch.Tensor | None = None):
+    """(loss, lse) of the softmax cross entropy over the logits of an FP8 linear
+    layer, which are never written:
+
+        z = scale_a * scale_b * (a @ b^T)
+        lse = log(sum(exp(z))),  loss = lse - z[target],  0 where target == ignore_index
+
+    a is M x K (a row for each position), b V x K (a row for each entry of the
+    vocabulary); operands, formats and scales are fp8_scaled_mm's.  target is M
+    int64; one that is no entry gives NaN.  loss and lse are fp32, one for each row
+    (a mean over rows is loss.sum() / (target != ignore_index).sum()).  The partial
+    results live in `workspace` (a GPU byte tensor with any contents) or in memory
+    that torch has back after the call."""
+    a, fa, b, fb, M, V, K, m, dev = _loss_args(a, b, scale_a, scale_b, target, ignore_index, mode, a_format,
+                                               b_format, (("workspace", workspace),))
+    L = lib()
+    ws, ws_bytes = _scratch(a.device, workspace, ("cross_entropy", M, V, K),
+                            lambda: L.fp8_linear_cross_entropy_workspace_size(M, V, K), "fp8_linear_cross_entropy")
+    loss = torch.empty(M, dtype=torch.float32, device=a.device)
+    lse = torch.empty(M, dtype=torch.float32, device=a.device)
+    st = _call(dev, L.fp8_linear_cross_entropy, a.data_ptr(), fa, b.data_ptr(), fb, scale_a.data_ptr(),
+               scale_b.data_ptr(), target.data_ptr(), ignore_index, loss.data_ptr(), lse.data_ptr(), M, V, K, m,
+               _stream_of(dev), ws.data_ptr(), ws_bytes)
+    if st != OK:
+        _mm_error("fp8_linear_cross_entropy", st)
+    return loss, lse
+
+
+def fp8_linear_cross_entropy_backward(dloss: torch.Tensor, a: torch.Tensor, b: torch.Tensor, scale_a: torch.Tensor,
+                                      scale_b: torch.Tensor, target: torch.Tensor, loss: torch.Tensor,
+                                      lse: torch.Tensor, x: torch.Tensor | None, wt: torch.Tensor | None,
+                                      wt_scale: torch.Tensor | None, *, dx=True, dw=True, ignore_index: int = -100,
+                                      mode="rowwise", a_format=None, b_format=None, wt_format=None,
+                                      workspace: torch.Tensor | None = None):
+    """(dx, dw) of fp8_linear_cross_entropy's loss, from dloss, its gradient, and the
+    call's operands and results:
+
+        dz = dloss (exp(z - lse) - onehot(target)),  dx = dz W,  dw = dz^T x
+
+    with dz in e5m2 (a scale for each row) and x, times the rows' scales, in e4m3fn (a
+    scale for each column).  The logits are made anew, in pieces of the vocabulary.
+
+    dloss is fp32, one for each row (an expanded value too) or one element for all of
+    them.  x is the M x K bf16 matrix that a holds the codes of, wt the K x Vp codes of
+    W transposed with K scales wt_scale, Vp being V rounded up to 16, zeros past V
+    (fp8_quantize_weight makes it).  dx (M x K) and dw (V x K) are bf16: True allocates
+    one, False leaves it (and what only it needs) out, or a buffer to write.  Ignored
+    rows and rows with dloss 0 take no part, whatever they hold.  Codes, scales and
+    sums live in `workspace` (a GPU byte tensor with any contents) or in memory that
+    torch has back after the call (a graph captured without torch.cuda.graph needs one
+    that stays)."""
+    for name, t in (("dx", dx), ("dw", dw)):
+        if t is not True and t is not False and not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} must be True, False or a tensor to write")
+    want_dx, want_dw = dx is not False, dw is not False
+    if not (want_dx or want_dw):
+        raise ValueError("nothing to compute: dx and dw are both False")
+    if want_dw and x is None:
+        raise ValueError("dw needs x")
+    if want_dx and (wt is None or wt_scale is None):
+        raise ValueError("dx needs wt and wt_scale")
+    x = x if want_dw else None
+    wt, wt_scale = (wt, wt_scale) if want_dx else (None, None)
+    a, fa, b, fb, M, V, K, m, dev = _loss_args(
+        a, b, scale_a, scale_b, target, ignore_index, mode, a_format, b_format,
+        (("dloss", dloss), ("loss", loss), ("lse", lse), ("x", x), ("wt", wt), ("wt_scale", wt_scale),
+         ("dx", dx if want_dx and dx is not True else None), ("dw", dw if want_dw and dw is not True else None),
+         ("workspace", workspace)))
+    if dloss.dtype != torch.float32 or not (dloss.numel() == 1 or dloss.shape == (M,) and dloss.stride(0) in (0, 1)):
+        raise ValueError(f"dloss must be one float32 element, or a contiguous or expanded vector of {M}")
+    stride = 0 if dloss.numel() == 1 else dloss.stride(0)
+    _ln_vector(loss, "loss", M)
+    _ln_vector(lse, "lse", M)
+    fw = E4M3FN
+    if want_dw:
+        _bf16_matrix("x", x, (M, K))
+        if dw is True:
+            dw = torch.empty((V, K), dtype=torch.bfloat16, device=a.device)
+        else:
+            _bf16_matrix("dw", dw, (V, K))
+    else:
+        dw = None
+    if want_dx:
+        wt, fw = _as_codes(wt, "wt", wt_format)
+        if wt.shape != (K, (V + 15) // 16 * 16) or not wt.is_contiguous():
+            raise ValueError(f"wt must be contiguous {K} x {(V + 15) // 16 * 16} codes (rows of whole 16 bytes), got "
+                             f"{tuple(wt.shape)}")
+        _ln_vector(wt_scale, "wt_scale", K)
+        if dx is True:
+            dx = torch.empty((M, K), dtype=torch.bfloat16, device=a.device)
+        else:
+            _bf16_matrix("dx", dx, (M, K))
+    else:
+        dx = None
+    L = lib()
+    ws, ws_bytes = _scratch(
+        a.device, workspace, ("cross_entropy_grad", M, V, K, want_dx, want_dw),
+        lambda: L.fp8_linear_cross_entropy_backward_workspace_size(M, V, K, want_dx, want_dw),
+        "fp8_linear_cross_entropy_backward")
+    st = _call(dev, L.fp8_linear_cross_entropy_backward, dloss.data_ptr(), stride, a.data_ptr(), fa, b.data_ptr(), fb,
+               scale_a.data_ptr(), scale_b.data_ptr(), target.data_ptr(), ignore_index, loss.data_ptr(),
+               lse.data_ptr(), _ptr(x), _ptr(wt), fw, _ptr(wt_scale), _ptr(dx), _ptr(dw), M, V, K, m, _stream_of(dev),
+               ws.data_ptr(), ws_bytes)
+    if st != OK:
+        _mm_error("fp8_linear_cross_entropy_backward", st)
+    return dx, dw
 
 
 def _bf16_matrix(name: str, t: torch.Tensor, shape: tuple) -> None:

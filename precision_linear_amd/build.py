@@ -19,11 +19,12 @@ ROOT = os.path.dirname(HERE)
 # the multiply's kernels (and of those with the linear layer's epilogue), the quantiser, the layer norm
 # and the linear layer's gradient.  They compile in parallel.
 SRCS = [os.path.join(HERE, "csrc", f) for f in
-        ["fp8_scaled_mm.hip"] + [f"fp8_{n}_f{k}.hip" for n in ("gemm", "linear") for k in range(4)] +
-        ["fp8_linear_pair.hip", "fp8_quantize.hip", "fp8_layer_norm.hip", "fp8_linear_grad.hip"]]
+        ["fp8_scaled_mm.hip"] + [f"fp8_{n}_f{k}.hip" for n in ("gemm", "loss_grad", "linear", "loss") for k in range(4)] +
+        ["fp8_linear_pair.hip", "fp8_loss_sum.hip", "fp8_quantize.hip", "fp8_layer_norm.hip", "fp8_linear_grad.hip",
+         "fp8_cross_entropy.hip"]]
 HEADERS = [os.path.join(HERE, "csrc", f) for f in
-           ("fp8_gemm_kernels.h", "fp8_convert.h", "lane_ops.h", "activation.h", "fp8_pair.h",
-            "enqueue_lock.h", "plan_cost_table.h")]
+           ("fp8_gemm_kernels.h", "fp8_convert.h", "lane_ops.h", "activation.h", "fp8_pair.h", "fp8_loss.h",
+            "column_codes.h", "enqueue_lock.h", "plan_cost_table.h")]
 LIB = os.path.join(HERE, "libfp8_scaled_mm.so")
 # The binding's short calls from torch tensors to the C ABI (host code only).
 CALLS_SRC = os.path.join(HERE, "csrc", "torch_calls.cpp")
@@ -54,7 +55,8 @@ def _run(cmd, verbose):
 SANITIZE_HOST = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
                  "-Xarch_host", "-fno-sanitize-recover=undefined",
                  "-Xarch_host", "-fno-omit-frame-pointer", "-Xarch_host", "-g"]
-HOST_LOGIC_SRCS = {"fp8_scaled_mm.hip", "fp8_quantize.hip", "fp8_layer_norm.hip", "fp8_linear_grad.hip"}
+HOST_LOGIC_SRCS = {"fp8_scaled_mm.hip", "fp8_quantize.hip", "fp8_layer_norm.hip", "fp8_linear_grad.hip",
+                    "fp8_cross_entropy.hip"}
 
 
 def _calls_command(out):

@@ -1,0 +1,307 @@
+// Float8 codes of a matrix with one scale for each column, transposed, and, beside
+// them, with one scale for each row, in place: the two layouts in which products
+// over the columns and over the rows take their operands.
+//
+// For x (M x K, bf16 or fp32, times factor[m] if given):
+//     q_cols[k][m] = RNE(x[m][k] / col_scale[k]),  col_scale[k] = max_m |x| / qmax
+//     q_rows[m][k] = RNE(x[m][k] / row_scale[m]),  row_scale[m] = max_k |x| / qmax
+// with correctly rounded quotients, as in fp8_quantize.h.  Both need maxima of whole
+// rows and columns, so x is read twice:
+//   1. maxima_kernel: partial maxima of columns (by strips of rows) and of rows (by
+//      blocks of columns);
+//   2. scales_kernel joins them, unless they are so few that pass 3 does it itself;
+//   3. codes_kernel.
+// A row whose factor is 0 counts as zeros whatever it holds.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "fp8_convert.h"
+#include "lane_ops.h"
+
+namespace {
+
+constexpr int kCodeThreads = 256;
+constexpr int kCodeCols = 128;                               // of a workgroup: 16 lanes x 8 columns
+constexpr int kCodeColLanes = kCodeCols / 8;                 // 16: a DPP row
+constexpr int kCodeRowLanes = kCodeThreads / kCodeColLanes;  // 16
+constexpr int kCodeUnroll = 4;                               // rows in flight per thread in pass 1
+constexpr int kCodeJoin = 64;                                // partial maxima that pass 3 joins itself
+
+struct CodeJob {
+    const void* x;
+    const float* factor;   // M, may be null
+    int64_t M, K;
+    int64_t Mp;            // row length of q_cols, M rounded up to 16 or more (zeros there)
+    int blocks, parts;     // column blocks, strips of rows in pass 1
+    int64_t strip;
+    float* col_max;        // [parts][K]
+    float* row_max;        // [blocks][M], null without row codes
+    float* col_scale;      // K
+    float* row_scale;      // M
+    uint8_t* q_cols;
+    uint8_t* q_rows;       // may be null
+    // Divides the column scales that are written (the quotients are of the scales
+    // as above).
+    float col_unit;
+};
+
+// 8 elements times the row's factor.
+template <class T, bool FACTOR>
+__device__ __forceinline__ void code_values(const Raw8<T>& a, float factor, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        f[i] = a.get(i);
+        if constexpr (FACTOR) f[i] = factor == 0.f ? 0.f : f[i] * factor;
+    }
+}
+
+template <class T, bool FACTOR, bool ROWS, bool NT>
+__global__ void __launch_bounds__(kCodeThreads) maxima_kernel(CodeJob p) {
+    __shared__ float s_max[kCodeRowLanes][kCodeCols];
+    const T* x = static_cast<const T*>(p.x);
+    const int cl = threadIdx.x % kCodeColLanes, rl = threadIdx.x / kCodeColLanes;
+    const int part = blockIdx.x / p.blocks, cb = blockIdx.x - part * p.blocks;
+    const int64_t col = (int64_t)cb * kCodeCols + cl * 8;
+    const bool ok = col < p.K;                         // K is a multiple of 16
+    const int64_t r1 = min(p.M, (part + 1) * p.strip);
+    float cmax[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) cmax[i] = 0.f;
+    for (int64_t r = part * p.strip + rl; r < r1; r += kCodeRowLanes * kCodeUnroll) {
+        Raw8<T> a[kCodeUnroll];
+        float factor[kCodeUnroll];
+#pragma unroll
+        for (int u = 0; u < kCodeUnroll; ++u) {
+            const int64_t row = r + u * kCodeRowLanes;
+            a[u].zero();
+            factor[u] = 1.f;
+            if (row < r1) {
+                if (ok) a[u].template load<NT>(x + row * p.K + col);
+                if constexpr (FACTOR) factor[u] = p.factor[row];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kCodeUnroll; ++u) {
+            float f[8], rmax = 0.f;
+            code_values<T, FACTOR>(a[u], factor[u], f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                cmax[i] = fmaxf(cmax[i], fabsf(f[i]));
+                if constexpr (ROWS) rmax = fmaxf(rmax, fabsf(f[i]));
+            }
+            if constexpr (ROWS) {
+                const int64_t row = r + u * kCodeRowLanes;
+                rmax = row16_max(rmax);
+                if (cl == 0 && row < r1) p.row_max[cb * p.M + row] = rmax;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s_max[rl][cl * 8 + i] = cmax[i];
+    __syncthreads();
+    const int64_t c = (int64_t)cb * kCodeCols + threadIdx.x;
+    if (threadIdx.x >= kCodeCols || c >= p.K) return;
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < kCodeRowLanes; ++i) m = fmaxf(m, s_max[i][threadIdx.x]);
+    p.col_max[part * p.K + c] = m;
+}
+
+// The largest of p[0], p[n], ... of `parts` values, every step-th from `first` on, 8
+// loaded at a time.
+__device__ __forceinline__ float join_max(const float* p, int64_t n, int parts, int first, int step) {
+    float m = 0.f;
+    for (int q0 = first; q0 < parts; q0 += step * 8) {
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = q0 + step * k < parts ? p[(q0 + step * k) * n] : 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m = fmaxf(m, v[k]);
+    }
+    return m;
+}
+
+// Workgroup: 64 rows or columns, 16 slices of their partial maxima each.  The joined
+// maxima take the place of the first partial ones of what the workgroup joins.
+constexpr int kScaleGroup = 64, kScaleSlices = 16;
+__global__ void __launch_bounds__(kScaleGroup* kScaleSlices) scales_kernel(CodeJob p, int blocks_rows) {
+    __shared__ float s_max[kScaleSlices][kScaleGroup];
+    const int lane = threadIdx.x % kScaleGroup, slice = threadIdx.x / kScaleGroup;
+    const bool rows = (int)blockIdx.x < blocks_rows;
+    const int64_t n = rows ? p.M : p.K;
+    const int64_t i = (int64_t)(rows ? blockIdx.x : blockIdx.x - blocks_rows) * kScaleGroup + lane;
+    float* part = rows ? p.row_max : p.col_max;
+    s_max[slice][lane] = i < n ? join_max(part + i, n, rows ? p.blocks : p.parts, slice, kScaleSlices) : 0.f;
+    __syncthreads();
+    if (slice != 0 || i >= n) return;
+    float m = 0.f;
+#pragma unroll
+    for (int q = 0; q < kScaleSlices; ++q) m = fmaxf(m, s_max[q][lane]);
+    part[i] = m;
+}
+
+// Workgroup: a tile of R rows x 128 columns.  A thread takes 4 consecutive rows of 8
+// columns at a time, so that 4 codes of a column make one word of the transposed
+// tile in LDS: 128 lines of R / 16 chunks of 16 bytes, chunk c of line n at c ^ ((n
+// >> 3) % (R / 16)), which spreads the 16 column lanes over the banks.
+template <class T, int FMT, bool FACTOR, bool ROWS, int R, bool NT>
+__global__ void __launch_bounds__(kCodeThreads) codes_kernel(CodeJob p, int col_parts, int row_parts) {
+    constexpr float kMax = Fp8Fmt<FMT>::kMax;
+    constexpr int kChunks = R / 16;
+    __shared__ __attribute__((aligned(16))) uint32_t s_t[kCodeCols][R / 4];
+    __shared__ float s_col[2][kCodeCols], s_row[3][R];   // scales, reciprocals, factors
+    __shared__ int s_slow[kCodeThreads / kWaveSize];
+    const T* x = static_cast<const T*>(p.x);
+    const int cl = threadIdx.x % kCodeColLanes, rl = threadIdx.x / kCodeColLanes;
+    // Last strips first: the caches still hold them from pass 1.
+    const int64_t turn = blockIdx.x / p.blocks;
+    const int cb = (int)(blockIdx.x - turn * p.blocks);
+    const int64_t strip = gridDim.x / p.blocks - 1 - turn;
+    const int64_t col = (int64_t)cb * kCodeCols + cl * 8, row0 = strip * R;
+    const bool ok = col < p.K;
+    constexpr int kSteps = R / (4 * kCodeRowLanes);
+    Raw8<T> a[4];
+    auto fetch = [&](int it) __attribute__((always_inline)) {
+        const int64_t r = row0 + (it * kCodeRowLanes + rl) * 4;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            a[k].zero();
+            if (ok && r + k < p.M) a[k].template load<NT>(x + (r + k) * p.K + col);
+        }
+    };
+    fetch(0);   // under way while the scales are found
+    static_assert(kCodeThreads >= kCodeCols + R, "one thread for each row and column");
+    int slow = 0;   // whether a division here is outside the fast one's range
+    {
+        const int t = threadIdx.x;
+        if (t < kCodeCols) {
+            const int64_t c = (int64_t)cb * kCodeCols + t;
+            float s = 0.f;
+            if (c < p.K) {
+                s = join_max(p.col_max + c, p.K, col_parts, 0, 1) / kMax;
+                if (strip == 0) p.col_scale[c] = s / p.col_unit;
+            }
+            const Div d = make_div(s);
+            slow = !d.fast && s != 0.f;
+            s_col[0][t] = s;
+            s_col[1][t] = s == 0.f ? 0.f : d.r;
+        } else if (t < kCodeCols + R) {
+            const int64_t r = row0 + t - kCodeCols;
+            float s = 0.f, factor = 1.f;
+            if (r < p.M) {
+                if constexpr (ROWS) {
+                    s = join_max(p.row_max + r, p.M, row_parts, 0, 1) / kMax;
+                    if (cb == 0) p.row_scale[r] = s;
+                }
+                if constexpr (FACTOR) factor = p.factor[r];
+            }
+            const Div d = make_div(s);
+            slow = !d.fast && s != 0.f;
+            s_row[0][t - kCodeCols] = s;
+            s_row[1][t - kCodeCols] = s == 0.f ? 0.f : d.r;
+            s_row[2][t - kCodeCols] = factor;
+        }
+        const bool any = __ballot(slow) != 0;
+        if (t % kWaveSize == 0) s_slow[t / kWaveSize] = any;
+        __syncthreads();
+        static_assert(kCodeThreads / kWaveSize == 4, "four waves' flags");
+        slow = __builtin_amdgcn_readfirstlane(s_slow[0] | s_slow[1] | s_slow[2] | s_slow[3]);
+    }
+    float cs[8], cr[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        cs[i] = s_col[0][cl * 8 + i];
+        cr[i] = s_col[1][cl * 8 + i];
+    }
+    // value / s: with s = 0 every finite value gives 0.
+    auto over = [&](float v, float s, float r) __attribute__((always_inline)) {
+        const Div d{s, r, true};
+        if (!slow) return quant1<FMT, true>(v, d);
+        return s == 0.f ? v * 0.f : quant1<FMT, false>(v, d);
+    };
+#pragma unroll 1
+    for (int it = 0; it < kSteps; ++it) {
+        const int mg = it * kCodeRowLanes + rl;            // group of 4 rows in the tile
+        const int64_t r = row0 + mg * 4;
+        float f[4][8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) code_values<T, FACTOR>(a[k], s_row[2][mg * 4 + k], f[k]);
+        if (it + 1 < kSteps) fetch(it + 1);
+        if constexpr (ROWS) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float s = s_row[0][mg * 4 + k], rr = s_row[1][mg * 4 + k];
+                u32x2 codes;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int w = Fp8Fmt<FMT>::template cvt_pk<false>(over(f[k][4 * h], s, rr), over(f[k][4 * h + 1], s, rr), 0);
+                    codes[h] = (uint32_t)Fp8Fmt<FMT>::template cvt_pk<true>(over(f[k][4 * h + 2], s, rr),
+                                                                            over(f[k][4 * h + 3], s, rr), w);
+                }
+                if (ok && r + k < p.M) store_hinted<NT>(reinterpret_cast<u32x2*>(p.q_rows + (r + k) * p.K + col), codes);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int w = Fp8Fmt<FMT>::template cvt_pk<false>(over(f[0][i], cs[i], cr[i]), over(f[1][i], cs[i], cr[i]), 0);
+            s_t[cl * 8 + i][(((mg >> 2) ^ (cl % kChunks)) << 2) | (mg & 3)] =
+                (uint32_t)Fp8Fmt<FMT>::template cvt_pk<true>(over(f[2][i], cs[i], cr[i]), over(f[3][i], cs[i], cr[i]), w);
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int it = 0; it < kCodeCols * kChunks / kCodeThreads; ++it) {
+        const int q = it * kCodeThreads + threadIdx.x;
+        const int n = q / kChunks, c = q % kChunks;
+        const int64_t line = (int64_t)cb * kCodeCols + n, m = row0 + c * 16;
+        if (line < p.K && m < p.Mp)
+            *reinterpret_cast<u32x4*>(p.q_cols + line * p.Mp + m) =
+                *reinterpret_cast<const u32x4*>(&s_t[n][(c ^ ((n >> 3) % kChunks)) << 2]);
+    }
+}
+
+// ---------------------------------------------------------------- host ---
+
+inline int64_t code_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Blocks, strips and the number of partial maxima, from the sizes.
+inline void plan_codes(CodeJob& p) {
+    p.blocks = (int)code_up(p.K, kCodeCols);
+    const int64_t round = kCodeRowLanes * kCodeUnroll;
+    p.strip = round;
+    while (p.strip < 256 && code_up(p.M, 2 * p.strip) * p.blocks >= 2048) p.strip *= 2;
+    if (code_up(p.M, p.strip) > kCodeJoin && p.M <= 65536)
+        p.strip = code_up(code_up(p.M, kCodeJoin), round) * round;
+    p.parts = (int)code_up(p.M, p.strip);
+}
+// Bytes of partial maxima: col_max, then row_max.
+inline int64_t code_partials(const CodeJob& p, bool rows) {
+    return 4 * ((int64_t)p.parts * p.K + (rows ? (int64_t)p.blocks * p.M : 0));
+}
+// Whether the grids' one dimension holds the tiles.
+inline bool code_grid_ok(int64_t M, int64_t K) {
+    return code_up(M, 64) * code_up(K, kCodeCols) <= INT32_MAX;
+}
+
+template <class T, int FMT, bool FACTOR, bool ROWS, bool NT>
+void launch_codes(const CodeJob& p, hipStream_t hs) {
+    hipLaunchKernelGGL((maxima_kernel<T, FACTOR, ROWS, NT>), dim3((unsigned)((int64_t)p.parts * p.blocks)),
+                       dim3(kCodeThreads), 0, hs, p);
+    int col_parts = p.parts, row_parts = p.blocks;
+    if (col_parts > kCodeJoin || (ROWS && row_parts > kCodeJoin)) {
+        const int rows = ROWS ? (int)code_up(p.M, kScaleGroup) : 0, cols = (int)code_up(p.K, kScaleGroup);
+        hipLaunchKernelGGL(scales_kernel, dim3((unsigned)(rows + cols)), dim3(kScaleGroup * kScaleSlices), 0, hs, p, rows);
+        col_parts = row_parts = 1;
+    }
+    // 64 rows a workgroup (half the work) where the grid is small.
+    if (code_up(p.M, 128) * p.blocks >= 512)
+        hipLaunchKernelGGL((codes_kernel<T, FMT, FACTOR, ROWS, 128, NT>), dim3((unsigned)(code_up(p.M, 128) * p.blocks)),
+                           dim3(kCodeThreads), 0, hs, p, col_parts, row_parts);
+    else
+        hipLaunchKernelGGL((codes_kernel<T, FMT, FACTOR, ROWS, 64, NT>), dim3((unsigned)(code_up(p.M, 64) * p.blocks)),
+                           dim3(kCodeThreads), 0, hs, p, col_parts, row_parts);
+}
+
+}  // namespace

@@ -1,0 +1,375 @@
+// The softmax cross entropy of an FP8 linear layer and its gradient for gfx950
+// (MI355X) (formulas: include/fp8_cross_entropy.h).
+//
+// Forward: the multiply's kernels with an epilogue that reduces each tile's logits
+// to the largest and the sum of exponentials of each row (by the 64 columns of a
+// wave, 16 to 128 in the generic tiles) and picks the target's logit;
+// loss_kernel joins them.  The product bounds it: 8 bytes leave the multiply for 64
+// logits.
+//
+// Gradient: the logits once more, with an epilogue that turns them into e5m2 codes
+// of dz, written by rows (for dx) and by columns (for dw), then the two products.
+// The row's scale is known beforehand (the target's element is a row's largest), and
+// the row's factor r = dloss h goes to the other operand of dw, so one set of codes
+// serves both products.  The vocabulary comes in pieces that keep the codes in
+// kCodeBytes of workspace; dx's fp32 sums stay in tiles of the accumulators' own
+// layout from piece to piece.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/fp8_cross_entropy.h"
+#include "activation.h"
+#include "column_codes.h"
+#include "enqueue_lock.h"
+#include "fp8_loss.h"
+#include "fp8_pair.h"
+
+namespace {
+
+constexpr int kLossThreads = 1024;
+constexpr float kE5m2Max = 57344.f;
+
+// ------------------------------------------------------------- forward ---
+
+// (largest, sum of 2^(x - largest)) of two sets.
+__device__ __forceinline__ float2 merge(float2 a, float2 b) {
+    const float m = fmaxf(a.x, b.x);
+    if (m == -__builtin_inff()) return float2{m, a.y + b.y};
+    return float2{m, a.y * __builtin_amdgcn_exp2f(a.x - m) + b.y * __builtin_amdgcn_exp2f(b.x - m)};
+}
+
+// The vocabulary entry of row m, -1 if the row is ignored, -2 if there is none.
+__device__ __forceinline__ int target_of(const int64_t* target, int64_t m, int64_t ignore, int64_t V) {
+    const int64_t t = target[m];
+    return t == ignore ? -1 : t >= 0 && t < V ? (int)t : -2;
+}
+
+// Workgroup: `group` rows (a power of two up to 64), 1024 / group slices of their
+// column blocks each.
+__global__ void __launch_bounds__(kLossThreads)
+loss_kernel(const float2* part, const float* target_logit, const int64_t* target, int64_t ignore, float* loss,
+            float* lse, int64_t M, int64_t V, int blocks, int group) {
+    __shared__ float2 s_part[kLossThreads];
+    const int slices = kLossThreads / group;
+    const int r = threadIdx.x % group, slice = threadIdx.x / group;
+    const int64_t m = (int64_t)blockIdx.x * group + r;
+    float2 acc{-__builtin_inff(), 0.f};
+    if (m < M)
+        for (int q0 = slice; q0 < blocks; q0 += slices * 8) {
+            float2 v[8];   // loaded together
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int q = q0 + slices * k;
+                v[k] = q < blocks ? part[(int64_t)q * M + m] : float2{-__builtin_inff(), 0.f};
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) acc = merge(acc, v[k]);
+        }
+    s_part[threadIdx.x] = acc;
+    __syncthreads();
+    for (int d = slices / 2; d > 0; d /= 2) {
+        if (slice < d) s_part[threadIdx.x] = merge(s_part[threadIdx.x], s_part[threadIdx.x + d * group]);
+        __syncthreads();
+    }
+    if (slice != 0 || m >= M) return;
+    acc = s_part[threadIdx.x];
+    constexpr float kLn2 = 0.69314718055994531f;
+    const float rest = log2f(acc.y);       // >= 0: the sum holds the largest one's 1
+    lse[m] = (acc.x + rest) * kLn2;
+    const int t = target_of(target, m, ignore, V);
+    // Not lse - z: what of the loss is below the logits' last bit is in `rest`.
+    loss[m] = t == -1 ? 0.f : t < 0 ? __builtin_nanf("") : ((acc.x - target_logit[m]) + rest) * kLn2;
+}
+
+__global__ void __launch_bounds__(256) clear_kernel(uint32_t* p, int64_t n) {
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) p[i] = 0u;
+}
+
+// ------------------------------------------------------------ gradient ---
+
+struct LossGrad {
+    const float* dloss;
+    int64_t dloss_stride;
+    const int64_t* target;
+    int64_t ignore;
+    const float* loss;
+    const float* lse;
+    int64_t M, V;
+    float2* rows;          // for the codes' epilogue (LossParams::rows)
+    float* factor;         // r
+    float* row_scale;      // r / 57344
+    float* ones;           // num_ones of 1
+    int64_t num_ones;
+    uint32_t* counters;    // of the products, cleared
+    int num_counters;
+};
+
+__global__ void __launch_bounds__(256) loss_rows_kernel(LossGrad p) {
+    const int64_t i0 = blockIdx.x * 256ll + threadIdx.x, step = gridDim.x * 256ll;
+    for (int64_t i = i0; i < p.num_counters; i += step) p.counters[i] = 0u;
+    for (int64_t i = i0; i < p.num_ones; i += step) p.ones[i] = 1.f;
+    for (int64_t m = i0; m < p.M; m += step) {
+        const int t = target_of(p.target, m, p.ignore, p.V);
+        const float l = p.loss[m], lse = p.lse[m];
+        float f = -__builtin_inff(), r = 0.f;
+        if (t != -1) {
+            const float h = l <= 0.f ? 0.f : -expm1f(-l);
+            r = p.dloss[m * p.dloss_stride] * h;
+            if (t < 0 || !(fabsf(lse) < __builtin_inff())) r = __builtin_nanf("");
+            else if (h > 0.f) f = __builtin_fmaf(lse, -kLog2E, log2f(kE5m2Max / h));
+        }
+        p.rows[m] = float2{f, __int_as_float(t)};
+        p.factor[m] = r;
+        p.row_scale[m] = r / kE5m2Max;
+    }
+}
+
+__global__ void __launch_bounds__(256) zero_bf16_kernel(uint16_t* p, int64_t n) {
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) p[i] = 0;
+}
+
+// ---------------------------------------------------------------- host ---
+
+int64_t align256(int64_t n) { return code_up(n, 256) * 256; }
+bool at(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+constexpr int64_t kMaxDim = int64_t(1) << 23;
+constexpr int64_t kCounterArea = int64_t(256) << 10;   // the multiply's arrival counters
+constexpr int64_t kCodeBytes = int64_t(512) << 20;     // of a piece's codes, both layouts
+
+int loss_shape(int64_t M, int64_t V, int64_t K) {
+    if (M < 0 || M > kMaxDim || V < 1 || V > kMaxDim || K < 16 || K > kMaxDim || K % 16 != 0) return FP8MM_ERR_SHAPE;
+    if (M > 0 && !fp8mm::loss_plan_fits(M, V, fp8mm::loss_plan(M, V, K))) return FP8MM_ERR_SHAPE;
+    return code_grid_ok(M, K) ? FP8MM_OK : FP8MM_ERR_SHAPE;
+}
+
+int loss_operands(const void* A, int fa, const void* B, int fb, const float* sa, const float* sb,
+                  const int64_t* target, int mode, int64_t M) {
+    if (mode != FP8MM_PER_TENSOR && mode != FP8MM_ROWWISE) return FP8MM_ERR_MODE;
+    if ((fa != FP8MM_E4M3FN && fa != FP8MM_E5M2) || (fb != FP8MM_E4M3FN && fb != FP8MM_E5M2)) return FP8MM_ERR_FORMAT;
+    if (M > 0 && (!A || !B || !sa || !sb || !target)) return FP8MM_ERR_NULL;
+    if (!at(A, 16) || !at(B, 16) || !at(sa, 4) || !at(sb, 4) || !at(target, 8)) return FP8MM_ERR_ALIGN;
+    return FP8MM_OK;
+}
+
+struct LossSpace {
+    int64_t mm, logit, part, total;   // byte offsets
+    fp8mm::LossPlan plan;
+    int64_t blocks;
+};
+
+LossSpace loss_space(int64_t M, int64_t V, int64_t K) {
+    LossSpace s{};
+    if (M == 0) return s;
+    s.plan = fp8mm::loss_plan(M, V, K);
+    s.blocks = fp8mm::loss_blocks(V, s.plan);
+    s.logit = align256(fp8mm::loss_workspace(M, V, s.plan));
+    s.part = s.logit + align256(4 * M);
+    s.total = s.part + align256(8 * M * s.blocks);
+    return s;
+}
+
+struct GradSpace {
+    int64_t mm, rows, factor, row_scale, ones, col_scale, partials, q, qt, qx, sums, total;   // byte offsets
+    int64_t piece, ldq, Mp;
+    bool one;              // the whole vocabulary in one piece
+    fp8mm::LossPlan plan;  // of a whole piece
+    fp8mm::PairPlan pair;
+    CodeJob x;
+};
+
+// The two products of the only piece (sizes only).
+void products(int64_t M, int64_t V, int64_t K, int64_t ldq, int64_t Mp, fp8mm::Product (&q)[2]) {
+    q[0] = fp8mm::Product{nullptr, nullptr, nullptr, nullptr, nullptr, M, K, ldq};
+    q[1] = fp8mm::Product{nullptr, nullptr, nullptr, nullptr, nullptr, V, K, Mp};
+}
+
+GradSpace grad_space(int64_t M, int64_t V, int64_t K, bool want_dx, bool want_dw) {
+    GradSpace g{};
+    g.pair.cfg = -1;
+    if (M == 0) return g;
+    g.Mp = M > 256 ? code_up(M, 64) * 64 : code_up(M, 16) * 16;
+    g.piece = kCodeBytes / (2 * g.Mp) / 256 * 256;
+    if (g.piece < 256) g.piece = 256;
+    g.one = g.piece >= V;
+    if (g.one) g.piece = V;
+    else g.piece = code_up(code_up(V, code_up(V, g.piece)), 256) * 256;   // (pieces of about one size)
+    g.ldq = code_up(g.piece, 16) * 16;
+    g.plan = fp8mm::loss_plan(M, g.piece, K);
+    const int64_t last = g.one ? g.piece : V - (V - 1) / g.piece * g.piece;
+    const fp8mm::LossPlan last_plan = fp8mm::loss_plan(M, last, K);
+    // The tiles write the codes' zeros past M as far as they reach.
+    if (fp8mm::loss_rows(M, g.plan) < g.Mp || fp8mm::loss_rows(M, last_plan) < g.Mp) g.Mp = code_up(M, 16) * 16;
+    int64_t mm = kCounterArea;
+    auto room = [&](int64_t n) { mm = n > mm ? n : mm; };
+    room(fp8mm::loss_workspace(M, g.piece, g.plan));
+    room(fp8mm::loss_workspace(M, last, last_plan));
+    if (want_dx && g.one) room(fp8_scaled_mm_workspace_size(M, K, g.ldq, FP8MM_ROWWISE, 0, -1, 0));
+    if (want_dw) {
+        room(fp8_scaled_mm_workspace_size(g.piece, K, g.Mp, FP8MM_ROWWISE, 0, -1, 0));
+        room(fp8_scaled_mm_workspace_size(last, K, g.Mp, FP8MM_ROWWISE, 0, -1, 0));
+    }
+    if (want_dx && want_dw && g.one) {
+        fp8mm::Product q[2];
+        products(M, V, K, g.ldq, g.Mp, q);
+        g.pair = fp8mm::plan_pair(q);
+        if (g.pair.cfg >= 0) room(fp8mm::pair_workspace(q, g.pair));
+    }
+    CodeJob& x = g.x;
+    x.M = M;
+    x.K = K;
+    x.Mp = g.Mp;
+    x.col_unit = kE5m2Max;
+    plan_codes(x);
+    g.rows = align256(mm);
+    g.factor = g.rows + align256(8 * M);
+    g.row_scale = g.factor + align256(4 * M);
+    g.ones = g.row_scale + align256(4 * M);
+    g.col_scale = g.ones + (want_dw ? align256(4 * g.piece) : 0);
+    g.partials = g.col_scale + (want_dw ? align256(4 * K) : 0);
+    g.q = g.partials + (want_dw ? align256(code_partials(x, false)) : 0);
+    g.qt = g.q + (want_dx ? align256(M * g.ldq) : 0);
+    g.qx = g.qt + (want_dw ? align256(g.piece * g.Mp) : 0);
+    g.sums = g.qx + (want_dw ? align256(K * g.Mp) : 0);
+    g.total = g.sums + (want_dx && !g.one ? align256(fp8mm::sum_workspace(M, K)) : 0);
+    return g;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t fp8_linear_cross_entropy_workspace_size(int64_t M, int64_t V, int64_t K) {
+    return loss_shape(M, V, K) != FP8MM_OK ? -1 : loss_space(M, V, K).total;
+}
+
+int fp8_linear_cross_entropy(const void* A, int a_format, const void* B, int b_format, const float* scale_a,
+                             const float* scale_b, const int64_t* target, int64_t ignore_index, float* loss,
+                             float* lse, int64_t M, int64_t V, int64_t K, int mode, struct ihipStream_t* stream,
+                             void* workspace, int64_t workspace_bytes) {
+    int st = loss_shape(M, V, K);
+    if (st == FP8MM_OK) st = loss_operands(A, a_format, B, b_format, scale_a, scale_b, target, mode, M);
+    if (st != FP8MM_OK) return st;
+    if (M == 0) return FP8MM_OK;
+    if (!loss || !lse) return FP8MM_ERR_NULL;
+    if (!at(loss, 4) || !at(lse, 4) || !at(workspace, 256)) return FP8MM_ERR_ALIGN;
+    const LossSpace s = loss_space(M, V, K);
+    if (!workspace || workspace_bytes < s.total) return FP8MM_ERR_WORKSPACE;
+    const hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+    std::lock_guard<std::mutex> together(fp8mm::enqueue_lock(workspace));
+    char* ws = static_cast<char*>(workspace);
+    (void)hipGetLastError();
+    const int counters = fp8mm::loss_counters(M, V, s.plan);
+    if (counters > 0)
+        hipLaunchKernelGGL(clear_kernel, dim3((unsigned)((counters + 255) / 256)), dim3(256), 0, hs,
+                           reinterpret_cast<uint32_t*>(ws), (int64_t)counters);
+    const fp8mm::Logits z{A, a_format, B, b_format, scale_a, scale_b, M, V, K, mode};
+    float2* part = reinterpret_cast<float2*>(ws + s.part);
+    float* logit = reinterpret_cast<float*>(ws + s.logit);
+    st = fp8mm::run_stats(z, s.plan, target, part, logit, hs, ws);
+    if (st != FP8MM_OK) return st;
+    int group = 1;
+    while (group < 64 && M / group > 256) group *= 2;
+    hipLaunchKernelGGL(loss_kernel, dim3((unsigned)code_up(M, group)), dim3(kLossThreads), 0, hs, part, logit, target,
+                       ignore_index, loss, lse, M, V, (int)s.blocks, group);
+    return hipGetLastError() == hipSuccess ? FP8MM_OK : FP8MM_ERR_LAUNCH;
+}
+
+int64_t fp8_linear_cross_entropy_backward_workspace_size(int64_t M, int64_t V, int64_t K, int want_dx, int want_dw) {
+    return loss_shape(M, V, K) != FP8MM_OK ? -1 : grad_space(M, V, K, want_dx != 0, want_dw != 0).total;
+}
+
+int fp8_linear_cross_entropy_backward(const float* dloss, int64_t dloss_stride, const void* A, int a_format,
+                                      const void* B, int b_format, const float* scale_a, const float* scale_b,
+                                      const int64_t* target, int64_t ignore_index, const float* loss,
+                                      const float* lse, const void* x, const void* wt, int wt_format,
+                                      const float* wt_scale, void* dx, void* dw, int64_t M, int64_t V, int64_t K,
+                                      int mode, struct ihipStream_t* stream, void* workspace,
+                                      int64_t workspace_bytes) {
+    int st = loss_shape(M, V, K);
+    if (st == FP8MM_OK && dloss_stride != 0 && dloss_stride != 1) st = FP8MM_ERR_SHAPE;
+    if (st == FP8MM_OK) st = loss_operands(A, a_format, B, b_format, scale_a, scale_b, target, mode, M);
+    if (st != FP8MM_OK) return st;
+    if (dx && wt_format != FP8MM_E4M3FN && wt_format != FP8MM_E5M2) return FP8MM_ERR_FORMAT;
+    if (M > 0 && ((!dx && !dw) || !dloss || !loss || !lse || (dx && (!wt || !wt_scale)) || (dw && !x)))
+        return FP8MM_ERR_NULL;
+    if (!at(dloss, 4) || !at(loss, 4) || !at(lse, 4) || !at(x, 2) || !at(wt, 16) || !at(wt_scale, 4) || !at(dx, 2) ||
+        !at(dw, 2) || !at(workspace, 256))
+        return FP8MM_ERR_ALIGN;
+    GradSpace g = grad_space(M, V, K, dx != nullptr, dw != nullptr);
+    if (M > 0 && (!workspace || workspace_bytes < g.total)) return FP8MM_ERR_WORKSPACE;
+    int dev = -1;
+    if (hipGetDevice(&dev) != hipSuccess) return FP8MM_ERR_DEVICE;
+    const hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+    (void)hipGetLastError();
+    if (M == 0) {
+        if (dw)
+            hipLaunchKernelGGL(zero_bf16_kernel, dim3(2048), dim3(256), 0, hs, static_cast<uint16_t*>(dw), V * K);
+        return hipGetLastError() == hipSuccess ? FP8MM_OK : FP8MM_ERR_LAUNCH;
+    }
+    std::lock_guard<std::mutex> together(fp8mm::enqueue_lock(workspace));
+    char* ws = static_cast<char*>(workspace);
+    auto f32 = [&](int64_t offset) { return reinterpret_cast<float*>(ws + offset); };
+    uint8_t* q = dx ? reinterpret_cast<uint8_t*>(ws + g.q) : nullptr;
+    uint8_t* qt = dw ? reinterpret_cast<uint8_t*>(ws + g.qt) : nullptr;
+    LossGrad p{};
+    p.dloss = dloss;
+    p.dloss_stride = dloss_stride;
+    p.target = target;
+    p.ignore = ignore_index;
+    p.loss = loss;
+    p.lse = lse;
+    p.M = M;
+    p.V = V;
+    p.rows = reinterpret_cast<float2*>(ws + g.rows);
+    p.factor = f32(g.factor);
+    p.row_scale = f32(g.row_scale);
+    p.ones = f32(g.ones);
+    p.num_ones = dw ? g.piece : 0;
+    p.counters = reinterpret_cast<uint32_t*>(ws);
+    p.num_counters = (int)(kCounterArea / 4);   // (a product leaves its counters at zero)
+    hipLaunchKernelGGL(loss_rows_kernel, dim3(256), dim3(256), 0, hs, p);
+    if (dw) {
+        CodeJob& c = g.x;
+        c.x = x;
+        c.factor = p.factor;
+        c.col_max = f32(g.partials);
+        c.col_scale = f32(g.col_scale);
+        c.q_cols = reinterpret_cast<uint8_t*>(ws + g.qx);
+        launch_codes<bf16_t, 0, true, false, false>(c, hs);
+    }
+    if (hipGetLastError() != hipSuccess) return FP8MM_ERR_LAUNCH;
+    const int64_t Vt = code_up(V, 16) * 16;
+    for (int64_t v0 = 0; v0 < V; v0 += g.piece) {
+        const int64_t n = V - v0 < g.piece ? V - v0 : g.piece;
+        const int64_t ldq = code_up(n, 16) * 16;
+        const fp8mm::LossPlan plan = n == g.piece ? g.plan : fp8mm::loss_plan(M, n, K);
+        const fp8mm::Logits z{A, a_format, static_cast<const uint8_t*>(B) + v0 * K, b_format, scale_a,
+                              mode == FP8MM_ROWWISE ? scale_b + v0 : scale_b, M, n, K, mode};
+        st = fp8mm::run_codes(z, plan, p.rows, q, ldq, qt, g.Mp, v0, hs, ws);
+        if (st != FP8MM_OK) return st;
+        uint16_t* dw_piece = static_cast<uint16_t*>(dw) + (dw ? v0 * K : 0);
+        if (g.one && dx && dw && wt_format == FP8MM_E4M3FN && g.pair.cfg >= 0) {
+            const fp8mm::Product two[2] = {
+                {q, wt, p.row_scale, wt_scale, dx, M, K, ldq},
+                {qt, ws + g.qx, p.ones, f32(g.col_scale), dw, V, K, g.Mp}};
+            return fp8mm::run_pair(two, g.pair, hs, ws);
+        }
+        if (dw) {
+            st = fp8_scaled_mm_typed(qt, FP8MM_E5M2, ws + g.qx, FP8MM_E4M3FN, p.ones, f32(g.col_scale), nullptr,
+                                     dw_piece, n, K, g.Mp, FP8MM_ROWWISE, stream, -1, 0, ws, g.rows);
+            if (st != FP8MM_OK) return st;
+        }
+        if (dx && g.one)
+            st = fp8_scaled_mm_typed(q, FP8MM_E5M2, wt, wt_format, p.row_scale, wt_scale, nullptr, dx, M, K, ldq,
+                                     FP8MM_ROWWISE, stream, -1, 0, ws, g.rows);
+        else if (dx)
+            st = fp8mm::run_sum({q, static_cast<const uint8_t*>(wt) + v0, wt_format, p.row_scale, wt_scale, dx, M, K,
+                                 ldq, Vt, v0 == 0, v0 + n == V},
+                                hs, ws + g.sums);
+        if (st != FP8MM_OK) return st;
+    }
+    return FP8MM_OK;
+}
+
+}  // extern "C"

@@ -81,7 +81,39 @@ struct LinearParams : Params {
     uint16_t* preact;           // M x N bf16, may be null
     int act;                    // enum Activation
 };
-template <bool EPI> using KernelParams = std::conditional_t<EPI, LinearParams, Params>;
+
+// With the cross entropy's epilogues (include/fp8_cross_entropy.h), which write
+// no product: kEpiStats, softmax statistics of each row, and kEpiCodes, the
+// gradient of the logits as e5m2 codes.
+struct LossParams : Params {
+    // kEpiStats
+    const int64_t* target;      // M
+    float2* part;               // [column block][M]: largest logit times log2(e), sum of
+                                // the exponentials over the largest one's
+    float* target_logit;        // M, times log2(e), written where the target is a column
+    // kEpiCodes
+    const float2* rows;         // M: log2 of the code's factor, target as an int's bits
+    uint8_t* q;                 // M x ldq, may be null
+    uint8_t* qt;                // N x ldqt, may be null
+    int ldq, ldqt;              // N and M rounded up to 16 or more (zeros there)
+    int col0;                   // B's first row in the vocabulary
+};
+
+// A product whose K range comes in pieces, one launch each (kEpiSum, ping-pong
+// kernel only): the unscaled fp32 sums go from launch to launch through
+// `partials` (num_tiles tiles).  Rows of B lie ldb bytes apart.
+struct SumParams : Params {
+    int ldb;
+    int first, last;
+};
+
+// Epilogues, the kernels' template parameter EPI.
+constexpr int kEpiScale = 0, kEpiLinear = 1, kEpiStats = 2, kEpiCodes = 3, kEpiSum = 4;
+template <int EPI> struct ParamsOf { typedef LossParams type; };
+template <> struct ParamsOf<kEpiScale> { typedef Params type; };
+template <> struct ParamsOf<kEpiLinear> { typedef LinearParams type; };
+template <> struct ParamsOf<kEpiSum> { typedef SumParams type; };
+template <int EPI> using KernelParams = typename ParamsOf<EPI>::type;
 
 // Two independent products in one launch (the PAIR instantiations; row-wise
 // scales, no bias): the grid's workgroups walk the units of p[0], then those of
@@ -148,6 +180,21 @@ extern LaunchPair kLinearF0[kNumConfigs];
 extern LaunchPair kLinearF1[kNumConfigs];
 extern LaunchPair kLinearF2[kNumConfigs];
 extern LaunchPair kLinearF3[kNumConfigs];
+
+// The same with the cross entropy's epilogues, defined in fp8_loss_f<k>.hip and
+// fp8_loss_grad_f<k>.hip.
+extern LaunchPair kStatsF0[kNumConfigs];
+extern LaunchPair kStatsF1[kNumConfigs];
+extern LaunchPair kStatsF2[kNumConfigs];
+extern LaunchPair kStatsF3[kNumConfigs];
+extern LaunchPair kCodesF0[kNumConfigs];
+extern LaunchPair kCodesF1[kNumConfigs];
+extern LaunchPair kCodesF2[kNumConfigs];
+extern LaunchPair kCodesF3[kNumConfigs];
+
+// The ping-pong kernel's launches with kEpiSum for A in e5m2 and B in e4m3fn or
+// e5m2, defined in fp8_loss_sum.hip.
+extern Launch kSum[2];
 
 // The generic configurations' pair launches for A in e5m2 and B in e4m3fn (the
 // linear layer's gradient), defined in fp8_linear_pair.hip.
@@ -1077,6 +1124,169 @@ __device__ __forceinline__ void epi_stage_and_store(
     }
 }
 
+// ------------------------------------------- the cross entropy's epilogues ---
+
+// Rows of JN blocks of a wave (first row m0, scales epi_sa) and its columns from
+// n0 on: this wave's share of each row's softmax statistics, as column block `block`
+// of p.part.  Logits are kept times log2(e), so that an exponential is a subtraction
+// and 2^x, and the largest one's exactly 1 (a row that is sure of its target keeps
+// what little the others add).  A lane holds FN * NACC logits of each of its rows,
+// the other kWave / MI - 1 lanes with the same lane % MI the rest.  A NaN or +inf among
+// the logits makes the sum a NaN.
+template <int MI, int FN, int JN>
+__device__ __forceinline__ void epi_stats(typename Mfma<MI>::acc_t (&z)[FN][JN], const LossParams& p, int m0,
+                                          int n0, int block, const float* epi_sa, const float* epi_sb, int lane) {
+    constexpr int G = Mfma<MI>::NACC / 4;
+    int target[JN];   // within the wave's columns, or outside them
+#pragma unroll
+    for (int j = 0; j < JN; ++j) {
+        const int m = m0 + j * MI + lane % MI;
+        const uint64_t t = m < p.M ? (uint64_t)p.target[m] - (uint64_t)n0 : ~0ull;
+        target[j] = t < (uint64_t)(FN * MI) ? (int)t : -1;
+    }
+    float sa_r[JN];
+#pragma unroll
+    for (int j = 0; j < JN; ++j) sa_r[j] = epi_sa[j * MI + lane % MI] * kLog2E;
+    const bool full = n0 + FN * MI <= p.N;
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const int cl = epi_col<MI>(i, g, lane);
+            const v4f sb_r = *reinterpret_cast<const v4f*>(epi_sb + cl);
+#pragma unroll
+            for (int j = 0; j < JN; ++j)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float v = z[i][j][4 * g + c] * (sa_r[j] * sb_r[c]);
+                    if (!full) v = n0 + cl + c < p.N ? v : -__builtin_inff();
+                    z[i][j][4 * g + c] = v;
+                }
+        }
+#pragma unroll
+    for (int j = 0; j < JN; ++j) {
+        const int m = m0 + j * MI + lane % MI;
+        float most = -__builtin_inff();
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int e = 0; e < 4 * G; ++e) most = fmaxf(most, z[i][j][e]);
+#pragma unroll
+        for (int d = MI; d < kWave; d *= 2) most = fmaxf(most, __shfl_xor(most, d));
+        const float from = most == -__builtin_inff() ? 0.f : most;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int e = 0; e < 4 * G; ++e)
+                sum += __builtin_amdgcn_exp2f(z[i][j][e] - from);
+#pragma unroll
+        for (int d = MI; d < kWave; d *= 2) sum += __shfl_xor(sum, d);
+        if (lane < MI && m < p.M) p.part[(size_t)block * p.M + m] = float2{most, sum};
+        if (__any(target[j] >= 0)) {
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int e = 0; e < 4 * G; ++e)
+                    if (epi_col<MI>(i, e / 4, lane) + e % 4 == target[j]) p.target_logit[m] = z[i][j][e];
+        }
+    }
+}
+
+// The e5m2 codes of the logits' gradient over the row's scale: 57344 p / h, at
+// the target -57344 (include/fp8_cross_entropy.h), as 2^(z log2(e) + f) with f from
+// p.rows.  Word w[i][j][g]: columns 4 .. of run g of block i in row j * MI + lane %
+// MI.  0 outside the matrix.
+template <int MI, int FN, int JN>
+__device__ __forceinline__ void epi_codes(const typename Mfma<MI>::acc_t (&acc)[FN][JN],
+                                          uint32_t (&w)[FN][JN][Mfma<MI>::NACC / 4], const LossParams& p, int m0,
+                                          int n0, const float* epi_sa, const float* epi_sb, int lane) {
+    constexpr int G = Mfma<MI>::NACC / 4;
+    constexpr float kMax = 57344.f;
+    const bool full = n0 + FN * MI <= p.N;
+    float sa_r[JN], f_r[JN];
+    int target[JN];
+#pragma unroll
+    for (int j = 0; j < JN; ++j) {
+        const int m = m0 + j * MI + lane % MI;
+        float2 r{-__builtin_inff(), __int_as_float(-1)};
+        if (m < p.M) r = p.rows[m];
+        sa_r[j] = epi_sa[j * MI + lane % MI] * kLog2E;
+        f_r[j] = r.x;
+        target[j] = __float_as_int(r.y) - p.col0 - n0;
+    }
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const int cl = epi_col<MI>(i, g, lane);
+            const v4f sb_r = *reinterpret_cast<const v4f*>(epi_sb + cl);
+#pragma unroll
+            for (int j = 0; j < JN; ++j) {
+                float y[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float e = __builtin_fmaf(acc[i][j][4 * g + c], sa_r[j] * sb_r[c], f_r[j]);
+                    y[c] = fminf(__builtin_amdgcn_exp2f(e), kMax);
+                    y[c] = cl + c == target[j] ? -kMax : y[c];
+                    if (!full) y[c] = n0 + cl + c < p.N ? y[c] : 0.f;
+                }
+                const int lo = __builtin_amdgcn_cvt_pk_bf8_f32(y[0], y[1], 0, false);
+                w[i][j][g] = (uint32_t)__builtin_amdgcn_cvt_pk_bf8_f32(y[2], y[3], lo, true);
+            }
+        }
+}
+
+// Four lanes' words of 4 bytes (lanes 4 a .. 4 a + 3), transposed: lane 4 a + b gets
+// byte b of each, in lane order.
+__device__ __forceinline__ uint32_t quad_transpose(uint32_t d, int lane) {
+    uint32_t t = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)d, 0xB1, 0xf, 0xf, true);   // lane ^ 1
+    d = __builtin_amdgcn_perm(t, d, lane & 1 ? 0x03070105u : 0x06020400u);
+    t = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)d, 0x4E, 0xf, 0xf, true);            // lane ^ 2
+    return __builtin_amdgcn_perm(t, d, lane & 2 ? 0x03020706u : 0x05040100u);
+}
+
+// Generic kernel: the tile's codes through two copies in LDS (rows of columns,
+// columns of rows), stored 16 bytes a lane.
+template <class C>
+__device__ __forceinline__ void epi_codes_tile(const typename Mfma<C::MI_>::acc_t (&acc)[C::FN][C::FM],
+                                               uint8_t* stg, const LossParams& p, int row0, int col0, int mbase,
+                                               int nbase, const float* epi_sa, const float* epi_sb, int lane,
+                                               int tid) {
+    constexpr int MI = C::MI_, G = Mfma<MI>::NACC / 4;
+    constexpr int RS = C::BN_ + 16, TS = C::BM_ + 16;
+    static_assert(C::BM_ * RS + C::BN_ * TS <= C::MAIN_BYTES && C::BM_ % 16 == 0 && C::BN_ % 16 == 0,
+                  "both copies of the codes fit the stage buffers");
+    uint8_t* stg_t = stg + C::BM_ * RS;
+    uint32_t w[C::FN][C::FM][G];
+    epi_codes<MI, C::FN, C::FM>(acc, w, p, row0 + mbase, col0 + nbase, epi_sa + mbase, epi_sb + nbase, lane);
+#pragma unroll
+    for (int i = 0; i < C::FN; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FM; ++j)
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const int r = mbase + j * MI + lane % MI, c = nbase + epi_col<MI>(i, g, lane);
+                *reinterpret_cast<uint32_t*>(stg + r * RS + c) = w[i][j][g];
+                *reinterpret_cast<uint32_t*>(stg_t + (c + lane % 4) * TS + (r & ~3)) = quad_transpose(w[i][j][g], lane);
+            }
+    barrier_lds();
+    if (p.q)
+        for (int x = tid; x < C::BM_ * (C::BN_ / 16); x += C::THREADS) {
+            const int r = x / (C::BN_ / 16), c = x % (C::BN_ / 16) * 16;
+            if (row0 + r < p.M && col0 + c < p.ldq)
+                *reinterpret_cast<v4i*>(p.q + (size_t)(row0 + r) * p.ldq + col0 + c) =
+                    *reinterpret_cast<const v4i*>(stg + r * RS + c);
+        }
+    if (p.qt)
+        for (int x = tid; x < C::BN_ * (C::BM_ / 16); x += C::THREADS) {
+            const int c = x / (C::BM_ / 16), r = x % (C::BM_ / 16) * 16;
+            if (col0 + c < p.N && row0 + r < p.ldqt)
+                *reinterpret_cast<v4i*>(p.qt + (size_t)(col0 + c) * p.ldqt + row0 + r) =
+                    *reinterpret_cast<const v4i*>(stg_t + c * TS + r);
+        }
+}
+
 // One K stage (BK bytes of K) of the software pipeline.  The fragments of
 // the stage's first K step are already in buffer CUR0.  Each step first
 // issues the LDS reads of the next step into the other buffer, then the MFMAs
@@ -1155,12 +1365,12 @@ __device__ __forceinline__ void run_stage(typename Mfma<C::MI_>::acc_t (&acc)[C:
     }
 }
 
-__device__ __forceinline__ const Params& first_product(const Params& p) { return p; }
-__device__ __forceinline__ const LinearParams& first_product(const LinearParams& p) { return p; }
+template <class P>
+__device__ __forceinline__ const P& first_product(const P& p) { return p; }
 __device__ __forceinline__ const Params& first_product(const PairParams& p) { return p.p[0]; }
 
 template <int BM, int BN, int BK, int WAVES_M, int WAVES_N, int STAGES, int MI, int GROUP_M,
-          bool NT_B, int FMT, bool SK = false, bool EPI = false, bool PAIR = false>
+          bool NT_B, int FMT, bool SK = false, int EPI = kEpiScale, bool PAIR = false>
 __global__ void __launch_bounds__(WAVES_M * WAVES_N * kWave,
                                   (Cfg<BM, BN, BK, WAVES_M, WAVES_N, STAGES, MI, GROUP_M>::OCCUPANCY))
 fp8_gemm_kernel(std::conditional_t<PAIR, PairParams, KernelParams<EPI>> args) {
@@ -1240,9 +1450,10 @@ fp8_gemm_kernel(std::conditional_t<PAIR, PairParams, KernelParams<EPI>> args) {
 
         // So is the residual, where a lane's share of it is small enough to be
         // held through the loop and this unit will need it for certain.
-        EpiResidual<MI, EPI ? C::FN : 1, EPI ? C::FM : 1> res;
+        constexpr bool kRes = EPI == kEpiLinear;
+        EpiResidual<MI, kRes ? C::FN : 1, kRes ? C::FM : 1> res;
         bool res_late = false;
-        if constexpr (EPI) {
+        if constexpr (kRes) {
             res_late = p.residual != nullptr;
             if (C::EARLY_RESIDUAL && res_late && nparts == 1) {
                 res.load(p, row0 + wm * C::WTM, col0 + wn * C::WTN, lane);
@@ -1349,7 +1560,7 @@ fp8_gemm_kernel(std::conditional_t<PAIR, PairParams, KernelParams<EPI>> args) {
             }
         }
 
-        if constexpr (EPI)
+        if constexpr (kRes)
             if (res_late) res.load(p, row0 + wm * C::WTM, col0 + wn * C::WTN, lane);
 
         // Epilogue parameters into LDS (beside the stage buffers).
@@ -1373,9 +1584,14 @@ fp8_gemm_kernel(std::conditional_t<PAIR, PairParams, KernelParams<EPI>> args) {
         // ones of slices past the end) must have landed.
         wait_vmcnt<0>();
         barrier_lds();
-        if constexpr (EPI)
+        if constexpr (EPI == kEpiLinear)
             epi_stage_and_store<C>(acc, smem, p, row0, col0, wm * C::WTM, wn * C::WTN, epi_sa, epi_sb,
                                    epi_bias, res, lane, tid);
+        else if constexpr (EPI == kEpiStats)
+            epi_stats<MI, C::FN, C::FM>(acc, p, row0 + wm * C::WTM, col0 + wn * C::WTN,
+                                        pn * WAVES_N + wn, epi_sa + wm * C::WTM, epi_sb + wn * C::WTN, lane);
+        else if constexpr (EPI == kEpiCodes)
+            epi_codes_tile<C>(acc, smem, p, row0, col0, wm * C::WTM, wn * C::WTN, epi_sa, epi_sb, lane, tid);
         else
             stage_and_store<C>(acc, smem, p, row0, col0, wm * C::WTM, wn * C::WTN, epi_sa, epi_sb,
                                epi_bias, s_pt, has_bias, lane, tid);
@@ -1501,16 +1717,35 @@ __device__ __forceinline__ void pp_dma(__amdgpu_buffer_rsrc_t r, uint8_t* dst, u
     dma16(r, dst, inside ? off : kOutOfRange, k0);
 }
 
+// This lane's id, recomputed (two VALU instructions) wherever the ping-pong
+// kernel needs it: volatile, so the compiler neither merges the calls nor
+// keeps the value live across the K loop (register pressure there made it
+// spill lane-derived values, and each reload of a spill waited for every
+// outstanding load, next tile's slices included).
+__device__ __forceinline__ int pp_lane() {
+    int l;
+    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
+    return l;
+}
+
 // Loads of slice s (K bytes s*BK ..) into stage buffer buf.  In the K-tail
 // slice, lanes whose chunk lies at or past K read zeros (offset beyond the
 // record limit).
+template <class P>
 __device__ __forceinline__ void pp_load_b(uint8_t* smem, int buf, int q, int s,
-                                          __amdgpu_buffer_rsrc_t rb, const PpLoads& L, int K) {
+                                          __amdgpu_buffer_rsrc_t rb, const PpLoads& L, const P& p) {
     const uint32_t k0 = (uint32_t)s * pp::BK;
-    const bool inside = k0 + L.cbyte < (uint32_t)K;
+    const bool inside = k0 + L.cbyte < (uint32_t)p.K;
     uint8_t* st = smem + buf * pp::STAGE_BYTES + pp::A_BYTES;
+    if constexpr (std::is_same_v<P, SumParams>) {   // rows of B further apart than A's
+        const uint32_t first = (uint32_t)((8 * q + pp_lane() / 8) * p.ldb) + L.cbyte;
 #pragma unroll
-    for (int i = 0; i < pp::NOFF; ++i) pp_dma(rb, st + (q + 4 * i) * 1024, L.off[i], k0, inside);
+        for (int i = 0; i < pp::NOFF; ++i)
+            pp_dma(rb, st + (q + 4 * i) * 1024, first + (uint32_t)(32 * i) * (uint32_t)p.ldb, k0, inside);
+    } else {
+#pragma unroll
+        for (int i = 0; i < pp::NOFF; ++i) pp_dma(rb, st + (q + 4 * i) * 1024, L.off[i], k0, inside);
+    }
 }
 
 template <bool BOTTOM>
@@ -1564,17 +1799,6 @@ __device__ __forceinline__ void pp_compute(pp::acc_t (&acc)[pp::FN][pp::FM],
 // One work unit: output tile t and its K slices kb .. kb + n - 1 (the whole
 // K range without split-K; one of `splits` consecutive ranges with it).  The
 // unit walks its slices starting at kb + rot and wraps (see the kernel head).
-// This lane's id, recomputed (two VALU instructions) wherever the ping-pong
-// kernel needs it: volatile, so the compiler neither merges the calls nor
-// keeps the value live across the K loop (register pressure there made it
-// spill lane-derived values, and each reload of a spill waited for every
-// outstanding load, next tile's slices included).
-__device__ __forceinline__ int pp_lane() {
-    int l;
-    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
-    return l;
-}
-
 // The offsets of PpLoads, made anew after the linear layer's epilogue so that
 // they take no registers from it.
 __device__ __forceinline__ PpLoads pp_loads(int K, int q, int lane) {
@@ -1597,7 +1821,8 @@ __device__ __forceinline__ int pp_slice(const PpTile& T, int step) {
     return T.kb + (s < T.n ? s : s - T.n);
 }
 
-__device__ __forceinline__ PpTile pp_tile(const Params& p, int u, int group_m, int xcd) {
+template <class P>
+__device__ __forceinline__ PpTile pp_tile(const P& p, int u, int group_m, int xcd) {
     PpTile T;
     T.t = u / p.splits;
     T.kb = (u - T.t * p.splits) * p.k_chunk;
@@ -1610,7 +1835,10 @@ __device__ __forceinline__ PpTile pp_tile(const Params& p, int u, int group_m, i
     const uint32_t rows_a = (uint32_t)min(pp::BM, p.M - T.row0);
     const uint32_t rows_b = (uint32_t)min(pp::BN, p.N - T.col0);
     T.ra = make_rsrc(p.A + (size_t)T.row0 * p.K, rows_a * (uint32_t)p.K);
-    T.rb = make_rsrc(p.B + (size_t)T.col0 * p.K, rows_b * (uint32_t)p.K);
+    if constexpr (std::is_same_v<P, SumParams>)   // (a slice's bytes past K are not loaded)
+        T.rb = make_rsrc(p.B + (size_t)T.col0 * p.ldb, (rows_b - 1) * (uint32_t)p.ldb + (uint32_t)p.K);
+    else
+        T.rb = make_rsrc(p.B + (size_t)T.col0 * p.K, rows_b * (uint32_t)p.K);
     return T;
 }
 
@@ -1627,7 +1855,7 @@ struct PpParams {
     uint16_t bias;
 };
 
-template <bool EPI>
+template <int EPI>
 __device__ __forceinline__ PpParams pp_params_load(const Params& p, const PpTile& T, int t,
                                                    bool has_bias, float s_pt) {
     PpParams v;
@@ -1647,10 +1875,11 @@ __device__ __forceinline__ void pp_params_store(const PpParams& v, int t, float*
 
 // A unit's first loads, all from group 0 (wave q): its first K slice whole
 // and A-top of its second.
-__device__ __forceinline__ void pp_tile_start(uint8_t* smem, const Params& p, const PpTile& T,
+template <class P>
+__device__ __forceinline__ void pp_tile_start(uint8_t* smem, const P& p, const PpTile& T,
                                               const PpLoads& L, int q) {
     const int s0 = pp_slice(T, 0);
-    pp_load_b(smem, 0, q, s0, T.rb, L, p.K);
+    pp_load_b(smem, 0, q, s0, T.rb, L, p);
     pp_load_a_half<false>(smem, 0, q, s0, T.ra, L, p.K);
     pp_load_a_half<true>(smem, 0, q, s0, T.ra, L, p.K);
     if (T.n > 1) pp_load_a_half<false>(smem, 1, q, pp_slice(T, 1), T.ra, L, p.K);
@@ -1932,7 +2161,101 @@ __device__ __forceinline__ bool pp_split_fixup(pp::acc_t (&acc)[pp::FN][pp::FM],
     return true;
 }
 
-template <int GROUP_M, int FMT, bool EPI = false>
+// The cross entropy's epilogues of one wave (128 x 64 logits), in bands of rows.
+__device__ __forceinline__ void pp_epi_stats(const pp::acc_t (&acc)[pp::FN][pp::FM], const LossParams& p,
+                                             const PpTile& T, int mbase, int q, const float* epi_sa,
+                                             const float* epi_sb) {
+    constexpr int MI = pp::MI, FN = pp::FN, JB = kPpBandBlocks;
+#pragma unroll
+    for (int band = 0; band < pp::FM / JB; ++band) {
+        pp::acc_t z[FN][JB];
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < JB; ++j) z[i][j] = acc[i][band * JB + j];
+        const int mb = mbase + band * 32;
+        epi_stats<MI, FN, JB>(z, p, T.row0 + mb, T.col0 + q * 64, T.col0 / 64 + q, epi_sa + mb, epi_sb + q * 64,
+                              pp_lane());
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// The codes go through the wave's 4 KiB staging area 64 rows at a time, first by
+// rows, then by columns: 64 x 64 bytes, 16-byte chunk c of line r at c ^ (r / 4) % 4,
+// which spreads a write's lanes over the banks.
+__device__ __forceinline__ void pp_codes_out(uint8_t* out, int ld, int lines, int line0, int at0, const uint8_t* stg,
+                                             int lane) {
+#pragma unroll
+    for (int pass = 0; pass < 4; ++pass) {
+        const int r = pass * 16 + lane / 4, c = lane % 4;
+        const v4i v = *reinterpret_cast<const v4i*>(stg + r * 64 + ((c ^ ((r >> 2) & 3)) * 16));
+        if (line0 + r < lines && at0 + c * 16 < ld)
+            *reinterpret_cast<v4i*>(out + (size_t)(line0 + r) * ld + at0 + c * 16) = v;
+    }
+}
+
+__device__ __forceinline__ void pp_epi_codes(const pp::acc_t (&acc)[pp::FN][pp::FM], const LossParams& p, int m0,
+                                             int n0, const float* epi_sa, const float* epi_sb, uint8_t* stg) {
+    constexpr int MI = pp::MI, FN = pp::FN, JH = 64 / MI, JB = kPpBandBlocks;
+#pragma unroll
+    for (int half = 0; half < pp::FM / JH; ++half) {
+        const int lane = pp_lane();
+        const int r0 = half * 64;
+        uint32_t w[FN][JH];
+#pragma unroll
+        for (int band = 0; band < JH / JB; ++band) {
+            pp::acc_t z[FN][JB];
+            uint32_t b[FN][JB][1];
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int j = 0; j < JB; ++j) z[i][j] = acc[i][half * JH + band * JB + j];
+            const int mb = r0 + band * JB * MI;
+            epi_codes<MI, FN, JB>(z, b, p, m0 + mb, n0, epi_sa + mb, epi_sb, lane);
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int j = 0; j < JB; ++j) w[i][band * JB + j] = b[i][j][0];
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        const int l = lane % MI, h = lane / MI;
+        if (p.q) {
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int j = 0; j < JH; ++j)
+                    *reinterpret_cast<uint32_t*>(stg + (j * MI + l) * 64 + ((i ^ ((l >> 2) & 3)) * 16) + h * 4) = w[i][j];
+            pp_codes_out(p.q, p.ldq, p.M, m0 + r0, n0, stg, lane);
+        }
+        if (p.qt) {
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int j = 0; j < JH; ++j)
+                    *reinterpret_cast<uint32_t*>(stg + (i * 16 + 4 * h + l % 4) * 64 + ((j ^ h) * 16) + (l & ~3)) =
+                        quad_transpose(w[i][j], lane);
+            pp_codes_out(p.qt, p.ldqt, p.N, n0, m0 + r0, stg, lane);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// A launch of a product in pieces: the sums so far into acc; false: they go on to
+// the next launch.
+template <class P>
+__device__ __forceinline__ bool pp_sum(pp::acc_t (&acc)[pp::FN][pp::FM], const P& p, int t, int wave, int lane) {
+    if constexpr (std::is_same_v<P, SumParams>) {
+        constexpr int PER_WAVE = 128 * 64;
+        float* at = p.partials + ((size_t)t * pp::WAVES + wave) * PER_WAVE;
+        if (!p.first) partial_accumulate<pp::FN, pp::FM>(acc, at, kWave, lane, PER_WAVE * 4);
+        if (p.last) return true;
+        partial_publish<pp::FN, pp::FM>(acc, at, kWave, lane, PER_WAVE * 4);
+        return false;
+    }
+    return true;
+}
+
+template <int GROUP_M, int FMT, int EPI = kEpiScale>
 __global__ void __launch_bounds__(pp::THREADS) fp8_gemm_pp_kernel(KernelParams<EPI> p) {
     using namespace pp;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[LDS_BYTES];
@@ -2003,7 +2326,7 @@ __global__ void __launch_bounds__(pp::THREADS) fp8_gemm_pp_kernel(KernelParams<E
             for (int s = 0; s < T.n; ++s) {
                 // memory phase 2s: fragments of slice s, B of slice s+1
                 pp_read(fa, fb, smem + (s & 1) * STAGE_BYTES, 0, q, pp_lane());
-                if (s + 1 < T.n) pp_load_b(smem, (s + 1) & 1, q, pp_slice(T, s + 1), T.rb, L, p.K);
+                if (s + 1 < T.n) pp_load_b(smem, (s + 1) & 1, q, pp_slice(T, s + 1), T.rb, L, p);
                 barrier_lds();
                 __builtin_amdgcn_sched_barrier(0);
                 // compute phase 2s+1
@@ -2026,10 +2349,15 @@ __global__ void __launch_bounds__(pp::THREADS) fp8_gemm_pp_kernel(KernelParams<E
             // rows all four waves of this group loaded, find them landed.
             const int un = u + G;
             if (!split || pp_split_fixup(acc, p, u, T.t, wave, pp_lane())) {
-                if constexpr (EPI)
+                if constexpr (EPI == kEpiLinear)
                     pp_epi_store(acc, p, T.row0, T.col0, 0, q * 64, epi_sa, epi_sb, epi_bias,
                                  smem + STG0 + q * STG_BYTES);
-                else
+                else if constexpr (EPI == kEpiStats)
+                    pp_epi_stats(acc, p, T, 0, q, epi_sa, epi_sb);
+                else if constexpr (EPI == kEpiCodes)
+                    pp_epi_codes(acc, p, T.row0 + 0, T.col0 + q * 64, epi_sa + 0, epi_sb + q * 64,
+                                 smem + STG0 + q * STG_BYTES);
+                else if (EPI != kEpiSum || pp_sum(acc, p, T.t, wave, pp_lane()))
                     pp_store(acc, p, T.row0, T.col0, 0, q * 64, epi_sa, epi_sb, epi_bias, s_pt,
                              has_bias, pp_lane(), smem + STG0 + q * STG_BYTES);
             }
@@ -2077,10 +2405,15 @@ __global__ void __launch_bounds__(pp::THREADS) fp8_gemm_pp_kernel(KernelParams<E
                 __builtin_amdgcn_sched_barrier(0);
             }
             if (!split || pp_split_fixup(acc, p, u, T.t, wave, pp_lane())) {
-                if constexpr (EPI)
+                if constexpr (EPI == kEpiLinear)
                     pp_epi_store(acc, p, T.row0, T.col0, 128, q * 64, epi_sa, epi_sb, epi_bias,
                                  smem + STG1 + q * STG_BYTES);
-                else
+                else if constexpr (EPI == kEpiStats)
+                    pp_epi_stats(acc, p, T, 128, q, epi_sa, epi_sb);
+                else if constexpr (EPI == kEpiCodes)
+                    pp_epi_codes(acc, p, T.row0 + 128, T.col0 + q * 64, epi_sa + 128, epi_sb + q * 64,
+                                 smem + STG1 + q * STG_BYTES);
+                else if (EPI != kEpiSum || pp_sum(acc, p, T.t, wave, pp_lane()))
                     pp_store(acc, p, T.row0, T.col0, 128, q * 64, epi_sa, epi_sb, epi_bias, s_pt,
                              has_bias, pp_lane(), smem + STG1 + q * STG_BYTES);
             }
@@ -2092,14 +2425,14 @@ __global__ void __launch_bounds__(pp::THREADS) fp8_gemm_pp_kernel(KernelParams<E
     }
 }
 
-template <int GROUP_M, int FMT, bool EPI = false>
+template <int GROUP_M, int FMT, int EPI = kEpiScale>
 void launch_pp(const Params& p, dim3 grid, hipStream_t stream) {
     hipLaunchKernelGGL((fp8_gemm_pp_kernel<GROUP_M, FMT, EPI>), grid, dim3(pp::THREADS), 0, stream,
                        static_cast<const KernelParams<EPI>&>(p));
 }
 
 template <int BM, int BN, int BK, int WAVES_M, int WAVES_N, int STAGES, int MI, int GROUP_M,
-          bool NT_B, int FMT, bool SK = false, bool EPI = false>
+          bool NT_B, int FMT, bool SK = false, int EPI = kEpiScale>
 void launch_cfg(const Params& p, dim3 grid, hipStream_t stream) {
     using C = Cfg<BM, BN, BK, WAVES_M, WAVES_N, STAGES, MI, GROUP_M, NT_B, FMT>;
     hipLaunchKernelGGL((fp8_gemm_kernel<BM, BN, BK, WAVES_M, WAVES_N, STAGES, MI, GROUP_M, NT_B, FMT, SK, EPI>),
@@ -2111,7 +2444,7 @@ template <int BM, int BN, int BK, int WAVES_M, int WAVES_N, int STAGES, int MI, 
 void launch_pair(const PairParams& p, dim3 grid, hipStream_t stream) {
     using C = Cfg<BM, BN, BK, WAVES_M, WAVES_N, STAGES, MI, GROUP_M>;
     hipLaunchKernelGGL((fp8_gemm_kernel<BM, BN, BK, WAVES_M, WAVES_N, STAGES, MI, GROUP_M, false, FMT, false,
-                                        false, true>),
+                                        kEpiScale, true>),
                        grid, dim3(C::THREADS), 0, stream, p);
 }
 
@@ -2147,8 +2480,8 @@ constexpr Launch stream_k_launch() {
 
 // The same for the linear layer's epilogue.
 #define FP8MM_LINEAR_PAIR(FMT, name, BM, BN, BK, WMW, WNW, ST, MI, GM)                        \
-    LaunchPair{&launch_cfg<BM, BN, BK, WMW, WNW, ST, MI, GM, false, FMT, false, true>,       \
-               &launch_cfg<BM, BN, BK, WMW, WNW, ST, MI, GM, true, FMT, false, true>, nullptr},
+    LaunchPair{&launch_cfg<BM, BN, BK, WMW, WNW, ST, MI, GM, false, FMT, false, kEpiLinear>, \
+               &launch_cfg<BM, BN, BK, WMW, WNW, ST, MI, GM, true, FMT, false, kEpiLinear>, nullptr},
 #define FP8MM_LINEAR_F(FMT) FP8MM_LINEAR_F_##FMT
 #define FP8MM_LINEAR_F_0(...) FP8MM_LINEAR_PAIR(0, __VA_ARGS__)
 #define FP8MM_LINEAR_F_1(...) FP8MM_LINEAR_PAIR(1, __VA_ARGS__)
@@ -2159,5 +2492,24 @@ constexpr Launch stream_k_launch() {
     namespace fp8mm {                                                             \
     LaunchPair NAME[kNumConfigs] = {                                              \
         FP8MM_GENERIC_CONFIGS(FP8MM_LINEAR_F(FMT))                                \
-        LaunchPair{&launch_pp<8, FMT, true>, nullptr, nullptr}};                  \
+        LaunchPair{&launch_pp<8, FMT, kEpiLinear>, nullptr, nullptr}};            \
+    }
+
+// The same for the cross entropy's epilogues (EPI: kEpiStats or kEpiCodes; one
+// table a file).
+#define FP8MM_LOSS_F(FMT) FP8MM_LOSS_F_##FMT
+#define FP8MM_LOSS_F_0(...) FP8MM_LOSS_PAIR(0, __VA_ARGS__)
+#define FP8MM_LOSS_F_1(...) FP8MM_LOSS_PAIR(1, __VA_ARGS__)
+#define FP8MM_LOSS_F_2(...) FP8MM_LOSS_PAIR(2, __VA_ARGS__)
+#define FP8MM_LOSS_F_3(...) FP8MM_LOSS_PAIR(3, __VA_ARGS__)
+#define FP8MM_LOSS_PAIR(FMT, name, BM, BN, BK, WMW, WNW, ST, MI, GM)                          \
+    LaunchPair{&launch_cfg<BM, BN, BK, WMW, WNW, ST, MI, GM, false, FMT, false, kLossEpi>,   \
+               &launch_cfg<BM, BN, BK, WMW, WNW, ST, MI, GM, true, FMT, false, kLossEpi>, nullptr},
+
+#define FP8MM_DEFINE_LOSS_TABLE(NAME, EPI, FMT)                                     \
+    namespace fp8mm {                                                             \
+    static constexpr int kLossEpi = EPI;                                          \
+    LaunchPair NAME[kNumConfigs] = {                                              \
+        FP8MM_GENERIC_CONFIGS(FP8MM_LOSS_F(FMT))                                  \
+        LaunchPair{&launch_pp<8, FMT, EPI>, nullptr, nullptr}};                   \
     }

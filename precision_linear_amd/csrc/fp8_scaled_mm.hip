@@ -28,7 +28,8 @@
 //
 // The kernels and their launch wrappers are in fp8_gemm_kernels.h; each
 // operand format pair's instances come from fp8_gemm_f<k>.hip, those with the
-// linear layer's epilogue (include/fp8_linear.h) from fp8_linear_f<k>.hip.
+// linear layer's epilogue (include/fp8_linear.h) from fp8_linear_f<k>.hip, those
+// with the cross entropy's (include/fp8_cross_entropy.h) from fp8_loss*.hip.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -39,6 +40,7 @@
 #include "../../include/fp8_linear.h"
 #include "../../include/fp8_scaled_mm.h"
 #include "fp8_gemm_kernels.h"
+#include "fp8_loss.h"
 #include "fp8_pair.h"
 #include "plan_cost_table.h"
 
@@ -54,6 +56,7 @@ struct ConfigInfo {
     int lds_bytes;
     int occupancy;   // workgroups per CU the persistent grid assumes
     bool stream_k_ok;
+    int waves_n;     // waves side by side in a tile
 };
 
 #define FP8MM_CFG_INFO(name, BM, BN, BK, WMW, WNW, ST, MI, GM)                               \
@@ -61,13 +64,13 @@ struct ConfigInfo {
                Cfg<BM, BN, BK, WMW, WNW, ST, MI, GM>::THREADS,                                \
                Cfg<BM, BN, BK, WMW, WNW, ST, MI, GM>::LDS_BYTES,                              \
                Cfg<BM, BN, BK, WMW, WNW, ST, MI, GM>::OCCUPANCY,                              \
-               Cfg<BM, BN, BK, WMW, WNW, ST, MI, GM>::STREAM_K_OK},
+               Cfg<BM, BN, BK, WMW, WNW, ST, MI, GM>::STREAM_K_OK, WNW},
 
 // Ids are the positions in this table (the C ABI's config_id).
 const ConfigInfo kConfigs[kNumConfigs] = {
     FP8MM_GENERIC_CONFIGS(FP8MM_CFG_INFO)
     ConfigInfo{"pp_bm256_bn256_bk128_w8_mfma16", pp::BM, pp::BN, pp::BK, true, pp::THREADS,
-               pp::LDS_BYTES, 1, false},
+               pp::LDS_BYTES, 1, false, pp::WAVES / 2},
 };
 #undef FP8MM_CFG_INFO
 
@@ -777,6 +780,109 @@ int run_pair(const Product (&q)[2], const PairPlan& plan, hipStream_t stream, vo
     const int64_t slots = (int64_t)cus * c.occupancy;
     (void)hipGetLastError();
     kPairF1[plan.cfg](args, dim3((unsigned)(units < slots ? units : slots)), stream);
+    return hipGetLastError() == hipSuccess ? FP8MM_OK : FP8MM_ERR_LAUNCH;
+}
+
+// ------------------------------------------------------- cross entropy ---
+
+// The multiply's plan for these sizes.  Its output's alignment plays no part, so
+// any vocabulary is planned as the next multiple of 16.
+LossPlan loss_plan(int64_t M, int64_t V, int64_t K) {
+    const int64_t n = cdiv(V, 16) * 16;
+    LossPlan plan;
+    plan.cfg = choose_config(M, n, K, FP8MM_ROWWISE, 0, true);
+    plan.splits = plan_splits(plan.cfg, M, n, K, 0);
+    return plan;
+}
+
+static int64_t loss_tiles(int64_t M, int64_t V, const LossPlan& plan) {
+    return cdiv(M, kConfigs[plan.cfg].bm) * cdiv(V, kConfigs[plan.cfg].bn);
+}
+
+bool loss_plan_fits(int64_t M, int64_t V, const LossPlan& plan) {
+    return loss_tiles(M, V, plan) * plan.splits <= INT32_MAX;
+}
+
+int64_t loss_blocks(int64_t V, const LossPlan& plan) {
+    return cdiv(V, kConfigs[plan.cfg].bn) * kConfigs[plan.cfg].waves_n;
+}
+
+int64_t loss_rows(int64_t M, const LossPlan& plan) { return cdiv(M, kConfigs[plan.cfg].bm) * kConfigs[plan.cfg].bm; }
+
+int64_t loss_workspace(int64_t M, int64_t V, const LossPlan& plan) {
+    return workspace_bytes(plan.cfg, M, V, plan.splits);
+}
+
+int loss_counters(int64_t M, int64_t V, const LossPlan& plan) {
+    return plan.splits > 1 ? (int)(loss_tiles(M, V, plan) * counters_per_tile(plan.cfg)) : 0;
+}
+
+static int run_loss(const LaunchPair* const (&tables)[kFormats], const Logits& z, const LossPlan& plan, LossParams& p,
+                    hipStream_t stream, void* ws) {
+    int dev = -1;
+    if (hipGetDevice(&dev) != hipSuccess) return FP8MM_ERR_DEVICE;
+    const int cus = device_cus(dev);
+    if (cus <= 0) return FP8MM_ERR_DEVICE;
+    const ConfigInfo& c = kConfigs[plan.cfg];
+    static_cast<Params&>(p) =
+        base_params(z.A, z.B, z.scale_a, z.scale_b, nullptr, nullptr, z.M, z.V, z.K, z.mode, c);
+    p.splits = plan.splits;
+    p.k_chunk = (int)cdiv(p.k_iters, plan.splits);
+    if (plan.splits > 1) {
+        p.counters = static_cast<unsigned*>(ws);
+        p.partials = reinterpret_cast<float*>(static_cast<char*>(ws) + kCounterBytes);
+    }
+    const int fmt = (z.a_format == FP8MM_E5M2 ? 1 : 0) | (z.b_format == FP8MM_E5M2 ? 2 : 0);
+    const LaunchPair& l = tables[fmt][plan.cfg];
+    const dim3 grid((unsigned)grid_for(plan.cfg, z.M, z.V, plan.splits, cus));
+    (void)hipGetLastError();
+    if (p.tiles_m == 1 && l.stream) l.stream(p, grid, stream);
+    else l.plain(p, grid, stream);
+    return hipGetLastError() == hipSuccess ? FP8MM_OK : FP8MM_ERR_LAUNCH;
+}
+
+int run_stats(const Logits& z, const LossPlan& plan, const int64_t* target, float2* part, float* target_logit,
+              hipStream_t stream, void* ws) {
+    static const LaunchPair* const tables[kFormats] = {kStatsF0, kStatsF1, kStatsF2, kStatsF3};
+    LossParams p{};
+    p.target = target;
+    p.part = part;
+    p.target_logit = target_logit;
+    return run_loss(tables, z, plan, p, stream, ws);
+}
+
+int run_codes(const Logits& z, const LossPlan& plan, const float2* rows, uint8_t* q, int64_t ldq, uint8_t* qt,
+              int64_t ldqt, int64_t col0, hipStream_t stream, void* ws) {
+    static const LaunchPair* const tables[kFormats] = {kCodesF0, kCodesF1, kCodesF2, kCodesF3};
+    LossParams p{};
+    p.rows = rows;
+    p.q = q;
+    p.ldq = (int)ldq;
+    p.qt = qt;
+    p.ldqt = (int)ldqt;
+    p.col0 = (int)col0;
+    return run_loss(tables, z, plan, p, stream, ws);
+}
+
+int64_t sum_workspace(int64_t M, int64_t N) {
+    const ConfigInfo& c = kConfigs[kPingPongConfig];
+    return cdiv(M, c.bm) * cdiv(N, c.bn) * c.bm * c.bn * 4;
+}
+
+int run_sum(const SumPiece& q, hipStream_t stream, void* sums) {
+    int dev = -1;
+    if (hipGetDevice(&dev) != hipSuccess) return FP8MM_ERR_DEVICE;
+    const int cus = device_cus(dev);
+    if (cus <= 0) return FP8MM_ERR_DEVICE;
+    SumParams p;
+    static_cast<Params&>(p) = base_params(q.A, q.B, q.scale_a, q.scale_b, nullptr, q.out, q.M, q.N, q.K,
+                                          FP8MM_ROWWISE, kConfigs[kPingPongConfig]);
+    p.partials = static_cast<float*>(sums);
+    p.ldb = (int)q.ldb;
+    p.first = q.first;
+    p.last = q.last;
+    (void)hipGetLastError();
+    kSum[q.b_format == FP8MM_E5M2](p, dim3((unsigned)grid_for(kPingPongConfig, q.M, q.N, 1, cus)), stream);
     return hipGetLastError() == hipSuccess ? FP8MM_OK : FP8MM_ERR_LAUNCH;
 }
 
