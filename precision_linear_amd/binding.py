@@ -72,6 +72,9 @@ CROSS_ENTROPY_EXPORTS = ("fp8_linear_cross_entropy", "fp8_linear_cross_entropy_w
                          "fp8_linear_cross_entropy_backward",
                          "fp8_linear_cross_entropy_backward_workspace_size")
 
+# functions from include/fp8_quantize_weight.h (status codes: those of fp8_scaled_mm.h)
+QUANTIZE_WEIGHT_EXPORTS = ("fp8_quantize_weight", "fp8_quantize_weight_workspace_size")
+
 # functions and status codes from include/fp8_layer_norm.h
 LAYER_NORM_EXPORTS = ("fp8_layer_norm", "fp8_layer_norm_backward",
                       "fp8_layer_norm_backward_workspace_size", "fp8_layer_norm_status_string")
@@ -164,6 +167,10 @@ def lib() -> ctypes.CDLL:
         L.fp8_linear_cross_entropy_backward.restype = i32
         L.fp8_linear_cross_entropy_backward_workspace_size.argtypes = [i64, i64, i64, i32, i32]
         L.fp8_linear_cross_entropy_backward_workspace_size.restype = i64
+        L.fp8_quantize_weight.argtypes = [vp, i32, i32, vp, vp, vp, vp, i64, i64, vp, vp, i64]
+        L.fp8_quantize_weight.restype = i32
+        L.fp8_quantize_weight_workspace_size.argtypes = [i64, i64]
+        L.fp8_quantize_weight_workspace_size.restype = i64
         f32 = ctypes.c_float
         L.fp8_layer_norm.argtypes = [vp, i32, vp, vp, i32, f32, vp, vp, i32, vp, vp, vp, i64, i64, vp]
         L.fp8_layer_norm.restype = i32
@@ -781,6 +788,55 @@ def fp8_quantize(x: torch.Tensor, mode="rowwise", q: torch.Tensor | None = None,
             raise ValueError(msg)
         raise RuntimeError(msg)
     return q, scale
+
+
+WeightCodes = collections.namedtuple("WeightCodes", "q scale qt scale_t")
+
+
+def fp8_quantize_weight(w: torch.Tensor, fmt="e4m3fn", *, q: torch.Tensor | None = None,
+                        scale: torch.Tensor | None = None, qt: torch.Tensor | None = None,
+                        scale_t: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> WeightCodes:
+    """Both layouts of an N x K bf16 or fp32 weight's float8 codes (uint8): q (N x K)
+    with a scale for each row, which forward products take as b, and qt (K x Np, Np = N
+    rounded up to 16, codes 0 past N) with a scale for each column of w, which gradients
+    take as wt.  The bits are those of fp8_quantize(w) and of its transpose, the
+    quotients correctly rounded.  K is a multiple of 16.  Each output may be passed to
+    reuse a buffer.  Partial maxima live in `workspace` (a GPU byte tensor with any
+    contents) or in memory that torch has back after the call."""
+    if fmt not in _FORMATS:
+        raise ValueError(f"fmt must be 'e4m3fn' or 'e5m2', got {fmt!r}")
+    f = _FORMATS[fmt]
+    _ln_matrix(w, "w")
+    N, K = w.shape
+    if K < 16 or K % 16 != 0:
+        raise ValueError(f"w's columns must be a multiple of 16, got {K}")
+    dev, device = w.get_device(), w.device
+    _check_devices(dev, (("q", q), ("scale", scale), ("qt", qt), ("scale_t", scale_t), ("workspace", workspace)))
+
+    def codes(t, name, rows, cols):
+        if t is None:
+            return torch.empty((rows, cols), dtype=torch.uint8, device=device)
+        if t.dtype not in (torch.uint8, torch.float8_e4m3fn if f == E4M3FN else torch.float8_e5m2) \
+                or t.shape != (rows, cols) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous uint8 (or float8_{fmt}) {rows} x {cols} tensor")
+        return t
+
+    def scales(t, name, n):
+        if t is None:
+            return torch.empty(n, dtype=torch.float32, device=device)
+        _ln_vector(t, name, n)
+        return t
+
+    q, qt = codes(q, "q", N, K), codes(qt, "qt", K, (N + 15) // 16 * 16)
+    scale, scale_t = scales(scale, "scale", N), scales(scale_t, "scale_t", K)
+    L = lib()
+    ws, ws_bytes = _scratch(device, workspace, ("weight", N, K), lambda: L.fp8_quantize_weight_workspace_size(N, K),
+                            "fp8_quantize_weight")
+    st = _call(dev, L.fp8_quantize_weight, w.data_ptr(), _LN_DTYPES[w.dtype], f, q.data_ptr(), scale.data_ptr(),
+               qt.data_ptr(), scale_t.data_ptr(), N, K, _stream_of(dev), ws.data_ptr(), ws_bytes)
+    if st != OK:
+        _mm_error("fp8_quantize_weight", st)
+    return WeightCodes(q, scale, qt, scale_t)
 
 
 # element types of the layer norm (enum fp8ln_dtype)
