@@ -84,10 +84,30 @@ _LN_ARG_ERRORS = {LN_ERR_NULL, LN_ERR_SHAPE, LN_ERR_ALIGN, LN_ERR_DTYPE, LN_ERR_
                   LN_ERR_VALUE}
 
 
+# functions and status codes from include/adamw.h
+ADAMW_EXPORTS = ("adamw_step", "adamw_status_string")
+(ADAMW_OK, ADAMW_ERR_NULL, ADAMW_ERR_SHAPE, ADAMW_ERR_ALIGN, ADAMW_ERR_DTYPE, ADAMW_ERR_VALUE, ADAMW_ERR_DEVICE,
+ ADAMW_ERR_LAUNCH, ADAMW_ERR_ALIAS) = range(9)
+_ADAMW_ARG_ERRORS = {ADAMW_ERR_NULL, ADAMW_ERR_SHAPE, ADAMW_ERR_ALIGN, ADAMW_ERR_DTYPE, ADAMW_ERR_VALUE,
+                     ADAMW_ERR_ALIAS}
+
+
+class _AdamwTensor(ctypes.Structure):        # struct adamw_tensor
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "grad", "exp_avg", "exp_avg_sq", "master", "exp_avg_scale",
+                                               "exp_avg_sq_scale")] + [("numel", ctypes.c_int64)]
+
+
+class _AdamwNumbers(ctypes.Structure):       # struct adamw_numbers
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay")] + \
+        [("step", ctypes.c_int64), ("seed", ctypes.c_uint32)] + \
+        [(n, ctypes.c_void_p) for n in ("lr_ptr", "step_ptr", "seed_ptr", "grad_scale_ptr")]
+
+
 # The entry points that _calls uses, in its order.
 _CALLS_ENTRIES = ("fp8_layer_norm", "fp8_layer_norm_backward", "fp8_layer_norm_backward_workspace_size",
                   "fp8_linear", "fp8_scaled_mm_workspace_size", "fp8_linear_backward",
-                  "fp8_linear_backward_workspace_size")
+                  "fp8_linear_backward_workspace_size", "fp8_linear_cross_entropy",
+                  "fp8_linear_cross_entropy_workspace_size", "adamw_step")
 
 
 class Fp8MMError(RuntimeError):
@@ -171,6 +191,10 @@ def lib() -> ctypes.CDLL:
         L.fp8_quantize_weight.restype = i32
         L.fp8_quantize_weight_workspace_size.argtypes = [i64, i64]
         L.fp8_quantize_weight_workspace_size.restype = i64
+        L.adamw_step.argtypes = [vp, i64, i32, i32, i32, vp, vp]
+        L.adamw_step.restype = i32
+        L.adamw_status_string.argtypes = [i32]
+        L.adamw_status_string.restype = ctypes.c_char_p
         f32 = ctypes.c_float
         L.fp8_layer_norm.argtypes = [vp, i32, vp, vp, i32, f32, vp, vp, i32, vp, vp, vp, i64, i64, vp]
         L.fp8_layer_norm.restype = i32
@@ -631,6 +655,13 @@ def fp8_linear_cross_entropy(a: torch.Tensor, b: torch.Tensor, scale_a: torch.Te
     (a mean over rows is loss.sum() / (target != ignore_index).sum()).  The partial
     results live in `workspace` (a GPU byte tensor with any contents) or in memory
     that torch has back after the call."""
+    if (_calls is not None and workspace is None and a_format is None and b_format is None
+            and isinstance(mode, (str, int))):
+        got = _calls.cross_entropy(a, b, scale_a, scale_b, target, ignore_index, _MODES.get(mode, -1))
+        if got.__class__ is tuple:
+            return got
+        if got is not None:
+            _mm_error("fp8_linear_cross_entropy", got)
     a, fa, b, fb, M, V, K, m, dev = _loss_args(a, b, scale_a, scale_b, target, ignore_index, mode, a_format,
                                                b_format, (("workspace", workspace),))
     L = lib()
@@ -1012,3 +1043,128 @@ def fp8_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tenso
     if st != LN_OK:
         _ln_error("fp8_layer_norm_backward", st)
     return dx, dw, db
+
+
+AdamWState = collections.namedtuple("AdamWState", "exp_avg exp_avg_sq exp_avg_scale exp_avg_sq_scale master")
+
+# Elements of a block of 8-bit moments.
+_ADAMW_BLOCK = 256
+
+
+def adamw_state(params, bits: int = 32, master: bool = False) -> AdamWState:
+    """The state of adamw_step's first step: moments of 0 in 32 bits, or in 8 with a scale
+    for each 256 elements of a tensor, and fp32 copies of the parameters if master.  Lists
+    of one tensor for each parameter (None: not needed)."""
+    if bits not in (8, 32):
+        raise ValueError(f"bits must be 8 or 32, got {bits!r}")
+    params = list(params)
+    for p in params:
+        if p.dtype not in _LN_DTYPES or not p.is_cuda or (master and p.dtype != torch.bfloat16):
+            raise ValueError("parameters must be bf16 or fp32 GPU tensors (with a master: bf16)")
+
+    def zeros(dtype, size=lambda p: p.shape):
+        return [torch.zeros(size(p), dtype=dtype, device=p.device) for p in params]
+
+    blocks = lambda p: (p.numel() + _ADAMW_BLOCK - 1) // _ADAMW_BLOCK      # noqa: E731
+    eight = bits == 8
+    moment = torch.float8_e4m3fn if eight else torch.float32
+    return AdamWState(zeros(moment), zeros(moment), zeros(torch.float32, blocks) if eight else None,
+                      zeros(torch.float32, blocks) if eight else None,
+                      [p.detach().float() for p in params] if master else None)
+
+
+def _adamw_list(ts, name: str, n: int, dtypes, shapes, dev: int):
+    """The addresses of a list of tensors of one of `dtypes` (None: no list)."""
+    if ts is None:
+        return [None] * n
+    if len(ts) != n:
+        raise ValueError(f"{name} must have one tensor for each of {n} parameters, got {len(ts)}")
+    for t, shape in zip(ts, shapes):
+        if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.dtype != ts[0].dtype or t.shape != shape \
+                or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous tensors of one type of {', '.join(map(str, dtypes))}, of the "
+                             f"parameters' shapes (scales: one for each {_ADAMW_BLOCK} elements)")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} has a tensor on {t.device}, expected cuda:{dev}")
+    return [t.data_ptr() for t in ts]
+
+
+def adamw_step(params, grads, exp_avg, exp_avg_sq, *, step, lr, betas=(0.9, 0.999), eps: float = 1e-8,
+               weight_decay: float = 0.01, master=None, exp_avg_scale=None, exp_avg_sq_scale=None,
+               grad_scale: torch.Tensor | None = None, seed=0) -> None:
+    """One AdamW step over lists of tensors, in place, in one launch for each 48 of them:
+
+        m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,   g = grad * grad_scale
+        p = p (1 - lr weight_decay) - lr m / (1 - beta1^step) / (sqrt(v / (1 - beta2^step)) + eps)
+
+    Parameters are fp32 or bf16, gradients either.  With `master`, fp32 copies of bf16
+    parameters, the step is theirs and the parameters are written rounded; without one,
+    steps below half a bf16 parameter's last bit are lost.  exp_avg and exp_avg_sq are
+    fp32, or e4m3fn codes (float8 or uint8) of m and of sqrt(v) with a scale for each 256
+    elements in exp_avg_scale and exp_avg_sq_scale (adamw_state makes them all); codes are
+    rounded up or down at random by a hash of `seed`, which should change from step to
+    step, and the element's place.  A gradient may be given to several parameters, anything
+    that is written only once.
+
+    step (from 1), lr and seed are numbers, or GPU tensors of one element (float32,
+    float32, int64) for a captured step; grad_scale is a float32 GPU tensor of one element
+    (1 / loss scale, a clipping factor) or None."""
+    if _calls is not None:
+        got = _calls.adamw_step(params, grads, exp_avg, exp_avg_sq, master, exp_avg_scale, exp_avg_sq_scale, step,
+                                lr, betas, eps, weight_decay, grad_scale, seed)
+        if got is not None:
+            if got != ADAMW_OK:
+                _adamw_error(got)
+            return
+    params, grads, exp_avg, exp_avg_sq, master, exp_avg_scale, exp_avg_sq_scale = (
+        ts if ts is None or isinstance(ts, (list, tuple)) else list(ts)
+        for ts in (params, grads, exp_avg, exp_avg_sq, master, exp_avg_scale, exp_avg_sq_scale))
+    n = len(params)
+    if n == 0:
+        return
+    first = params[0]
+    if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        raise ValueError("params must be GPU tensors")
+    dev = first.get_device()
+    shapes = [p.shape for p in params]
+    floats = tuple(_LN_DTYPES)
+    pp = _adamw_list(params, "params", n, floats, shapes, dev)
+    pg = _adamw_list(grads, "grads", n, floats, shapes, dev)
+    eight = len(exp_avg) == n and exp_avg[0].dtype != torch.float32
+    moment = (torch.float8_e4m3fn, torch.uint8) if eight else (torch.float32,)
+    pm = _adamw_list(exp_avg, "exp_avg", n, moment, shapes, dev)
+    pv = _adamw_list(exp_avg_sq, "exp_avg_sq", n, moment, shapes, dev)
+    if (exp_avg_scale is None) == eight or (exp_avg_sq_scale is None) == eight:
+        raise ValueError("exp_avg_scale and exp_avg_sq_scale belong to moments of 8 bits")
+    blocks = [((p.numel() + _ADAMW_BLOCK - 1) // _ADAMW_BLOCK,) for p in params]
+    ps = _adamw_list(exp_avg_scale, "exp_avg_scale", n, (torch.float32,), blocks, dev)
+    pvs = _adamw_list(exp_avg_sq_scale, "exp_avg_sq_scale", n, (torch.float32,), blocks, dev)
+    if master is not None and first.dtype != torch.bfloat16:
+        raise ValueError("a master belongs to bf16 parameters")
+    pw = _adamw_list(master, "master", n, (torch.float32,), shapes, dev)
+
+    numbers = _AdamwNumbers(beta1=betas[0], beta2=betas[1], eps=eps, weight_decay=weight_decay)
+    for name, value, dtype in (("lr", lr, torch.float32), ("step", step, torch.float32), ("seed", seed, torch.int64),
+                               ("grad_scale", grad_scale, torch.float32)):
+        if isinstance(value, torch.Tensor):
+            if value.dtype != dtype or value.numel() != 1 or value.get_device() != dev:
+                raise ValueError(f"{name} must be a {dtype} tensor of one element on cuda:{dev}")
+            setattr(numbers, name + "_ptr", value.data_ptr())
+        elif name == "grad_scale":
+            if value is not None:
+                raise ValueError("grad_scale must be a GPU tensor or None")
+        elif not isinstance(value, (int, float) if name == "lr" else int):
+            raise ValueError(f"{name} must be a number or a GPU tensor, got {value!r}")
+        else:
+            setattr(numbers, name, value & 0xffffffff if name == "seed" else value)
+    entries = (_AdamwTensor * n)(*(_AdamwTensor(*row) for row in
+                                   zip(pp, pg, pm, pv, pw, ps, pvs, (p.numel() for p in params))))
+    st = _call(dev, lib().adamw_step, ctypes.byref(entries), n, _LN_DTYPES[first.dtype], _LN_DTYPES[grads[0].dtype],
+               8 if eight else 32, ctypes.byref(numbers), _stream_of(dev))
+    if st != ADAMW_OK:
+        _adamw_error(st)
+
+
+def _adamw_error(st: int) -> None:
+    msg = f"adamw_step: {lib().adamw_status_string(st).decode()} (status {st})"
+    raise ValueError(msg) if st in _ADAMW_ARG_ERRORS else RuntimeError(msg)

@@ -21,7 +21,7 @@ ROOT = os.path.dirname(HERE)
 SRCS = [os.path.join(HERE, "csrc", f) for f in
         ["fp8_scaled_mm.hip"] + [f"fp8_{n}_f{k}.hip" for n in ("gemm", "loss_grad", "linear", "loss") for k in range(4)] +
         ["fp8_linear_pair.hip", "fp8_loss_sum.hip", "fp8_quantize.hip", "fp8_layer_norm.hip", "fp8_linear_grad.hip",
-         "fp8_cross_entropy.hip", "fp8_quantize_weight.hip"]]
+         "fp8_cross_entropy.hip", "fp8_quantize_weight.hip", "adamw.hip"]]
 HEADERS = [os.path.join(HERE, "csrc", f) for f in
            ("fp8_gemm_kernels.h", "fp8_convert.h", "lane_ops.h", "activation.h", "fp8_pair.h", "fp8_loss.h",
             "column_codes.h", "enqueue_lock.h", "plan_cost_table.h")]
@@ -56,7 +56,7 @@ SANITIZE_HOST = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize
                  "-Xarch_host", "-fno-sanitize-recover=undefined",
                  "-Xarch_host", "-fno-omit-frame-pointer", "-Xarch_host", "-g"]
 HOST_LOGIC_SRCS = {"fp8_scaled_mm.hip", "fp8_quantize.hip", "fp8_layer_norm.hip", "fp8_linear_grad.hip",
-                    "fp8_cross_entropy.hip", "fp8_quantize_weight.hip"}
+                    "fp8_cross_entropy.hip", "fp8_quantize_weight.hip", "adamw.hip"}
 
 
 def _calls_command(out):

@@ -1,0 +1,389 @@
+// The AdamW step over many tensors for gfx950 (MI355X) (formulas and the random
+// rounding: include/adamw.h).
+//
+// Bound by memory: with fp32 moments, an fp32 parameter and a bf16 gradient an element
+// is 14 bytes read and 12 written; with 8-bit moments 8 and 6.  The tensors' addresses go
+// into the kernel's arguments (48 tensors a launch), so nothing is copied to the GPU
+// beforehand and a capture holds them.  A workgroup takes 4096 elements of one tensor,
+// which it finds by the first chunks of all; a wave takes 256 elements, a block of the
+// 8-bit moments, at a time, with four of them in flight.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <vector>
+
+#include "../../include/adamw.h"
+#include "lane_ops.h"
+
+namespace {
+
+constexpr int kTensors = 48;              // of a launch (the arguments stay under 4 KiB)
+constexpr int kBlock = 256;               // elements of a block and of a wave at a time
+constexpr int kStepThreads = 256;
+constexpr int kWaves = kStepThreads / kWaveSize;
+constexpr int kInFlight = 4;              // blocks of a wave
+constexpr int kChunk = kBlock * kWaves * kInFlight;
+
+struct Entry {
+    void* param;
+    const void* grad;
+    void* m;
+    void* v;
+    float* master;
+    float* m_scale;
+    float* v_scale;
+    int64_t numel;
+    int64_t first_block;                  // blocks of the call's tensors before this one
+};
+
+struct StepArgs {
+    Entry t[kTensors];
+    uint32_t first_chunk[kTensors];
+    int count;
+    float beta1, beta1_rest, beta2, beta2_rest, eps;
+    float lr, weight_decay;
+    float corr1, corr2;                   // 1 / (1 - beta1^step), 1 / sqrt(1 - beta2^step)
+    uint32_t seed;
+    double log_beta1, log_beta2;
+    const float* lr_ptr;
+    const float* step_ptr;
+    const int64_t* seed_ptr;
+    const float* grad_scale_ptr;
+};
+static_assert(sizeof(StepArgs) <= 4096, "kernel arguments");
+
+// Four elements as they lie in memory, at any address that suits one.
+template <class T> struct Raw4;
+template <> struct Raw4<float> {
+    u32x4 v;
+    __device__ __forceinline__ float get(int i) const { return __uint_as_float(v[i]); }
+    __device__ __forceinline__ void set(const float (&f)[4]) {
+        v = u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+    }
+    typedef u32x4_a4 memory;
+};
+template <> struct Raw4<bf16_t> {
+    u32x2 v;
+    __device__ __forceinline__ float get(int i) const { return i % 2 ? bf16_hi(v[i / 2]) : bf16_lo(v[i / 2]); }
+    __device__ __forceinline__ void set(const float (&f)[4]) { v = u32x2{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3])}; }
+    typedef u32x2 memory __attribute__((aligned(2)));
+};
+template <> struct Raw4<uint8_t> {        // e4m3fn
+    uint32_t v;
+    __device__ __forceinline__ float get(int i) const {
+        return i == 0   ? __builtin_amdgcn_cvt_f32_fp8((int)v, 0)
+               : i == 1 ? __builtin_amdgcn_cvt_f32_fp8((int)v, 1)
+               : i == 2 ? __builtin_amdgcn_cvt_f32_fp8((int)v, 2)
+                        : __builtin_amdgcn_cvt_f32_fp8((int)v, 3);
+    }
+    __device__ __forceinline__ void set(const float (&f)[4]) {
+        const int w = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
+        v = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], w, true);
+    }
+    typedef uint32_t memory __attribute__((aligned(1)));
+};
+
+// The elements from `at` on, `left` of them (4 or more: all).
+template <bool NT, class T>
+__device__ __forceinline__ Raw4<T> load4(const T* p, int64_t at, int64_t left) {
+    Raw4<T> r;
+    if (left >= 4) {
+        r.v = load_hinted<NT, decltype(r.v)>(reinterpret_cast<const typename Raw4<T>::memory*>(p + at));
+    } else {
+        T e[4] = {};
+        for (int i = 0; i < left; ++i) e[i] = p[at + i];
+        __builtin_memcpy(&r.v, e, sizeof(e));
+    }
+    return r;
+}
+template <bool NT, class T>
+__device__ __forceinline__ void store4(T* p, int64_t at, int64_t left, const float (&f)[4]) {
+    Raw4<T> r;
+    r.set(f);
+    if (left >= 4) {
+        store_hinted<NT>(reinterpret_cast<typename Raw4<T>::memory*>(p + at), r.v);
+    } else {
+        T e[4];
+        __builtin_memcpy(e, &r.v, sizeof(e));
+        for (int i = 0; i < left; ++i) p[at + i] = e[i];
+    }
+}
+
+// 32 random bits of a position.
+__device__ __forceinline__ uint32_t random_bits(uint32_t n, uint32_t seed_part) {
+    uint32_t h = n * 0x6A09E667u + seed_part;
+    h = (h ^ (h >> 15)) * 0x3C6EF373u;
+    h = (h ^ (h >> 13)) * 0xA54FF53Bu;
+    return h ^ (h >> 16);
+}
+
+// y, |y| <= 448 up to a rounding, to one of its neighbours in e4m3fn: up (in
+// magnitude) where the part of a step that is left and r / 2^16 make one.  Below 2^-6
+// the steps are those of 2^-6, so that is added meanwhile.  NaN stays NaN.
+template <bool POSITIVE>
+__device__ __forceinline__ float round_at_random(float y, uint32_t r) {
+    float t = fabsf(y);
+    t = t > 448.f ? 448.f : t;
+    const float lift = t < 0x1p-6f ? 0x1p-6f : 0.f;
+    t = __uint_as_float((__float_as_uint(t + lift) + (r << 4)) & 0xfff00000u) - lift;
+    if (POSITIVE) return y > 0.f && t == 0.f ? 0x1p-9f : t;
+    return copysignf(t, y);
+}
+
+// The scale of a block whose largest magnitude is amax, and what values are
+// multiplied by.
+__device__ __forceinline__ float2 block_scale(float amax) {
+    float s = amax / 448.f;
+    if (s < 0x1p-100f) s = 0.f;
+    return float2{s, s == 0.f ? 0.f : 1.f / s};
+}
+
+template <class P, class G, int BITS, bool MASTER, bool NT>
+__global__ void __launch_bounds__(kStepThreads) adamw_kernel(StepArgs a) {
+    typedef std::conditional_t<BITS == 8, uint8_t, float> S;
+    typedef std::conditional_t<MASTER, float, P> W;       // what the step reads and writes
+    // This workgroup's tensor.
+    int lo = 0, hi = a.count;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (a.first_chunk[mid] <= blockIdx.x) lo = mid;
+        else hi = mid;
+    }
+    const Entry& e = a.t[lo];
+    const int64_t base = (int64_t)(blockIdx.x - a.first_chunk[lo]) * kChunk;
+    const int wave = threadIdx.x / kWaveSize, lane = threadIdx.x % kWaveSize;
+    W* w = MASTER ? reinterpret_cast<W*>(e.master) : static_cast<W*>(e.param);
+    P* param = static_cast<P*>(e.param);
+    const G* grad = static_cast<const G*>(e.grad);
+    S* m = static_cast<S*>(e.m);
+    S* v = static_cast<S*>(e.v);
+
+    // Blocks wave, wave + kWaves, ... of the chunk.
+    int64_t at[kInFlight], left[kInFlight];
+    Raw4<W> rw[kInFlight];
+    Raw4<G> rg[kInFlight];
+    Raw4<S> rm[kInFlight], rv[kInFlight];
+    float ms[kInFlight], vs[kInFlight];
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) {
+        at[u] = base + (u * kWaves + wave) * kBlock + lane * 4;
+        left[u] = e.numel - at[u];
+        rw[u] = load4<NT>(w, at[u], left[u]);
+        rg[u] = load4<NT>(grad, at[u], left[u]);
+        rm[u] = load4<NT>(m, at[u], left[u]);
+        rv[u] = load4<NT>(v, at[u], left[u]);
+        if constexpr (BITS == 8) {
+            const int64_t b = at[u] / kBlock;
+            const bool live = at[u] - lane * 4 < e.numel;
+            ms[u] = live ? e.m_scale[b] : 0.f;
+            vs[u] = live ? e.v_scale[b] : 0.f;
+        }
+    }
+    float lr = a.lr, corr1 = a.corr1, corr2 = a.corr2;
+    if (a.lr_ptr) lr = *a.lr_ptr;
+    if (a.step_ptr) {
+        const double t = (double)*a.step_ptr;
+        corr1 = (float)(-1.0 / expm1(t * a.log_beta1));
+        corr2 = (float)sqrt(-1.0 / expm1(t * a.log_beta2));
+    }
+    const float decay = 1.f - lr * a.weight_decay, rate = lr * corr1;
+    const float gs = a.grad_scale_ptr ? *a.grad_scale_ptr : 1.f;
+    const uint32_t seed = (a.seed_ptr ? (uint32_t)*a.seed_ptr : a.seed) * 0xBB67AE85u;
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) {
+        float fm[4], root[4], fv[4], fw[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float g = rg[u].get(i) * gs;
+            float m0 = rm[u].get(i), v0 = rv[u].get(i);
+            if constexpr (BITS == 8) {
+                m0 *= ms[u];
+                v0 *= vs[u];
+                v0 *= v0;
+            }
+            fm[i] = fmaf(a.beta1, m0, a.beta1_rest * g);
+            fv[i] = fmaf(a.beta2, v0, a.beta2_rest * (g * g));
+            root[i] = sqrtf(fv[i]);
+            const float step = fm[i] / fmaf(root[i], corr2, a.eps);
+            fw[i] = fmaf(rw[u].get(i), decay, -rate * step);
+        }
+        if constexpr (BITS == 8) {
+            float amax_m = 0.f, amax_v = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < left[u]) {
+                    amax_m = fmaxf(amax_m, fabsf(fm[i]));
+                    amax_v = fmaxf(amax_v, root[i]);
+                }
+            const float2 sm = block_scale(wave_max(amax_m)), sv = block_scale(wave_max(amax_v));
+            const uint32_t n = (uint32_t)e.first_block * (uint32_t)kBlock + (uint32_t)at[u];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t r = random_bits(n + i, seed);
+                fm[i] = round_at_random<false>(fm[i] * sm.y, r & 0xffff);
+                fv[i] = round_at_random<true>(root[i] * sv.y, r >> 16);
+            }
+            if (lane == 0 && left[u] > 0) {
+                e.m_scale[at[u] / kBlock] = sm.x;
+                e.v_scale[at[u] / kBlock] = sv.x;
+            }
+        }
+        store4<NT>(m, at[u], left[u], fm);
+        store4<NT>(v, at[u], left[u], fv);
+        store4<NT>(w, at[u], left[u], fw);
+        if constexpr (MASTER) store4<NT>(param, at[u], left[u], fw);
+    }
+}
+
+// ---------------------------------------------------------------- host ---
+
+template <class P, class G, int BITS, bool MASTER>
+void launch(const StepArgs& a, uint32_t chunks, bool stream_memory, hipStream_t hs) {
+    if (stream_memory)
+        hipLaunchKernelGGL((adamw_kernel<P, G, BITS, MASTER, true>), dim3(chunks), dim3(kStepThreads), 0, hs, a);
+    else
+        hipLaunchKernelGGL((adamw_kernel<P, G, BITS, MASTER, false>), dim3(chunks), dim3(kStepThreads), 0, hs, a);
+}
+
+typedef void (*StepLaunch)(const StepArgs&, uint32_t, bool, hipStream_t);
+// [gradient][32 bits][parameter: bf16, bf16 with a master, fp32]
+const StepLaunch kLaunches[2][2][3] = {
+    {{launch<bf16_t, bf16_t, 8, false>, launch<bf16_t, bf16_t, 8, true>, launch<float, bf16_t, 8, false>},
+     {launch<bf16_t, bf16_t, 32, false>, launch<bf16_t, bf16_t, 32, true>, launch<float, bf16_t, 32, false>}},
+    {{launch<bf16_t, float, 8, false>, launch<bf16_t, float, 8, true>, launch<float, float, 8, false>},
+     {launch<bf16_t, float, 32, false>, launch<bf16_t, float, 32, true>, launch<float, float, 32, false>}}};
+
+bool at_multiple(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+int check_numbers(const adamw_numbers& n) {
+    auto ok = [](double x) { return x >= 0.0 && std::isfinite(x); };
+    if (!ok(n.lr) || !ok(n.eps) || !ok(n.weight_decay) || !(n.beta1 >= 0.0 && n.beta1 < 1.0) ||
+        !(n.beta2 >= 0.0 && n.beta2 < 1.0) || (!n.step_ptr && n.step < 1))
+        return ADAMW_ERR_VALUE;
+    if (!at_multiple(n.lr_ptr, 4) || !at_multiple(n.step_ptr, 4) || !at_multiple(n.seed_ptr, 8) ||
+        !at_multiple(n.grad_scale_ptr, 4))
+        return ADAMW_ERR_ALIGN;
+    return ADAMW_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+const char* adamw_status_string(int s) {
+    switch (s) {
+        case ADAMW_OK: return "ok";
+        case ADAMW_ERR_NULL: return "a required pointer is NULL, or one is given that does not belong";
+        case ADAMW_ERR_SHAPE: return "a negative size, or more than 2^43 elements";
+        case ADAMW_ERR_ALIGN: return "a pointer is not aligned to its element";
+        case ADAMW_ERR_DTYPE: return "unknown type (parameters and gradients: bf16 or fp32, moments: 8 or 32 bits), or a master of fp32 parameters";
+        case ADAMW_ERR_VALUE: return "lr, betas, eps, weight_decay or step out of range";
+        case ADAMW_ERR_DEVICE: return "no usable HIP device";
+        case ADAMW_ERR_LAUNCH: return "kernel launch failed";
+        case ADAMW_ERR_ALIAS: return "a parameter or its state is given twice";
+        default: return "unknown status";
+    }
+}
+
+int adamw_step(const adamw_tensor* tensors, int64_t count, int param_dtype, int grad_dtype, int state_bits,
+               const adamw_numbers* numbers, struct ihipStream_t* stream) try {
+    if ((param_dtype != ADAMW_BF16 && param_dtype != ADAMW_FP32) ||
+        (grad_dtype != ADAMW_BF16 && grad_dtype != ADAMW_FP32) || (state_bits != 8 && state_bits != 32))
+        return ADAMW_ERR_DTYPE;
+    if (!numbers || (count > 0 && !tensors)) return ADAMW_ERR_NULL;
+    if (count < 0) return ADAMW_ERR_SHAPE;
+    const int st = check_numbers(*numbers);
+    if (st != ADAMW_OK) return st;
+    const uintptr_t pa = param_dtype == ADAMW_BF16 ? 2 : 4, ga = grad_dtype == ADAMW_BF16 ? 2 : 4;
+    const uintptr_t sa = state_bits == 8 ? 1 : 4;
+    const bool master = count > 0 && tensors[0].master != nullptr;
+    if (master && param_dtype == ADAMW_FP32) return ADAMW_ERR_DTYPE;
+    std::vector<const void*> written;
+    written.reserve((size_t)count * 3);
+    int64_t total = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        const adamw_tensor& t = tensors[i];
+        if (t.numel < 0 || t.numel > (int64_t(1) << 43) - total) return ADAMW_ERR_SHAPE;
+        total += t.numel;
+        if (t.numel == 0) continue;
+        const bool scales = state_bits == 8;
+        if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq || (t.master != nullptr) != master ||
+            (t.exp_avg_scale != nullptr) != scales || (t.exp_avg_sq_scale != nullptr) != scales)
+            return ADAMW_ERR_NULL;
+        if (!at_multiple(t.param, pa) || !at_multiple(t.grad, ga) || !at_multiple(t.exp_avg, sa) ||
+            !at_multiple(t.exp_avg_sq, sa) || !at_multiple(t.master, 4) || !at_multiple(t.exp_avg_scale, 4) ||
+            !at_multiple(t.exp_avg_sq_scale, 4))
+            return ADAMW_ERR_ALIGN;
+        written.push_back(t.param);
+        written.push_back(t.exp_avg);
+        written.push_back(t.exp_avg_sq);
+    }
+    std::sort(written.begin(), written.end());
+    if (std::adjacent_find(written.begin(), written.end()) != written.end()) return ADAMW_ERR_ALIAS;
+    int dev = -1;
+    if (hipGetDevice(&dev) != hipSuccess) return ADAMW_ERR_DEVICE;
+    const hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+    const int64_t bytes = total * (int64_t)((master ? 10 : 2 * pa) + ga + (state_bits == 8 ? 4 : 16));
+    StepArgs a;
+    a.beta1 = (float)numbers->beta1;
+    a.beta1_rest = (float)(1.0 - numbers->beta1);
+    a.beta2 = (float)numbers->beta2;
+    a.beta2_rest = (float)(1.0 - numbers->beta2);
+    a.eps = (float)numbers->eps;
+    a.lr = (float)numbers->lr;
+    a.weight_decay = (float)numbers->weight_decay;
+    a.log_beta1 = log(numbers->beta1);
+    a.log_beta2 = log(numbers->beta2);
+    const double step = numbers->step_ptr ? 1.0 : (double)numbers->step;
+    a.corr1 = (float)(-1.0 / expm1(step * a.log_beta1));
+    a.corr2 = (float)sqrt(-1.0 / expm1(step * a.log_beta2));
+    a.seed = numbers->seed;
+    a.lr_ptr = numbers->lr_ptr;
+    a.step_ptr = numbers->step_ptr;
+    a.seed_ptr = numbers->seed_ptr;
+    a.grad_scale_ptr = numbers->grad_scale_ptr;
+    const StepLaunch run = kLaunches[grad_dtype][state_bits == 32][param_dtype == ADAMW_FP32 ? 2 : master];
+    (void)hipGetLastError();
+    // A launch takes up to kTensors tensors and kMaxChunks chunks; a larger tensor is
+    // cut at whole blocks.
+    constexpr int64_t kMaxChunks = int64_t(1) << 22;
+    int64_t block = 0, chunks = 0;
+    a.count = 0;
+    auto flush = [&]() {
+        if (a.count > 0) run(a, (uint32_t)chunks, bytes > kCachedBytes, hs);
+        a.count = 0;
+        chunks = 0;
+    };
+    for (int64_t i = 0; i < count; ++i) {
+        const adamw_tensor& t = tensors[i];
+        for (int64_t done = 0; done < t.numel;) {
+            const int64_t n = std::min(t.numel - done, (kMaxChunks - chunks) * kChunk);
+            Entry& e = a.t[a.count];
+            auto step_on = [&](auto* p, int64_t size) {
+                return p ? (decltype(p))((uintptr_t)p + (uintptr_t)(done * size)) : p;
+            };
+            e.param = step_on(t.param, pa);
+            e.grad = step_on(t.grad, ga);
+            e.m = step_on(t.exp_avg, sa);
+            e.v = step_on(t.exp_avg_sq, sa);
+            e.master = step_on(t.master, 4);
+            e.m_scale = t.exp_avg_scale ? t.exp_avg_scale + done / kBlock : nullptr;
+            e.v_scale = t.exp_avg_sq_scale ? t.exp_avg_sq_scale + done / kBlock : nullptr;
+            e.numel = n;
+            e.first_block = block;
+            a.first_chunk[a.count++] = (uint32_t)chunks;
+            chunks += (n + kChunk - 1) / kChunk;
+            block += (n + kBlock - 1) / kBlock;
+            done += n;
+            if (a.count == kTensors || chunks == kMaxChunks) flush();
+        }
+    }
+    flush();
+    return hipGetLastError() == hipSuccess ? ADAMW_OK : ADAMW_ERR_LAUNCH;
+} catch (...) {
+    return ADAMW_ERR_SHAPE;   // (no host memory for the list)
+}
+
+}  // extern "C"

@@ -26,6 +26,8 @@
 #include <cstring>
 #include <vector>
 
+#include "../../include/adamw.h"
+#include "../../include/fp8_cross_entropy.h"
 #include "../../include/fp8_layer_norm.h"
 #include "../../include/fp8_linear.h"
 
@@ -41,6 +43,9 @@ struct Library {
     decltype(&fp8_scaled_mm_workspace_size) mm_workspace;
     decltype(&fp8_linear_backward) linear_backward;
     decltype(&fp8_linear_backward_workspace_size) linear_backward_workspace;
+    decltype(&fp8_linear_cross_entropy) cross_entropy;
+    decltype(&fp8_linear_cross_entropy_workspace_size) cross_entropy_workspace;
+    decltype(&adamw_step) adamw;
 };
 Library g_lib{};
 PyObject* g_workspace = nullptr;   // binding._workspace(device, stream, bytes, kind)
@@ -320,6 +325,159 @@ PyObject* linear_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// (a, b, scale_a, scale_b, target, ignore_index, mode) -> (loss, lse)
+PyObject* cross_entropy(PyObject*, PyObject* const* arg, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 7 || !g_lib.norm) Py_RETURN_NONE;
+    const Arg a(arg[0]), b(arg[1]), sa(arg[2]), sb(arg[3]), target(arg[4]);
+    const int dev = device_of(a);
+    if (dev < 0 || !PyLong_CheckExact(arg[5]) || !PyLong_CheckExact(arg[6])) Py_RETURN_NONE;
+    int overflow = 0;
+    const int64_t ignore = PyLong_AsLongLongAndOverflow(arg[5], &overflow);
+    const int mode = (int)PyLong_AsLong(arg[6]);
+    if (overflow || !a.on(dev) || !b.on(dev) || a.t->dim() != 2 || b.t->dim() != 2) Py_RETURN_NONE;
+    const int64_t M = a.t->size(0), K = a.t->size(1), V = b.t->size(0);
+    const int fa = code_format(*a.t), fb = code_format(*b.t);
+    const bool rowwise = mode == FP8MM_ROWWISE;
+    if (M == 0 || b.t->size(1) != K || fa < 0 || fb < 0 || (!rowwise && mode != FP8MM_PER_TENSOR) ||
+        !sa.vector(dev, at::kFloat, rowwise ? M : 1) || !sb.vector(dev, at::kFloat, rowwise ? V : 1) ||
+        !target.vector(dev, at::kLong, M) || target.t->dim() != 1)
+        Py_RETURN_NONE;
+    const int64_t need = g_lib.cross_entropy_workspace(M, V, K);
+    if (need < 0) Py_RETURN_NONE;
+    const hipStream_t stream = c10::hip::getCurrentHIPStream(dev).stream();
+    const at::Tensor ws = allocate(*a.t, {need}, at::kByte);
+    at::Tensor out[2];
+    for (at::Tensor& t : out) t = allocate(*a.t, {M}, at::kFloat);
+    int st;
+    {
+        pybind11::gil_scoped_release free_interpreter;
+        st = g_lib.cross_entropy(a.ptr(), fa, b.ptr(), fb, static_cast<const float*>(sa.ptr()),
+                                 static_cast<const float*>(sb.ptr()), static_cast<const int64_t*>(target.ptr()), ignore,
+                                 out[0].data_ptr<float>(), out[1].data_ptr<float>(), M, V, K, mode,
+                                 reinterpret_cast<ihipStream_t*>(stream), ws.data_ptr(), need);
+    }
+    if (st != FP8MM_OK) return PyLong_FromLong(st);
+    return tuple_of(out);
+    END_HANDLE_TH_ERRORS
+}
+
+// A list of tensors as adamw_step's must be: one for each parameter, of one type.
+struct List {
+    PyObject* const* items = nullptr;
+    Py_ssize_t size = 0;
+    bool given = false, ok = true;
+    explicit List(PyObject* o) {
+        if (o == Py_None) return;
+        given = true;
+        ok = PyList_CheckExact(o) || PyTuple_CheckExact(o);
+        if (!ok) return;
+        items = PySequence_Fast_ITEMS(o);
+        size = PySequence_Fast_GET_SIZE(o);
+    }
+    // Tensor i if it is on GPU `dev`, contiguous and of `type`, else null.
+    const at::Tensor* get(Py_ssize_t i, int dev, at::ScalarType type) const {
+        if (!THPVariable_CheckExact(items[i]) && !THPVariable_Check(items[i])) return nullptr;
+        const at::Tensor& t = THPVariable_Unpack(items[i]);
+        return t.is_cuda() && t.get_device() == dev && t.is_contiguous() && t.scalar_type() == type ? &t : nullptr;
+    }
+    at::ScalarType type() const {
+        return size > 0 && THPVariable_Check(items[0]) ? THPVariable_Unpack(items[0]).scalar_type() : at::kDouble;
+    }
+};
+
+// A number, or a tensor of one element on the GPU.
+bool number(PyObject* o, int dev, at::ScalarType type, double* value, const void** ptr) {
+    if (PyFloat_CheckExact(o)) *value = PyFloat_AS_DOUBLE(o);
+    else if (PyLong_CheckExact(o)) {
+        *value = PyLong_AsDouble(o);
+        if (PyErr_Occurred()) {
+            PyErr_Clear();
+            return false;
+        }
+    } else {
+        const Arg t(o);
+        if (!t.vector(dev, type, 1)) return false;
+        *ptr = t.ptr();
+    }
+    return true;
+}
+
+// (params, grads, exp_avg, exp_avg_sq, master, exp_avg_scale, exp_avg_sq_scale, step,
+// lr, betas, eps, weight_decay, grad_scale, seed) -> status
+PyObject* adamw(PyObject*, PyObject* const* arg, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 14 || !g_lib.norm) Py_RETURN_NONE;
+    const List p(arg[0]), g(arg[1]), m(arg[2]), v(arg[3]), w(arg[4]), ms(arg[5]), vs(arg[6]);
+    const Py_ssize_t count = p.size;
+    if (!p.ok || count == 0 || !THPVariable_Check(p.items[0])) Py_RETURN_NONE;
+    for (const List* l : {&g, &m, &v, &w, &ms, &vs})
+        if (!l->ok || (l->given && l->size != count)) Py_RETURN_NONE;
+    const at::Tensor& first = THPVariable_Unpack(p.items[0]);
+    if (!first.is_cuda() || c10::hip::current_device() != first.get_device()) Py_RETURN_NONE;
+    const int dev = first.get_device();
+    const at::ScalarType pt = p.type(), gt = g.type(), mt = m.type(), vt = v.type();
+    auto wide = [](at::ScalarType t) { return t == at::kFloat || t == at::kBFloat16; };
+    auto codes = [](at::ScalarType t) { return t == at::kByte || t == at::kFloat8_e4m3fn; };
+    const bool eight = codes(mt);
+    if (!g.given || !m.given || !v.given || !wide(pt) || !wide(gt) || (eight ? !codes(vt) : mt != at::kFloat || vt != at::kFloat) ||
+        ms.given != eight || vs.given != eight || (w.given && pt != at::kBFloat16))
+        Py_RETURN_NONE;
+    adamw_numbers num{};
+    double step = 1, seed = 0, grad_scale = 0;
+    const void *lr_ptr = nullptr, *step_ptr = nullptr, *seed_ptr = nullptr, *scale_ptr = nullptr;
+    if (!PyTuple_CheckExact(arg[9]) || PyTuple_GET_SIZE(arg[9]) != 2 || !PyFloat_Check(PyTuple_GET_ITEM(arg[9], 0)) ||
+        !PyFloat_Check(PyTuple_GET_ITEM(arg[9], 1)) || !PyFloat_Check(arg[10]) || !PyFloat_Check(arg[11]) ||
+        PyFloat_CheckExact(arg[7]) || PyFloat_CheckExact(arg[13]) ||
+        !number(arg[7], dev, at::kFloat, &step, &step_ptr) || !number(arg[8], dev, at::kFloat, &num.lr, &lr_ptr) ||
+        (arg[12] != Py_None && (!number(arg[12], dev, at::kFloat, &grad_scale, &scale_ptr) || !scale_ptr)))
+        Py_RETURN_NONE;
+    if (PyLong_CheckExact(arg[13])) num.seed = (uint32_t)PyLong_AsUnsignedLongLongMask(arg[13]);
+    else if (!number(arg[13], dev, at::kLong, &seed, &seed_ptr)) Py_RETURN_NONE;
+    if (!(step >= 1 && step < 9e15)) Py_RETURN_NONE;
+    num.step = (int64_t)step;
+    num.beta1 = PyFloat_AS_DOUBLE(PyTuple_GET_ITEM(arg[9], 0));
+    num.beta2 = PyFloat_AS_DOUBLE(PyTuple_GET_ITEM(arg[9], 1));
+    num.eps = PyFloat_AS_DOUBLE(arg[10]);
+    num.weight_decay = PyFloat_AS_DOUBLE(arg[11]);
+    num.lr_ptr = static_cast<const float*>(lr_ptr);
+    num.step_ptr = static_cast<const float*>(step_ptr);
+    num.seed_ptr = static_cast<const int64_t*>(seed_ptr);
+    num.grad_scale_ptr = static_cast<const float*>(scale_ptr);
+    std::vector<adamw_tensor> list((size_t)count);
+    for (Py_ssize_t i = 0; i < count; ++i) {
+        const at::Tensor *tp = p.get(i, dev, pt), *tg = g.get(i, dev, gt), *tm = m.get(i, dev, mt), *tv = v.get(i, dev, vt);
+        if (!tp || !tg || !tm || !tv || tg->sizes() != tp->sizes() || tm->sizes() != tp->sizes() ||
+            tv->sizes() != tp->sizes())
+            Py_RETURN_NONE;
+        adamw_tensor& t = list[(size_t)i];
+        t = adamw_tensor{tp->data_ptr(), tg->data_ptr(), tm->data_ptr(), tv->data_ptr(), nullptr, nullptr, nullptr,
+                         tp->numel()};
+        if (w.given) {
+            const at::Tensor* tw = w.get(i, dev, at::kFloat);
+            if (!tw || tw->sizes() != tp->sizes()) Py_RETURN_NONE;
+            t.master = tw->data_ptr<float>();
+        }
+        if (eight) {
+            const at::Tensor *a = ms.get(i, dev, at::kFloat), *b = vs.get(i, dev, at::kFloat);
+            const int64_t blocks = (t.numel + 255) / 256;
+            if (!a || !b || a->dim() != 1 || b->dim() != 1 || a->numel() != blocks || b->numel() != blocks) Py_RETURN_NONE;
+            t.exp_avg_scale = a->data_ptr<float>();
+            t.exp_avg_sq_scale = b->data_ptr<float>();
+        }
+    }
+    const hipStream_t stream = c10::hip::getCurrentHIPStream(dev).stream();
+    int st;
+    {
+        pybind11::gil_scoped_release free_interpreter;
+        st = g_lib.adamw(list.data(), count, pt == at::kFloat ? ADAMW_FP32 : ADAMW_BF16,
+                         gt == at::kFloat ? ADAMW_FP32 : ADAMW_BF16, eight ? 8 : 32, &num,
+                         reinterpret_cast<ihipStream_t*>(stream));
+    }
+    return PyLong_FromLong(st);
+    END_HANDLE_TH_ERRORS
+}
+
 // (addresses of the entry points in Library's order, workspace function)
 PyObject* use_library(PyObject*, PyObject* args) {
     constexpr int kEntries = sizeof(Library) / sizeof(void*);
@@ -351,7 +509,8 @@ constexpr PyMethodDef fast(const char* name) {
 
 PyMethodDef g_methods[] = {
     fast<layer_norm>("layer_norm"), fast<layer_norm_backward>("layer_norm_backward"), fast<linear>("linear"),
-    fast<linear_backward>("linear_backward"), {"use_library", use_library, METH_VARARGS, nullptr},
+    fast<linear_backward>("linear_backward"), fast<cross_entropy>("cross_entropy"), fast<adamw>("adamw_step"),
+    {"use_library", use_library, METH_VARARGS, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

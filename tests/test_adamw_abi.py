@@ -1,0 +1,111 @@
+"""Host-side checks of the AdamW step's C ABI and binding: exports, structures and
+every refusal before anything touches a device."""
+import ctypes
+import math
+import os
+import re
+
+import pytest
+import torch
+
+from precision_linear_amd import binding
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+P = 0x10000          # a 64 KiB-aligned fake device address, never dereferenced
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(binding.library_path):
+        from precision_linear_amd import build
+        build.build()
+    return binding.lib()
+
+
+def test_exports_every_declared_function(L):
+    text = open(os.path.join(ROOT, "include", "adamw.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    names = set(re.findall(r"\b(adamw_\w+)\s*\(", text))
+    assert names == set(binding.ADAMW_EXPORTS)
+    for n in names:
+        assert hasattr(L, n), n
+
+
+def test_status_strings(L):
+    for s in range(9):
+        assert L.adamw_status_string(s) != b"unknown status"
+    assert L.adamw_status_string(9) == b"unknown status"
+
+
+def test_structures_as_in_the_header():
+    text = open(os.path.join(ROOT, "include", "adamw.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    for name, struct in (("adamw_tensor", binding._AdamwTensor), ("adamw_numbers", binding._AdamwNumbers)):
+        body = re.search(r"struct %s \{(.*?)\}" % name, text, flags=re.S).group(1)
+        fields = [f for line in body.split(";") for f in re.findall(r"\*?(\w+)(?:,|$)", line.strip())]
+        assert fields == [f[0] for f in struct._fields_]
+
+
+def tensor(i=0, **kw):
+    at = lambda k: P * (8 * i + k + 1)                      # noqa: E731
+    t = dict(param=at(0), grad=at(1), exp_avg=at(2), exp_avg_sq=at(3), master=None, exp_avg_scale=None,
+             exp_avg_sq_scale=None, numel=1000)
+    return binding._AdamwTensor(**{**t, **kw})
+
+
+def call(L, tensors, pd=1, gd=1, bits=32, count=None, numbers=True, **kw):
+    n = binding._AdamwNumbers(**{**dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.1, step=1), **kw})
+    array = (binding._AdamwTensor * max(1, len(tensors)))(*tensors)
+    return L.adamw_step(ctypes.byref(array), len(tensors) if count is None else count, pd, gd, bits,
+                        ctypes.byref(n) if numbers else None, None)
+
+
+E = binding
+
+
+@pytest.mark.parametrize("t,kw,code", [
+    ({}, dict(pd=2), E.ADAMW_ERR_DTYPE), ({}, dict(gd=-1), E.ADAMW_ERR_DTYPE), ({}, dict(bits=16), E.ADAMW_ERR_DTYPE),
+    (dict(master=P * 7), dict(), E.ADAMW_ERR_DTYPE), ({}, dict(numbers=False), E.ADAMW_ERR_NULL),
+    ({}, dict(count=-1), E.ADAMW_ERR_SHAPE), (dict(numel=-1), dict(), E.ADAMW_ERR_SHAPE),
+    (dict(numel=1 << 44), dict(), E.ADAMW_ERR_SHAPE),
+    (dict(param=None), dict(), E.ADAMW_ERR_NULL), (dict(grad=None), dict(), E.ADAMW_ERR_NULL),
+    (dict(exp_avg=None), dict(), E.ADAMW_ERR_NULL), (dict(exp_avg_sq=None), dict(), E.ADAMW_ERR_NULL),
+    (dict(exp_avg_scale=P), dict(), E.ADAMW_ERR_NULL), ({}, dict(bits=8), E.ADAMW_ERR_NULL),
+    (dict(exp_avg_scale=P * 6), dict(bits=8), E.ADAMW_ERR_NULL),
+    (dict(param=P + 2), dict(), E.ADAMW_ERR_ALIGN), (dict(param=P + 1), dict(pd=0), E.ADAMW_ERR_ALIGN),
+    (dict(grad=P + 2), dict(), E.ADAMW_ERR_ALIGN), (dict(exp_avg=P + 2), dict(), E.ADAMW_ERR_ALIGN),
+    (dict(master=P * 7 + 2), dict(pd=0), E.ADAMW_ERR_ALIGN),
+    (dict(exp_avg_scale=P * 6 + 1, exp_avg_sq_scale=P * 7), dict(bits=8), E.ADAMW_ERR_ALIGN),
+    (dict(exp_avg=P), dict(), E.ADAMW_ERR_ALIAS),
+    ({}, dict(lr=-1.0), E.ADAMW_ERR_VALUE), ({}, dict(lr=math.inf), E.ADAMW_ERR_VALUE),
+    ({}, dict(lr=math.nan), E.ADAMW_ERR_VALUE), ({}, dict(beta1=1.0), E.ADAMW_ERR_VALUE),
+    ({}, dict(beta2=-0.5), E.ADAMW_ERR_VALUE), ({}, dict(beta2=math.nan), E.ADAMW_ERR_VALUE),
+    ({}, dict(eps=-1.0), E.ADAMW_ERR_VALUE), ({}, dict(weight_decay=math.inf), E.ADAMW_ERR_VALUE),
+    ({}, dict(step=0), E.ADAMW_ERR_VALUE), ({}, dict(lr_ptr=P + 2), E.ADAMW_ERR_ALIGN),
+    ({}, dict(seed_ptr=P + 4), E.ADAMW_ERR_ALIGN),
+])
+def test_refusals(L, t, kw, code):
+    assert call(L, [tensor(**t)], **kw) == code
+
+
+def test_lists(L):
+    assert call(L, [tensor(0), tensor(0)]) == E.ADAMW_ERR_ALIAS
+    assert call(L, [tensor(0), tensor(1, exp_avg_sq=P * 4)]) == E.ADAMW_ERR_ALIAS
+    assert call(L, [tensor(0, master=P * 7), tensor(1)], pd=0) == E.ADAMW_ERR_NULL
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present: these cases would launch on fake pointers")
+    reached = (E.ADAMW_ERR_DEVICE, E.ADAMW_ERR_LAUNCH)
+    assert call(L, [tensor(0), tensor(1)]) in reached
+    assert call(L, [tensor(0, grad=P), tensor(1, grad=P)]) in reached
+    assert call(L, [tensor(0)], step=0, step_ptr=P) in reached
+    assert call(L, [tensor(0, exp_avg=P * 3 + 1, exp_avg_scale=P * 6, exp_avg_sq_scale=P * 7)], bits=8) in reached
+
+
+def test_binding_refuses_before_the_library():
+    p, g = [torch.zeros(4)], [torch.zeros(4)]
+    for args in ((p, g, g, g), (p, [], g, g), ([3], g, g, g), (p, g, [], g)):
+        with pytest.raises(ValueError):
+            binding.adamw_step(*args, step=1, lr=0.1)
+    with pytest.raises(ValueError):
+        binding.adamw_state(p)
+    assert binding.adamw_step([], [], [], [], step=1, lr=0.1) is None
