@@ -2,13 +2,13 @@
 // them, with one scale for each row, in place: the two layouts in which products
 // over the columns and over the rows take their operands.
 //
-// For x (M x K, bf16 or fp32, times factor[m] if given):
+// For x (M x K, bf16 or fp32, its rows times factors if given):
 //     q_cols[k][m] = RNE(x[m][k] / col_scale[k]),  col_scale[k] = max_m |x| / qmax
 //     q_rows[m][k] = RNE(x[m][k] / row_scale[m]),  row_scale[m] = max_k |x| / qmax
 // with correctly rounded quotients, as in fp8_quantize.h.  Both need maxima of whole
 // rows and columns, so x is read twice:
 //   1. maxima_kernel: partial maxima of columns (by strips of rows) and of rows (by
-//      blocks of columns);
+//      blocks of columns), with the rows' factors made on the way;
 //   2. scales_kernel joins them, unless they are so few that pass 3 does it itself;
 //   3. codes_kernel.
 // A row whose factor is 0 counts as zeros whatever it holds.
@@ -29,9 +29,17 @@ constexpr int kCodeRowLanes = kCodeThreads / kCodeColLanes;  // 16
 constexpr int kCodeUnroll = 4;                               // rows in flight per thread in pass 1
 constexpr int kCodeJoin = 64;                                // partial maxima that pass 3 joins itself
 
+// A kernel argument that makes the rows' factors in pass 1: of(m, write) is row m's,
+// and where `write` is set leaves it in `factor`; begin() is what else the launch does.
+struct NoFactor {
+    static constexpr bool kGiven = false;
+    __device__ __forceinline__ void begin() const {}
+    __device__ __forceinline__ float of(int64_t, bool) const { return 1.f; }
+};
+
 struct CodeJob {
     const void* x;
-    const float* factor;   // M, may be null
+    const float* factor;   // M, for pass 3 where there are factors
     int64_t M, K;
     int64_t Mp;            // row length of q_cols, M rounded up to 16 or more (zeros there)
     int blocks, parts;     // column blocks, strips of rows in pass 1
@@ -57,9 +65,11 @@ __device__ __forceinline__ void code_values(const Raw8<T>& a, float factor, floa
     }
 }
 
-template <class T, bool FACTOR, bool ROWS, bool NT>
-__global__ void __launch_bounds__(kCodeThreads) maxima_kernel(CodeJob p) {
+template <class T, class F, bool ROWS, bool NT>
+__global__ void __launch_bounds__(kCodeThreads) maxima_kernel(CodeJob p, F factors) {
+    constexpr bool FACTOR = F::kGiven;
     __shared__ float s_max[kCodeRowLanes][kCodeCols];
+    factors.begin();
     const T* x = static_cast<const T*>(p.x);
     const int cl = threadIdx.x % kCodeColLanes, rl = threadIdx.x / kCodeColLanes;
     const int part = blockIdx.x / p.blocks, cb = blockIdx.x - part * p.blocks;
@@ -76,11 +86,14 @@ __global__ void __launch_bounds__(kCodeThreads) maxima_kernel(CodeJob p) {
         for (int u = 0; u < kCodeUnroll; ++u) {
             const int64_t row = r + u * kCodeRowLanes;
             a[u].zero();
+            if (ok && row < r1) a[u].template load<NT>(x + row * p.K + col);
+        }
+#pragma unroll
+        for (int u = 0; u < kCodeUnroll; ++u) {
+            const int64_t row = r + u * kCodeRowLanes;
             factor[u] = 1.f;
-            if (row < r1) {
-                if (ok) a[u].template load<NT>(x + row * p.K + col);
-                if constexpr (FACTOR) factor[u] = p.factor[row];
-            }
+            if constexpr (FACTOR)
+                if (row < r1) factor[u] = factors.of(row, cb == 0 && cl == 0);
         }
 #pragma unroll
         for (int u = 0; u < kCodeUnroll; ++u) {
@@ -109,16 +122,17 @@ __global__ void __launch_bounds__(kCodeThreads) maxima_kernel(CodeJob p) {
     p.col_max[part * p.K + c] = m;
 }
 
-// The largest of p[0], p[n], ... of `parts` values, every step-th from `first` on, 8
-// loaded at a time.
+// The largest of p[0], p[n], ... of `parts` values, every step-th from `first` on, U
+// loaded at a time (one memory latency).
+template <int U>
 __device__ __forceinline__ float join_max(const float* p, int64_t n, int parts, int first, int step) {
     float m = 0.f;
-    for (int q0 = first; q0 < parts; q0 += step * 8) {
-        float v[8];
+    for (int q0 = first; q0 < parts; q0 += step * U) {
+        float v[U];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = q0 + step * k < parts ? p[(q0 + step * k) * n] : 0.f;
+        for (int k = 0; k < U; ++k) v[k] = q0 + step * k < parts ? p[(q0 + step * k) * n] : 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) m = fmaxf(m, v[k]);
+        for (int k = 0; k < U; ++k) m = fmaxf(m, v[k]);
     }
     return m;
 }
@@ -133,7 +147,7 @@ __global__ void __launch_bounds__(kScaleGroup* kScaleSlices) scales_kernel(CodeJ
     const int64_t n = rows ? p.M : p.K;
     const int64_t i = (int64_t)(rows ? blockIdx.x : blockIdx.x - blocks_rows) * kScaleGroup + lane;
     float* part = rows ? p.row_max : p.col_max;
-    s_max[slice][lane] = i < n ? join_max(part + i, n, rows ? p.blocks : p.parts, slice, kScaleSlices) : 0.f;
+    s_max[slice][lane] = i < n ? join_max<8>(part + i, n, rows ? p.blocks : p.parts, slice, kScaleSlices) : 0.f;
     __syncthreads();
     if (slice != 0 || i >= n) return;
     float m = 0.f;
@@ -180,7 +194,7 @@ __global__ void __launch_bounds__(kCodeThreads) codes_kernel(CodeJob p, int col_
             const int64_t c = (int64_t)cb * kCodeCols + t;
             float s = 0.f;
             if (c < p.K) {
-                s = join_max(p.col_max + c, p.K, col_parts, 0, 1) / kMax;
+                s = join_max<32>(p.col_max + c, p.K, col_parts, 0, 1) / kMax;
                 if (strip == 0) p.col_scale[c] = s / p.col_unit;
             }
             const Div d = make_div(s);
@@ -192,7 +206,7 @@ __global__ void __launch_bounds__(kCodeThreads) codes_kernel(CodeJob p, int col_
             float s = 0.f, factor = 1.f;
             if (r < p.M) {
                 if constexpr (ROWS) {
-                    s = join_max(p.row_max + r, p.M, row_parts, 0, 1) / kMax;
+                    s = join_max<32>(p.row_max + r, p.M, row_parts, 0, 1) / kMax;
                     if (cb == 0) p.row_scale[r] = s;
                 }
                 if constexpr (FACTOR) factor = p.factor[r];
@@ -285,10 +299,11 @@ inline bool code_grid_ok(int64_t M, int64_t K) {
     return code_up(M, 64) * code_up(K, kCodeCols) <= INT32_MAX;
 }
 
-template <class T, int FMT, bool FACTOR, bool ROWS, bool NT>
-void launch_codes(const CodeJob& p, hipStream_t hs) {
-    hipLaunchKernelGGL((maxima_kernel<T, FACTOR, ROWS, NT>), dim3((unsigned)((int64_t)p.parts * p.blocks)),
-                       dim3(kCodeThreads), 0, hs, p);
+template <class T, int FMT, bool ROWS, bool NT, class F>
+void launch_codes(const CodeJob& p, const F& factors, hipStream_t hs) {
+    constexpr bool FACTOR = F::kGiven;
+    hipLaunchKernelGGL((maxima_kernel<T, F, ROWS, NT>), dim3((unsigned)((int64_t)p.parts * p.blocks)),
+                       dim3(kCodeThreads), 0, hs, p, factors);
     int col_parts = p.parts, row_parts = p.blocks;
     if (col_parts > kCodeJoin || (ROWS && row_parts > kCodeJoin)) {
         const int rows = ROWS ? (int)code_up(p.M, kScaleGroup) : 0, cols = (int)code_up(p.K, kScaleGroup);

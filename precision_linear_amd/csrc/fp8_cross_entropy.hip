@@ -17,6 +17,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/fp8_cross_entropy.h"
 #include "activation.h"
 #include "column_codes.h"
@@ -87,7 +89,10 @@ __global__ void __launch_bounds__(256) clear_kernel(uint32_t* p, int64_t n) {
 
 // ------------------------------------------------------------ gradient ---
 
+// What the gradient needs of each row, made once: in x's first pass where dw is asked
+// for, else in a kernel of its own.
 struct LossGrad {
+    static constexpr bool kGiven = true;
     const float* dloss;
     int64_t dloss_stride;
     const int64_t* target;
@@ -102,26 +107,35 @@ struct LossGrad {
     int64_t num_ones;
     uint32_t* counters;    // of the products, cleared
     int num_counters;
-};
 
-__global__ void __launch_bounds__(256) loss_rows_kernel(LossGrad p) {
-    const int64_t i0 = blockIdx.x * 256ll + threadIdx.x, step = gridDim.x * 256ll;
-    for (int64_t i = i0; i < p.num_counters; i += step) p.counters[i] = 0u;
-    for (int64_t i = i0; i < p.num_ones; i += step) p.ones[i] = 1.f;
-    for (int64_t m = i0; m < p.M; m += step) {
-        const int t = target_of(p.target, m, p.ignore, p.V);
-        const float l = p.loss[m], lse = p.lse[m];
+    __device__ __forceinline__ void begin() const {
+        const int64_t i0 = blockIdx.x * (int64_t)blockDim.x + threadIdx.x, step = (int64_t)gridDim.x * blockDim.x;
+        for (int64_t i = i0; i < num_counters; i += step) counters[i] = 0u;
+        for (int64_t i = i0; i < num_ones; i += step) ones[i] = 1.f;
+    }
+    __device__ __forceinline__ float of(int64_t m, bool write) const {
+        const int t = target_of(target, m, ignore, V);
+        const float l = loss[m], e = lse[m], d = dloss[m * dloss_stride];
         float f = -__builtin_inff(), r = 0.f;
         if (t != -1) {
             const float h = l <= 0.f ? 0.f : -expm1f(-l);
-            r = p.dloss[m * p.dloss_stride] * h;
-            if (t < 0 || !(fabsf(lse) < __builtin_inff())) r = __builtin_nanf("");
-            else if (h > 0.f) f = __builtin_fmaf(lse, -kLog2E, log2f(kE5m2Max / h));
+            r = d * h;
+            if (t < 0 || !(fabsf(e) < __builtin_inff())) r = __builtin_nanf("");
+            else if (write && h > 0.f) f = __builtin_fmaf(e, -kLog2E, log2f(kE5m2Max / h));
         }
-        p.rows[m] = float2{f, __int_as_float(t)};
-        p.factor[m] = r;
-        p.row_scale[m] = r / kE5m2Max;
+        if (write) {
+            rows[m] = float2{f, __int_as_float(t)};
+            factor[m] = r;
+            row_scale[m] = r / kE5m2Max;
+        }
+        return r;
     }
+};
+
+__global__ void __launch_bounds__(256) loss_rows_kernel(LossGrad p) {
+    p.begin();
+    const int64_t step = gridDim.x * 256ll;
+    for (int64_t m = blockIdx.x * 256ll + threadIdx.x; m < p.M; m += step) p.of(m, true);
 }
 
 __global__ void __launch_bounds__(256) zero_bf16_kernel(uint16_t* p, int64_t n) {
@@ -152,20 +166,51 @@ int loss_operands(const void* A, int fa, const void* B, int fb, const float* sa,
     return FP8MM_OK;
 }
 
+// A product's launches over the vocabulary (or a piece of it): one, or a second one for
+// what would leave most of a round idle.
+struct Ranges {
+    int64_t end[2];
+    int count;
+};
+Ranges ranges_of(int64_t fixed, int64_t n, int64_t k, bool ping_pong) {
+    const int64_t cut = ping_pong ? fp8mm::whole_rounds(fixed, n, k) : n;
+    return cut < n ? Ranges{{cut, n}, 2} : Ranges{{n, n}, 1};
+}
+// (the plan of the whole may be another kernel's)
+Ranges logit_ranges(int64_t M, int64_t n, int64_t K) {
+    const fp8mm::LossPlan p = fp8mm::loss_plan(M, n, K);
+    return ranges_of(M, n, K, p.cfg == fp8mm::ping_pong_config() && p.splits == 1);
+}
+// dw's rows: those of the codes qt.
+Ranges dw_ranges(int64_t n, int64_t K, int64_t Mp) {
+    return ranges_of(K, n, Mp,
+                     fp8_scaled_mm_select_config(n, K, Mp, FP8MM_ROWWISE, 0, 1) == fp8mm::ping_pong_config() &&
+                         fp8_scaled_mm_select_splits(n, K, Mp, FP8MM_ROWWISE, 0, -1) == 1);
+}
+
 struct LossSpace {
-    int64_t mm, logit, part, total;   // byte offsets
-    fp8mm::LossPlan plan;
-    int64_t blocks;
+    int64_t logit, part, total;   // byte offsets (the multiply's workspace is first)
+    Ranges ranges;
+    fp8mm::LossPlan plan[2];
+    int64_t blocks[2];
 };
 
 LossSpace loss_space(int64_t M, int64_t V, int64_t K) {
     LossSpace s{};
     if (M == 0) return s;
-    s.plan = fp8mm::loss_plan(M, V, K);
-    s.blocks = fp8mm::loss_blocks(V, s.plan);
-    s.logit = align256(fp8mm::loss_workspace(M, V, s.plan));
+    s.ranges = logit_ranges(M, V, K);
+    int64_t at = 0, mm = 0, blocks = 0;
+    for (int i = 0; i < s.ranges.count; ++i) {
+        const int64_t n = s.ranges.end[i] - at;
+        s.plan[i] = fp8mm::loss_plan(M, n, K);
+        s.blocks[i] = fp8mm::loss_blocks(n, s.plan[i]);
+        blocks += s.blocks[i];
+        mm = std::max(mm, fp8mm::loss_workspace(M, n, s.plan[i]));
+        at = s.ranges.end[i];
+    }
+    s.logit = align256(mm);
     s.part = s.logit + align256(4 * M);
-    s.total = s.part + align256(8 * M * s.blocks);
+    s.total = s.part + align256(8 * M * blocks);
     return s;
 }
 
@@ -173,7 +218,8 @@ struct GradSpace {
     int64_t mm, rows, factor, row_scale, ones, col_scale, partials, q, qt, qx, sums, total;   // byte offsets
     int64_t piece, ldq, Mp;
     bool one;              // the whole vocabulary in one piece
-    fp8mm::LossPlan plan;  // of a whole piece
+    int counters;          // to clear (a product leaves those that it uses at zero)
+    int dx_splits;         // units of a tile of its dx, 0: the automatic plan
     fp8mm::PairPlan pair;
     CodeJob x;
 };
@@ -195,25 +241,43 @@ GradSpace grad_space(int64_t M, int64_t V, int64_t K, bool want_dx, bool want_dw
     if (g.one) g.piece = V;
     else g.piece = code_up(code_up(V, code_up(V, g.piece)), 256) * 256;   // (pieces of about one size)
     g.ldq = code_up(g.piece, 16) * 16;
-    g.plan = fp8mm::loss_plan(M, g.piece, K);
     const int64_t last = g.one ? g.piece : V - (V - 1) / g.piece * g.piece;
-    const fp8mm::LossPlan last_plan = fp8mm::loss_plan(M, last, K);
-    // The tiles write the codes' zeros past M as far as they reach.
-    if (fp8mm::loss_rows(M, g.plan) < g.Mp || fp8mm::loss_rows(M, last_plan) < g.Mp) g.Mp = code_up(M, 16) * 16;
     int64_t mm = kCounterArea;
-    auto room = [&](int64_t n) { mm = n > mm ? n : mm; };
-    room(fp8mm::loss_workspace(M, g.piece, g.plan));
-    room(fp8mm::loss_workspace(M, last, last_plan));
-    if (want_dx && g.one) room(fp8_scaled_mm_workspace_size(M, K, g.ldq, FP8MM_ROWWISE, 0, -1, 0));
-    if (want_dw) {
-        room(fp8_scaled_mm_workspace_size(g.piece, K, g.Mp, FP8MM_ROWWISE, 0, -1, 0));
-        room(fp8_scaled_mm_workspace_size(last, K, g.Mp, FP8MM_ROWWISE, 0, -1, 0));
+    auto room = [&](int64_t n) { mm = std::max(mm, n); };
+    auto product = [&](int64_t m, int64_t n, int64_t k) {
+        room(fp8_scaled_mm_workspace_size(m, n, k, FP8MM_ROWWISE, 0, -1, 0));
+        g.counters = std::max(g.counters, fp8mm::product_counters({nullptr, nullptr, nullptr, nullptr, nullptr, m, n, k}));
+    };
+    // The tiles write the codes' zeros past M as far as they reach.
+    bool reach = true;
+    for (const int64_t n : {g.piece, last}) {
+        const Ranges r = logit_ranges(M, n, K);
+        for (int i = 0; i < r.count; ++i) {
+            const int64_t part = r.end[i] - (i ? r.end[0] : 0);
+            const fp8mm::LossPlan plan = fp8mm::loss_plan(M, part, K);
+            reach = reach && fp8mm::loss_rows(M, plan) >= g.Mp;
+            room(fp8mm::loss_workspace(M, part, plan));
+            g.counters = std::max(g.counters, fp8mm::loss_counters(M, part, plan));
+        }
     }
-    if (want_dx && want_dw && g.one) {
+    if (!reach) g.Mp = code_up(M, 16) * 16;
+    if (want_dx && g.one) {
+        g.dx_splits = fp8mm::long_sum_splits(M, K, g.ldq);
+        if (g.dx_splits == 0) product(M, K, g.ldq);
+    }
+    if (want_dw)
+        for (const int64_t n : {g.piece, last}) {
+            const Ranges r = dw_ranges(n, K, g.Mp);
+            for (int i = 0; i < r.count; ++i) product(r.end[i] - (i ? r.end[0] : 0), K, g.Mp);
+        }
+    if (want_dx && want_dw && g.one && g.dx_splits == 0) {
         fp8mm::Product q[2];
         products(M, V, K, g.ldq, g.Mp, q);
         g.pair = fp8mm::plan_pair(q);
-        if (g.pair.cfg >= 0) room(fp8mm::pair_workspace(q, g.pair));
+        if (g.pair.cfg >= 0) {
+            room(fp8mm::pair_workspace(q, g.pair));
+            g.counters = std::max(g.counters, fp8mm::pair_counters(q, g.pair));
+        }
     }
     CodeJob& x = g.x;
     x.M = M;
@@ -231,7 +295,7 @@ GradSpace grad_space(int64_t M, int64_t V, int64_t K, bool want_dx, bool want_dw
     g.qt = g.q + (want_dx ? align256(M * g.ldq) : 0);
     g.qx = g.qt + (want_dw ? align256(g.piece * g.Mp) : 0);
     g.sums = g.qx + (want_dw ? align256(K * g.Mp) : 0);
-    g.total = g.sums + (want_dx && !g.one ? align256(fp8mm::sum_workspace(M, K)) : 0);
+    g.total = g.sums + (want_dx && (!g.one || g.dx_splits > 0) ? align256(fp8mm::sum_workspace(M, K, g.one ? g.dx_splits : 1)) : 0);
     return g;
 }
 
@@ -259,19 +323,27 @@ int fp8_linear_cross_entropy(const void* A, int a_format, const void* B, int b_f
     std::lock_guard<std::mutex> together(fp8mm::enqueue_lock(workspace));
     char* ws = static_cast<char*>(workspace);
     (void)hipGetLastError();
-    const int counters = fp8mm::loss_counters(M, V, s.plan);
+    int counters = 0;
+    for (int i = 0; i < s.ranges.count; ++i)
+        counters = std::max(counters, fp8mm::loss_counters(M, s.ranges.end[i] - (i ? s.ranges.end[0] : 0), s.plan[i]));
     if (counters > 0)
         hipLaunchKernelGGL(clear_kernel, dim3((unsigned)((counters + 255) / 256)), dim3(256), 0, hs,
                            reinterpret_cast<uint32_t*>(ws), (int64_t)counters);
-    const fp8mm::Logits z{A, a_format, B, b_format, scale_a, scale_b, M, V, K, mode};
     float2* part = reinterpret_cast<float2*>(ws + s.part);
     float* logit = reinterpret_cast<float*>(ws + s.logit);
-    st = fp8mm::run_stats(z, s.plan, target, part, logit, hs, ws);
-    if (st != FP8MM_OK) return st;
+    int64_t v0 = 0, blocks = 0;
+    for (int i = 0; i < s.ranges.count; ++i) {
+        const fp8mm::Logits z{A, a_format, static_cast<const uint8_t*>(B) + v0 * K, b_format, scale_a,
+                              mode == FP8MM_ROWWISE ? scale_b + v0 : scale_b, M, s.ranges.end[i] - v0, K, mode};
+        st = fp8mm::run_stats(z, s.plan[i], target, part + blocks * M, logit, v0, hs, ws);
+        if (st != FP8MM_OK) return st;
+        blocks += s.blocks[i];
+        v0 = s.ranges.end[i];
+    }
     int group = 1;
     while (group < 64 && M / group > 256) group *= 2;
     hipLaunchKernelGGL(loss_kernel, dim3((unsigned)code_up(M, group)), dim3(kLossThreads), 0, hs, part, logit, target,
-                       ignore_index, loss, lse, M, V, (int)s.blocks, group);
+                       ignore_index, loss, lse, M, V, (int)blocks, group);
     return hipGetLastError() == hipSuccess ? FP8MM_OK : FP8MM_ERR_LAUNCH;
 }
 
@@ -327,8 +399,7 @@ int fp8_linear_cross_entropy_backward(const float* dloss, int64_t dloss_stride, 
     p.ones = f32(g.ones);
     p.num_ones = dw ? g.piece : 0;
     p.counters = reinterpret_cast<uint32_t*>(ws);
-    p.num_counters = (int)(kCounterArea / 4);   // (a product leaves its counters at zero)
-    hipLaunchKernelGGL(loss_rows_kernel, dim3(256), dim3(256), 0, hs, p);
+    p.num_counters = g.counters;
     if (dw) {
         CodeJob& c = g.x;
         c.x = x;
@@ -336,18 +407,24 @@ int fp8_linear_cross_entropy_backward(const float* dloss, int64_t dloss_stride, 
         c.col_max = f32(g.partials);
         c.col_scale = f32(g.col_scale);
         c.q_cols = reinterpret_cast<uint8_t*>(ws + g.qx);
-        launch_codes<bf16_t, 0, true, false, false>(c, hs);
+        launch_codes<bf16_t, 0, false, false>(c, p, hs);
+    } else {
+        hipLaunchKernelGGL(loss_rows_kernel, dim3((unsigned)std::min<int64_t>(code_up(M, 256), 256)), dim3(256), 0, hs, p);
     }
     if (hipGetLastError() != hipSuccess) return FP8MM_ERR_LAUNCH;
     const int64_t Vt = code_up(V, 16) * 16;
     for (int64_t v0 = 0; v0 < V; v0 += g.piece) {
         const int64_t n = V - v0 < g.piece ? V - v0 : g.piece;
         const int64_t ldq = code_up(n, 16) * 16;
-        const fp8mm::LossPlan plan = n == g.piece ? g.plan : fp8mm::loss_plan(M, n, K);
-        const fp8mm::Logits z{A, a_format, static_cast<const uint8_t*>(B) + v0 * K, b_format, scale_a,
-                              mode == FP8MM_ROWWISE ? scale_b + v0 : scale_b, M, n, K, mode};
-        st = fp8mm::run_codes(z, plan, p.rows, q, ldq, qt, g.Mp, v0, hs, ws);
-        if (st != FP8MM_OK) return st;
+        const Ranges r = logit_ranges(M, n, K);
+        for (int i = 0; i < r.count; ++i) {
+            const int64_t c0 = i ? r.end[0] : 0, v = v0 + c0;
+            const fp8mm::Logits z{A, a_format, static_cast<const uint8_t*>(B) + v * K, b_format, scale_a,
+                                  mode == FP8MM_ROWWISE ? scale_b + v : scale_b, M, r.end[i] - c0, K, mode};
+            st = fp8mm::run_codes(z, fp8mm::loss_plan(M, z.V, K), p.rows, q ? q + c0 : nullptr, ldq,
+                                  qt ? qt + c0 * g.Mp : nullptr, g.Mp, v, hs, ws);
+            if (st != FP8MM_OK) return st;
+        }
         uint16_t* dw_piece = static_cast<uint16_t*>(dw) + (dw ? v0 * K : 0);
         if (g.one && dx && dw && wt_format == FP8MM_E4M3FN && g.pair.cfg >= 0) {
             const fp8mm::Product two[2] = {
@@ -355,18 +432,23 @@ int fp8_linear_cross_entropy_backward(const float* dloss, int64_t dloss_stride, 
                 {qt, ws + g.qx, p.ones, f32(g.col_scale), dw, V, K, g.Mp}};
             return fp8mm::run_pair(two, g.pair, hs, ws);
         }
-        if (dw) {
-            st = fp8_scaled_mm_typed(qt, FP8MM_E5M2, ws + g.qx, FP8MM_E4M3FN, p.ones, f32(g.col_scale), nullptr,
-                                     dw_piece, n, K, g.Mp, FP8MM_ROWWISE, stream, -1, 0, ws, g.rows);
-            if (st != FP8MM_OK) return st;
-        }
-        if (dx && g.one)
+        // dx first: the caches still hold the codes, and what dw writes would push them out.
+        if (dx && g.one && g.dx_splits == 0)
             st = fp8_scaled_mm_typed(q, FP8MM_E5M2, wt, wt_format, p.row_scale, wt_scale, nullptr, dx, M, K, ldq,
                                      FP8MM_ROWWISE, stream, -1, 0, ws, g.rows);
         else if (dx)
             st = fp8mm::run_sum({q, static_cast<const uint8_t*>(wt) + v0, wt_format, p.row_scale, wt_scale, dx, M, K,
-                                 ldq, Vt, v0 == 0, v0 + n == V},
+                                 ldq, Vt, v0 == 0, v0 + n == V, g.one ? g.dx_splits : 1},
                                 hs, ws + g.sums);
+        if (st != FP8MM_OK) return st;
+        const Ranges d = dw ? dw_ranges(n, K, g.Mp) : Ranges{};
+        for (int i = 0; i < d.count; ++i) {
+            const int64_t c0 = i ? d.end[0] : 0;
+            st = fp8mm::run_streamed({qt + c0 * g.Mp, ws + g.qx, p.ones, f32(g.col_scale), dw_piece + c0 * K,
+                                      d.end[i] - c0, K, g.Mp},
+                                     hs, ws, g.rows);
+            if (st != FP8MM_OK) return st;
+        }
         if (st != FP8MM_OK) return st;
     }
     return FP8MM_OK;

@@ -86,6 +86,7 @@ struct LinearParams : Params {
 // no product: kEpiStats, softmax statistics of each row, and kEpiCodes, the
 // gradient of the logits as e5m2 codes.
 struct LossParams : Params {
+    int col0;                   // B's first row in the vocabulary
     // kEpiStats
     const int64_t* target;      // M
     float2* part;               // [column block][M]: largest logit times log2(e), sum of
@@ -95,13 +96,15 @@ struct LossParams : Params {
     const float2* rows;         // M: log2 of the code's factor, target as an int's bits
     uint8_t* q;                 // M x ldq, may be null
     uint8_t* qt;                // N x ldqt, may be null
-    int ldq, ldqt;              // N and M rounded up to 16 or more (zeros there)
-    int col0;                   // B's first row in the vocabulary
+    int ldq, ldqt;              // row lengths of both: beyond N and M, zeros up to a multiple of 16 and
+                                // as far as the tiles reach
 };
 
-// A product whose K range comes in pieces, one launch each (kEpiSum, ping-pong
-// kernel only): the unscaled fp32 sums go from launch to launch through
-// `partials` (num_tiles tiles).  Rows of B lie ldb bytes apart.
+// A product whose sums leave the kernel unscaled, in fp32 and in the accumulators'
+// own layout (kEpiSum, ping-pong kernel only).  Either its K range comes in pieces,
+// one launch each, and the sums go from launch to launch through `partials` (num_tiles
+// tiles, splits 1); or each work unit leaves its own for join_sums (num_tiles * splits
+// tiles).  Rows of B lie ldb bytes apart.
 struct SumParams : Params {
     int ldb;
     int first, last;
@@ -195,6 +198,7 @@ extern LaunchPair kCodesF3[kNumConfigs];
 // The ping-pong kernel's launches with kEpiSum for A in e5m2 and B in e4m3fn or
 // e5m2, defined in fp8_loss_sum.hip.
 extern Launch kSum[2];
+void join_sums(const SumParams& p, hipStream_t stream);
 
 // The generic configurations' pair launches for A in e5m2 and B in e4m3fn (the
 // linear layer's gradient), defined in fp8_linear_pair.hip.
@@ -545,7 +549,7 @@ __device__ __forceinline__ void acc_chunk_add(A (&acc)[FN][FM], int c, v4f x) {
 
 // This thread's share of a partial tile of `bytes` bytes at base: chunk c at
 // byte (c * stride + idx) * 16 (each wave writes and reads 1 KiB runs).
-template <int FN, int FM, class A>
+template <int FN, int FM, int POLICY = kPolicyCoherent, class A>
 __device__ __forceinline__ void partial_publish(const A (&acc)[FN][FM], float* base, int stride,
                                                 int idx, uint32_t bytes) {
     constexpr int NC = FN * FM * (int)(sizeof(A) / 16);
@@ -553,14 +557,14 @@ __device__ __forceinline__ void partial_publish(const A (&acc)[FN][FM], float* b
 #pragma unroll
     for (int c = 0; c < NC; ++c)
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, acc_chunk<FN, FM>(acc, c)), r,
-                                               (c * stride + idx) * 16, 0, kPolicyCoherent);
+                                               (c * stride + idx) * 16, 0, POLICY);
 }
 
 // acc += this thread's share of a partial tile (same layout).  Loads go out
 // in batches of up to 16 chunks, all issued before the first add (the
 // scheduling barrier keeps the compiler from trading that for registers by
 // waiting on one load at a time).
-template <int FN, int FM, class A>
+template <int FN, int FM, int POLICY = kPolicyCoherent, class A>
 __device__ __forceinline__ void partial_accumulate(A (&acc)[FN][FM], const float* base, int stride,
                                                    int idx, uint32_t bytes) {
     constexpr int NC = FN * FM * (int)(sizeof(A) / 16);
@@ -572,8 +576,7 @@ __device__ __forceinline__ void partial_accumulate(A (&acc)[FN][FM], const float
         v4u x[B];
 #pragma unroll
         for (int k = 0; k < B; ++k)
-            x[k] = __builtin_amdgcn_raw_buffer_load_b128(r, ((b + k) * stride + idx) * 16, 0,
-                                                         kPolicyCoherent);
+            x[k] = __builtin_amdgcn_raw_buffer_load_b128(r, ((b + k) * stride + idx) * 16, 0, POLICY);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int k = 0; k < B; ++k) acc_chunk_add<FN, FM>(acc, b + k, __builtin_bit_cast(v4f, x[k]));
@@ -1126,6 +1129,26 @@ __device__ __forceinline__ void epi_stage_and_store(
 
 // ------------------------------------------- the cross entropy's epilogues ---
 
+// f over the lanes with the same lane % MI, in each of them.
+template <int MI, class F>
+__device__ __forceinline__ float over_columns(float x, F f) {
+    auto both = [&](auto pair) { return f(__uint_as_float(pair[0]), __uint_as_float(pair[1])); };
+    const uint32_t h = __float_as_uint(x);
+    x = both(__builtin_amdgcn_permlane32_swap(h, h, false, false));
+    if constexpr (MI == 16) {
+        const uint32_t r = __float_as_uint(x);
+        x = both(__builtin_amdgcn_permlane16_swap(r, r, false, false));
+    }
+    return x;
+}
+
+// Where row m's target is, from column n0 of this launch's B on (as an unsigned number:
+// beyond every column if it is elsewhere or there is none).
+__device__ __forceinline__ uint32_t stats_target(const LossParams& p, int m, int n0) {
+    const uint64_t t = m < p.M ? (uint64_t)p.target[m] - (uint64_t)(p.col0 + n0) : ~0ull;
+    return t < 0x10000 ? (uint32_t)t : ~0u;
+}
+
 // Rows of JN blocks of a wave (first row m0, scales epi_sa) and its columns from
 // n0 on: this wave's share of each row's softmax statistics, as column block `block`
 // of p.part.  Logits are kept times log2(e), so that an exponential is a subtraction
@@ -1135,15 +1158,9 @@ __device__ __forceinline__ void epi_stage_and_store(
 // the logits makes the sum a NaN.
 template <int MI, int FN, int JN>
 __device__ __forceinline__ void epi_stats(typename Mfma<MI>::acc_t (&z)[FN][JN], const LossParams& p, int m0,
-                                          int n0, int block, const float* epi_sa, const float* epi_sb, int lane) {
+                                          int n0, int block, const float* epi_sa, const float* epi_sb,
+                                          const uint32_t (&target)[JN], int lane) {
     constexpr int G = Mfma<MI>::NACC / 4;
-    int target[JN];   // within the wave's columns, or outside them
-#pragma unroll
-    for (int j = 0; j < JN; ++j) {
-        const int m = m0 + j * MI + lane % MI;
-        const uint64_t t = m < p.M ? (uint64_t)p.target[m] - (uint64_t)n0 : ~0ull;
-        target[j] = t < (uint64_t)(FN * MI) ? (int)t : -1;
-    }
     float sa_r[JN];
 #pragma unroll
     for (int j = 0; j < JN; ++j) sa_r[j] = epi_sa[j * MI + lane % MI] * kLog2E;
@@ -1171,8 +1188,7 @@ __device__ __forceinline__ void epi_stats(typename Mfma<MI>::acc_t (&z)[FN][JN],
         for (int i = 0; i < FN; ++i)
 #pragma unroll
             for (int e = 0; e < 4 * G; ++e) most = fmaxf(most, z[i][j][e]);
-#pragma unroll
-        for (int d = MI; d < kWave; d *= 2) most = fmaxf(most, __shfl_xor(most, d));
+        most = over_columns<MI>(most, [](float a, float b) { return fmaxf(a, b); });
         const float from = most == -__builtin_inff() ? 0.f : most;
         float sum = 0.f;
 #pragma unroll
@@ -1180,15 +1196,14 @@ __device__ __forceinline__ void epi_stats(typename Mfma<MI>::acc_t (&z)[FN][JN],
 #pragma unroll
             for (int e = 0; e < 4 * G; ++e)
                 sum += __builtin_amdgcn_exp2f(z[i][j][e] - from);
-#pragma unroll
-        for (int d = MI; d < kWave; d *= 2) sum += __shfl_xor(sum, d);
+        sum = over_columns<MI>(sum, [](float a, float b) { return a + b; });
         if (lane < MI && m < p.M) p.part[(size_t)block * p.M + m] = float2{most, sum};
-        if (__any(target[j] >= 0)) {
+        if (__any(target[j] < (uint32_t)(FN * MI))) {   // (few blocks hold a target)
 #pragma unroll
             for (int i = 0; i < FN; ++i)
 #pragma unroll
                 for (int e = 0; e < 4 * G; ++e)
-                    if (epi_col<MI>(i, e / 4, lane) + e % 4 == target[j]) p.target_logit[m] = z[i][j][e];
+                    if ((uint32_t)(epi_col<MI>(i, e / 4, lane) + e % 4) == target[j]) p.target_logit[m] = z[i][j][e];
         }
     }
 }
@@ -1199,42 +1214,55 @@ __device__ __forceinline__ void epi_stats(typename Mfma<MI>::acc_t (&z)[FN][JN],
 // MI.  0 outside the matrix.
 template <int MI, int FN, int JN>
 __device__ __forceinline__ void epi_codes(const typename Mfma<MI>::acc_t (&acc)[FN][JN],
-                                          uint32_t (&w)[FN][JN][Mfma<MI>::NACC / 4], const LossParams& p, int m0,
-                                          int n0, const float* epi_sa, const float* epi_sb, int lane) {
+                                          uint32_t (&w)[FN][JN][Mfma<MI>::NACC / 4], const LossParams& p, int n0,
+                                          const float* epi_sa, const float* epi_sb, const float (&f)[JN],
+                                          const uint32_t (&target)[JN], int lane) {
     constexpr int G = Mfma<MI>::NACC / 4;
     constexpr float kMax = 57344.f;
-    const bool full = n0 + FN * MI <= p.N;
-    float sa_r[JN], f_r[JN];
-    int target[JN];
+    constexpr uint32_t kLeast = 0xfb;   // the code of -57344
+    float sa_r[JN];
 #pragma unroll
-    for (int j = 0; j < JN; ++j) {
-        const int m = m0 + j * MI + lane % MI;
-        float2 r{-__builtin_inff(), __int_as_float(-1)};
-        if (m < p.M) r = p.rows[m];
-        sa_r[j] = epi_sa[j * MI + lane % MI] * kLog2E;
-        f_r[j] = r.x;
-        target[j] = __float_as_int(r.y) - p.col0 - n0;
-    }
+    for (int j = 0; j < JN; ++j) sa_r[j] = epi_sa[j * MI + lane % MI] * kLog2E;
 #pragma unroll
     for (int i = 0; i < FN; ++i)
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            const int cl = epi_col<MI>(i, g, lane);
-            const v4f sb_r = *reinterpret_cast<const v4f*>(epi_sb + cl);
+            const v4f sb_r = *reinterpret_cast<const v4f*>(epi_sb + epi_col<MI>(i, g, lane));
 #pragma unroll
             for (int j = 0; j < JN; ++j) {
                 float y[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const float e = __builtin_fmaf(acc[i][j][4 * g + c], sa_r[j] * sb_r[c], f_r[j]);
-                    y[c] = fminf(__builtin_amdgcn_exp2f(e), kMax);
-                    y[c] = cl + c == target[j] ? -kMax : y[c];
-                    if (!full) y[c] = n0 + cl + c < p.N ? y[c] : 0.f;
-                }
+                for (int c = 0; c < 4; ++c)
+                    y[c] = fminf(__builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][4 * g + c], sa_r[j] * sb_r[c], f[j])), kMax);
                 const int lo = __builtin_amdgcn_cvt_pk_bf8_f32(y[0], y[1], 0, false);
                 w[i][j][g] = (uint32_t)__builtin_amdgcn_cvt_pk_bf8_f32(y[2], y[3], lo, true);
             }
         }
+    bool here = false;
+#pragma unroll
+    for (int j = 0; j < JN; ++j) here = here || target[j] < (uint32_t)(FN * MI);
+    if (__any(here)) {   // (few blocks hold a target)
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int j = 0; j < JN; ++j) {
+                    const uint32_t at = target[j] - (uint32_t)epi_col<MI>(i, g, lane);
+                    if (at < 4) w[i][j][g] = (w[i][j][g] & ~(0xffu << (8 * at))) | kLeast << (8 * at);
+                }
+    }
+    if (n0 + FN * MI > p.N) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const int in = p.N - (n0 + epi_col<MI>(i, g, lane));   // of the word's columns
+                const uint32_t mask = in >= 4 ? ~0u : in <= 0 ? 0u : (1u << (8 * in)) - 1;
+#pragma unroll
+                for (int j = 0; j < JN; ++j) w[i][j][g] &= mask;
+            }
+    }
 }
 
 // Four lanes' words of 4 bytes (lanes 4 a .. 4 a + 3), transposed: lane 4 a + b gets
@@ -1244,6 +1272,13 @@ __device__ __forceinline__ uint32_t quad_transpose(uint32_t d, int lane) {
     d = __builtin_amdgcn_perm(t, d, lane & 1 ? 0x03070105u : 0x06020400u);
     t = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)d, 0x4E, 0xf, 0xf, true);            // lane ^ 2
     return __builtin_amdgcn_perm(t, d, lane & 2 ? 0x03020706u : 0x05040100u);
+}
+
+// A row past the last: codes 0.
+__device__ __forceinline__ float2 no_row() { return float2{-__builtin_inff(), __int_as_float(-1)}; }
+// As stats_target, from column n0 of the vocabulary on, for a row of p.rows.
+__device__ __forceinline__ uint32_t codes_target(float2 r, int n0) {
+    return (uint32_t)(__float_as_int(r.y) - n0);
 }
 
 // Generic kernel: the tile's codes through two copies in LDS (rows of columns,
@@ -1259,7 +1294,16 @@ __device__ __forceinline__ void epi_codes_tile(const typename Mfma<C::MI_>::acc_
                   "both copies of the codes fit the stage buffers");
     uint8_t* stg_t = stg + C::BM_ * RS;
     uint32_t w[C::FN][C::FM][G];
-    epi_codes<MI, C::FN, C::FM>(acc, w, p, row0 + mbase, col0 + nbase, epi_sa + mbase, epi_sb + nbase, lane);
+    float f[C::FM];
+    uint32_t target[C::FM];
+#pragma unroll
+    for (int j = 0; j < C::FM; ++j) {
+        const int m = row0 + mbase + j * MI + lane % MI;
+        const float2 r = m < p.M ? p.rows[m] : no_row();
+        f[j] = r.x;
+        target[j] = codes_target(r, p.col0 + col0 + nbase);
+    }
+    epi_codes<MI, C::FN, C::FM>(acc, w, p, col0 + nbase, epi_sa + mbase, epi_sb + nbase, f, target, lane);
 #pragma unroll
     for (int i = 0; i < C::FN; ++i)
 #pragma unroll
@@ -1274,7 +1318,7 @@ __device__ __forceinline__ void epi_codes_tile(const typename Mfma<C::MI_>::acc_
     if (p.q)
         for (int x = tid; x < C::BM_ * (C::BN_ / 16); x += C::THREADS) {
             const int r = x / (C::BN_ / 16), c = x % (C::BN_ / 16) * 16;
-            if (row0 + r < p.M && col0 + c < p.ldq)
+            if (row0 + r < p.M && col0 + c < p.N)
                 *reinterpret_cast<v4i*>(p.q + (size_t)(row0 + r) * p.ldq + col0 + c) =
                     *reinterpret_cast<const v4i*>(stg + r * RS + c);
         }
@@ -1587,10 +1631,14 @@ fp8_gemm_kernel(std::conditional_t<PAIR, PairParams, KernelParams<EPI>> args) {
         if constexpr (EPI == kEpiLinear)
             epi_stage_and_store<C>(acc, smem, p, row0, col0, wm * C::WTM, wn * C::WTN, epi_sa, epi_sb,
                                    epi_bias, res, lane, tid);
-        else if constexpr (EPI == kEpiStats)
-            epi_stats<MI, C::FN, C::FM>(acc, p, row0 + wm * C::WTM, col0 + wn * C::WTN,
-                                        pn * WAVES_N + wn, epi_sa + wm * C::WTM, epi_sb + wn * C::WTN, lane);
-        else if constexpr (EPI == kEpiCodes)
+        else if constexpr (EPI == kEpiStats) {
+            uint32_t target[C::FM];
+#pragma unroll
+            for (int j = 0; j < C::FM; ++j)
+                target[j] = stats_target(p, row0 + wm * C::WTM + j * MI + lane % MI, col0 + wn * C::WTN);
+            epi_stats<MI, C::FN, C::FM>(acc, p, row0 + wm * C::WTM, col0 + wn * C::WTN, pn * WAVES_N + wn,
+                                        epi_sa + wm * C::WTM, epi_sb + wn * C::WTN, target, lane);
+        } else if constexpr (EPI == kEpiCodes)
             epi_codes_tile<C>(acc, smem, p, row0, col0, wm * C::WTM, wn * C::WTN, epi_sa, epi_sb, lane, tid);
         else
             stage_and_store<C>(acc, smem, p, row0, col0, wm * C::WTM, wn * C::WTN, epi_sa, epi_sb,
@@ -1691,14 +1739,17 @@ constexpr int FM = 128 / MI, FN = 64 / MI;          // MFMA blocks per wave
 constexpr int KSTEPS = BK / Mfma<MI>::KSTEP;        // MFMA K steps per slice
 constexpr int NOFF = 8;                             // load row groups per wave
 constexpr int EPI_BYTES = BM * 4 + BN * 4 + BN * 2; // row scales, column scales, bias
+constexpr int ROW_BYTES = BM * 8;                   // what the cross entropy's epilogues need of a row
 // Output staging: group 0's waves use 4 KiB each after the parameters; group 1's
 // waves use the A-bottom part of stage buffer 1, which is idle while they write
 // their outputs (the next tile's first loads fill buffer 0 and buffer 1's A-top).
 constexpr int STG_BYTES = 4096;
 constexpr int STG0 = MAIN_BYTES + 2 * EPI_BYTES;
 constexpr int STG1 = STAGE_BYTES + HALF_A;
-constexpr int LDS_BYTES = STG0 + 4 * STG_BYTES;
-static_assert(LDS_BYTES <= 160 * 1024, "gfx950 LDS is 160 KiB per workgroup");
+constexpr int ROWS0 = STG0 + 4 * STG_BYTES;         // (two areas, in those kernels only)
+constexpr int LDS_BYTES = ROWS0;
+constexpr int LOSS_LDS_BYTES = ROWS0 + 2 * ROW_BYTES;
+static_assert(LOSS_LDS_BYTES <= 160 * 1024, "gfx950 LDS is 160 KiB per workgroup");
 static_assert(4 * STG_BYTES <= HALF_A, "group 1 staging fits in the A-bottom half");
 }  // namespace pp
 
@@ -1824,8 +1875,14 @@ __device__ __forceinline__ int pp_slice(const PpTile& T, int step) {
 template <class P>
 __device__ __forceinline__ PpTile pp_tile(const P& p, int u, int group_m, int xcd) {
     PpTile T;
-    T.t = u / p.splits;
-    T.kb = (u - T.t * p.splits) * p.k_chunk;
+    if constexpr (std::is_same_v<P, SumParams>) {
+        // Units of one K range side by side: an XCD's then share their operands in its L2.
+        T.t = u % p.num_tiles;
+        T.kb = u / p.num_tiles * p.k_chunk;
+    } else {
+        T.t = u / p.splits;
+        T.kb = (u - T.t * p.splits) * p.k_chunk;
+    }
     T.n = min(p.k_chunk, p.k_iters - T.kb);   // >= 1: the host leaves no empty unit
     T.rot = xcd * T.n / kXcds;
     int pm, pn;
@@ -1853,16 +1910,23 @@ __device__ __forceinline__ PpTile pp_tile(const P& p, int u, int group_m, int xc
 struct PpParams {
     float sa, sb;
     uint16_t bias;
+    float2 row;   // (codes' factor, target's column in the tile as an unsigned int's bits)
 };
 
-template <int EPI>
-__device__ __forceinline__ PpParams pp_params_load(const Params& p, const PpTile& T, int t,
+template <int EPI, class P>
+__device__ __forceinline__ PpParams pp_params_load(const P& p, const PpTile& T, int t,
                                                    bool has_bias, float s_pt) {
     PpParams v;
     const bool row_ok = T.row0 + t < p.M, col_ok = T.col0 + t < p.N;
     v.sa = (p.rowwise && row_ok) ? p.scale_a[T.row0 + t] : EPI ? s_pt : 0.f;
     v.sb = (p.rowwise && col_ok) ? p.scale_b[T.col0 + t] : EPI && !p.rowwise ? 1.f : 0.f;
     v.bias = (has_bias && col_ok) ? p.bias[T.col0 + t] : (uint16_t)0;
+    if constexpr (EPI == kEpiStats) {
+        v.row = float2{0.f, __uint_as_float(stats_target(p, T.row0 + t, T.col0))};
+    } else if constexpr (EPI == kEpiCodes) {
+        const float2 r = row_ok ? p.rows[T.row0 + t] : no_row();
+        v.row = float2{r.x, __uint_as_float(codes_target(r, p.col0 + T.col0))};
+    }
     return v;
 }
 
@@ -2161,21 +2225,34 @@ __device__ __forceinline__ bool pp_split_fixup(pp::acc_t (&acc)[pp::FN][pp::FM],
     return true;
 }
 
-// The cross entropy's epilogues of one wave (128 x 64 logits), in bands of rows.
-__device__ __forceinline__ void pp_epi_stats(const pp::acc_t (&acc)[pp::FN][pp::FM], const LossParams& p,
-                                             const PpTile& T, int mbase, int q, const float* epi_sa,
-                                             const float* epi_sb) {
+// The cross entropy's epilogues of one wave (128 x 64 logits), in bands of rows.  `rows`:
+// the wave's part of the tile's row area, target columns counted from the tile's first.
+template <int JN>
+__device__ __forceinline__ void pp_rows(const float2* rows, int q, int lane, float (&f)[JN], uint32_t (&target)[JN]) {
+#pragma unroll
+    for (int j = 0; j < JN; ++j) {
+        const float2 r = rows[j * pp::MI + lane % pp::MI];
+        f[j] = r.x;
+        target[j] = __float_as_uint(r.y) - (uint32_t)(q * 64);
+    }
+}
+
+__device__ __forceinline__ void pp_epi_stats(const pp::acc_t (&acc)[pp::FN][pp::FM], const LossParams& p, int row0,
+                                             int col0, int mbase, int q, const float* epi_sa, const float* epi_sb,
+                                             const float2* rows) {
     constexpr int MI = pp::MI, FN = pp::FN, JB = kPpBandBlocks;
 #pragma unroll
     for (int band = 0; band < pp::FM / JB; ++band) {
+        const int mb = mbase + band * 32, lane = pp_lane();
+        float f[JB];
+        uint32_t target[JB];
+        pp_rows<JB>(rows + mb, q, lane, f, target);
         pp::acc_t z[FN][JB];
 #pragma unroll
         for (int i = 0; i < FN; ++i)
 #pragma unroll
             for (int j = 0; j < JB; ++j) z[i][j] = acc[i][band * JB + j];
-        const int mb = mbase + band * 32;
-        epi_stats<MI, FN, JB>(z, p, T.row0 + mb, T.col0 + q * 64, T.col0 / 64 + q, epi_sa + mb, epi_sb + q * 64,
-                              pp_lane());
+        epi_stats<MI, FN, JB>(z, p, row0 + mb, col0 + q * 64, col0 / 64 + q, epi_sa + mb, epi_sb + q * 64, target, lane);
         __builtin_amdgcn_sched_barrier(0);
     }
 }
@@ -2183,49 +2260,62 @@ __device__ __forceinline__ void pp_epi_stats(const pp::acc_t (&acc)[pp::FN][pp::
 // The codes go through the wave's 4 KiB staging area 64 rows at a time, first by
 // rows, then by columns: 64 x 64 bytes, 16-byte chunk c of line r at c ^ (r / 4) % 4,
 // which spreads a write's lanes over the banks.
-__device__ __forceinline__ void pp_codes_out(uint8_t* out, int ld, int lines, int line0, int at0, const uint8_t* stg,
-                                             int lane) {
+template <bool NT>
+__device__ __forceinline__ void pp_codes_out(uint8_t* out, int ld, int end, int lines, int line0, int at0,
+                                             const uint8_t* stg, int lane) {
 #pragma unroll
     for (int pass = 0; pass < 4; ++pass) {
         const int r = pass * 16 + lane / 4, c = lane % 4;
         const v4i v = *reinterpret_cast<const v4i*>(stg + r * 64 + ((c ^ ((r >> 2) & 3)) * 16));
-        if (line0 + r < lines && at0 + c * 16 < ld)
-            *reinterpret_cast<v4i*>(out + (size_t)(line0 + r) * ld + at0 + c * 16) = v;
+        if (line0 + r < lines && at0 + c * 16 < end) {
+            v4i* to = reinterpret_cast<v4i*>(out + (size_t)(line0 + r) * ld + at0 + c * 16);
+            if constexpr (NT) __builtin_nontemporal_store(v, to);
+            else *to = v;
+        }
     }
 }
 
-__device__ __forceinline__ void pp_epi_codes(const pp::acc_t (&acc)[pp::FN][pp::FM], const LossParams& p, int m0,
-                                             int n0, const float* epi_sa, const float* epi_sb, uint8_t* stg) {
-    constexpr int MI = pp::MI, FN = pp::FN, JH = 64 / MI, JB = kPpBandBlocks;
+__device__ __forceinline__ void pp_epi_codes(const pp::acc_t (&acc)[pp::FN][pp::FM], uint32_t (&w)[pp::FN][pp::FM],
+                                             const LossParams& p, int col0, int mbase, int q, const float* epi_sa,
+                                             const float* epi_sb, const float2* rows) {
+    constexpr int MI = pp::MI, FN = pp::FN, JB = kPpBandBlocks;
+#pragma unroll
+    for (int band = 0; band < pp::FM / JB; ++band) {
+        pp::acc_t z[FN][JB];
+        uint32_t b[FN][JB][1];
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < JB; ++j) z[i][j] = acc[i][band * JB + j];
+        const int mb = mbase + band * JB * MI, lane = pp_lane();
+        float f[JB];
+        uint32_t target[JB];
+        pp_rows<JB>(rows + mb, q, lane, f, target);
+        epi_codes<MI, FN, JB>(z, b, p, col0 + q * 64, epi_sa + mb, epi_sb + q * 64, f, target, lane);
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < JB; ++j) w[i][band * JB + j] = b[i][j][0];
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+template <bool NT>
+__device__ __forceinline__ void pp_codes_store(const uint32_t (&w)[pp::FN][pp::FM], const LossParams& p, int m0,
+                                               int n0, uint8_t* stg) {
+    constexpr int MI = pp::MI, FN = pp::FN, JH = 64 / MI;
 #pragma unroll
     for (int half = 0; half < pp::FM / JH; ++half) {
         const int lane = pp_lane();
-        const int r0 = half * 64;
-        uint32_t w[FN][JH];
-#pragma unroll
-        for (int band = 0; band < JH / JB; ++band) {
-            pp::acc_t z[FN][JB];
-            uint32_t b[FN][JB][1];
-#pragma unroll
-            for (int i = 0; i < FN; ++i)
-#pragma unroll
-                for (int j = 0; j < JB; ++j) z[i][j] = acc[i][half * JH + band * JB + j];
-            const int mb = r0 + band * JB * MI;
-            epi_codes<MI, FN, JB>(z, b, p, m0 + mb, n0, epi_sa + mb, epi_sb, lane);
-#pragma unroll
-            for (int i = 0; i < FN; ++i)
-#pragma unroll
-                for (int j = 0; j < JB; ++j) w[i][band * JB + j] = b[i][j][0];
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        const int l = lane % MI, h = lane / MI;
+        const int r0 = half * 64, l = lane % MI, h = lane / MI;
         if (p.q) {
 #pragma unroll
             for (int i = 0; i < FN; ++i)
 #pragma unroll
                 for (int j = 0; j < JH; ++j)
-                    *reinterpret_cast<uint32_t*>(stg + (j * MI + l) * 64 + ((i ^ ((l >> 2) & 3)) * 16) + h * 4) = w[i][j];
-            pp_codes_out(p.q, p.ldq, p.M, m0 + r0, n0, stg, lane);
+                    *reinterpret_cast<uint32_t*>(stg + (j * MI + l) * 64 + ((i ^ ((l >> 2) & 3)) * 16) + h * 4) =
+                        w[i][half * JH + j];
+            pp_codes_out<NT>(p.q, p.ldq, p.N, p.M, m0 + r0, n0, stg, lane);
         }
         if (p.qt) {
 #pragma unroll
@@ -2233,23 +2323,23 @@ __device__ __forceinline__ void pp_epi_codes(const pp::acc_t (&acc)[pp::FN][pp::
 #pragma unroll
                 for (int j = 0; j < JH; ++j)
                     *reinterpret_cast<uint32_t*>(stg + (i * 16 + 4 * h + l % 4) * 64 + ((j ^ h) * 16) + (l & ~3)) =
-                        quad_transpose(w[i][j], lane);
-            pp_codes_out(p.qt, p.ldqt, p.N, n0, m0 + r0, stg, lane);
+                        quad_transpose(w[i][half * JH + j], lane);
+            pp_codes_out<NT>(p.qt, p.ldqt, p.ldqt, p.N, n0, m0 + r0, stg, lane);
         }
         __builtin_amdgcn_sched_barrier(0);
     }
 }
 
-// A launch of a product in pieces: the sums so far into acc; false: they go on to
-// the next launch.
+// kEpiSum for unit u: the sums so far into acc; false: they go on to the next launch.
 template <class P>
-__device__ __forceinline__ bool pp_sum(pp::acc_t (&acc)[pp::FN][pp::FM], const P& p, int t, int wave, int lane) {
+__device__ __forceinline__ bool pp_sum(pp::acc_t (&acc)[pp::FN][pp::FM], const P& p, int u, int wave, int lane) {
     if constexpr (std::is_same_v<P, SumParams>) {
         constexpr int PER_WAVE = 128 * 64;
-        float* at = p.partials + ((size_t)t * pp::WAVES + wave) * PER_WAVE;
-        if (!p.first) partial_accumulate<pp::FN, pp::FM>(acc, at, kWave, lane, PER_WAVE * 4);
+        float* at = p.partials + ((size_t)u * pp::WAVES + wave) * PER_WAVE;
+        // (read by a later launch only: no policy of their own)
+        if (!p.first) partial_accumulate<pp::FN, pp::FM, 0>(acc, at, kWave, lane, PER_WAVE * 4);
         if (p.last) return true;
-        partial_publish<pp::FN, pp::FM>(acc, at, kWave, lane, PER_WAVE * 4);
+        partial_publish<pp::FN, pp::FM, 0>(acc, at, kWave, lane, PER_WAVE * 4);
         return false;
     }
     return true;
@@ -2258,7 +2348,11 @@ __device__ __forceinline__ bool pp_sum(pp::acc_t (&acc)[pp::FN][pp::FM], const P
 template <int GROUP_M, int FMT, int EPI = kEpiScale>
 __global__ void __launch_bounds__(pp::THREADS) fp8_gemm_pp_kernel(KernelParams<EPI> p) {
     using namespace pp;
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[LDS_BYTES];
+    // The cross entropy's epilogues: arithmetic on every logit, and little or nothing to
+    // store.  The next unit's first slices are issued ahead of them (kEarly) and land
+    // meanwhile.
+    constexpr bool kEarly = EPI == kEpiStats || EPI == kEpiCodes;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[kEarly ? LOSS_LDS_BYTES : LDS_BYTES];
 
     const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -2294,6 +2388,8 @@ __global__ void __launch_bounds__(pp::THREADS) fp8_gemm_pp_kernel(KernelParams<E
         bias = reinterpret_cast<uint16_t*>(sb + BN);
     };
 
+    auto row_area = [&](int parity) { return reinterpret_cast<float2*>(smem + ROWS0 + parity * ROW_BYTES); };
+
     int parity = 0;
     PpTile T = pp_tile(p, wg, GROUP_M, xcd);
     if (grp == 0) {
@@ -2306,6 +2402,7 @@ __global__ void __launch_bounds__(pp::THREADS) fp8_gemm_pp_kernel(KernelParams<E
             uint16_t* bias;
             epi_area(0, sa, sb, bias);
             pp_params_store(pv, tid, sa, sb, bias);
+            if constexpr (kEarly) row_area(0)[tid] = pv.row;
         }
     }
     barrier_lds();
@@ -2348,16 +2445,32 @@ __global__ void __launch_bounds__(pp::THREADS) fp8_gemm_pp_kernel(KernelParams<E
             // this group's wait, so the next unit's first reads, which take
             // rows all four waves of this group loaded, find them landed.
             const int un = u + G;
-            if (!split || pp_split_fixup(acc, p, u, T.t, wave, pp_lane())) {
+            PpTile Tn;
+            PpParams pn;
+            if constexpr (kEarly) {
+                if (un < num_units) {
+                    Tn = pp_tile(p, un, GROUP_M, xcd);
+                    pn = pp_params_load<EPI>(p, Tn, tid, has_bias, s_pt);
+                    pp_tile_start(smem, p, Tn, pp_loads(p.K, q, pp_lane()), q);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (EPI == kEpiSum || !split || pp_split_fixup(acc, p, u, T.t, wave, pp_lane())) {
                 if constexpr (EPI == kEpiLinear)
                     pp_epi_store(acc, p, T.row0, T.col0, 0, q * 64, epi_sa, epi_sb, epi_bias,
                                  smem + STG0 + q * STG_BYTES);
                 else if constexpr (EPI == kEpiStats)
-                    pp_epi_stats(acc, p, T, 0, q, epi_sa, epi_sb);
-                else if constexpr (EPI == kEpiCodes)
-                    pp_epi_codes(acc, p, T.row0 + 0, T.col0 + q * 64, epi_sa + 0, epi_sb + q * 64,
-                                 smem + STG0 + q * STG_BYTES);
-                else if (EPI != kEpiSum || pp_sum(acc, p, T.t, wave, pp_lane()))
+                    pp_epi_stats(acc, p, T.row0, T.col0, 0, q, epi_sa, epi_sb, row_area(parity));
+                else if constexpr (EPI == kEpiCodes) {
+                    uint32_t w[FN][FM];
+                    pp_epi_codes(acc, w, p, T.col0, 0, q, epi_sa, epi_sb, row_area(parity));
+                    // The next unit's slices first, which a wait after the stores would
+                    // only see behind them.
+                    wait_vmcnt<0>();
+                    if (p.stream_out) pp_codes_store<true>(w, p, T.row0, T.col0 + q * 64, smem + STG0 + q * STG_BYTES);
+                    else pp_codes_store<false>(w, p, T.row0, T.col0 + q * 64, smem + STG0 + q * STG_BYTES);
+                }
+                else if (EPI != kEpiSum || pp_sum(acc, p, u, wave, pp_lane()))
                     pp_store(acc, p, T.row0, T.col0, 0, q * 64, epi_sa, epi_sb, epi_bias, s_pt,
                              has_bias, pp_lane(), smem + STG0 + q * STG_BYTES);
             }
@@ -2371,16 +2484,22 @@ __global__ void __launch_bounds__(pp::THREADS) fp8_gemm_pp_kernel(KernelParams<E
             __builtin_amdgcn_sched_barrier(0);
             if constexpr (EPI) L = pp_loads(p.K, q, pp_lane());
             if (un < num_units) {
-                T = pp_tile(p, un, GROUP_M, xcd);
                 PpParams pv;
-                if (need_epi) pv = pp_params_load<EPI>(p, T, tid, has_bias, s_pt);
-                pp_tile_start(smem, p, T, L, q);
-                wait_vmcnt<0>();
+                if constexpr (kEarly) {
+                    T = Tn;
+                    pv = pn;
+                } else {
+                    T = pp_tile(p, un, GROUP_M, xcd);
+                    if (need_epi) pv = pp_params_load<EPI>(p, T, tid, has_bias, s_pt);
+                    pp_tile_start(smem, p, T, L, q);
+                }
+                if (EPI != kEpiCodes || split) wait_vmcnt<0>();   // (with codes: before their stores)
                 if (need_epi) {
                     float *sa, *sb;
                     uint16_t* bias;
                     epi_area(parity ^ 1, sa, sb, bias);
                     pp_params_store(pv, tid, sa, sb, bias);
+                    if constexpr (kEarly) row_area(parity ^ 1)[tid] = pv.row;
                 }
             }
             barrier_lds();   // group 1's outputs issued; this group's first slices landed
@@ -2404,16 +2523,19 @@ __global__ void __launch_bounds__(pp::THREADS) fp8_gemm_pp_kernel(KernelParams<E
                 if (!EPI || s + 1 < T.n) barrier_lds();
                 __builtin_amdgcn_sched_barrier(0);
             }
-            if (!split || pp_split_fixup(acc, p, u, T.t, wave, pp_lane())) {
+            if (EPI == kEpiSum || !split || pp_split_fixup(acc, p, u, T.t, wave, pp_lane())) {
                 if constexpr (EPI == kEpiLinear)
                     pp_epi_store(acc, p, T.row0, T.col0, 128, q * 64, epi_sa, epi_sb, epi_bias,
                                  smem + STG1 + q * STG_BYTES);
                 else if constexpr (EPI == kEpiStats)
-                    pp_epi_stats(acc, p, T, 128, q, epi_sa, epi_sb);
-                else if constexpr (EPI == kEpiCodes)
-                    pp_epi_codes(acc, p, T.row0 + 128, T.col0 + q * 64, epi_sa + 128, epi_sb + q * 64,
-                                 smem + STG1 + q * STG_BYTES);
-                else if (EPI != kEpiSum || pp_sum(acc, p, T.t, wave, pp_lane()))
+                    pp_epi_stats(acc, p, T.row0, T.col0, 128, q, epi_sa, epi_sb, row_area(parity));
+                else if constexpr (EPI == kEpiCodes) {
+                    uint32_t w[FN][FM];
+                    pp_epi_codes(acc, w, p, T.col0, 128, q, epi_sa, epi_sb, row_area(parity));
+                    if (p.stream_out) pp_codes_store<true>(w, p, T.row0 + 128, T.col0 + q * 64, smem + STG1 + q * STG_BYTES);
+                    else pp_codes_store<false>(w, p, T.row0 + 128, T.col0 + q * 64, smem + STG1 + q * STG_BYTES);
+                }
+                else if (EPI != kEpiSum || pp_sum(acc, p, u, wave, pp_lane()))
                     pp_store(acc, p, T.row0, T.col0, 128, q * 64, epi_sa, epi_sb, epi_bias, s_pt,
                              has_bias, pp_lane(), smem + STG1 + q * STG_BYTES);
             }

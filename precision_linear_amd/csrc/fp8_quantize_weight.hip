@@ -35,8 +35,8 @@ __global__ void __launch_bounds__(256) zero_floats_kernel(float* p, int64_t n) {
 
 template <class T, int FMT>
 void launch_weight(const CodeJob& p, hipStream_t hs) {
-    if (p.M * p.K * (int64_t)sizeof(T) > kCachedBytes && sizeof(T) == 2) launch_codes<T, FMT, false, true, sizeof(T) == 2>(p, hs);
-    else launch_codes<T, FMT, false, true, false>(p, hs);
+    if (p.M * p.K * (int64_t)sizeof(T) > kCachedBytes && sizeof(T) == 2) launch_codes<T, FMT, true, sizeof(T) == 2>(p, NoFactor(), hs);
+    else launch_codes<T, FMT, true, false>(p, NoFactor(), hs);
 }
 
 }  // namespace

@@ -482,6 +482,10 @@ __global__ void __launch_bounds__(256) clear_counters_kernel(unsigned* c, int n)
 // Where a call's split-K workspace comes from.
 enum class WsSource { kNone, kCaller, kScratch };
 
+// Operands and output of more bytes than the memory-side cache holds: see
+// pp_store_staged.
+constexpr int64_t kStreamBytes = int64_t(256) << 20;
+
 Params base_params(const void* A, const void* B, const float* scale_a, const float* scale_b,
                    const void* bias, void* out, int64_t M, int64_t N, int64_t K, int mode,
                    const ConfigInfo& c) {
@@ -502,7 +506,7 @@ Params base_params(const void* A, const void* B, const float* scale_a, const flo
     p.rowwise = mode == FP8MM_ROWWISE;
     p.vec_store = (N % 4 == 0) && aligned(out, 8);
     p.vec16 = (N % 8 == 0) && aligned(out, 16);
-    p.stream_out = N <= kStreamCols && M * K + N * K + 2 * M * N > (int64_t(256) << 20);
+    p.stream_out = N <= kStreamCols && M * K + N * K + 2 * M * N > kStreamBytes;
     p.splits = 1;
     p.k_chunk = p.k_iters;
     p.counters = nullptr;
@@ -573,7 +577,8 @@ struct Epilogue {
 int run_mm(const void* A, int a_format, const void* B, int b_format, const float* scale_a,
            const float* scale_b, const void* bias, void* out, int64_t M, int64_t N, int64_t K,
            int mode, struct ihipStream_t* stream, int config_id, int splits, void* workspace,
-           int64_t workspace_size, WsSource src, const Epilogue* epi = nullptr) {
+           int64_t workspace_size, WsSource src, const Epilogue* epi = nullptr,
+           int64_t stream_from = kStreamBytes) {
     if ((a_format != FP8MM_E4M3FN && a_format != FP8MM_E5M2) ||
         (b_format != FP8MM_E4M3FN && b_format != FP8MM_E5M2))
         return FP8MM_ERR_FORMAT;
@@ -630,6 +635,7 @@ int run_mm(const void* A, int a_format, const void* B, int b_format, const float
 
     LinearParams p;
     static_cast<Params&>(p) = base_params(A, B, scale_a, scale_b, bias, out, M, N, K, mode, c);
+    p.stream_out = N <= kStreamCols && M * K + N * K + 2 * M * N > stream_from;
     p.splits = sp;
     p.k_chunk = (int)cdiv(k_iters, sp);
     if (epi) {
@@ -817,6 +823,33 @@ int loss_counters(int64_t M, int64_t V, const LossPlan& plan) {
     return plan.splits > 1 ? (int)(loss_tiles(M, V, plan) * counters_per_tile(plan.cfg)) : 0;
 }
 
+// A round of 256 tiles of the ping-pong kernel takes about 1.35 us for each K slice and
+// 8 us more; tiles that fill a part of the CUs run on smaller tiles at about 0.65 of its
+// rate, after 5 us of a launch's own.
+int64_t whole_rounds(int64_t fixed, int64_t n, int64_t k) {
+    const ConfigInfo& c = kConfigs[kPingPongConfig];
+    const int64_t across = cdiv(fixed, c.bm), tiles = across * cdiv(n, c.bn);
+    const int64_t rounds = tiles / 256, rest = tiles % 256;
+    if (rounds == 0 || rest == 0 || rounds * 256 / across == 0) return n;
+    const double round = 1.35 * (double)cdiv(k, c.bk) + 8.0;
+    if (5.0 + round * (double)rest / 256.0 / 0.65 > 0.9 * round) return n;
+    return rounds * 256 / across * c.bn;
+}
+
+// The plan model was fitted up to K of 28672.  Beyond, where the 256 x 256 tiles leave CUs
+// idle, units that fill most of them with 16 slices and more are the better plan, their
+// sums joined by a launch of its own (the wave that is last to arrive would read them all: 1001 x 2048 x
+// 50256 in 8 units, 115 us with that).
+int long_sum_splits(int64_t M, int64_t N, int64_t k) {
+    const ConfigInfo& c = kConfigs[kPingPongConfig];
+    const int64_t tiles = cdiv(M, c.bm) * cdiv(N, c.bn), slices = cdiv(k, c.bk);
+    if (k <= 28672 || M <= 128 || tiles > 128) return 0;
+    const int64_t splits = 256 / tiles;
+    return tiles * splits >= 192 && slices / splits >= 16 ? (int)cdiv(slices, cdiv(slices, splits)) : 0;
+}
+
+int ping_pong_config() { return kPingPongConfig; }
+
 static int run_loss(const LaunchPair* const (&tables)[kFormats], const Logits& z, const LossPlan& plan, LossParams& p,
                     hipStream_t stream, void* ws) {
     int dev = -1;
@@ -826,6 +859,10 @@ static int run_loss(const LaunchPair* const (&tables)[kFormats], const Logits& z
     const ConfigInfo& c = kConfigs[plan.cfg];
     static_cast<Params&>(p) =
         base_params(z.A, z.B, z.scale_a, z.scale_b, nullptr, nullptr, z.M, z.V, z.K, z.mode, c);
+    // Non-temporal stores of codes that the memory-side cache does not hold (us of the whole
+    // gradient on one MI355X without and with: 8192 x 131072 x 4096 9240 and 9015; 1001 x
+    // 50255 x 2048, whose codes it holds, 367 and 389).
+    p.stream_out = z.M * z.V * ((p.q != nullptr) + (p.qt != nullptr)) > (int64_t(256) << 20);
     p.splits = plan.splits;
     p.k_chunk = (int)cdiv(p.k_iters, plan.splits);
     if (plan.splits > 1) {
@@ -842,12 +879,13 @@ static int run_loss(const LaunchPair* const (&tables)[kFormats], const Logits& z
 }
 
 int run_stats(const Logits& z, const LossPlan& plan, const int64_t* target, float2* part, float* target_logit,
-              hipStream_t stream, void* ws) {
+              int64_t col0, hipStream_t stream, void* ws) {
     static const LaunchPair* const tables[kFormats] = {kStatsF0, kStatsF1, kStatsF2, kStatsF3};
     LossParams p{};
     p.target = target;
     p.part = part;
     p.target_logit = target_logit;
+    p.col0 = (int)col0;
     return run_loss(tables, z, plan, p, stream, ws);
 }
 
@@ -864,9 +902,17 @@ int run_codes(const Logits& z, const LossPlan& plan, const float2* rows, uint8_t
     return run_loss(tables, z, plan, p, stream, ws);
 }
 
-int64_t sum_workspace(int64_t M, int64_t N) {
+// (us of the whole gradient on one MI355X with the multiply's own 256 MB and with 128: 1001 x
+// 50255 x 2048, whose dw and operands are 259 MB, 370 and 351.)
+int run_streamed(const Product& p, hipStream_t stream, void* ws, int64_t ws_bytes) {
+    return run_mm(p.A, FP8MM_E5M2, p.B, FP8MM_E4M3FN, p.scale_a, p.scale_b, nullptr, p.out, p.M, p.N, p.K, FP8MM_ROWWISE,
+                  reinterpret_cast<struct ihipStream_t*>(stream), -1, 0, ws, ws_bytes, WsSource::kCaller, nullptr,
+                  int64_t(128) << 20);
+}
+
+int64_t sum_workspace(int64_t M, int64_t N, int splits) {
     const ConfigInfo& c = kConfigs[kPingPongConfig];
-    return cdiv(M, c.bm) * cdiv(N, c.bn) * c.bm * c.bn * 4;
+    return cdiv(M, c.bm) * cdiv(N, c.bn) * splits * c.bm * c.bn * 4;
 }
 
 int run_sum(const SumPiece& q, hipStream_t stream, void* sums) {
@@ -880,9 +926,12 @@ int run_sum(const SumPiece& q, hipStream_t stream, void* sums) {
     p.partials = static_cast<float*>(sums);
     p.ldb = (int)q.ldb;
     p.first = q.first;
-    p.last = q.last;
+    p.last = q.last && q.splits == 1;
+    p.splits = q.splits;
+    p.k_chunk = (int)cdiv(p.k_iters, q.splits);
     (void)hipGetLastError();
-    kSum[q.b_format == FP8MM_E5M2](p, dim3((unsigned)grid_for(kPingPongConfig, q.M, q.N, 1, cus)), stream);
+    kSum[q.b_format == FP8MM_E5M2](p, dim3((unsigned)grid_for(kPingPongConfig, q.M, q.N, q.splits, cus)), stream);
+    if (q.splits > 1) join_sums(p, stream);
     return hipGetLastError() == hipSuccess ? FP8MM_OK : FP8MM_ERR_LAUNCH;
 }
 
