@@ -107,7 +107,9 @@ class _AdamwNumbers(ctypes.Structure):       # struct adamw_numbers
 _CALLS_ENTRIES = ("fp8_layer_norm", "fp8_layer_norm_backward", "fp8_layer_norm_backward_workspace_size",
                   "fp8_linear", "fp8_scaled_mm_workspace_size", "fp8_linear_backward",
                   "fp8_linear_backward_workspace_size", "fp8_linear_cross_entropy",
-                  "fp8_linear_cross_entropy_workspace_size", "adamw_step")
+                  "fp8_linear_cross_entropy_workspace_size", "fp8_linear_cross_entropy_backward",
+                  "fp8_linear_cross_entropy_backward_workspace_size", "fp8_quantize_weight",
+                  "fp8_quantize_weight_workspace_size", "adamw_step")
 
 
 class Fp8MMError(RuntimeError):
@@ -700,6 +702,14 @@ def fp8_linear_cross_entropy_backward(dloss: torch.Tensor, a: torch.Tensor, b: t
     sums live in `workspace` (a GPU byte tensor with any contents) or in memory that
     torch has back after the call (a graph captured without torch.cuda.graph needs one
     that stays)."""
+    if (_calls is not None and dx is dw is True and a_format is b_format is wt_format is workspace is None
+            and isinstance(mode, (str, int))):
+        got = _calls.cross_entropy_backward(dloss, a, b, scale_a, scale_b, target, loss, lse, x, wt, wt_scale,
+                                            ignore_index, _MODES.get(mode, -1))
+        if got.__class__ is tuple:
+            return got
+        if got is not None:
+            _mm_error("fp8_linear_cross_entropy_backward", got)
     for name, t in (("dx", dx), ("dw", dw)):
         if t is not True and t is not False and not isinstance(t, torch.Tensor):
             raise ValueError(f"{name} must be True, False or a tensor to write")
@@ -837,6 +847,12 @@ def fp8_quantize_weight(w: torch.Tensor, fmt="e4m3fn", *, q: torch.Tensor | None
     if fmt not in _FORMATS:
         raise ValueError(f"fmt must be 'e4m3fn' or 'e5m2', got {fmt!r}")
     f = _FORMATS[fmt]
+    if _calls is not None and q is scale is qt is scale_t is workspace is None:
+        got = _calls.quantize_weight(w, f)
+        if got.__class__ is tuple:
+            return tuple.__new__(WeightCodes, got)
+        if got is not None:
+            _mm_error("fp8_quantize_weight", got)
     _ln_matrix(w, "w")
     N, K = w.shape
     if K < 16 or K % 16 != 0:

@@ -4,9 +4,9 @@
 // Bound by memory: with fp32 moments, an fp32 parameter and a bf16 gradient an element
 // is 14 bytes read and 12 written; with 8-bit moments 8 and 6.  The tensors' addresses go
 // into the kernel's arguments (48 tensors a launch), so nothing is copied to the GPU
-// beforehand and a capture holds them.  A workgroup takes 4096 elements of one tensor,
-// which it finds by the first chunks of all; a wave takes 256 elements, a block of the
-// 8-bit moments, at a time, with four of them in flight.
+// beforehand and a capture holds them.  A workgroup takes a chunk of one tensor, which it
+// finds by the first chunks of all; a wave takes 256 elements, a block of the 8-bit
+// moments, at a time, with several of them in flight.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -23,8 +23,12 @@ constexpr int kTensors = 48;              // of a launch (the arguments stay und
 constexpr int kBlock = 256;               // elements of a block and of a wave at a time
 constexpr int kStepThreads = 256;
 constexpr int kWaves = kStepThreads / kWaveSize;
-constexpr int kInFlight = 4;              // blocks of a wave
-constexpr int kChunk = kBlock * kWaves * kInFlight;
+
+// Blocks of a wave in flight: loads enough, and registers few enough for more waves (us on
+// one MI355X of 2, 3 and 4: 4.7e8 elements with fp32 moments 2196, 2202 and 2128, with 8-bit
+// ones 1143, 1152 and 1171; 1.1e8 with a master 524, 533 and 561).
+constexpr int in_flight(int bits, bool master) { return bits == 8 || master ? 2 : 4; }
+constexpr int chunk_size(int bits, bool master) { return kBlock * kWaves * in_flight(bits, master); }
 
 struct Entry {
     void* param;
@@ -90,7 +94,9 @@ template <bool NT, class T>
 __device__ __forceinline__ Raw4<T> load4(const T* p, int64_t at, int64_t left) {
     Raw4<T> r;
     if (left >= 4) {
-        r.v = load_hinted<NT, decltype(r.v)>(reinterpret_cast<const typename Raw4<T>::memory*>(p + at));
+        const auto* from = reinterpret_cast<const typename Raw4<T>::memory*>(p + at);
+        if constexpr (NT) r.v = __builtin_nontemporal_load(from);
+        else r.v = *from;
     } else {
         T e[4] = {};
         for (int i = 0; i < left; ++i) e[i] = p[at + i];
@@ -103,7 +109,9 @@ __device__ __forceinline__ void store4(T* p, int64_t at, int64_t left, const flo
     Raw4<T> r;
     r.set(f);
     if (left >= 4) {
-        store_hinted<NT>(reinterpret_cast<typename Raw4<T>::memory*>(p + at), r.v);
+        auto* to = reinterpret_cast<typename Raw4<T>::memory*>(p + at);
+        if constexpr (NT) __builtin_nontemporal_store(r.v, to);
+        else *to = r.v;
     } else {
         T e[4];
         __builtin_memcpy(e, &r.v, sizeof(e));
@@ -132,6 +140,20 @@ __device__ __forceinline__ float round_at_random(float y, uint32_t r) {
     return copysignf(t, y);
 }
 
+// sqrt(v) for v >= 0.  With 8-bit moments the step is bound by its arithmetic unless the
+// square root and the quotient are the hardware's (1 ulp; 4.7e8 elements 1330 and 1150
+// us); it takes values below 2^-96 for 0, so those are lifted.
+template <bool FAST>
+__device__ __forceinline__ float root_of(float v) {
+    if constexpr (!FAST) return sqrtf(v);
+    const bool tiny = v < 0x1p-96f;
+    return __builtin_amdgcn_sqrtf(tiny ? v * 0x1p64f : v) * (tiny ? 0x1p-32f : 1.f);
+}
+template <bool FAST>
+__device__ __forceinline__ float quotient(float a, float b) {
+    return FAST ? a * __builtin_amdgcn_rcpf(b) : a / b;
+}
+
 // The scale of a block whose largest magnitude is amax, and what values are
 // multiplied by.
 __device__ __forceinline__ float2 block_scale(float amax) {
@@ -144,6 +166,7 @@ template <class P, class G, int BITS, bool MASTER, bool NT>
 __global__ void __launch_bounds__(kStepThreads) adamw_kernel(StepArgs a) {
     typedef std::conditional_t<BITS == 8, uint8_t, float> S;
     typedef std::conditional_t<MASTER, float, P> W;       // what the step reads and writes
+    constexpr int kInFlight = in_flight(BITS, MASTER), kChunk = chunk_size(BITS, MASTER);
     // This workgroup's tensor.
     int lo = 0, hi = a.count;
     while (hi - lo > 1) {
@@ -205,8 +228,8 @@ __global__ void __launch_bounds__(kStepThreads) adamw_kernel(StepArgs a) {
             }
             fm[i] = fmaf(a.beta1, m0, a.beta1_rest * g);
             fv[i] = fmaf(a.beta2, v0, a.beta2_rest * (g * g));
-            root[i] = sqrtf(fv[i]);
-            const float step = fm[i] / fmaf(root[i], corr2, a.eps);
+            root[i] = root_of<BITS == 8>(fv[i]);
+            const float step = quotient<BITS == 8>(fm[i], fmaf(root[i], corr2, a.eps));
             fw[i] = fmaf(rw[u].get(i), decay, -rate * step);
         }
         if constexpr (BITS == 8) {
@@ -325,6 +348,7 @@ int adamw_step(const adamw_tensor* tensors, int64_t count, int param_dtype, int 
     int dev = -1;
     if (hipGetDevice(&dev) != hipSuccess) return ADAMW_ERR_DEVICE;
     const hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+    const int64_t chunk = chunk_size(state_bits, master);
     const int64_t bytes = total * (int64_t)((master ? 10 : 2 * pa) + ga + (state_bits == 8 ? 4 : 16));
     StepArgs a;
     a.beta1 = (float)numbers->beta1;
@@ -359,7 +383,7 @@ int adamw_step(const adamw_tensor* tensors, int64_t count, int param_dtype, int 
     for (int64_t i = 0; i < count; ++i) {
         const adamw_tensor& t = tensors[i];
         for (int64_t done = 0; done < t.numel;) {
-            const int64_t n = std::min(t.numel - done, (kMaxChunks - chunks) * kChunk);
+            const int64_t n = std::min(t.numel - done, (kMaxChunks - chunks) * chunk);
             Entry& e = a.t[a.count];
             auto step_on = [&](auto* p, int64_t size) {
                 return p ? (decltype(p))((uintptr_t)p + (uintptr_t)(done * size)) : p;
@@ -374,7 +398,7 @@ int adamw_step(const adamw_tensor* tensors, int64_t count, int param_dtype, int 
             e.numel = n;
             e.first_block = block;
             a.first_chunk[a.count++] = (uint32_t)chunks;
-            chunks += (n + kChunk - 1) / kChunk;
+            chunks += (n + chunk - 1) / chunk;
             block += (n + kBlock - 1) / kBlock;
             done += n;
             if (a.count == kTensors || chunks == kMaxChunks) flush();

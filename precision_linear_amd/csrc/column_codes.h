@@ -17,6 +17,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "fp8_convert.h"
 #include "lane_ops.h"
 
@@ -229,20 +231,16 @@ __global__ void __launch_bounds__(kCodeThreads) codes_kernel(CodeJob p, int col_
         cs[i] = s_col[0][cl * 8 + i];
         cr[i] = s_col[1][cl * 8 + i];
     }
-    // value / s: with s = 0 every finite value gives 0.
-    auto over = [&](float v, float s, float r) __attribute__((always_inline)) {
-        const Div d{s, r, true};
-        if (!slow) return quant1<FMT, true>(v, d);
-        return s == 0.f ? v * 0.f : quant1<FMT, false>(v, d);
-    };
-#pragma unroll 1
-    for (int it = 0; it < kSteps; ++it) {
-        const int mg = it * kCodeRowLanes + rl;            // group of 4 rows in the tile
+    // The 4 rows of group `mg` in f, FAST: every division here is in the fast one's range.
+    auto rows_of = [&](auto fast, int mg, const float (&f)[4][8]) __attribute__((always_inline)) {
+        constexpr bool FAST = decltype(fast)::value;
         const int64_t r = row0 + mg * 4;
-        float f[4][8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) code_values<T, FACTOR>(a[k], s_row[2][mg * 4 + k], f[k]);
-        if (it + 1 < kSteps) fetch(it + 1);
+        // value / s: with s = 0 every finite value gives 0.
+        auto over = [](float v, float s, float rr) __attribute__((always_inline)) {
+            const Div d{s, rr, true};
+            if constexpr (FAST) return quant1<FMT, true>(v, d);
+            else return s == 0.f ? v * 0.f : quant1<FMT, false>(v, d);
+        };
         if constexpr (ROWS) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -263,6 +261,16 @@ __global__ void __launch_bounds__(kCodeThreads) codes_kernel(CodeJob p, int col_
             s_t[cl * 8 + i][(((mg >> 2) ^ (cl % kChunks)) << 2) | (mg & 3)] =
                 (uint32_t)Fp8Fmt<FMT>::template cvt_pk<true>(over(f[2][i], cs[i], cr[i]), over(f[3][i], cs[i], cr[i]), w);
         }
+    };
+#pragma unroll 1
+    for (int it = 0; it < kSteps; ++it) {
+        const int mg = it * kCodeRowLanes + rl;            // group of 4 rows in the tile
+        float f[4][8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) code_values<T, FACTOR>(a[k], s_row[2][mg * 4 + k], f[k]);
+        if (it + 1 < kSteps) fetch(it + 1);
+        if (!slow) rows_of(std::true_type(), mg, f);
+        else rows_of(std::false_type(), mg, f);
     }
     __syncthreads();
 #pragma unroll

@@ -30,6 +30,7 @@
 #include "../../include/fp8_cross_entropy.h"
 #include "../../include/fp8_layer_norm.h"
 #include "../../include/fp8_linear.h"
+#include "../../include/fp8_quantize_weight.h"
 
 namespace {
 
@@ -45,6 +46,10 @@ struct Library {
     decltype(&fp8_linear_backward_workspace_size) linear_backward_workspace;
     decltype(&fp8_linear_cross_entropy) cross_entropy;
     decltype(&fp8_linear_cross_entropy_workspace_size) cross_entropy_workspace;
+    decltype(&fp8_linear_cross_entropy_backward) cross_entropy_backward;
+    decltype(&fp8_linear_cross_entropy_backward_workspace_size) cross_entropy_backward_workspace;
+    decltype(&fp8_quantize_weight) quantize_weight;
+    decltype(&fp8_quantize_weight_workspace_size) quantize_weight_workspace;
     decltype(&adamw_step) adamw;
 };
 Library g_lib{};
@@ -362,6 +367,82 @@ PyObject* cross_entropy(PyObject*, PyObject* const* arg, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// (dloss, a, b, scale_a, scale_b, target, loss, lse, x, wt, wt_scale, ignore_index,
+// mode) -> (dx, dw)
+PyObject* cross_entropy_backward(PyObject*, PyObject* const* arg, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 13 || !g_lib.norm) Py_RETURN_NONE;
+    const Arg dl(arg[0]), a(arg[1]), b(arg[2]), sa(arg[3]), sb(arg[4]), target(arg[5]), loss(arg[6]), lse(arg[7]);
+    const Arg x(arg[8]), wt(arg[9]), swt(arg[10]);
+    const int dev = device_of(a);
+    if (dev < 0 || !PyLong_CheckExact(arg[11]) || !PyLong_CheckExact(arg[12])) Py_RETURN_NONE;
+    int overflow = 0;
+    const int64_t ignore = PyLong_AsLongLongAndOverflow(arg[11], &overflow);
+    const int mode = (int)PyLong_AsLong(arg[12]);
+    if (overflow || !a.on(dev) || !b.on(dev) || a.t->dim() != 2 || b.t->dim() != 2 || !wt.on(dev)) Py_RETURN_NONE;
+    const int64_t M = a.t->size(0), K = a.t->size(1), V = b.t->size(0), Vp = (V + 15) / 16 * 16;
+    const int fa = code_format(*a.t), fb = code_format(*b.t), fw = code_format(*wt.t);
+    const bool rowwise = mode == FP8MM_ROWWISE;
+    if (M == 0 || V == 0 || b.t->size(1) != K || fa < 0 || fb < 0 || fw < 0 ||
+        (!rowwise && mode != FP8MM_PER_TENSOR) || !sa.vector(dev, at::kFloat, rowwise ? M : 1) ||
+        !sb.vector(dev, at::kFloat, rowwise ? V : 1) || !target.vector(dev, at::kLong, M) || target.t->dim() != 1 ||
+        !dl.vector(dev, at::kFloat, M) || dl.t->dim() != 1 || !loss.vector(dev, at::kFloat, M) ||
+        !lse.vector(dev, at::kFloat, M) || !x.matrix(dev, at::kBFloat16, M, K) || wt.t->dim() != 2 ||
+        wt.t->size(0) != K || wt.t->size(1) != Vp || !swt.vector(dev, at::kFloat, K))
+        Py_RETURN_NONE;
+    const int64_t need = g_lib.cross_entropy_backward_workspace(M, V, K, 1, 1);
+    if (need < 0) Py_RETURN_NONE;
+    const hipStream_t stream = c10::hip::getCurrentHIPStream(dev).stream();
+    const at::Tensor ws = allocate(*a.t, {need}, at::kByte);
+    at::Tensor out[2];
+    out[0] = allocate(*a.t, {M, K}, at::kBFloat16);
+    out[1] = allocate(*a.t, {V, K}, at::kBFloat16);
+    auto f32 = [](const Arg& t) { return static_cast<const float*>(t.ptr()); };
+    int st;
+    {
+        pybind11::gil_scoped_release free_interpreter;
+        st = g_lib.cross_entropy_backward(f32(dl), 1, a.ptr(), fa, b.ptr(), fb, f32(sa), f32(sb),
+                                          static_cast<const int64_t*>(target.ptr()), ignore, f32(loss), f32(lse),
+                                          x.ptr(), wt.ptr(), fw, f32(swt), out[0].data_ptr(), out[1].data_ptr(), M, V,
+                                          K, mode, reinterpret_cast<ihipStream_t*>(stream), ws.data_ptr(), need);
+    }
+    if (st != FP8MM_OK) return PyLong_FromLong(st);
+    return tuple_of(out);
+    END_HANDLE_TH_ERRORS
+}
+
+// (w, format) -> (q, scale, qt, scale_t)
+PyObject* quantize_weight(PyObject*, PyObject* const* arg, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 2 || !g_lib.norm) Py_RETURN_NONE;
+    const Arg w(arg[0]);
+    const int dev = device_of(w);
+    if (dev < 0 || !PyLong_CheckExact(arg[1]) || !w.on(dev) || w.t->dim() != 2) Py_RETURN_NONE;
+    const at::ScalarType type = w.t->scalar_type();
+    const int64_t N = w.t->size(0), K = w.t->size(1);
+    if ((type != at::kBFloat16 && type != at::kFloat) || N == 0) Py_RETURN_NONE;
+    const int64_t need = g_lib.quantize_weight_workspace(N, K);
+    if (need < 0) Py_RETURN_NONE;
+    const hipStream_t stream = c10::hip::getCurrentHIPStream(dev).stream();
+    const at::Tensor ws = allocate(*w.t, {need}, at::kByte);
+    at::Tensor out[4];
+    out[0] = allocate(*w.t, {N, K}, at::kByte);
+    out[1] = allocate(*w.t, {N}, at::kFloat);
+    out[2] = allocate(*w.t, {K, (N + 15) / 16 * 16}, at::kByte);
+    out[3] = allocate(*w.t, {K}, at::kFloat);
+    int st;
+    {
+        pybind11::gil_scoped_release free_interpreter;
+        st = g_lib.quantize_weight(w.ptr(), type == at::kFloat ? FP8W_FP32 : FP8W_BF16, (int)PyLong_AsLong(arg[1]),
+                                   out[0].data_ptr(), out[1].data_ptr<float>(), out[2].data_ptr(),
+                                   out[3].data_ptr<float>(), N, K, reinterpret_cast<ihipStream_t*>(stream),
+                                   ws.data_ptr(), need);
+    }
+    if (st != FP8MM_OK) return PyLong_FromLong(st);
+    return tuple_of(out);
+    END_HANDLE_TH_ERRORS
+}
+
 // A list of tensors as adamw_step's must be: one for each parameter, of one type.
 struct List {
     PyObject* const* items = nullptr;
@@ -509,7 +590,8 @@ constexpr PyMethodDef fast(const char* name) {
 
 PyMethodDef g_methods[] = {
     fast<layer_norm>("layer_norm"), fast<layer_norm_backward>("layer_norm_backward"), fast<linear>("linear"),
-    fast<linear_backward>("linear_backward"), fast<cross_entropy>("cross_entropy"), fast<adamw>("adamw_step"),
+    fast<linear_backward>("linear_backward"), fast<cross_entropy>("cross_entropy"), fast<cross_entropy_backward>("cross_entropy_backward"),
+    fast<quantize_weight>("quantize_weight"), fast<adamw>("adamw_step"),
     {"use_library", use_library, METH_VARARGS, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

@@ -3,9 +3,10 @@
 Tolerances, with u = 2^-24.  m = fma(b1, m0, c1 g): the two constants, the product and
 the sum round once each, so m is off by dm = 3 u (b1 |m0| + c1 |g|); v likewise, with g^2
 rounded too, by 4 u v.  The denominator (a square root, a product by a rounded factor
-and a sum) is then off by 6 u of itself, the quotient rounds by u, lr / (1 - b1^t) by 3 u
+and a sum) is then off by 5 u of itself, the quotient rounds by u, lr / (1 - b1^t) by 3 u
 and the products by 2 u: a step of size s is off by 12 u s + dm s / |m|, and p (its
-factor 1 - lr wd off by 2 u, the sum by u) by 3 u |p| more.  A bf16 output is rounded once
+factor 1 - lr wd off by 2 u, the sum by u) by 3 u |p| more.  With 8-bit moments the square
+root and the reciprocal are the hardware's, off by 2 u each, and their products round: 4 u more.  A bf16 output is rounded once
 more (torch.finfo(bf16).eps / 2).
 
 Moments of 8 bits.  What is rounded to a code, x / scale, is off by dm / scale (m), 3 u
@@ -99,10 +100,11 @@ def check(before, after, step, seed=0, gs=1.0, lr=HYPER["lr"], betas=HYPER["beta
         extra = 4 * U if eight else 0                       # (the stored values are products, squared)
         dm = (3 * U + extra + 2 * U * (gs != 1)) * (b1 * m0.abs() + (1 - b1) * g.abs())
         rv = 4 * U + extra + 4 * U * (gs != 1)              # of v
+        fast = 4 * U * eight
         den = v.sqrt() / math.sqrt(1 - b2 ** step) + eps
         rate = lr / (1 - b1 ** step)
         w = w0 * (1 - lr * weight_decay) - rate * m / den
-        tol = 3 * U * w0.abs() + rate / den * (dm + (12 * U + rv) * m.abs()) + 1e-44
+        tol = 3 * U * w0.abs() + rate / den * (dm + (12 * U + rv + fast) * m.abs()) + 1e-44
         for x, half in ((after["params"][i], HALF if p.dtype == BF16 else 0),
                         (None if after["master"] is None else after["master"][i], 0)):
             if x is not None:
@@ -115,7 +117,7 @@ def check(before, after, step, seed=0, gs=1.0, lr=HYPER["lr"], betas=HYPER["beta
         r = random_bits(seed, torch.arange(n, device=DEV) + 256 * blocks_before)
         blocks_before += blocks
         for name, x, d, bits, positive in (("exp_avg", m, dm, r & 0xffff, False),
-                                           ("exp_avg_sq", v.sqrt(), rv * v.sqrt(), r >> 16, True)):
+                                           ("exp_avg_sq", v.sqrt(), (rv + fast) * v.sqrt(), r >> 16, True)):
             scale = torch.zeros(blocks, dtype=torch.float64, device=DEV).scatter_reduce(0, of, x.abs(), "amax") / 448
             most = torch.zeros(blocks, dtype=torch.float64, device=DEV).scatter_reduce(0, of, d, "amax") / 448
             got = after[name + "_scale"][i].double()
@@ -224,6 +226,19 @@ def test_small_second_moments_are_never_lost():
     # Each step is at most lr (1 + what m may be rounded up by: a whole code of 2^-9) / (...) of the
     # stored sqrt(v), itself at least a code: no more than a few lr, where m / eps would be 10^4 lr.
     assert (t["params"][0] - p0).abs().max() < 19 * HYPER["lr"] * 40
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_gradients_whose_squares_are_next_to_nothing(bits):
+    """v down to fp32's subnormal numbers: its root is no 0."""
+    t = make([256, 256, 256], FP32, FP32, bits)
+    s = binding.adamw_state(t["params"], bits)
+    t |= dict(exp_avg=s.exp_avg, exp_avg_sq=s.exp_avg_sq, exp_avg_scale=s.exp_avg_scale, exp_avg_sq_scale=s.exp_avg_sq_scale)
+    for g, size in zip(t["grads"], (1e-14, 1e-16, 1e-18)):
+        g.copy_(size * (1 + torch.rand(256, device=DEV)))
+    before = copies(t)
+    binding.adamw_step(**t, step=1, **HYPER | dict(eps=0.0, betas=(0.0, 0.5)))
+    check(before, t, 1, eps=0.0, betas=(0.0, 0.5))
 
 
 @pytest.mark.parametrize("bits", [32, 8])
