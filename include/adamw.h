@@ -9,7 +9,8 @@
  *     p = p (1 - lr weight_decay)
  *           - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
  *
- *   in fp32 (1 - beta^step in fp64, then rounded).  p is the master weight where there
+ *   in fp32 (1 - beta and 1 - beta^step in fp64, then rounded); in m, v and sqrt(v) every
+ *   product, sum and root is rounded as it is written.  p is the master weight where there
  *   is one; the parameter is then p rounded to bf16.  A bf16 parameter without a master
  *   is rounded to nearest, so steps below half its last bit leave it as it is.
  *

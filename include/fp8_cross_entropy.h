@@ -10,9 +10,10 @@
  *     lse[m]  = log sum_{j<V} exp(z[m][j])
  *     loss[m] = lse[m] - z[m][target[m]],  0 where target[m] == ignore_index
  *
- *   Sums, maxima and both outputs are fp32.  A target outside 0 .. V - 1 that is not
- *   ignore_index gives a NaN, and so does a row with a NaN or infinite logit (lse of
- *   ignored rows included).
+ *   Sums, maxima and both outputs are fp32; the loss is made as log(1 + sum over the
+ *   others of exp(z - z[target])), which keeps it exact next to 0.  A target outside 0 ..
+ *   V - 1 that is not ignore_index gives a loss of NaN; a NaN or +inf among a row's
+ *   logits makes its loss (unless the row is ignored) and lse NaN.
  */
 #ifndef FP8_CROSS_ENTROPY_H
 #define FP8_CROSS_ENTROPY_H

@@ -140,15 +140,22 @@ __device__ __forceinline__ float round_at_random(float y, uint32_t r) {
     return copysignf(t, y);
 }
 
-// sqrt(v) for v >= 0.  With 8-bit moments the step is bound by its arithmetic unless the
-// square root and the quotient are the hardware's (1 ulp; 4.7e8 elements 1330 and 1150
-// us); it takes values below 2^-96 for 0, so those are lifted.
-template <bool FAST>
+// sqrt(v) for v >= 0, correctly rounded.  The hardware's s is at most one step h off (and takes
+// values next to 0 for 0, so those are lifted): v lies below the midpoint to its lower
+// neighbour, (s - h / 2)^2 = s (s - h) + h^2 / 4, where v <= s (s - h), and above the one to the
+// upper where v > s (s + h), h^2 / 4 being less than a last bit of v.
 __device__ __forceinline__ float root_of(float v) {
-    if constexpr (!FAST) return sqrtf(v);
     const bool tiny = v < 0x1p-96f;
-    return __builtin_amdgcn_sqrtf(tiny ? v * 0x1p64f : v) * (tiny ? 0x1p-32f : 1.f);
+    v = tiny ? v * 0x1p64f : v;
+    float s = __builtin_amdgcn_sqrtf(v);
+    const float down = __uint_as_float(__float_as_uint(s) - 1), up = __uint_as_float(__float_as_uint(s) + 1);
+    const float by_down = fmaf(-down, s, v), by_up = fmaf(-up, s, v);
+    const float r = by_down <= 0.f ? down : by_up > 0.f ? up : s;
+    s = v > 0.f && v < __builtin_inff() ? r : s;
+    return s * (tiny ? 0x1p-32f : 1.f);
 }
+// a / b; with 8-bit moments by the hardware's reciprocal (1 ulp), as the step would
+// otherwise be bound by its arithmetic.
 template <bool FAST>
 __device__ __forceinline__ float quotient(float a, float b) {
     return FAST ? a * __builtin_amdgcn_rcpf(b) : a / b;
@@ -226,9 +233,14 @@ __global__ void __launch_bounds__(kStepThreads) adamw_kernel(StepArgs a) {
                 v0 *= vs[u];
                 v0 *= v0;
             }
-            fm[i] = fmaf(a.beta1, m0, a.beta1_rest * g);
-            fv[i] = fmaf(a.beta2, v0, a.beta2_rest * (g * g));
-            root[i] = root_of<BITS == 8>(fv[i]);
+            {
+                // Each product and sum rounds, as the formulas are written: which code a moment of
+                // 8 bits is rounded to hangs on its last bit.
+#pragma clang fp contract(off)
+                fm[i] = a.beta1 * m0 + a.beta1_rest * g;
+                fv[i] = a.beta2 * v0 + a.beta2_rest * (g * g);
+            }
+            root[i] = root_of(fv[i]);
             const float step = quotient<BITS == 8>(fm[i], fmaf(root[i], corr2, a.eps));
             fw[i] = fmaf(rw[u].get(i), decay, -rate * step);
         }

@@ -3,9 +3,11 @@
 //
 // Forward: the multiply's kernels with an epilogue that reduces each tile's logits
 // to the largest and the sum of exponentials of each row (by the 64 columns of a
-// wave, 16 to 128 in the generic tiles) and picks the target's logit;
-// loss_kernel joins them.  The product bounds it: 8 bytes leave the multiply for 64
-// logits.
+// wave, 16 to 128 in the generic tiles), the target's left out; loss_kernel joins them
+// with the target's logit, which it makes itself in fp32: the matrix instruction keeps a product
+// to 2^-13 of its largest, which averages out among the others.  The loss is log(1 +
+// sum of the others over the target's), so that a row that is sure of its target keeps
+// what little is left.  The product bounds it: 8 bytes leave the multiply for 64 logits.
 //
 // Gradient: the logits once more, with an epilogue that turns them into e5m2 codes
 // of dz, written by rows (for dx) and by columns (for dw), then the two products.
@@ -46,12 +48,69 @@ __device__ __forceinline__ int target_of(const int64_t* target, int64_t m, int64
     return t == ignore ? -1 : t >= 0 && t < V ? (int)t : -2;
 }
 
+// Code i of four.
+template <int FMT>
+__device__ __forceinline__ float code_value(uint32_t w, int i) {
+    const int v = (int)w;
+    if constexpr (FMT == 0)
+        return i == 0   ? __builtin_amdgcn_cvt_f32_fp8(v, 0)
+               : i == 1 ? __builtin_amdgcn_cvt_f32_fp8(v, 1)
+               : i == 2 ? __builtin_amdgcn_cvt_f32_fp8(v, 2)
+                        : __builtin_amdgcn_cvt_f32_fp8(v, 3);
+    else
+        return i == 0   ? __builtin_amdgcn_cvt_f32_bf8(v, 0)
+               : i == 1 ? __builtin_amdgcn_cvt_f32_bf8(v, 1)
+               : i == 2 ? __builtin_amdgcn_cvt_f32_bf8(v, 2)
+                        : __builtin_amdgcn_cvt_f32_bf8(v, 3);
+}
+
+// sum_k a[k] b[k] of two rows of codes, by a wave.
+template <int FA, int FB>
+__device__ __forceinline__ float dot_rows(const uint8_t* a, const uint8_t* b, int64_t K) {
+    float acc[4] = {};
+    for (int64_t k = threadIdx.x % kWaveSize * 16; k < K; k += kWaveSize * 16) {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(a + k), y = *reinterpret_cast<const u32x4*>(b + k);
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[w] = fmaf(code_value<FA>(x[w], i), code_value<FB>(y[w], i), acc[w]);
+    }
+    return wave_sum((acc[0] + acc[1]) + (acc[2] + acc[3]));
+}
+
+struct LossJoin {
+    const float2* part;
+    const uint8_t* A;
+    const uint8_t* B;
+    const float* scale_a;
+    const float* scale_b;
+    int rowwise;
+    const int64_t* target;
+    int64_t ignore;
+    float* loss;
+    float* lse;
+    int64_t M, V, K;
+    int blocks, group;
+};
+
 // Workgroup: `group` rows (a power of two up to 64), 1024 / group slices of their
-// column blocks each.
-__global__ void __launch_bounds__(kLossThreads)
-loss_kernel(const float2* part, const float* target_logit, const int64_t* target, int64_t ignore, float* loss,
-            float* lse, int64_t M, int64_t V, int blocks, int group) {
+// column blocks each; a wave for each row's target.
+template <int FA, int FB>
+__global__ void __launch_bounds__(kLossThreads) loss_kernel(LossJoin p) {
     __shared__ float2 s_part[kLossThreads];
+    __shared__ float s_target[64];        // logits times log2(e)
+    const float2* part = p.part;
+    const int64_t M = p.M;
+    const int blocks = p.blocks, group = p.group;
+    for (int i = threadIdx.x / kWaveSize; i < group; i += kLossThreads / kWaveSize) {
+        const int64_t m = (int64_t)blockIdx.x * group + i;
+        if (m >= M) break;
+        const int t = target_of(p.target, m, p.ignore, p.V);
+        if (t < 0) continue;
+        const float dot = dot_rows<FA, FB>(p.A + m * p.K, p.B + t * p.K, p.K);
+        const float s = (p.rowwise ? p.scale_a[m] : p.scale_a[0]) * kLog2E * (p.rowwise ? p.scale_b[t] : p.scale_b[0]);
+        if (threadIdx.x % kWaveSize == 0) s_target[i] = dot * s;
+    }
     const int slices = kLossThreads / group;
     const int r = threadIdx.x % group, slice = threadIdx.x / group;
     const int64_t m = (int64_t)blockIdx.x * group + r;
@@ -76,11 +135,26 @@ loss_kernel(const float2* part, const float* target_logit, const int64_t* target
     if (slice != 0 || m >= M) return;
     acc = s_part[threadIdx.x];
     constexpr float kLn2 = 0.69314718055994531f;
-    const float rest = log2f(acc.y);       // >= 0: the sum holds the largest one's 1
-    lse[m] = (acc.x + rest) * kLn2;
-    const int t = target_of(target, m, ignore, V);
-    // Not lse - z: what of the loss is below the logits' last bit is in `rest`.
-    loss[m] = t == -1 ? 0.f : t < 0 ? __builtin_nanf("") : ((acc.x - target_logit[m]) + rest) * kLn2;
+    const float others = (acc.x + log2f(acc.y)) * kLn2;       // (all, where there is no target)
+    const int t = target_of(p.target, m, p.ignore, p.V);
+    float loss = t == -1 ? 0.f : __builtin_nanf(""), lse = others;
+    if (t >= 0) {
+        const float z = s_target[r];
+        if (z == -__builtin_inff()) {
+            loss = -z;
+        } else {
+            // loss = log(1 + S 2^d), d the others' largest above the target's; lse from the
+            // larger of the two, so that nothing cancels.
+            const float d = acc.x - z;
+            const float rest = d > 0.f ? logf(acc.y + __builtin_amdgcn_exp2f(-d))
+                                       : log1pf(acc.y * __builtin_amdgcn_exp2f(d));
+            loss = d > 0.f ? fmaf(d, kLn2, rest) : rest;
+            lse = fmaf(d > 0.f ? acc.x : z, kLn2, rest);
+            if (z == __builtin_inff()) loss = lse = __builtin_nanf("");
+        }
+    }
+    p.loss[m] = loss;
+    p.lse[m] = lse;
 }
 
 __global__ void __launch_bounds__(256) clear_kernel(uint32_t* p, int64_t n) {
@@ -189,7 +263,7 @@ Ranges dw_ranges(int64_t n, int64_t K, int64_t Mp) {
 }
 
 struct LossSpace {
-    int64_t logit, part, total;   // byte offsets (the multiply's workspace is first)
+    int64_t part, total;   // byte offsets (the multiply's workspace is first)
     Ranges ranges;
     fp8mm::LossPlan plan[2];
     int64_t blocks[2];
@@ -208,8 +282,7 @@ LossSpace loss_space(int64_t M, int64_t V, int64_t K) {
         mm = std::max(mm, fp8mm::loss_workspace(M, n, s.plan[i]));
         at = s.ranges.end[i];
     }
-    s.logit = align256(mm);
-    s.part = s.logit + align256(4 * M);
+    s.part = align256(mm);
     s.total = s.part + align256(8 * M * blocks);
     return s;
 }
@@ -330,20 +403,22 @@ int fp8_linear_cross_entropy(const void* A, int a_format, const void* B, int b_f
         hipLaunchKernelGGL(clear_kernel, dim3((unsigned)((counters + 255) / 256)), dim3(256), 0, hs,
                            reinterpret_cast<uint32_t*>(ws), (int64_t)counters);
     float2* part = reinterpret_cast<float2*>(ws + s.part);
-    float* logit = reinterpret_cast<float*>(ws + s.logit);
     int64_t v0 = 0, blocks = 0;
     for (int i = 0; i < s.ranges.count; ++i) {
         const fp8mm::Logits z{A, a_format, static_cast<const uint8_t*>(B) + v0 * K, b_format, scale_a,
                               mode == FP8MM_ROWWISE ? scale_b + v0 : scale_b, M, s.ranges.end[i] - v0, K, mode};
-        st = fp8mm::run_stats(z, s.plan[i], target, part + blocks * M, logit, v0, hs, ws);
+        st = fp8mm::run_stats(z, s.plan[i], target, part + blocks * M, v0, hs, ws);
         if (st != FP8MM_OK) return st;
         blocks += s.blocks[i];
         v0 = s.ranges.end[i];
     }
     int group = 1;
     while (group < 64 && M / group > 256) group *= 2;
-    hipLaunchKernelGGL(loss_kernel, dim3((unsigned)code_up(M, group)), dim3(kLossThreads), 0, hs, part, logit, target,
-                       ignore_index, loss, lse, M, V, (int)blocks, group);
+    const LossJoin j{part, static_cast<const uint8_t*>(A), static_cast<const uint8_t*>(B), scale_a, scale_b,
+                     mode == FP8MM_ROWWISE, target, ignore_index, loss, lse, M, V, K, (int)blocks, group};
+    const dim3 grid((unsigned)code_up(M, group));
+    void (*const kernels[2][2])(LossJoin) = {{loss_kernel<0, 0>, loss_kernel<0, 1>}, {loss_kernel<1, 0>, loss_kernel<1, 1>}};
+    hipLaunchKernelGGL(kernels[a_format == FP8MM_E5M2][b_format == FP8MM_E5M2], grid, dim3(kLossThreads), 0, hs, j);
     return hipGetLastError() == hipSuccess ? FP8MM_OK : FP8MM_ERR_LAUNCH;
 }
 

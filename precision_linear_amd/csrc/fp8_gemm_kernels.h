@@ -90,8 +90,7 @@ struct LossParams : Params {
     // kEpiStats
     const int64_t* target;      // M
     float2* part;               // [column block][M]: largest logit times log2(e), sum of
-                                // the exponentials over the largest one's
-    float* target_logit;        // M, times log2(e), written where the target is a column
+                                // the exponentials over the largest one's, the target's left out
     // kEpiCodes
     const float2* rows;         // M: log2 of the code's factor, target as an int's bits
     uint8_t* q;                 // M x ldq, may be null
@@ -1151,9 +1150,8 @@ __device__ __forceinline__ uint32_t stats_target(const LossParams& p, int m, int
 
 // Rows of JN blocks of a wave (first row m0, scales epi_sa) and its columns from
 // n0 on: this wave's share of each row's softmax statistics, as column block `block`
-// of p.part.  Logits are kept times log2(e), so that an exponential is a subtraction
-// and 2^x, and the largest one's exactly 1 (a row that is sure of its target keeps
-// what little the others add).  A lane holds FN * NACC logits of each of its rows,
+// of p.part, the target's logit left out.  Logits are kept times log2(e), so that an
+// exponential is a subtraction and 2^x.  A lane holds FN * NACC logits of each of its rows,
 // the other kWave / MI - 1 lanes with the same lane % MI the rest.  A NaN or +inf among
 // the logits makes the sum a NaN.
 template <int MI, int FN, int JN>
@@ -1180,6 +1178,18 @@ __device__ __forceinline__ void epi_stats(typename Mfma<MI>::acc_t (&z)[FN][JN],
                     z[i][j][4 * g + c] = v;
                 }
         }
+    bool here = false;
+#pragma unroll
+    for (int j = 0; j < JN; ++j) here = here || target[j] < (uint32_t)(FN * MI);
+    if (__any(here)) {   // (few blocks hold a target)
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < JN; ++j)
+#pragma unroll
+                for (int e = 0; e < 4 * G; ++e)
+                    if ((uint32_t)(epi_col<MI>(i, e / 4, lane) + e % 4) == target[j]) z[i][j][e] = -__builtin_inff();
+    }
 #pragma unroll
     for (int j = 0; j < JN; ++j) {
         const int m = m0 + j * MI + lane % MI;
@@ -1198,13 +1208,6 @@ __device__ __forceinline__ void epi_stats(typename Mfma<MI>::acc_t (&z)[FN][JN],
                 sum += __builtin_amdgcn_exp2f(z[i][j][e] - from);
         sum = over_columns<MI>(sum, [](float a, float b) { return a + b; });
         if (lane < MI && m < p.M) p.part[(size_t)block * p.M + m] = float2{most, sum};
-        if (__any(target[j] < (uint32_t)(FN * MI))) {   // (few blocks hold a target)
-#pragma unroll
-            for (int i = 0; i < FN; ++i)
-#pragma unroll
-                for (int e = 0; e < 4 * G; ++e)
-                    if ((uint32_t)(epi_col<MI>(i, e / 4, lane) + e % 4) == target[j]) p.target_logit[m] = z[i][j][e];
-        }
     }
 }
 

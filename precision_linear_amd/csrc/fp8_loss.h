@@ -51,8 +51,8 @@ int ping_pong_config();
 
 // Each enqueues one launch and returns an FP8MM_* status; the pointers have been
 // checked.
-int run_stats(const Logits& z, const LossPlan& plan, const int64_t* target, float2* part, float* target_logit,
-              int64_t col0, hipStream_t stream, void* workspace);
+int run_stats(const Logits& z, const LossPlan& plan, const int64_t* target, float2* part, int64_t col0,
+              hipStream_t stream, void* workspace);
 int run_codes(const Logits& z, const LossPlan& plan, const float2* rows, uint8_t* q, int64_t ldq, uint8_t* qt,
               int64_t ldqt, int64_t col0, hipStream_t stream, void* workspace);
 

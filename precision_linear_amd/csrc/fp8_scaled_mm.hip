@@ -878,13 +878,12 @@ static int run_loss(const LaunchPair* const (&tables)[kFormats], const Logits& z
     return hipGetLastError() == hipSuccess ? FP8MM_OK : FP8MM_ERR_LAUNCH;
 }
 
-int run_stats(const Logits& z, const LossPlan& plan, const int64_t* target, float2* part, float* target_logit,
-              int64_t col0, hipStream_t stream, void* ws) {
+int run_stats(const Logits& z, const LossPlan& plan, const int64_t* target, float2* part, int64_t col0,
+              hipStream_t stream, void* ws) {
     static const LaunchPair* const tables[kFormats] = {kStatsF0, kStatsF1, kStatsF2, kStatsF3};
     LossParams p{};
     p.target = target;
     p.part = part;
-    p.target_logit = target_logit;
     p.col0 = (int)col0;
     return run_loss(tables, z, plan, p, stream, ws);
 }

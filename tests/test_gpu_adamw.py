@@ -1,12 +1,12 @@
 """The AdamW step over many tensors on the GPU against 64 bits.
 
-Tolerances, with u = 2^-24.  m = fma(b1, m0, c1 g): the two constants, the product and
-the sum round once each, so m is off by dm = 3 u (b1 |m0| + c1 |g|); v likewise, with g^2
+Tolerances, with u = 2^-24.  m = b1 m0 + c1 g: the constants, the products and the sum
+round once each, so m is off by dm = 3 u (b1 |m0| + c1 |g|); v likewise, with g^2
 rounded too, by 4 u v.  The denominator (a square root, a product by a rounded factor
 and a sum) is then off by 5 u of itself, the quotient rounds by u, lr / (1 - b1^t) by 3 u
 and the products by 2 u: a step of size s is off by 12 u s + dm s / |m|, and p (its
-factor 1 - lr wd off by 2 u, the sum by u) by 3 u |p| more.  With 8-bit moments the square
-root and the reciprocal are the hardware's, off by 2 u each, and their products round: 4 u more.  A bf16 output is rounded once
+factor 1 - lr wd off by 2 u, the sum by u) by 3 u |p| more.  With 8-bit moments the quotient is
+by the hardware's reciprocal, off by 2 u, and its product rounds: 4 u more.  A bf16 output is rounded once
 more (torch.finfo(bf16).eps / 2).
 
 Moments of 8 bits.  What is rounded to a code, x / scale, is off by dm / scale (m), 3 u
@@ -312,6 +312,41 @@ def test_numbers_on_the_gpu_and_both_paths(bits, monkeypatch):
             results.append(t)
     for r in results[1:]:
         same(r, results[0])
+
+
+def block_codes(x, r, positive):
+    """The definition in fp32, as include/adamw.h has it; x is whole blocks."""
+    amax = x.view(-1, 256).abs().amax(1, keepdim=True)
+    scale = amax / torch.full_like(amax, 448.0)
+    y = (x.view(-1, 256) * torch.where(scale > 0, 1 / scale, 0.0)).view(-1)
+    t = y.abs().clamp(max=448.0)
+    lift = torch.where(t < 2.0 ** -6, 2.0 ** -6, 0.0)
+    t = (((t + lift).view(torch.int32) + (r << 4).to(torch.int32)) & ~0xfffff).view(torch.float32) - lift
+    if positive:
+        t = torch.where((y > 0) & (t == 0), 2.0 ** -9, t)
+    return torch.copysign(t, y).to(torch.float8_e4m3fn).view(torch.uint8), scale[:, 0]
+
+
+def test_codes_are_the_definitions_bit_for_bit():
+    """Every product, sum and root of the moments is rounded as it is written, so over steps
+    the codes and scales are those of fp32 arithmetic, none off by a neighbour."""
+    n = 1 << 22
+    t = make([n], FP32, BF16, 8)
+    b1, b2 = HYPER["betas"]
+    m8, v8, ms, vs = (t[k][0].clone() for k in ("exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale"))
+    g = torch.Generator(device=DEV).manual_seed(8)
+    for step in range(1, 6):
+        t["grads"][0].copy_(1e-3 * torch.randn(n, generator=g, device=DEV))
+        binding.adamw_step(**t, step=step, seed=step, **HYPER)
+        grad = t["grads"][0].float()
+        m = b1 * (m8.view(torch.float8_e4m3fn).float().view(-1, 256) * ms[:, None]).view(-1) + (1 - b1) * grad
+        v = (v8.view(torch.float8_e4m3fn).float().view(-1, 256) * vs[:, None]).view(-1)
+        v = b2 * (v * v) + (1 - b2) * (grad * grad)
+        r = random_bits(step, torch.arange(n, device=DEV))
+        m8, ms = block_codes(m, r & 0xffff, False)
+        v8, vs = block_codes(v.double().sqrt().float(), r >> 16, True)
+        for name, want in (("exp_avg", m8), ("exp_avg_sq", v8), ("exp_avg_scale", ms), ("exp_avg_sq_scale", vs)):
+            assert torch.equal(t[name][0], want), (step, name)
 
 
 def test_equal_calls_equal_bits_and_seeds_differ():

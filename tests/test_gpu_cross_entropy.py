@@ -137,8 +137,8 @@ def test_a_sure_row_keeps_its_small_loss():
     b[t[1:]] = 0
     loss, lse = binding.fp8_linear_cross_entropy(a[:1], b, sa[:1], sb, t[:1])
     want = math.log1p(999 * math.exp(-40.0))
-    # fp32 holds 1 + 4e-15 as 1
-    assert 0 <= float(loss) <= want + U
+    # the exponent, 40 log2(e) after three roundings and a difference, is off by 5 u of itself
+    assert abs(float(loss) - want) <= 2 * 5 * U * 40 * want
     # 40 log2(e) after three multiplications, back by a fourth, each rounding by u, and the
     # two constants' own u / 4 and u / 20
     assert abs(float(lse) - 40) <= 5 * U * 40
@@ -172,6 +172,27 @@ def test_nan_rows_show(M, V):
     b.view(torch.uint8)[V - 1, 0] = 0x7f      # an entry of the vocabulary: every row
     loss, lse = binding.fp8_linear_cross_entropy(a, b, sa, sb, t)
     assert lse.isnan().all()
+
+
+def test_infinite_logits():
+    """-inf is no more than an exponential of 0, unless the target's; +inf shows."""
+    M, V, K = 70, 1000, 64
+    a, b, sa, sb, t = make(M, V, K, fb="e5m2", seed=12, whole=True)
+    a.view(torch.uint8)[:, 0] = 0x38                     # 1
+    clean = b.clone()
+    clean[5] = 0
+    b.view(torch.uint8)[5, 0] = 0xfc                     # -inf
+    t[:] = torch.where(t == 5, 6, t)
+    t[1] = 5
+    loss, lse = binding.fp8_linear_cross_entropy(a, b, sa, sb, t)
+    z = logits64(a, clean, sa, sb)[0]
+    z[:, 5] = -math.inf
+    want = torch.logsumexp(z, 1)
+    assert ((lse.double() - want).abs() < 1e-5 * (1 + want.abs())).all()
+    assert loss[1] == math.inf and loss[torch.arange(M, device=DEV) != 1].isfinite().all()
+    b.view(torch.uint8)[5, 0] = 0x7c                     # +inf
+    loss, lse = binding.fp8_linear_cross_entropy(a, b, sa, sb, t)
+    assert loss.isnan().all() and lse.isnan().all()
 
 
 def test_no_rows():
