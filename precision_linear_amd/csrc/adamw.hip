@@ -119,40 +119,50 @@ __device__ __forceinline__ void store4(T* p, int64_t at, int64_t left, const flo
     }
 }
 
-// 32 random bits of a position.
-__device__ __forceinline__ uint32_t random_bits(uint32_t n, uint32_t seed_part) {
-    uint32_t h = n * 0x6A09E667u + seed_part;
+// 32 random bits of the i-th position from the one whose h0 is `start`.
+__device__ __forceinline__ uint32_t random_bits(uint32_t start, uint32_t i) {
+    uint32_t h = start + i * 0x6A09E667u;
     h = (h ^ (h >> 15)) * 0x3C6EF373u;
     h = (h ^ (h >> 13)) * 0xA54FF53Bu;
     return h ^ (h >> 16);
 }
 
-// y, |y| <= 448 up to a rounding, to one of its neighbours in e4m3fn: up (in
-// magnitude) where the part of a step that is left and r / 2^16 make one.  Below 2^-6
-// the steps are those of 2^-6, so that is added meanwhile.  NaN stays NaN.
+// y, |y| <= 448 up to a rounding or two, to one of its neighbours in e4m3fn: up (in
+// magnitude) where the part of a step that is left and r / 2^16 make one (r4 is r 2^4; the
+// last bits of a y that rounding has put above 448 are too few for that).  Below 2^-6
+// the steps are those of 2^-6, so that is added meanwhile.  NaN stays NaN: the addition
+// saturates.
 template <bool POSITIVE>
-__device__ __forceinline__ float round_at_random(float y, uint32_t r) {
+__device__ __forceinline__ float round_at_random(float y, int r4) {
     float t = fabsf(y);
-    t = t > 448.f ? 448.f : t;
     const float lift = t < 0x1p-6f ? 0x1p-6f : 0.f;
-    t = __uint_as_float((__float_as_uint(t + lift) + (r << 4)) & 0xfff00000u) - lift;
+    t = __int_as_float(__builtin_elementwise_add_sat(__float_as_int(t + lift), r4) & (int)0xfff00000) - lift;
     if (POSITIVE) return y > 0.f && t == 0.f ? 0x1p-9f : t;
     return copysignf(t, y);
 }
 
-// sqrt(v) for v >= 0, correctly rounded.  The hardware's s is at most one step h off (and takes
-// values next to 0 for 0, so those are lifted): v lies below the midpoint to its lower
-// neighbour, (s - h / 2)^2 = s (s - h) + h^2 / 4, where v <= s (s - h), and above the one to the
-// upper where v > s (s + h), h^2 / 4 being less than a last bit of v.
+// sqrt(v), correctly rounded, for v = 0, 2^-96 and more, inf (which gives itself: the
+// tests are of NaNs) and NaN.  The hardware's s is at most one step h off: v lies below the
+// midpoint to its lower neighbour, (s - h / 2)^2 = s (s - h) + h^2 / 4, where v <= s (s - h), and
+// above the one to the upper where v > s (s + h), h^2 / 4 being less than a last bit of v.
 __device__ __forceinline__ float root_of(float v) {
-    const bool tiny = v < 0x1p-96f;
-    v = tiny ? v * 0x1p64f : v;
-    float s = __builtin_amdgcn_sqrtf(v);
+    const float s = __builtin_amdgcn_sqrtf(v);
     const float down = __uint_as_float(__float_as_uint(s) - 1), up = __uint_as_float(__float_as_uint(s) + 1);
     const float by_down = fmaf(-down, s, v), by_up = fmaf(-up, s, v);
-    const float r = by_down <= 0.f ? down : by_up > 0.f ? up : s;
-    s = v > 0.f && v < __builtin_inff() ? r : s;
-    return s * (tiny ? 0x1p-32f : 1.f);
+    return by_down <= 0.f ? down : by_up > 0.f ? up : s;
+}
+// The same of four, smaller ones too (which the hardware takes for 0): those are lifted.
+__device__ __forceinline__ void roots_of(const float (&v)[4], float (&root)[4]) {
+    uint32_t least = ~0u;   // (0 becomes the largest)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) least = min(least, __float_as_uint(v[i]) - 1u);
+    if (__any(least < 0x0f800000u - 1u)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) root[i] = v[i] < 0x1p-96f ? root_of(v[i] * 0x1p64f) * 0x1p-32f : root_of(v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) root[i] = root_of(v[i]);
+    }
 }
 // a / b; with 8-bit moments by the hardware's reciprocal (1 ulp), as the step would
 // otherwise be bound by its arithmetic.
@@ -223,10 +233,15 @@ __global__ void __launch_bounds__(kStepThreads) adamw_kernel(StepArgs a) {
     const uint32_t seed = (a.seed_ptr ? (uint32_t)*a.seed_ptr : a.seed) * 0xBB67AE85u;
 #pragma unroll
     for (int u = 0; u < kInFlight; ++u) {
-        float fm[4], root[4], fv[4], fw[4];
+        float fm[4], root[4], fv[4], fw[4], fg[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) fg[i] = rg[u].get(i);
+        if (a.grad_scale_ptr)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) fg[i] *= gs;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float g = rg[u].get(i) * gs;
+            const float g = fg[i];
             float m0 = rm[u].get(i), v0 = rv[u].get(i);
             if constexpr (BITS == 8) {
                 m0 *= ms[u];
@@ -240,25 +255,27 @@ __global__ void __launch_bounds__(kStepThreads) adamw_kernel(StepArgs a) {
                 fm[i] = a.beta1 * m0 + a.beta1_rest * g;
                 fv[i] = a.beta2 * v0 + a.beta2_rest * (g * g);
             }
-            root[i] = root_of(fv[i]);
+        }
+        roots_of(fv, root);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
             const float step = quotient<BITS == 8>(fm[i], fmaf(root[i], corr2, a.eps));
             fw[i] = fmaf(rw[u].get(i), decay, -rate * step);
         }
         if constexpr (BITS == 8) {
             float amax_m = 0.f, amax_v = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (i < left[u]) {
-                    amax_m = fmaxf(amax_m, fabsf(fm[i]));
-                    amax_v = fmaxf(amax_v, root[i]);
-                }
+            for (int i = 0; i < 4; ++i) {   // (zeros past the tensor's end)
+                amax_m = fmaxf(amax_m, fabsf(fm[i]));
+                amax_v = fmaxf(amax_v, root[i]);
+            }
             const float2 sm = block_scale(wave_max(amax_m)), sv = block_scale(wave_max(amax_v));
-            const uint32_t n = (uint32_t)e.first_block * (uint32_t)kBlock + (uint32_t)at[u];
+            const uint32_t start = ((uint32_t)e.first_block * (uint32_t)kBlock + (uint32_t)at[u]) * 0x6A09E667u + seed;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t r = random_bits(n + i, seed);
-                fm[i] = round_at_random<false>(fm[i] * sm.y, r & 0xffff);
-                fv[i] = round_at_random<true>(root[i] * sv.y, r >> 16);
+                const uint32_t r = random_bits(start, i);
+                fm[i] = round_at_random<false>(fm[i] * sm.y, (int)((r & 0xffff) << 4));
+                fv[i] = round_at_random<true>(root[i] * sv.y, (int)(r >> 16 << 4));
             }
             if (lane == 0 && left[u] > 0) {
                 e.m_scale[at[u] / kBlock] = sm.x;
