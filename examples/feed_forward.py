@@ -44,9 +44,9 @@ class FeedForward:
         """The weights' codes: N x K for the forward pass, K x N for the backward one."""
         self.codes = {}
         for name in ("w1", "w2"):
-            w = self.params[name].bfloat16()
-            self.codes[name] = binding.fp8_quantize(w, "rowwise")
-            self.codes[name + "t"] = binding.fp8_quantize(w.t().contiguous(), "rowwise")
+            q, scale, qt, scale_t = binding.fp8_quantize_weight(self.params[name].bfloat16())
+            self.codes[name] = q, scale
+            self.codes[name + "t"] = qt, scale_t
         self.bias = {name: self.params[name].bfloat16() for name in ("b1", "b2")}
 
     def forward(self, x, train=True):
