@@ -2,8 +2,8 @@
 // (MI355X) (formulas: include/fp8_cross_entropy.h).
 //
 // Forward: the multiply's kernels with an epilogue that reduces each tile's logits
-// to the largest and the sum of exponentials of each row (by the 64 columns of a
-// wave, 16 to 128 in the generic tiles), the target's left out; loss_kernel joins them
+// to the largest and the sum of exponentials of each row (by tiles, in the ping-pong
+// kernel by the 64 columns of a wave), the target's left out; loss_kernel joins them
 // with the target's logit, which it makes itself in fp32: the matrix instruction keeps a product
 // to 2^-13 of its largest, which averages out among the others.  The loss is log(1 +
 // sum of the others over the target's), so that a row that is sure of its target keeps
@@ -97,43 +97,48 @@ struct LossJoin {
 // column blocks each; a wave for each row's target.
 template <int FA, int FB>
 __global__ void __launch_bounds__(kLossThreads) loss_kernel(LossJoin p) {
-    __shared__ float2 s_part[kLossThreads];
+    constexpr int kWaves = kLossThreads / kWaveSize;
+    __shared__ float2 s_part[kWaves][64];
     __shared__ float s_target[64];        // logits times log2(e)
-    const float2* part = p.part;
     const int64_t M = p.M;
-    const int blocks = p.blocks, group = p.group;
-    for (int i = threadIdx.x / kWaveSize; i < group; i += kLossThreads / kWaveSize) {
-        const int64_t m = (int64_t)blockIdx.x * group + i;
-        if (m >= M) break;
-        const int t = target_of(p.target, m, p.ignore, p.V);
-        if (t < 0) continue;
-        const float dot = dot_rows<FA, FB>(p.A + m * p.K, p.B + t * p.K, p.K);
-        const float s = (p.rowwise ? p.scale_a[m] : p.scale_a[0]) * kLog2E * (p.rowwise ? p.scale_b[t] : p.scale_b[0]);
-        if (threadIdx.x % kWaveSize == 0) s_target[i] = dot * s;
-    }
-    const int slices = kLossThreads / group;
-    const int r = threadIdx.x % group, slice = threadIdx.x / group;
+    const int blocks = p.blocks, group = p.group, slices = kLossThreads / group;
+    const int wave = threadIdx.x / kWaveSize, lane = threadIdx.x % kWaveSize;
+    const int r = threadIdx.x % group;
     const int64_t m = (int64_t)blockIdx.x * group + r;
-    float2 acc{-__builtin_inff(), 0.f};
-    if (m < M)
-        for (int q0 = slice; q0 < blocks; q0 += slices * 8) {
-            float2 v[8];   // loaded together
+    float2 v[8];
+    auto fetch = [&](int q0) __attribute__((always_inline)) {   // together: one memory latency
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int q = q0 + slices * k;
-                v[k] = q < blocks ? part[(int64_t)q * M + m] : float2{-__builtin_inff(), 0.f};
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) acc = merge(acc, v[k]);
+        for (int k = 0; k < 8; ++k) {
+            const int q = q0 + slices * k;
+            v[k] = m < M && q < blocks ? p.part[(int64_t)q * M + m] : float2{-__builtin_inff(), 0.f};
         }
-    s_part[threadIdx.x] = acc;
-    __syncthreads();
-    for (int d = slices / 2; d > 0; d /= 2) {
-        if (slice < d) s_part[threadIdx.x] = merge(s_part[threadIdx.x], s_part[threadIdx.x + d * group]);
-        __syncthreads();
+    };
+    int q0 = threadIdx.x / group;
+    fetch(q0);   // under way while the targets' logits are made
+    for (int i = wave; i < group; i += kWaves) {
+        const int64_t row = (int64_t)blockIdx.x * group + i;
+        if (row >= M) break;
+        const int t = target_of(p.target, row, p.ignore, p.V);
+        if (t < 0) continue;
+        const float dot = dot_rows<FA, FB>(p.A + row * p.K, p.B + t * p.K, p.K);
+        const float s = (p.rowwise ? p.scale_a[row] : p.scale_a[0]) * kLog2E * (p.rowwise ? p.scale_b[t] : p.scale_b[0]);
+        if (lane == 0) s_target[i] = dot * s;
     }
-    if (slice != 0 || m >= M) return;
-    acc = s_part[threadIdx.x];
+    float2 acc{-__builtin_inff(), 0.f};
+    while (true) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc = merge(acc, v[k]);
+        q0 += slices * 8;
+        if (q0 - threadIdx.x / group >= blocks) break;
+        fetch(q0);
+    }
+    for (int d = kWaveSize / 2; d >= group; d /= 2)   // a wave's slices of a row
+        acc = merge(acc, float2{__shfl_xor(acc.x, d), __shfl_xor(acc.y, d)});
+    if (lane < group) s_part[wave][lane] = acc;
+    __syncthreads();
+    if (threadIdx.x >= group || m >= M) return;
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) acc = merge(acc, s_part[w][r]);
     constexpr float kLn2 = 0.69314718055994531f;
     const float others = (acc.x + log2f(acc.y)) * kLn2;       // (all, where there is no target)
     const int t = target_of(p.target, m, p.ignore, p.V);
@@ -412,8 +417,11 @@ int fp8_linear_cross_entropy(const void* A, int a_format, const void* B, int b_f
         blocks += s.blocks[i];
         v0 = s.ranges.end[i];
     }
+    // Rows of a workgroup: whole lines of a column block's rows are better read together, many
+    // workgroups better than few (us of the call with groups from 1, 8 and 16 on: 300 x 50000 x 256
+    // 29.0, 27.4 and 29.0; 64 x 131072 x 512 48.0, 47.6 and 56.3).
     int group = 1;
-    while (group < 64 && M / group > 256) group *= 2;
+    while ((group < 8 && group < M) || (group < 64 && M / group > 256)) group *= 2;
     const LossJoin j{part, static_cast<const uint8_t*>(A), static_cast<const uint8_t*>(B), scale_a, scale_b,
                      mode == FP8MM_ROWWISE, target, ignore_index, loss, lse, M, V, K, (int)blocks, group};
     const dim3 grid((unsigned)code_up(M, group));

@@ -1148,16 +1148,23 @@ __device__ __forceinline__ uint32_t stats_target(const LossParams& p, int m, int
     return t < 0x10000 ? (uint32_t)t : ~0u;
 }
 
-// Rows of JN blocks of a wave (first row m0, scales epi_sa) and its columns from
-// n0 on: this wave's share of each row's softmax statistics, as column block `block`
-// of p.part, the target's logit left out.  Logits are kept times log2(e), so that an
+// (largest, sum of 2^(x - largest)) of two sets.
+__device__ __forceinline__ float2 stats_join(float2 a, float2 b) {
+    const float m = fmaxf(a.x, b.x);
+    if (m == -__builtin_inff()) return float2{m, a.y + b.y};
+    return float2{m, a.y * __builtin_amdgcn_exp2f(a.x - m) + b.y * __builtin_amdgcn_exp2f(b.x - m)};
+}
+
+// Rows of JN blocks of a wave (scales epi_sa) and its columns from n0 on: this wave's
+// share of each row's softmax statistics, handed to out(row among these, share) by one lane
+// a row, the target's logit left out.  Logits are kept times log2(e), so that an
 // exponential is a subtraction and 2^x.  A lane holds FN * NACC logits of each of its rows,
 // the other kWave / MI - 1 lanes with the same lane % MI the rest.  A NaN or +inf among
 // the logits makes the sum a NaN.
-template <int MI, int FN, int JN>
-__device__ __forceinline__ void epi_stats(typename Mfma<MI>::acc_t (&z)[FN][JN], const LossParams& p, int m0,
-                                          int n0, int block, const float* epi_sa, const float* epi_sb,
-                                          const uint32_t (&target)[JN], int lane) {
+template <int MI, int FN, int JN, class Out>
+__device__ __forceinline__ void epi_stats(typename Mfma<MI>::acc_t (&z)[FN][JN], const LossParams& p, int n0,
+                                          const float* epi_sa, const float* epi_sb, const uint32_t (&target)[JN],
+                                          int lane, Out out) {
     constexpr int G = Mfma<MI>::NACC / 4;
     float sa_r[JN];
 #pragma unroll
@@ -1192,7 +1199,6 @@ __device__ __forceinline__ void epi_stats(typename Mfma<MI>::acc_t (&z)[FN][JN],
     }
 #pragma unroll
     for (int j = 0; j < JN; ++j) {
-        const int m = m0 + j * MI + lane % MI;
         float most = -__builtin_inff();
 #pragma unroll
         for (int i = 0; i < FN; ++i)
@@ -1207,7 +1213,7 @@ __device__ __forceinline__ void epi_stats(typename Mfma<MI>::acc_t (&z)[FN][JN],
             for (int e = 0; e < 4 * G; ++e)
                 sum += __builtin_amdgcn_exp2f(z[i][j][e] - from);
         sum = over_columns<MI>(sum, [](float a, float b) { return a + b; });
-        if (lane < MI && m < p.M) p.part[(size_t)block * p.M + m] = float2{most, sum};
+        if (lane < MI) out(j * MI + lane, float2{most, sum});
     }
 }
 
@@ -1639,8 +1645,18 @@ fp8_gemm_kernel(std::conditional_t<PAIR, PairParams, KernelParams<EPI>> args) {
 #pragma unroll
             for (int j = 0; j < C::FM; ++j)
                 target[j] = stats_target(p, row0 + wm * C::WTM + j * MI + lane % MI, col0 + wn * C::WTN);
-            epi_stats<MI, C::FN, C::FM>(acc, p, row0 + wm * C::WTM, col0 + wn * C::WTN, pn * WAVES_N + wn,
-                                        epi_sa + wm * C::WTM, epi_sb + wn * C::WTN, target, lane);
+            // The waves side by side join theirs in LDS: one column block a tile.
+            float2* shares = reinterpret_cast<float2*>(smem);   // [wn][BM]
+            static_assert(WAVES_N * BM * 8 <= C::MAIN_BYTES, "the shares fit the stage buffers");
+            epi_stats<MI, C::FN, C::FM>(acc, p, col0 + wn * C::WTN, epi_sa + wm * C::WTM, epi_sb + wn * C::WTN, target,
+                                        lane, [&](int r, float2 v) { shares[wn * BM + wm * C::WTM + r] = v; });
+            barrier_lds();
+            for (int r = tid; r < BM; r += C::THREADS) {
+                float2 v = shares[r];
+#pragma unroll
+                for (int w = 1; w < WAVES_N; ++w) v = stats_join(v, shares[w * BM + r]);
+                if (row0 + r < p.M) p.part[(size_t)pn * p.M + row0 + r] = v;
+            }
         } else if constexpr (EPI == kEpiCodes)
             epi_codes_tile<C>(acc, smem, p, row0, col0, wm * C::WTM, wn * C::WTN, epi_sa, epi_sb, lane, tid);
         else
@@ -2255,7 +2271,10 @@ __device__ __forceinline__ void pp_epi_stats(const pp::acc_t (&acc)[pp::FN][pp::
         for (int i = 0; i < FN; ++i)
 #pragma unroll
             for (int j = 0; j < JB; ++j) z[i][j] = acc[i][band * JB + j];
-        epi_stats<MI, FN, JB>(z, p, row0 + mb, col0 + q * 64, col0 / 64 + q, epi_sa + mb, epi_sb + q * 64, target, lane);
+        float2* part = p.part + (size_t)(col0 / 64 + q) * p.M + row0 + mb;
+        epi_stats<MI, FN, JB>(z, p, col0 + q * 64, epi_sa + mb, epi_sb + q * 64, target, lane, [&](int r, float2 v) {
+            if (row0 + mb + r < p.M) part[r] = v;
+        });
         __builtin_amdgcn_sched_barrier(0);
     }
 }

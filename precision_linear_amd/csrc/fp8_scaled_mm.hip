@@ -56,7 +56,6 @@ struct ConfigInfo {
     int lds_bytes;
     int occupancy;   // workgroups per CU the persistent grid assumes
     bool stream_k_ok;
-    int waves_n;     // waves side by side in a tile
 };
 
 #define FP8MM_CFG_INFO(name, BM, BN, BK, WMW, WNW, ST, MI, GM)                               \
@@ -64,13 +63,13 @@ struct ConfigInfo {
                Cfg<BM, BN, BK, WMW, WNW, ST, MI, GM>::THREADS,                                \
                Cfg<BM, BN, BK, WMW, WNW, ST, MI, GM>::LDS_BYTES,                              \
                Cfg<BM, BN, BK, WMW, WNW, ST, MI, GM>::OCCUPANCY,                              \
-               Cfg<BM, BN, BK, WMW, WNW, ST, MI, GM>::STREAM_K_OK, WNW},
+               Cfg<BM, BN, BK, WMW, WNW, ST, MI, GM>::STREAM_K_OK},
 
 // Ids are the positions in this table (the C ABI's config_id).
 const ConfigInfo kConfigs[kNumConfigs] = {
     FP8MM_GENERIC_CONFIGS(FP8MM_CFG_INFO)
     ConfigInfo{"pp_bm256_bn256_bk128_w8_mfma16", pp::BM, pp::BN, pp::BK, true, pp::THREADS,
-               pp::LDS_BYTES, 1, false, pp::WAVES / 2},
+               pp::LDS_BYTES, 1, false},
 };
 #undef FP8MM_CFG_INFO
 
@@ -810,7 +809,8 @@ bool loss_plan_fits(int64_t M, int64_t V, const LossPlan& plan) {
 }
 
 int64_t loss_blocks(int64_t V, const LossPlan& plan) {
-    return cdiv(V, kConfigs[plan.cfg].bn) * kConfigs[plan.cfg].waves_n;
+    // (the ping-pong kernel's waves work alone)
+    return cdiv(V, kConfigs[plan.cfg].bn) * (plan.cfg == kPingPongConfig ? pp::WAVES / 2 : 1);
 }
 
 int64_t loss_rows(int64_t M, const LossPlan& plan) { return cdiv(M, kConfigs[plan.cfg].bm) * kConfigs[plan.cfg].bm; }
