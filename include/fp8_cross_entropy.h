@@ -64,9 +64,9 @@ int64_t fp8_linear_cross_entropy_workspace_size(int64_t M, int64_t V, int64_t K)
  *          not computed (wt with its scales, or x, may then be NULL too).  At least
  *          one of them is needed.
  *
- * Ignored rows and rows with dloss 0 take no part, whatever they hold.  A NaN in
- * dloss, loss or lse, an infinite lse, and a target outside the vocabulary that is
- * not ignore_index, come out as NaN in their row of dx and in dw.
+ * Ignored rows and rows with dloss 0 take no part, whatever else they hold.  In the
+ * others a NaN in dloss, loss or lse, an infinite lse, and a target outside the
+ * vocabulary come out as NaN in their row of dx and in dw.
  * Preconditions: as for the forward call; fp32 tensors are 4-byte aligned, bf16 ones
  * 2-byte, wt 16-byte.  Outputs must not overlap inputs or each other.  With M == 0,
  * dw is zeros.  The workspace is as for the forward call, of its own size.  Equal

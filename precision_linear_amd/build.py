@@ -1,5 +1,5 @@
-"""Builds libfp8_scaled_mm.so (the HIP kernels -- scaled multiply,
-quantiser, layer norm and linear layer -- and their C ABI) for gfx950, and,
+"""Builds libfp8_scaled_mm.so (the HIP kernels -- scaled multiply, quantisers,
+layer norm, linear layer, cross entropy and AdamW -- and their C ABI) for gfx950, and,
 where it compiles, _calls.so (the binding's short calls into it, host code).
 
 hipcc cross-compiles without a GPU.  The library is written next to this
@@ -15,9 +15,9 @@ import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-# The host logic and C ABI, one translation unit per operand-format pair of
-# the multiply's kernels (and of those with the linear layer's epilogue), the quantiser, the layer norm
-# and the linear layer's gradient.  They compile in parallel.
+# The host logic and C ABI, one translation unit per operand-format pair of the
+# multiply's kernels and of those with each epilogue, the quantisers, the layer norm, the
+# linear layer's gradient, the cross entropy and AdamW.  They compile in parallel.
 SRCS = [os.path.join(HERE, "csrc", f) for f in
         ["fp8_scaled_mm.hip"] + [f"fp8_{n}_f{k}.hip" for n in ("gemm", "loss_grad", "linear", "loss") for k in range(4)] +
         ["fp8_linear_pair.hip", "fp8_loss_sum.hip", "fp8_quantize.hip", "fp8_layer_norm.hip", "fp8_linear_grad.hip",

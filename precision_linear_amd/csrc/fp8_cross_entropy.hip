@@ -196,7 +196,7 @@ struct LossGrad {
         const int t = target_of(target, m, ignore, V);
         const float l = loss[m], e = lse[m], d = dloss[m * dloss_stride];
         float f = -__builtin_inff(), r = 0.f;
-        if (t != -1) {
+        if (t != -1 && d != 0.f) {
             const float h = l <= 0.f ? 0.f : -expm1f(-l);
             r = d * h;
             if (t < 0 || !(fabsf(e) < __builtin_inff())) r = __builtin_nanf("");

@@ -2370,9 +2370,10 @@ __device__ __forceinline__ bool pp_sum(pp::acc_t (&acc)[pp::FN][pp::FM], const P
 template <int GROUP_M, int FMT, int EPI = kEpiScale>
 __global__ void __launch_bounds__(pp::THREADS) fp8_gemm_pp_kernel(KernelParams<EPI> p) {
     using namespace pp;
-    // The cross entropy's epilogues: arithmetic on every logit, and little or nothing to
-    // store.  The next unit's first slices are issued ahead of them (kEarly) and land
-    // meanwhile.
+    // The cross entropy's epilogues: arithmetic on every logit ahead of what they store.
+    // The next unit's first slices are issued before them (kEarly) and land meanwhile (us
+    // on one MI355X without and with: 8192 x 131072 x 4096 loss 3294 and 3278, 1001 x 50255 x 2048
+    // loss 99.0 and 98.4, gradient 352.5 and 350.7).
     constexpr bool kEarly = EPI == kEpiStats || EPI == kEpiCodes;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[kEarly ? LOSS_LDS_BYTES : LDS_BYTES];
 

@@ -255,6 +255,23 @@ def test_rows_that_do_not_count(M, V):
     assert (dx == 0).all() and (dw == 0).all()
 
 
+@pytest.mark.parametrize("M,V", [(6, 100), (600, 9000)])
+def test_a_weight_of_0_hides_what_is_no_number(M, V):
+    t = make(M, V, 64, seed=19)
+    x, wt, swt, dloss = more(t)
+    off = torch.arange(M, device=DEV) % 3 == 1
+    dloss = torch.where(off, 0.0, dloss)
+    _, want = run(t, (x, wt, swt, dloss))
+    a, b, sa, sb, target = t
+    a.view(torch.uint8)[off] = 0x7f
+    x[off] = math.nan
+    target = torch.where(off, V + 5, target)
+    loss, lse = binding.fp8_linear_cross_entropy(a, b, sa, sb, target)
+    assert loss[off].isnan().all() and lse[off].isnan().all()
+    dx, dw = binding.fp8_linear_cross_entropy_backward(dloss, a, b, sa, sb, target, loss, lse, x, wt, swt)
+    assert (dx[off] == 0).all() and torch.equal(dx[~off], want[0][~off]) and torch.equal(dw, want[1])
+
+
 @pytest.mark.parametrize("what", ["dloss", "loss", "lse", "inf lse", "target"])
 @pytest.mark.parametrize("M,V", [(6, 100), (600, 9000)])
 def test_what_is_no_number_shows(M, V, what):
