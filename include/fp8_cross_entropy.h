@@ -11,9 +11,10 @@
  *     loss[m] = lse[m] - z[m][target[m]],  0 where target[m] == ignore_index
  *
  *   Sums, maxima and both outputs are fp32; the loss is made as log(1 + sum over the
- *   others of exp(z - z[target])), which keeps it exact next to 0.  A target outside 0 ..
- *   V - 1 that is not ignore_index gives a loss of NaN; a NaN or +inf among a row's
- *   logits makes its loss (unless the row is ignored) and lse NaN.
+ *   others of exp(z - z[target])), which keeps it exact next to 0.  ignore_index may be
+ *   an entry of the vocabulary: its rows' loss is 0, their lse the same sum.  A target
+ *   outside 0 .. V - 1 that is not ignore_index gives a loss of NaN; a NaN or +inf among a
+ *   row's logits makes its loss (unless the row is ignored) and lse NaN.
  */
 #ifndef FP8_CROSS_ENTROPY_H
 #define FP8_CROSS_ENTROPY_H

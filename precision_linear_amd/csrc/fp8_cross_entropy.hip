@@ -42,10 +42,12 @@ __device__ __forceinline__ float2 merge(float2 a, float2 b) {
     return float2{m, a.y * __builtin_amdgcn_exp2f(a.x - m) + b.y * __builtin_amdgcn_exp2f(b.x - m)};
 }
 
-// The vocabulary entry of row m, -1 if the row is ignored, -2 if there is none.
+// The vocabulary entry that t is, -2 if it is none.
+__device__ __forceinline__ int entry_of(int64_t t, int64_t V) { return t >= 0 && t < V ? (int)t : -2; }
+// The same of row m's target, -1 if the row is ignored.
 __device__ __forceinline__ int target_of(const int64_t* target, int64_t m, int64_t ignore, int64_t V) {
     const int64_t t = target[m];
-    return t == ignore ? -1 : t >= 0 && t < V ? (int)t : -2;
+    return t == ignore ? -1 : entry_of(t, V);
 }
 
 // Code i of four.
@@ -118,7 +120,7 @@ __global__ void __launch_bounds__(kLossThreads) loss_kernel(LossJoin p) {
     for (int i = wave; i < group; i += kWaves) {
         const int64_t row = (int64_t)blockIdx.x * group + i;
         if (row >= M) break;
-        const int t = target_of(p.target, row, p.ignore, p.V);
+        const int t = entry_of(p.target[row], p.V);   // (of an ignored row too: lse has it)
         if (t < 0) continue;
         const float dot = dot_rows<FA, FB>(p.A + row * p.K, p.B + t * p.K, p.K);
         const float s = (p.rowwise ? p.scale_a[row] : p.scale_a[0]) * kLog2E * (p.rowwise ? p.scale_b[t] : p.scale_b[0]);
@@ -141,9 +143,9 @@ __global__ void __launch_bounds__(kLossThreads) loss_kernel(LossJoin p) {
     for (int w = 1; w < kWaves; ++w) acc = merge(acc, s_part[w][r]);
     constexpr float kLn2 = 0.69314718055994531f;
     const float others = (acc.x + log2f(acc.y)) * kLn2;       // (all, where there is no target)
-    const int t = target_of(p.target, m, p.ignore, p.V);
-    float loss = t == -1 ? 0.f : __builtin_nanf(""), lse = others;
-    if (t >= 0) {
+    const int64_t target = p.target[m];
+    float loss = __builtin_nanf(""), lse = others;
+    if (entry_of(target, p.V) >= 0) {
         const float z = s_target[r];
         if (z == -__builtin_inff()) {
             loss = -z;
@@ -158,7 +160,7 @@ __global__ void __launch_bounds__(kLossThreads) loss_kernel(LossJoin p) {
             if (z == __builtin_inff()) loss = lse = __builtin_nanf("");
         }
     }
-    p.loss[m] = loss;
+    p.loss[m] = target == p.ignore ? 0.f : loss;
     p.lse[m] = lse;
 }
 

@@ -159,6 +159,15 @@ def test_rows_that_do_not_count(M, V):
     assert (binding.fp8_linear_cross_entropy(a, b, sa, sb, everything)[0] == 0).all()
 
 
+@pytest.mark.parametrize("M,V", [(1, 20), (6, 100), (600, 9000)])
+def test_an_ignored_entry_of_the_vocabulary_is_in_the_sum(M, V):
+    t = make(M, V, 64, seed=21, whole=True)
+    for ignore in {int(t[4][0]), V - 1}:
+        t[4][M // 2:] = ignore
+        loss, lse = binding.fp8_linear_cross_entropy(*t, ignore_index=ignore)
+        check(loss, lse, *t, ignore=ignore)
+
+
 @pytest.mark.parametrize("M,V", [(6, 100), (600, 9000)])
 def test_nan_rows_show(M, V):
     a, b, sa, sb, t = make(M, V, 64, seed=11)
