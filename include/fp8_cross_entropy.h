@@ -14,7 +14,8 @@
  *   others of exp(z - z[target])), which keeps it exact next to 0.  ignore_index may be
  *   an entry of the vocabulary: its rows' loss is 0, their lse the same sum.  A target
  *   outside 0 .. V - 1 that is not ignore_index gives a loss of NaN; a NaN or +inf among a
- *   row's logits makes its loss (unless the row is ignored) and lse NaN.
+ *   row's logits makes its loss (unless the row is ignored) and lse NaN, logits of -inf
+ *   alone the loss.
  */
 #ifndef FP8_CROSS_ENTROPY_H
 #define FP8_CROSS_ENTROPY_H

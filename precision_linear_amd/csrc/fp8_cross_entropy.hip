@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kLossThreads) loss_kernel(LossJoin p) {
     if (entry_of(target, p.V) >= 0) {
         const float z = s_target[r];
         if (z == -__builtin_inff()) {
-            loss = -z;
+            loss = others - z;   // (of no numbers, and where all are -inf, none)
         } else {
             // loss = log(1 + S 2^d), d the others' largest above the target's; lse from the
             // larger of the two, so that nothing cancels.

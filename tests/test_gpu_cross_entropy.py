@@ -204,6 +204,21 @@ def test_infinite_logits():
     assert loss.isnan().all() and lse.isnan().all()
 
 
+def test_a_target_of_minus_infinity_hides_no_nan():
+    a, b, sa, sb, t = make(70, 1000, 64, fb="e5m2", seed=22, whole=True)
+    a.view(torch.uint8)[:, 0] = 0x38                     # 1
+    b.view(torch.uint8)[5, 0] = 0xfc                     # -inf
+    t[:] = 5
+    loss, lse = binding.fp8_linear_cross_entropy(a, b, sa, sb, t)
+    assert (loss == math.inf).all() and lse.isfinite().all()
+    b.view(torch.uint8)[900, 0] = 0x7f
+    loss, lse = binding.fp8_linear_cross_entropy(a, b, sa, sb, t)
+    assert loss.isnan().all() and lse.isnan().all()
+    # nothing but -inf: lse is that, and its difference to the target's no number
+    loss, lse = binding.fp8_linear_cross_entropy(a, b[5:6], sa, sb[5:6], torch.zeros_like(t))
+    assert loss.isnan().all() and (lse == -math.inf).all()
+
+
 def test_no_rows():
     t = make(0, 100, 64)
     loss, lse = binding.fp8_linear_cross_entropy(*t)
