@@ -31,7 +31,7 @@
 namespace {
 
 constexpr int kLossThreads = 1024;
-constexpr float kE5m2Max = 57344.f;
+constexpr float kE5m2Max = 57344.f, kLog2E5m2Max = 15.807354922057604f;
 
 // ------------------------------------------------------------- forward ---
 
@@ -202,7 +202,7 @@ struct LossGrad {
             const float h = l <= 0.f ? 0.f : -expm1f(-l);
             r = d * h;
             if (t < 0 || !(fabsf(e) < __builtin_inff())) r = __builtin_nanf("");
-            else if (write && h > 0.f) f = __builtin_fmaf(e, -kLog2E, log2f(kE5m2Max / h));
+            else if (write && h > 0.f) f = __builtin_fmaf(e, -kLog2E, kLog2E5m2Max - log2f(h));   // (57344 / h may pass the largest float)
         }
         if (write) {
             rows[m] = float2{f, __int_as_float(t)};

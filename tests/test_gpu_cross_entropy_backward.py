@@ -299,6 +299,23 @@ def test_a_sure_row_has_no_gradient():
     close((dx, dw), gradient64(*args))
 
 
+def test_a_nearly_sure_row_keeps_the_shape_of_its_gradient():
+    """h = 1 - p of the target is so small that 57344 / h passes the largest float."""
+    a, b, sa, sb, t = make(20, 1000, 64)
+    for codes, value in ((a, 1.0), (b, 0.0)):
+        codes[:] = torch.full_like(codes.float(), value).to(codes.dtype)
+    b[1::2] = torch.full((500, 64), -0.5, device=DEV).to(b.dtype)
+    t = torch.arange(20, device=DEV) * 48
+    b[t] = torch.ones(20, 64, device=DEV).to(b.dtype)
+    a, sa, sb, t = a[:1], torch.full((1,), 86 / 64, device=DEV), torch.ones_like(sb), t[3:4]
+    b[t.item() + 48::48] = 0
+    b[:t.item():48] = 0
+    t = (a.contiguous(), b, sa, sb, t)
+    tensors, got = run(t, more(t, dloss=torch.full((1,), 2.0 ** 100, device=DEV)))
+    assert 0 < float(tensors[6]) < 57344 / torch.finfo(torch.float32).max
+    close(got, gradient64(*tensors))
+
+
 def test_one_dloss_for_all_rows():
     t = make(300, 5000, 128, seed=13, ignore=-100)
     x, wt, swt, _ = more(t)
