@@ -57,7 +57,7 @@ enum adamw_status {
     ADAMW_ERR_VALUE = 5,  /* lr, betas, eps, weight_decay or step out of range */
     ADAMW_ERR_DEVICE = 6, /* no usable HIP device */
     ADAMW_ERR_LAUNCH = 7, /* a kernel launch failed */
-    ADAMW_ERR_ALIAS = 8   /* a parameter (or its state) is given twice */
+    ADAMW_ERR_ALIAS = 8   /* parameters or their states overlap */
 };
 
 /* One tensor: device pointers.  exp_avg and exp_avg_sq are fp32, or codes; the scales
@@ -89,11 +89,11 @@ struct adamw_numbers {
 
 /* One step over `count` tensors, `tensors` being a host array that the call has read
  * when it returns.  All parameters have one type, all gradients one, all states
- * state_bits (8 or 32); either every tensor has a master or none has.  Tensors are
- * written in place and overlap nothing, whatever their sizes (0 included) and
- * alignment above their element's.  Asynchronous on `stream`, one launch for each 48
- * tensors; nothing is allocated, so it may be captured.  On an error nothing is
- * enqueued (ADAMW_ERR_LAUNCH aside). */
+ * state_bits (8 or 32); either every tensor has a master or none has.  Parameters,
+ * masters, moments and scales are written in place, of any sizes (0 included) and
+ * alignment above their element's; two of them must not overlap, nor one a gradient.
+ * Asynchronous on `stream`, one launch for each 48 tensors; nothing is allocated, so it
+ * may be captured.  On an error nothing is enqueued (ADAMW_ERR_LAUNCH aside). */
 int adamw_step(const struct adamw_tensor* tensors, int64_t count, int param_dtype, int grad_dtype,
                int state_bits, const struct adamw_numbers* numbers, struct ihipStream_t* stream);
 

@@ -12,6 +12,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <utility>
 #include <vector>
 
 #include "../../include/adamw.h"
@@ -334,7 +335,7 @@ const char* adamw_status_string(int s) {
         case ADAMW_ERR_VALUE: return "lr, betas, eps, weight_decay or step out of range";
         case ADAMW_ERR_DEVICE: return "no usable HIP device";
         case ADAMW_ERR_LAUNCH: return "kernel launch failed";
-        case ADAMW_ERR_ALIAS: return "a parameter or its state is given twice";
+        case ADAMW_ERR_ALIAS: return "parameters or their states overlap (one is given twice)";
         default: return "unknown status";
     }
 }
@@ -352,8 +353,11 @@ int adamw_step(const adamw_tensor* tensors, int64_t count, int param_dtype, int 
     const uintptr_t sa = state_bits == 8 ? 1 : 4;
     const bool master = count > 0 && tensors[0].master != nullptr;
     if (master && param_dtype == ADAMW_FP32) return ADAMW_ERR_DTYPE;
-    std::vector<const void*> written;
-    written.reserve((size_t)count * 3);
+    std::vector<std::pair<uintptr_t, uintptr_t>> written;   // [from, to) of what the step writes
+    written.reserve((size_t)count * (3 + (master ? 1 : 0) + (state_bits == 8 ? 2 : 0)));
+    auto writes = [&](const void* p, int64_t bytes) {
+        if (p) written.emplace_back((uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes);
+    };
     int64_t total = 0;
     for (int64_t i = 0; i < count; ++i) {
         const adamw_tensor& t = tensors[i];
@@ -368,12 +372,17 @@ int adamw_step(const adamw_tensor* tensors, int64_t count, int param_dtype, int 
             !at_multiple(t.exp_avg_sq, sa) || !at_multiple(t.master, 4) || !at_multiple(t.exp_avg_scale, 4) ||
             !at_multiple(t.exp_avg_sq_scale, 4))
             return ADAMW_ERR_ALIGN;
-        written.push_back(t.param);
-        written.push_back(t.exp_avg);
-        written.push_back(t.exp_avg_sq);
+        const int64_t blocks = (t.numel + kBlock - 1) / kBlock;
+        writes(t.param, t.numel * (int64_t)pa);
+        writes(t.exp_avg, t.numel * (int64_t)sa);
+        writes(t.exp_avg_sq, t.numel * (int64_t)sa);
+        writes(t.master, t.numel * 4);
+        writes(t.exp_avg_scale, blocks * 4);
+        writes(t.exp_avg_sq_scale, blocks * 4);
     }
     std::sort(written.begin(), written.end());
-    if (std::adjacent_find(written.begin(), written.end()) != written.end()) return ADAMW_ERR_ALIAS;
+    for (size_t i = 1; i < written.size(); ++i)
+        if (written[i].first < written[i - 1].second) return ADAMW_ERR_ALIAS;
     int dev = -1;
     if (hipGetDevice(&dev) != hipSuccess) return ADAMW_ERR_DEVICE;
     const hipStream_t hs = reinterpret_cast<hipStream_t>(stream);

@@ -101,6 +101,29 @@ def test_lists(L):
     assert call(L, [tensor(0, exp_avg=P * 3 + 1, exp_avg_scale=P * 6, exp_avg_sq_scale=P * 7)], bits=8) in reached
 
 
+@pytest.mark.parametrize("first,second,kw", [
+    ({}, dict(param=P + 3996), {}), ({}, dict(exp_avg=P * 3 + 400), {}), (dict(exp_avg_sq=P * 3 + 3996), {}, {}),
+    (dict(numel=1 << 20), dict(numel=4), {}),
+    (dict(master=P * 7), dict(master=P * 7), dict(pd=0)), (dict(master=P * 7), dict(master=P * 7 + 3996), dict(pd=0)),
+    (dict(exp_avg_scale=P * 6, exp_avg_sq_scale=P * 7), dict(exp_avg_scale=P * 6, exp_avg_sq_scale=P * 15), dict(bits=8)),
+    (dict(exp_avg_scale=P * 6, exp_avg_sq_scale=P * 7), dict(exp_avg_scale=P * 14, exp_avg_sq_scale=P * 7 + 12), dict(bits=8)),
+    (dict(exp_avg_scale=P * 6, exp_avg_sq_scale=P * 6 + 12), dict(exp_avg_scale=P * 14, exp_avg_sq_scale=P * 15), dict(bits=8)),
+])
+def test_what_overlaps_is_refused(L, first, second, kw):
+    """1000 elements are 4000 bytes of fp32 and 16 of scales."""
+    tensors = [tensor(0, **first), tensor(1, **second)]
+    assert call(L, tensors, **kw) == E.ADAMW_ERR_ALIAS
+    assert call(L, tensors[::-1], **kw) == E.ADAMW_ERR_ALIAS
+
+
+def test_neighbours_are_taken(L):
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present: these cases would launch on fake pointers")
+    reached = (E.ADAMW_ERR_DEVICE, E.ADAMW_ERR_LAUNCH)
+    assert call(L, [tensor(0), tensor(1, param=P + 4000, exp_avg=P * 3 + 4000, exp_avg_sq=P * 4 + 4000)]) in reached
+    assert call(L, [tensor(0), tensor(1, param=P, exp_avg=P, exp_avg_sq=P, numel=0)]) in reached
+
+
 def test_binding_refuses_before_the_library():
     p, g = [torch.zeros(4)], [torch.zeros(4)]
     for args in ((p, g, g, g), (p, [], g, g), ([3], g, g, g), (p, g, [], g)):
