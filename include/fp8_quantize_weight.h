@@ -19,8 +19,8 @@
  *
  * All pointers are device pointers of the current device; the library keeps none.
  * Execution is asynchronous on `stream`, nothing is allocated, and every call may be
- * captured.  Preconditions (checked before anything is enqueued): 0 <= N <= 2^31 - 16,
- * 16 <= K <= 2^23, K % 16 == 0, at most 2^31 - 1 tiles of 64 x 128; w aligned to its
+ * captured.  Preconditions (checked before anything is enqueued): 0 <= N <= 2^27,
+ * 16 <= K <= 2^23, K % 16 == 0, at most 2^24 - 1 tiles of 128 x 128; w aligned to its
  * element, q and qt to 16 bytes, scales to 4; outputs overlap nothing.  With N == 0
  * only scale_t (zeros) is written.  `workspace` is 256-byte aligned, of any contents,
  * and at least fp8_quantize_weight_workspace_size() bytes; it may serve calls of any

@@ -302,9 +302,11 @@ inline void plan_codes(CodeJob& p) {
 inline int64_t code_partials(const CodeJob& p, bool rows) {
     return 4 * ((int64_t)p.parts * p.K + (rows ? (int64_t)p.blocks * p.M : 0));
 }
-// Whether the grids' one dimension holds the tiles.
+// Whether the launches' threads, of which there are fewer than 2^32, can be counted (pass 1
+// takes strips of 128 rows or more, but for a few thousand workgroups).
 inline bool code_grid_ok(int64_t M, int64_t K) {
-    return code_up(M, 64) * code_up(K, kCodeCols) <= INT32_MAX;
+    return code_up(M, 128) * code_up(K, kCodeCols) * kCodeThreads <= UINT32_MAX &&
+           (code_up(M, kScaleGroup) + code_up(K, kScaleGroup)) * kScaleGroup * kScaleSlices <= UINT32_MAX;
 }
 
 template <class T, int FMT, bool ROWS, bool NT, class F>

@@ -11,10 +11,10 @@ namespace {
 
 bool at(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
-constexpr int64_t kMaxCols = int64_t(1) << 23;
+constexpr int64_t kMaxRows = int64_t(1) << 27, kMaxCols = int64_t(1) << 23;
 
 int weight_shape(int64_t N, int64_t K) {
-    if (N < 0 || N > INT32_MAX - 15 || K < 16 || K > kMaxCols || K % 16 != 0 || !code_grid_ok(N, K))
+    if (N < 0 || N > kMaxRows || K < 16 || K > kMaxCols || K % 16 != 0 || !code_grid_ok(N, K))
         return FP8MM_ERR_SHAPE;
     return FP8MM_OK;
 }

@@ -135,6 +135,24 @@ def test_given_buffers_and_any_workspace():
         binding.fp8_quantize_weight(w, workspace=ws[:-1])
 
 
+def test_the_most_rows():
+    N, K = 2 ** 27 - 13, 16                     # elements past 2^31
+    w = torch.empty(N, K, dtype=torch.bfloat16, device=DEV)
+    w.uniform_(-1, 1, generator=torch.Generator(device=DEV).manual_seed(3))
+    w[N - 5] *= 3
+    w[:, 3] /= 4
+    got = binding.fp8_quantize_weight(w)
+    most = w.abs().amax(1).cpu().float()
+    assert torch.equal(got.scale.cpu(), most / torch.full_like(most, 448))
+    most = w.abs().amax(0).cpu().float()
+    assert torch.equal(got.scale_t.cpu(), most / torch.full_like(most, 448))
+    assert (got.qt[:, N:] == 0).all()
+    for r in (0, 2 ** 26 - 40, 2 ** 27 - 100):
+        part = w[r:r + 87].cpu().float()
+        for codes, scale in ((got.q[r:r + 87], got.scale[r:r + 87, None]), (got.qt[:, r:r + 87].t(), got.scale_t)):
+            assert torch.equal(codes.cpu(), (part / scale.cpu()).to(FP8["e4m3fn"]).view(torch.uint8)), r
+
+
 def test_captured_and_replayed():
     ws = [make(N, K, dt) for N, K, dt in ((50, 64, torch.bfloat16), (3000, 4096, torch.float32), (100, 9008, torch.bfloat16))]
     want = [binding.fp8_quantize_weight(w) for w in ws]

@@ -64,6 +64,16 @@ def test_workspace_sizes(L):
         assert call(L, N=N, K=K, nbytes=n - 1) == binding.ERR_WORKSPACE
 
 
+def test_the_largest_sizes_are_those_that_can_be_launched(L):
+    """A launch has fewer than 2^32 threads: 1024 for each 64 rows, 256 for each 128 x 128."""
+    size = L.fp8_quantize_weight_workspace_size
+    for N, K in ((2 ** 27, 16), (2 ** 27, 1920), (2 ** 24, 16256), (1, 2 ** 23)):
+        assert size(N, K) > 0
+        assert call(L, N=N, K=K, nbytes=64) == binding.ERR_WORKSPACE
+    for N, K in ((2 ** 27 + 1, 16), (2 ** 27, 2048), (2 ** 24, 16384), (2 ** 28, 16)):
+        assert size(N, K) == -1 and call(L, N=N, K=K) == binding.ERR_SHAPE
+
+
 def test_binding_refuses_before_the_library():
     w = torch.zeros(4, 32)
     for args, kw in (((w,), dict()), ((w, "int8"), dict()), ((w.half(),), dict()), ((w[0],), dict())):
