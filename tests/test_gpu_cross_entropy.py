@@ -219,6 +219,13 @@ def test_a_target_of_minus_infinity_hides_no_nan():
     assert loss.isnan().all() and (lse == -math.inf).all()
 
 
+@pytest.mark.parametrize("M,V", [(2 ** 23 - 5, 40), (3, 2 ** 23 - 5)])
+def test_the_largest_sizes(M, V):
+    t = make(M, V, 16, seed=23, whole=True)
+    loss, lse = binding.fp8_linear_cross_entropy(*t)
+    check(loss, lse, *t)
+
+
 def test_no_rows():
     t = make(0, 100, 64)
     loss, lse = binding.fp8_linear_cross_entropy(*t)

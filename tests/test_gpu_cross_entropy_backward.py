@@ -316,6 +316,22 @@ def test_a_nearly_sure_row_keeps_the_shape_of_its_gradient():
     close(got, gradient64(*tensors))
 
 
+@pytest.mark.parametrize("M,V,rows", [(2 ** 23 - 5, 40, None), (3, 2 ** 23 - 5, None), (130, 2 ** 23 - 5, (3, 127))])
+def test_the_largest_sizes(M, V, rows):
+    """All rows, or `rows` of them and the others with a weight of 0."""
+    t = make(M, V, 16, seed=24)
+    extra = more(t)
+    if rows:
+        rows = torch.tensor(rows, device=DEV)
+        extra[3][torch.ones(M, dtype=torch.bool, device=DEV).index_fill(0, rows, False)] = 0
+    (dloss, a, b, sa, sb, target, loss, lse, x, wt, swt), (dx, dw) = run(t, extra)
+    if rows is not None:
+        dloss, a, sa, target, loss, lse, x = (v[rows].contiguous() for v in (dloss, a, sa, target, loss, lse, x))
+        assert int((dx != 0).any(1).sum()) == len(rows)
+        dx = dx[rows]
+    close((dx, dw), gradient64(dloss, a, b, sa, sb, target, loss, lse, x, wt, swt))
+
+
 def test_one_dloss_for_all_rows():
     t = make(300, 5000, 128, seed=13, ignore=-100)
     x, wt, swt, _ = more(t)
