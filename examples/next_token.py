@@ -74,8 +74,10 @@ class AdamW:
         for dtype in sorted({g.dtype for g in grads.values()}, key=str):
             names = [k for k, g in grads.items() if g.dtype == dtype]
             params = [self.params[k] for k in names]
-            state = self.groups.setdefault((dtype, tuple(names)), binding.adamw_state(params, self.bits))
-            binding.adamw_step(params, [grads[k] for k in names], **state._asdict(), step=self.count, lr=rate,
+            key = (dtype, tuple(names))
+            if key not in self.groups:
+                self.groups[key] = binding.adamw_state(params, self.bits)
+            binding.adamw_step(params, [grads[k] for k in names], **self.groups[key]._asdict(), step=self.count, lr=rate,
                                weight_decay=decay, seed=self.count)
 
 

@@ -11,12 +11,13 @@ multiply's, held to its parity bound of 1e-3 of the sum of magnitudes; outputs a
 rounded once (torch.finfo(bf16).eps / 2).
 """
 import math
+import threading
 
 import pytest
 import torch
 
 from precision_linear_amd import binding
-from test_gpu_cross_entropy import DEV, FP8, U, logits64
+from test_gpu_cross_entropy import DEV, FP8, U, check, logits64
 from test_gpu_cross_entropy import make as make_any
 
 pytestmark = pytest.mark.gpu
@@ -360,6 +361,54 @@ def test_equal_calls_equal_bits_whatever_the_buffers_hold(M, V, K):
         assert got[0] is dx and got[1] is dw and torch.equal(dx, want[0]) and torch.equal(dw, want[1])
     with pytest.raises(ValueError):
         binding.fp8_linear_cross_entropy_backward(*args, workspace=torch.empty(need - 1, dtype=torch.uint8, device=DEV))
+
+
+def moved(t, align):
+    """t's values, contiguous, at an address that suits `align` bytes but not twice as many."""
+    size = t.element_size()
+    flat = torch.empty(t.numel() * size + 512, dtype=torch.uint8, device=DEV)
+    at = -flat.data_ptr() % 256 + align
+    out = flat[at:at + t.numel() * size].view(t.dtype).view(t.shape)
+    assert out.data_ptr() % (2 * align) == align
+    return out.copy_(t)
+
+
+@pytest.mark.parametrize("M,V,K", [(3, 1001, 512), (260, 9000, 272), (1500, 9000, 256), (300, 30000, 64)])
+def test_odd_addresses(M, V, K):
+    t = make(M, V, K, seed=25, ignore=-100)
+    x, wt, swt, dloss = more(t)
+    aligns = (16, 16, 4, 4, 8)
+    t = tuple(moved(v.view(torch.uint8) if n == 16 else v, n).view(v.dtype) for v, n in zip(t, aligns))
+    swt, dloss, x, wt = moved(swt, 4), moved(dloss, 4), moved(x, 2), moved(wt.view(torch.uint8), 16).view(wt.dtype)
+    loss, lse = (moved(v, 4) for v in binding.fp8_linear_cross_entropy(*t))
+    check(loss, lse, *t)
+    out = [moved(torch.full(s, 7.0, dtype=BF16, device=DEV), 2) for s in ((M, K), (V, K))]
+    got = binding.fp8_linear_cross_entropy_backward(dloss, *t, loss, lse, x, wt, swt, dx=out[0], dw=out[1])
+    assert got[0] is out[0] and got[1] is out[1]
+    close(got, gradient64(dloss, *t, loss, lse, x, wt, swt))
+
+
+def test_threads_with_streams_of_their_own():
+    problems = [make(M, V, K, seed=26) for M, V, K in ((40, 5000, 256), (1200, 9000, 128), (300, 30000, 64), (1, 3000, 512))]
+    extras = [more(t) for t in problems]
+    want = [run(t, e) for t, e in zip(problems, extras)]
+    torch.cuda.synchronize()
+    got = [None] * len(problems)
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(5):
+                got[i] = run(problems[i], extras[i])
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(problems))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for (args, out), (args0, out0) in zip(got, want):
+        assert torch.equal(args[6], args0[6]) and torch.equal(args[7], args0[7])
+        assert torch.equal(out[0], out0[0]) and torch.equal(out[1], out0[1])
 
 
 def test_captured_and_replayed():
