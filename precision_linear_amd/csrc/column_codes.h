@@ -6,7 +6,7 @@
 //     q_cols[k][m] = RNE(x[m][k] / col_scale[k]),  col_scale[k] = max_m |x| / qmax
 //     q_rows[m][k] = RNE(x[m][k] / row_scale[m]),  row_scale[m] = max_k |x| / qmax
 // with correctly rounded quotients, as in fp8_quantize.h.  Both need maxima of whole
-// rows and columns, so x is read twice:
+// rows and columns, so x is read twice (but for column codes of few rows, few_rows_kernel):
 //   1. maxima_kernel: partial maxima of columns (by strips of rows) and of rows (by
 //      blocks of columns), with the rows' factors made on the way;
 //   2. scales_kernel joins them, unless they are so few that pass 3 does it itself;
@@ -284,6 +284,102 @@ __global__ void __launch_bounds__(kCodeThreads) codes_kernel(CodeJob p, int col_
     }
 }
 
+// Column codes of up to 2 THREADS rows in one launch: a workgroup holds 16 columns of them
+// all in its registers, 8 columns a lane of rows 4 r .. 4 r + 3 for r = threadIdx.x / 2, so x
+// is read once and nothing is left to join.  (us of the cross entropy's gradient on one
+// MI355X with the two passes and with this: 100 x 32000 x 1024 57.3 and 52.6, 1001 x 50255 x
+// 2048 349.7 and 345.8; 5.1 and 12.5 of them here, memory latencies one after the other.)
+constexpr int kFewCols = 16, kFewLanes = kFewCols / 8;
+// Over the lanes of a wave with the same lane % kFewLanes.
+__device__ __forceinline__ float few_max(float x) {
+    static_assert(kFewLanes == 2, "the first step is lane ^ 2");
+    constexpr int kTurn4 = 0x124, kTurn8 = 0x128;   // of 16 lanes
+    x = fmaxf(x, dpp<kSwap2>(x));
+    x = fmaxf(x, dpp<kTurn4>(x));
+    x = fmaxf(x, dpp<kTurn8>(x));
+    uint32_t h = __float_as_uint(x);
+    const auto half = __builtin_amdgcn_permlane32_swap(h, h, false, false);
+    x = fmaxf(__uint_as_float(half[0]), __uint_as_float(half[1]));
+    h = __float_as_uint(x);
+    const auto row = __builtin_amdgcn_permlane16_swap(h, h, false, false);
+    return fmaxf(__uint_as_float(row[0]), __uint_as_float(row[1]));
+}
+template <class T, int FMT, class F, int THREADS>
+__global__ void __launch_bounds__(THREADS) few_rows_kernel(CodeJob p, F factors) {
+    constexpr int kWaves = THREADS / kWaveSize;
+    __shared__ float s_factor[2 * THREADS];
+    __shared__ float s_max[kWaves][kFewCols], s_col[2][kFewCols];
+    __shared__ int s_slow;
+    const T* x = static_cast<const T*>(p.x);
+    const int cl = threadIdx.x % kFewLanes, r = threadIdx.x / kFewLanes * 4;
+    const int64_t col0 = (int64_t)blockIdx.x * kFewCols, col = col0 + cl * 8;   // K is a multiple of 16
+    Raw8<T> a[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        a[k].zero();
+        if (r + k < p.M) a[k].load(x + (r + k) * p.K + col);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int i = k * THREADS + threadIdx.x;
+        s_factor[i] = i < p.M ? factors.of(i, blockIdx.x == 0) : 1.f;
+    }
+    factors.begin();
+    __syncthreads();
+    float f[4][8], cs[8], cr[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) code_values<T, F::kGiven>(a[k], s_factor[r + k], f[k]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float m = 0.f;   // (no NaN)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m = fmaxf(m, fabsf(f[k][i]));
+        m = few_max(m);
+        if (threadIdx.x % kWaveSize < kFewLanes) s_max[threadIdx.x / kWaveSize][cl * 8 + i] = m;
+    }
+    __syncthreads();
+    if (threadIdx.x < kWaveSize) {
+        bool slow = false;   // whether a division here is outside the fast one's range
+        if (threadIdx.x < kFewCols) {
+            float m = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) m = fmaxf(m, s_max[w][threadIdx.x]);
+            const float s = m / Fp8Fmt<FMT>::kMax;
+            p.col_scale[col0 + threadIdx.x] = s / p.col_unit;
+            const Div d = make_div(s);
+            slow = !d.fast && s != 0.f;
+            s_col[0][threadIdx.x] = s;
+            s_col[1][threadIdx.x] = s == 0.f ? 0.f : d.r;
+        }
+        slow = __any(slow);
+        if (threadIdx.x == 0) s_slow = slow;
+    }
+    __syncthreads();
+    const bool slow = __builtin_amdgcn_readfirstlane(s_slow);
+    if (r >= p.Mp) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        cs[i] = s_col[0][cl * 8 + i];
+        cr[i] = s_col[1][cl * 8 + i];
+    }
+    auto codes = [&](auto fast) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const Div d{cs[i], cr[i], true};
+                if constexpr (decltype(fast)::value) y[k] = quant1<FMT, true>(f[k][i], d);
+                else y[k] = cs[i] == 0.f ? f[k][i] * 0.f : quant1<FMT, false>(f[k][i], d);
+            }
+            const int w = Fp8Fmt<FMT>::template cvt_pk<false>(y[0], y[1], 0);
+            *reinterpret_cast<int*>(p.q_cols + (col + i) * p.Mp + r) = Fp8Fmt<FMT>::template cvt_pk<true>(y[2], y[3], w);
+        }
+    };
+    if (!slow) codes(std::true_type());
+    else codes(std::false_type());
+}
+
 // ---------------------------------------------------------------- host ---
 
 inline int64_t code_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -312,6 +408,17 @@ inline bool code_grid_ok(int64_t M, int64_t K) {
 template <class T, int FMT, bool ROWS, bool NT, class F>
 void launch_codes(const CodeJob& p, const F& factors, hipStream_t hs) {
     constexpr bool FACTOR = F::kGiven;
+    if constexpr (!ROWS && !NT) {
+        const dim3 grid((unsigned)code_up(p.K, kFewCols));
+        if (p.Mp <= 256) {
+            hipLaunchKernelGGL((few_rows_kernel<T, FMT, F, 128>), grid, dim3(128), 0, hs, p, factors);
+            return;
+        }
+        if (p.Mp <= 1024) {
+            hipLaunchKernelGGL((few_rows_kernel<T, FMT, F, 512>), grid, dim3(512), 0, hs, p, factors);
+            return;
+        }
+    }
     hipLaunchKernelGGL((maxima_kernel<T, F, ROWS, NT>), dim3((unsigned)((int64_t)p.parts * p.blocks)),
                        dim3(kCodeThreads), 0, hs, p, factors);
     int col_parts = p.parts, row_parts = p.blocks;

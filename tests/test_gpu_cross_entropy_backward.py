@@ -150,6 +150,18 @@ def test_formats(fa, fb, fw, M, V, K):
     close(got, gradient64(*args))
 
 
+@pytest.mark.parametrize("M", [255, 256, 257, 512, 513, 1023, 1024, 1025])
+def test_rows_around_the_variants_of_their_codes(M):
+    """Also with x's column scales below 2^-60, where quotients are divisions."""
+    t = make(M, 300, 80, seed=27, ignore=-100)
+    x, wt, swt, dloss = more(t)
+    x[:, 5] = 0
+    for size in (1.0, 2.0 ** -80):
+        args, got = run(t, (x, wt, swt, dloss * size))
+        close(got, gradient64(*args), size)
+        assert (got[1][:, 5] == 0).all()
+
+
 @pytest.mark.parametrize("M,V,K", [(60, 700, 64), (512, 4096, 512), (300, 10000, 512)])
 def test_every_code(M, V, K):
     """With x the identity, column m of dw holds row m's codes times r[m] / 57344; the
