@@ -15,7 +15,8 @@
  *   an entry of the vocabulary: its rows' loss is 0, their lse the same sum.  A target
  *   outside 0 .. V - 1 that is not ignore_index gives a loss of NaN; a NaN or +inf among a
  *   row's logits makes its loss (unless the row is ignored) and lse NaN, logits of -inf
- *   alone the loss.
+ *   alone the loss.  The target's logit is summed in fp32, the others by the matrix
+ *   instruction, which keeps products to 2^-13 of the largest that it adds.
  */
 #ifndef FP8_CROSS_ENTROPY_H
 #define FP8_CROSS_ENTROPY_H
