@@ -304,9 +304,70 @@ __device__ __forceinline__ float few_max(float x) {
     const auto row = __builtin_amdgcn_permlane16_swap(h, h, false, false);
     return fmaxf(__uint_as_float(row[0]), __uint_as_float(row[1]));
 }
-template <class T, int FMT, class F, int THREADS>
+// Row codes are made by further workgroups, a wave a row, which read x once more (us a call
+// from Python with the two passes and with this: 3 x 112 and 100 x 4096 fp32 13.2 and
+// 10.1, 128 x 8192 13.2 and 10.1, 1024 x 1024 13.3 and 10.1, but 1000 x 4160 bf16 13.1 and 13.1, 32 x 28672
+// 16.2 and 17.9, 1024 x 8192 17.2 and 23.5).
+constexpr int64_t kFewElements = int64_t(1) << 20, kFewRowLength = 8192;
+template <class T, int FMT>
+__device__ __forceinline__ void row_codes(const CodeJob& p, int64_t row) {
+    constexpr int kAhead = 4, kStep = kWaveSize * 8;   // elements of a wave's load; loads in flight
+    const T* x = static_cast<const T*>(p.x) + row * p.K;
+    const int64_t first = threadIdx.x % kWaveSize * 8;
+    Raw8<T> a[kAhead];
+    auto fetch = [&](int64_t c0) __attribute__((always_inline)) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            a[k].zero();
+            if (c0 + k * kStep < p.K) a[k].load(x + c0 + k * kStep);
+        }
+    };
+    float m = 0.f;
+    for (int64_t c0 = first; c0 < p.K; c0 += kAhead * kStep) {
+        fetch(c0);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(a[k].get(i)));
+    }
+    const float s = wave_max(m) / Fp8Fmt<FMT>::kMax;
+    if (threadIdx.x % kWaveSize == 0) p.row_scale[row] = s;
+    const Div d = make_div(s);
+    const bool fast = d.fast;
+    for (int64_t c0 = first; c0 < p.K; c0 += kAhead * kStep) {
+        if (p.K > kAhead * kStep) fetch(c0);   // (else a still holds the row)
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            float y[8];
+            if (fast) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = quant1<FMT, true>(a[k].get(i), d);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = s == 0.f ? a[k].get(i) * 0.f : quant1<FMT, false>(a[k].get(i), d);
+            }
+            u32x2 codes;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int w = Fp8Fmt<FMT>::template cvt_pk<false>(y[4 * h], y[4 * h + 1], 0);
+                codes[h] = (uint32_t)Fp8Fmt<FMT>::template cvt_pk<true>(y[4 * h + 2], y[4 * h + 3], w);
+            }
+            const int64_t c = c0 + k * kStep;
+            if (c < p.K) *reinterpret_cast<u32x2*>(p.q_rows + row * p.K + c) = codes;
+        }
+    }
+}
+template <class T, int FMT, class F, bool ROWS, int THREADS>
 __global__ void __launch_bounds__(THREADS) few_rows_kernel(CodeJob p, F factors) {
     constexpr int kWaves = THREADS / kWaveSize;
+    if constexpr (ROWS) {
+        const int64_t block = (int64_t)blockIdx.x - p.K / kFewCols;
+        if (block >= 0) {
+            const int64_t row = block * kWaves + threadIdx.x / kWaveSize;
+            if (row < p.M) row_codes<T, FMT>(p, row);
+            return;
+        }
+    }
     __shared__ float s_factor[2 * THREADS];
     __shared__ float s_max[kWaves][kFewCols], s_col[2][kFewCols];
     __shared__ int s_slow;
@@ -408,14 +469,12 @@ inline bool code_grid_ok(int64_t M, int64_t K) {
 template <class T, int FMT, bool ROWS, bool NT, class F>
 void launch_codes(const CodeJob& p, const F& factors, hipStream_t hs) {
     constexpr bool FACTOR = F::kGiven;
-    if constexpr (!ROWS && !NT) {
-        const dim3 grid((unsigned)code_up(p.K, kFewCols));
-        if (p.Mp <= 256) {
-            hipLaunchKernelGGL((few_rows_kernel<T, FMT, F, 128>), grid, dim3(128), 0, hs, p, factors);
-            return;
-        }
-        if (p.Mp <= 1024) {
-            hipLaunchKernelGGL((few_rows_kernel<T, FMT, F, 512>), grid, dim3(512), 0, hs, p, factors);
+    if constexpr (!NT) {
+        const int threads = p.Mp <= 256 ? 128 : 512;
+        const dim3 grid((unsigned)(p.K / kFewCols + (ROWS ? code_up(p.M, threads / kWaveSize) : 0)));
+        if (p.Mp <= 1024 && (!ROWS || (p.K <= kFewRowLength && p.M * p.K <= kFewElements))) {
+            if (threads == 128) hipLaunchKernelGGL((few_rows_kernel<T, FMT, F, ROWS, 128>), grid, dim3(128), 0, hs, p, factors);
+            else hipLaunchKernelGGL((few_rows_kernel<T, FMT, F, ROWS, 512>), grid, dim3(512), 0, hs, p, factors);
             return;
         }
     }

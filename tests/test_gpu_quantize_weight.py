@@ -60,6 +60,19 @@ def test_codes(N, K, dtype):
         check(w, binding.fp8_quantize_weight(w, fmt), fmt)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N,K", [(255, 2048), (256, 4096), (256, 4112), (257, 2064), (128, 8192), (128, 8208), (1023, 1024),
+                                 (1024, 1024), (1025, 1008), (1009, 32), (1, 8192), (1, 8208)])
+def test_around_the_variants(N, K, dtype):
+    w = make(N, K, dtype, seed=4)
+    w[N // 2] = 0
+    w[:, K - 1] = 0
+    check(w, binding.fp8_quantize_weight(w), "e4m3fn")
+    w[N // 3] *= 2.0 ** -70                    # (scales whose quotients are divisions)
+    w[:, 5] *= 2.0 ** -75
+    check(w, binding.fp8_quantize_weight(w, "e5m2"), "e5m2")
+
+
 @pytest.mark.parametrize("N,K", [(2000, 4096), (64, 144)])
 def test_the_quantisers_own_bits(N, K):
     w = make(N, K, torch.bfloat16)
