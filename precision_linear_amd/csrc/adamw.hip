@@ -351,7 +351,9 @@ int adamw_step(const adamw_tensor* tensors, int64_t count, int param_dtype, int 
     if (st != ADAMW_OK) return st;
     const uintptr_t pa = param_dtype == ADAMW_BF16 ? 2 : 4, ga = grad_dtype == ADAMW_BF16 ? 2 : 4;
     const uintptr_t sa = state_bits == 8 ? 1 : 4;
-    const bool master = count > 0 && tensors[0].master != nullptr;
+    // (an empty tensor's pointers say nothing: torch's are all NULL)
+    const adamw_tensor* first = std::find_if(tensors, tensors + count, [](const adamw_tensor& t) { return t.numel > 0; });
+    const bool master = first != tensors + count && first->master != nullptr;
     if (master && param_dtype == ADAMW_FP32) return ADAMW_ERR_DTYPE;
     std::vector<std::pair<uintptr_t, uintptr_t>> written;   // [from, to) of what the step writes
     written.reserve((size_t)count * (3 + (master ? 1 : 0) + (state_bits == 8 ? 2 : 0)));

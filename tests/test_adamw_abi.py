@@ -124,6 +124,25 @@ def test_neighbours_are_taken(L):
     assert call(L, [tensor(0), tensor(1, param=P, exp_avg=P, exp_avg_sq=P, numel=0)]) in reached
 
 
+@pytest.mark.parametrize("empty", [{}, dict(param=None, grad=None, exp_avg=None, exp_avg_sq=None),
+                                   dict(master=P * 7, exp_avg_scale=P * 6, exp_avg_sq_scale=P * 7)])
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("master", [True, False])
+def test_empty_tensors_anywhere(L, empty, bits, master):
+    """Pointers of empty tensors (torch's are NULL) count neither for nor against masters, wherever they are."""
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present: these cases would launch on fake pointers")
+    reached = (E.ADAMW_ERR_DEVICE, E.ADAMW_ERR_LAUNCH)
+    more = dict(exp_avg_scale=P * 6, exp_avg_sq_scale=P * 7) if bits == 8 else {}
+    full = tensor(0, **more, **(dict(master=P * 8) if master else {}))
+    none = tensor(1, numel=0, **empty)
+    for tensors in ([none, full], [full, none], [none, none, full, none], [none]):
+        assert call(L, tensors, pd=0, bits=bits) in reached
+    if master:
+        assert call(L, [none, full], pd=1, bits=bits) == E.ADAMW_ERR_DTYPE
+        assert call(L, [none, full, tensor(2, **more)], pd=0, bits=bits) == E.ADAMW_ERR_NULL
+
+
 def test_binding_refuses_before_the_library():
     p, g = [torch.zeros(4)], [torch.zeros(4)]
     for args in ((p, g, g, g), (p, [], g, g), ([3], g, g, g), (p, g, [], g)):

@@ -151,6 +151,19 @@ def test_step(sizes, param, grad, master, bits):
         assert all(torch.equal(a, b) for a, b in zip(t["grads"], before["grads"]))
 
 
+@pytest.mark.parametrize("path", ["short", "whole"])
+@pytest.mark.parametrize("master", [True, False])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_an_empty_tensor_first(bits, master, path, monkeypatch):
+    if path == "whole":
+        monkeypatch.setattr(binding, "_calls", None)
+    for sizes in ([0, 1000], [0, 0, 300, 0, 4097], [0]):
+        t = make(sizes, BF16, BF16, bits, master)
+        before = copies(t)
+        binding.adamw_step(**t, step=5, seed=11, **HYPER)
+        check(before, t, 5, 11)
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_many_tensors(bits):
     """More than a launch takes; positions go on through the list."""
