@@ -764,7 +764,14 @@ def fp8_linear_cross_entropy_backward(dloss: torch.Tensor, a: torch.Tensor, b: t
                ws.data_ptr(), ws_bytes)
     if st != OK:
         _mm_error("fp8_linear_cross_entropy_backward", st)
+    _count_written(dx, dw)
     return dx, dw
+
+
+def _count_written(*tensors) -> None:
+    """Tensors of the caller's that a call has written (others, None and False among them, are
+    passed over): a graph of torch's that saved one before refuses to use it after."""
+    torch.autograd.graph.increment_version([t for t in tensors if isinstance(t, torch.Tensor)])
 
 
 def _bf16_matrix(name: str, t: torch.Tensor, shape: tuple) -> None:
@@ -883,6 +890,7 @@ def fp8_quantize_weight(w: torch.Tensor, fmt="e4m3fn", *, q: torch.Tensor | None
                qt.data_ptr(), scale_t.data_ptr(), N, K, _stream_of(dev), ws.data_ptr(), ws_bytes)
     if st != OK:
         _mm_error("fp8_quantize_weight", st)
+    _count_written(q, scale, qt, scale_t)
     return WeightCodes(q, scale, qt, scale_t)
 
 
@@ -1120,7 +1128,9 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, *, step, lr, betas=(0.9, 0.99
     elements in exp_avg_scale and exp_avg_sq_scale (adamw_state makes them all); codes are
     rounded up or down at random by a hash of `seed`, which should change from step to
     step, and the element's place.  A gradient may be given to several parameters, anything
-    that is written only once.
+    that is written only once.  What is written counts as changed in place: a graph of
+    torch's that saved it before refuses to run backward after (a replayed capture
+    counts nothing).
 
     step (from 1), lr and seed are numbers, or GPU tensors of one element (float32,
     float32, int64) for a captured step; grad_scale is a float32 GPU tensor of one element
@@ -1179,6 +1189,8 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, *, step, lr, betas=(0.9, 0.99
                8 if eight else 32, ctypes.byref(numbers), _stream_of(dev))
     if st != ADAMW_OK:
         _adamw_error(st)
+    for ts in (params, exp_avg, exp_avg_sq, master, exp_avg_scale, exp_avg_sq_scale):
+        _count_written(*(ts or ()))
 
 
 def _adamw_error(st: int) -> None:

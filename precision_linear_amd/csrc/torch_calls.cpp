@@ -443,8 +443,10 @@ PyObject* quantize_weight(PyObject*, PyObject* const* arg, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// A list of tensors as adamw_step's must be: one for each parameter, of one type.
+// A list of tensors as adamw_step's must be: one for each parameter, of one type.  It is
+// held as a tuple, whose tensors stay while the interpreter is free.
 struct List {
+    PyObject* held = nullptr;
     PyObject* const* items = nullptr;
     Py_ssize_t size = 0;
     bool given = false, ok = true;
@@ -453,8 +455,23 @@ struct List {
         given = true;
         ok = PyList_CheckExact(o) || PyTuple_CheckExact(o);
         if (!ok) return;
-        items = PySequence_Fast_ITEMS(o);
-        size = PySequence_Fast_GET_SIZE(o);
+        held = PySequence_Tuple(o);
+        if (!held) {
+            PyErr_Clear();
+            ok = false;
+            return;
+        }
+        items = PySequence_Fast_ITEMS(held);
+        size = PyTuple_GET_SIZE(held);
+    }
+    List(const List&) = delete;
+    ~List() { Py_XDECREF(held); }
+    // Their contents have changed: what torch's graphs saved of them before is no longer there.
+    void written() const {
+        for (Py_ssize_t i = 0; i < size; ++i) {
+            c10::TensorImpl* t = THPVariable_Unpack(items[i]).unsafeGetTensorImpl();
+            if (!t->is_inference()) t->bump_version();   // (those have no version)
+        }
     }
     // Tensor i if it is on GPU `dev`, contiguous and of `type`, else null.
     const at::Tensor* get(Py_ssize_t i, int dev, at::ScalarType type) const {
@@ -555,6 +572,8 @@ PyObject* adamw(PyObject*, PyObject* const* arg, Py_ssize_t n) {
                          gt == at::kFloat ? ADAMW_FP32 : ADAMW_BF16, eight ? 8 : 32, &num,
                          reinterpret_cast<ihipStream_t*>(stream));
     }
+    if (st == ADAMW_OK)
+        for (const List* l : {&p, &m, &v, &w, &ms, &vs}) l->written();
     return PyLong_FromLong(st);
     END_HANDLE_TH_ERRORS
 }

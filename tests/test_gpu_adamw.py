@@ -462,3 +462,42 @@ def test_refusals(monkeypatch, path):
     binding.adamw_step([], [], [], [], step=1, lr=0.1)
     with pytest.raises(ValueError):
         binding.adamw_state(t["params"], 16)
+
+
+@pytest.mark.parametrize("path", ["short", "whole"])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_graph_sees_that_its_parameter_has_moved(bits, path, monkeypatch):
+    """What a step writes counts as written: a backward pass that saved it before the step refuses to run
+    on the new values, as after torch's own steps."""
+    if path == "whole":
+        monkeypatch.setattr(binding, "_calls", None)
+    t = make([300, 0, 70], BF16, BF16, bits, True)
+    written = [x for k, v in t.items() if k != "grads" and v is not None for x in v]
+    before = [x._version for x in written], [x._version for x in t["grads"]]
+    x = torch.ones(300, device=DEV, dtype=BF16, requires_grad=True)
+    y = (x * t["params"][0]).sum()
+    binding.adamw_step(**t, step=1, **HYPER)
+    assert all(x._version > v for x, v in zip(written, before[0]))
+    assert [x._version for x in t["grads"]] == before[1]
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    after = [x._version for x in written]
+    with pytest.raises(ValueError):                          # a refused step writes nothing
+        binding.adamw_step(**t, step=0, **HYPER)
+    assert [x._version for x in written] == after
+
+
+@pytest.mark.parametrize("path", ["short", "whole"])
+def test_tensors_of_inference_mode(path, monkeypatch):
+    """They have no version counter."""
+    if path == "whole":
+        monkeypatch.setattr(binding, "_calls", None)
+    with torch.inference_mode():
+        t = make([300, 5], FP32, FP32, 8)
+        before = copies(t)
+        binding.adamw_step(**t, step=1, **HYPER)
+    binding.adamw_step(**t, step=2, **HYPER)
+    with torch.inference_mode():
+        binding.adamw_step(**before, step=1, **HYPER)
+        binding.adamw_step(**before, step=2, **HYPER)
+        same(t, before)

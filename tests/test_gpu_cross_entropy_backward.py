@@ -400,6 +400,17 @@ def test_odd_addresses(M, V, K):
     close(got, gradient64(dloss, *t, loss, lse, x, wt, swt))
 
 
+def test_given_buffers_count_as_written():
+    t = make(40, 100, 64)
+    x, wt, swt, dloss = more(t)
+    loss, lse = binding.fp8_linear_cross_entropy(*t)
+    dx, dw = (torch.empty(n, 64, dtype=BF16, device=DEV) for n in (40, 100))
+    for kw in (dict(dx=dx), dict(dw=dw), dict(dx=dx, dw=dw), dict(dx=dx, dw=False)):
+        before = dx._version, dw._version
+        binding.fp8_linear_cross_entropy_backward(dloss, *t, loss, lse, x, wt, swt, **kw)
+        assert (dx._version > before[0]) == (kw.get("dx") is dx) and (dw._version > before[1]) == (kw.get("dw") is dw)
+
+
 def test_threads_with_streams_of_their_own():
     problems = [make(M, V, K, seed=26) for M, V, K in ((40, 5000, 256), (1200, 9000, 128), (300, 30000, 64), (1, 3000, 512))]
     extras = [more(t) for t in problems]

@@ -148,6 +148,19 @@ def test_given_buffers_and_any_workspace():
         binding.fp8_quantize_weight(w, workspace=ws[:-1])
 
 
+def test_given_buffers_count_as_written():
+    """A graph that saved the old codes refuses to run backward on the new ones."""
+    w = make(64, 32, torch.float32)
+    out = binding.fp8_quantize_weight(w)
+    x = torch.ones(64, device=DEV, requires_grad=True)
+    y = (x * out.scale).sum()
+    before = [t._version for t in out]
+    binding.fp8_quantize_weight(w, **out._asdict())
+    assert all(t._version > v for t, v in zip(out, before))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+
+
 def test_the_most_rows():
     N, K = 2 ** 27 - 13, 16                     # elements past 2^31
     w = torch.empty(N, K, dtype=torch.bfloat16, device=DEV)
