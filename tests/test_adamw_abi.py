@@ -3,6 +3,7 @@ every refusal before anything touches a device."""
 import ctypes
 import math
 import os
+import random
 import re
 
 import pytest
@@ -141,6 +142,49 @@ def test_empty_tensors_anywhere(L, empty, bits, master):
     if master:
         assert call(L, [none, full], pd=1, bits=bits) == E.ADAMW_ERR_DTYPE
         assert call(L, [none, full, tensor(2, **more)], pd=0, bits=bits) == E.ADAMW_ERR_NULL
+
+
+@pytest.mark.parametrize("kinds", ["bits 32", "masters", "bits 8", "bits 8, masters"])
+@pytest.mark.parametrize("order", ["tensor by tensor", "kind by kind", "kinds side by side", "shuffled", "each kind shuffled"])
+@pytest.mark.parametrize("count", [1, 2, 7, 40, 64, 131, 300])
+def test_overlaps_among_many(L, count, order, kinds):
+    """Ranges that touch are taken, one byte more is refused, whatever the order of the list."""
+    rng = random.Random(f"{count} {order} {kinds}")
+    bits, master = 8 if "8" in kinds else 32, "masters" in kinds
+    names = ["param", "exp_avg", "exp_avg_sq"] + ["master"] * master + ["exp_avg_scale", "exp_avg_sq_scale"] * (bits == 8)
+    numel = [rng.choice((1, 3, 256, 257, rng.randrange(1, 5000))) for _ in range(count)]
+    size = lambda i, k: {"param": 2 * numel[i], "master": 4 * numel[i], "exp_avg": numel[i] * bits // 8,        # noqa: E731
+                         "exp_avg_sq": numel[i] * bits // 8}.get(k, 4 * ((numel[i] + 255) // 256))
+    spots = [(i, k) for i in range(count) for k in names]
+    if order == "kinds side by side":              # one kind's between another's
+        spots = [(i, k) for ks in (names[:2], names[2:]) for i in range(count) for k in ks]
+    elif order != "tensor by tensor":
+        spots.sort(key=lambda s: names.index(s[1]))
+    if order == "each kind shuffled":
+        rng.shuffle(spots)
+    at, starts = 1 << 44, {}
+    for i, k in spots:
+        at = (at + 3) // 4 * 4 + rng.choice((0, 0, 4, 512, 1 << 30))
+        starts[i, k] = at
+        at += size(i, k)
+    ranges = sorted((starts[s], starts[s] + size(*s), s) for s in spots)
+    perm = list(range(count))
+    if order == "shuffled":
+        rng.shuffle(perm)
+
+    def status(starts):
+        return call(L, [tensor(0, numel=numel[i], **{k: starts[i, k] for k in names}) for i in perm], pd=0, bits=bits)
+
+    if not torch.cuda.is_available():              # (a launch on these addresses would fault)
+        assert status(starts) in (E.ADAMW_ERR_DEVICE, E.ADAMW_ERR_LAUNCH)
+    for _ in range(30):
+        (a, b, s), (c, d, t) = rng.choice([(x, y) for x, y in zip(ranges, ranges[1:])])
+        if rng.random() < 0.5:                     # the later one begins in the earlier one's last bytes
+            c = (b - 1) // 4 * 4
+            assert status(starts | {t: c}) == E.ADAMW_ERR_ALIAS
+        else:                                      # any two begin at one address
+            x, y = rng.sample(spots, 2)
+            assert status(starts | {x: starts[y]}) == E.ADAMW_ERR_ALIAS
 
 
 def test_binding_refuses_before_the_library():
