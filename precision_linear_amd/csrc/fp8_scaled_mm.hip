@@ -901,8 +901,13 @@ int run_codes(const Logits& z, const LossPlan& plan, const float2* rows, uint8_t
     return run_loss(tables, z, plan, p, stream, ws);
 }
 
-// (us of the whole gradient on one MI355X with the multiply's own 256 MB and with 128: 1001 x
-// 50255 x 2048, whose dw and operands are 259 MB, 370 and 351.)
+// (The multiply's own threshold is 256 MB.  us of the whole gradient, one call after another, rows x
+// vocabulary x features, on one MI355X with 256 MB and with 128: 512 x 32000 x 2048 151 and 140, 300 x 50000 x 2048 224 and 199, 256 x 100000 x
+// 1024 203 and 179, 200 x 64000 x 1536 156 and 137, 1024 x 40000 x 2048 298 and 279, 1500 x 16000 x
+// 5120 380 and 369, 2048 x 10000 x 8192 448 and 437, 2000 x 20000 x 4096 468 and 457, 4096 x 20000 x
+// 2048 472 and 467, 700 x 30000 x 2992 318 and 315, 100 x 25000 x 4096 113 and 111.  With 128 and with 64,
+// the products of 70 to 118 MB: 400 x 16000 x 2048 83.4 and 81.9, 200 x 32000 x 1536 83.5 and 80.1,
+// 300 x 28000 x 2048 124 and 118, 1000 x 10000 x 4096 186 and 159, 128 x 60000 x 768 76.1 and 75.4.)
 int run_streamed(const Product& p, hipStream_t stream, void* ws, int64_t ws_bytes) {
     return run_mm(p.A, FP8MM_E5M2, p.B, FP8MM_E4M3FN, p.scale_a, p.scale_b, nullptr, p.out, p.M, p.N, p.K, FP8MM_ROWWISE,
                   reinterpret_cast<struct ihipStream_t*>(stream), -1, 0, ws, ws_bytes, WsSource::kCaller, nullptr,
