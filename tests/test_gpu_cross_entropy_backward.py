@@ -268,6 +268,29 @@ def test_rows_that_do_not_count(M, V):
     assert (dx == 0).all() and (dw == 0).all()
 
 
+@pytest.mark.parametrize("path", ["short", "whole"])
+@pytest.mark.parametrize("M,V", [(1, 20), (6, 100), (600, 9000)])
+def test_another_ignored_index(M, V, path, monkeypatch):
+    """Entries of the vocabulary, whose rows have a loss of 0 and an lse like any other, and numbers outside it."""
+    if path == "whole":
+        monkeypatch.setattr(binding, "_calls", None)
+    for ignore in (0, V - 1, V + 7, -1, 2 ** 40):
+        t = make(M, V, 64, seed=31)
+        target = t[4]
+        target[M // 2::3] = ignore
+        if M > 1:
+            target[0] = 7
+        x, wt, swt, dloss = more(t)
+        loss, lse = binding.fp8_linear_cross_entropy(*t, ignore_index=ignore)
+        args = (dloss, *t, loss, lse, x, wt, swt)
+        got = binding.fp8_linear_cross_entropy_backward(*args, ignore_index=ignore)
+        assert (got[0][target == ignore] == 0).all() and lse.isfinite().all()
+        close(got, gradient64(*args, ignore=ignore), ignore)
+        # (the default one is then no entry as any other)
+        target[0] = -100
+        assert binding.fp8_linear_cross_entropy_backward(*args, ignore_index=ignore)[0][0].isnan().all()
+
+
 @pytest.mark.parametrize("M,V", [(6, 100), (600, 9000)])
 def test_a_weight_of_0_hides_what_is_no_number(M, V):
     t = make(M, V, 64, seed=19)
