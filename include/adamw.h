@@ -10,9 +10,11 @@
  *           - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
  *
  *   in fp32 (1 - beta and 1 - beta^step in fp64, then rounded); in m, v and sqrt(v) every
- *   product, sum and root is rounded as it is written.  p is the master weight where there
- *   is one; the parameter is then p rounded to bf16.  A bf16 parameter without a master
- *   is rounded to nearest, so steps below half its last bit leave it as it is.
+ *   product, sum and root is rounded as it is written.  An eps above 0 counts as 2^-149
+ *   at least, as 2^-126 with moments of 8 bits.  p
+ *   is the master weight where there is one; the parameter is then p rounded to bf16.  A bf16
+ *   parameter without a master is rounded to nearest, so steps below half its last bit
+ *   leave it as it is.
  *
  * Moments of 8 bits.  A tensor is cut into blocks of 256 elements, the last one
  * shorter.  exp_avg holds e4m3fn codes of m over the block's scale, max |m| / 448;

@@ -450,7 +450,8 @@ int adamw_step(const adamw_tensor* tensors, int64_t count, int param_dtype, int 
     a.beta1_rest = (float)(1.0 - numbers->beta1);
     a.beta2 = (float)numbers->beta2;
     a.beta2_rest = (float)(1.0 - numbers->beta2);
-    a.eps = (float)numbers->eps;
+    // An eps that is more than 0 stays so, and its reciprocal a number: 0 over it is 0.
+    a.eps = numbers->eps > 0.0 ? std::max((float)numbers->eps, state_bits == 8 ? 0x1p-126f : 0x1p-149f) : 0.f;
     a.lr = (float)numbers->lr;
     a.weight_decay = (float)numbers->weight_decay;
     a.log_beta1 = log(numbers->beta1);

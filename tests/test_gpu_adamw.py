@@ -225,6 +225,21 @@ def test_zero_gradients_and_states():
             assert all((x.view(torch.uint8) == 0).all() for x in t[name])
 
 
+@pytest.mark.parametrize("eps", [1e-38, 1e-40, 1e-44, 1e-60])
+def test_an_eps_below_the_smallest_normal_number(eps):
+    """0 over it is 0, in 8 bits too, where the quotient is by a reciprocal."""
+    for bits in (32, 8):
+        t = make([700, 20], FP32, FP32, bits)
+        s = binding.adamw_state(t["params"], bits)
+        t |= dict(exp_avg=s.exp_avg, exp_avg_sq=s.exp_avg_sq, exp_avg_scale=s.exp_avg_scale,
+                  exp_avg_sq_scale=s.exp_avg_sq_scale)
+        for g in t["grads"]:
+            g[::2] = 0
+        before = copies(t)
+        binding.adamw_step(**t, step=1, **HYPER | dict(eps=eps))
+        check(before, t, 1, eps=eps)
+
+
 def test_small_second_moments_are_never_lost():
     """A block with one large gradient: the others' sqrt(v) would be 0 in 8 bits, and their step m / eps."""
     t = make([256], FP32, FP32, 8)
