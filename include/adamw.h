@@ -10,8 +10,9 @@
  *           - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
  *
  *   in fp32 (1 - beta and 1 - beta^step in fp64, then rounded); in m, v and sqrt(v) every
- *   product, sum and root is rounded as it is written.  An eps above 0 counts as 2^-149
- *   at least, as 2^-126 with moments of 8 bits.  p
+ *   product, sum and root is rounded as it is written.  The step's quotient is fp32's with
+ *   moments of 32 bits, with 8 a product by the hardware's reciprocal (off by 2^-22 of
+ *   itself at most); an eps above 0 counts as 2^-149 at least, as 2^-126 with 8 bits.  p
  *   is the master weight where there is one; the parameter is then p rounded to bf16.  A bf16
  *   parameter without a master is rounded to nearest, so steps below half its last bit
  *   leave it as it is.
@@ -93,7 +94,8 @@ struct adamw_numbers {
  * when it returns.  All parameters have one type, all gradients one, all states
  * state_bits (8 or 32); either every tensor has a master or none has.  Parameters,
  * masters, moments and scales are written in place, of any sizes (0 included) and
- * alignment above their element's; two of them must not overlap, nor one a gradient.
+ * alignment above their element's; two of them must not overlap (ADAMW_ERR_ALIAS), nor one a gradient
+ * (which is not checked; one gradient may be several tensors').
  * Asynchronous on `stream`, one launch for each 48 tensors; nothing is allocated, so it
  * may be captured.  On an error nothing is enqueued (ADAMW_ERR_LAUNCH aside). */
 int adamw_step(const struct adamw_tensor* tensors, int64_t count, int param_dtype, int grad_dtype,

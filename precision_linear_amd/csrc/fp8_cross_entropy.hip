@@ -13,9 +13,10 @@
 // of dz, written by rows (for dx) and by columns (for dw), then the two products.
 // The row's scale is known beforehand (the target's element is a row's largest), and
 // the row's factor r = dloss h goes to the other operand of dw, so one set of codes
-// serves both products.  The vocabulary comes in pieces that keep the codes in
-// kCodeBytes of workspace; dx's fp32 sums stay in tiles of the accumulators' own
-// layout from piece to piece.
+// serves both products.  The vocabulary comes in pieces of 256 entries or
+// more that keep the codes in kCodeBytes of workspace (up to 2^20 rows; beyond, 256 entries take 512
+// bytes a row, 4 GiB at 2^23); dx's fp32 sums stay in 256 x 256 tiles of the accumulators' own
+// layout from piece to piece (1 KiB for each row and 256 columns begun).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -230,7 +231,7 @@ bool at(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 constexpr int64_t kMaxDim = int64_t(1) << 23;
 constexpr int64_t kCounterArea = int64_t(256) << 10;   // the multiply's arrival counters
-constexpr int64_t kCodeBytes = int64_t(512) << 20;     // of a piece's codes, both layouts
+constexpr int64_t kCodeBytes = int64_t(512) << 20;     // of a piece's codes, both layouts, up to 2^20 rows
 
 int loss_shape(int64_t M, int64_t V, int64_t K) {
     if (M < 0 || M > kMaxDim || V < 1 || V > kMaxDim || K < 16 || K > kMaxDim || K % 16 != 0) return FP8MM_ERR_SHAPE;

@@ -1866,9 +1866,6 @@ __device__ __forceinline__ void pp_compute(pp::acc_t (&acc)[pp::FN][pp::FM],
                 acc[i][j] = Mfma<pp::MI>::template run<FMT>(fb[ks][i], fa[ks][j], acc[i][j]);
 }
 
-// One work unit: output tile t and its K slices kb .. kb + n - 1 (the whole
-// K range without split-K; one of `splits` consecutive ranges with it).  The
-// unit walks its slices starting at kb + rot and wraps (see the kernel head).
 // The offsets of PpLoads, made anew after the linear layer's epilogue so that
 // they take no registers from it.
 __device__ __forceinline__ PpLoads pp_loads(int K, int q, int lane) {
@@ -1880,6 +1877,9 @@ __device__ __forceinline__ PpLoads pp_loads(int K, int q, int lane) {
     return L;
 }
 
+// One work unit: output tile t and its K slices kb .. kb + n - 1 (the whole
+// K range without split-K; one of `splits` consecutive ranges with it).  The
+// unit walks its slices starting at kb + rot and wraps (see the kernel head).
 struct PpTile {
     int row0, col0;
     int t, kb, n, rot;
